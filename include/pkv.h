@@ -470,6 +470,167 @@ pkv_status pkv_paged_extend_attn_append(const pkv_cache_desc* desc, void* k_cach
                                         float* lse_out, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * A cache held in 8 bits with a scale for each block of tokens and kv head.
+ *
+ * The fp8_e4m3 cache above has one scale per tensor, which its user has to know
+ * before the first token arrives.  The calls below keep, beside the same
+ * pools of codes, k_scales and v_scales: float [num_blocks][num_kv_heads],
+ * device, owned by the caller; value = code * scale of its block and head.
+ * desc->cache_dtype must be PKV_FP8_E4M3 (else PKV_ERR_UNSUPPORTED);
+ * desc->k_scale / v_scale are not used (finite and > 0 all the same).
+ *
+ * pkv_kv_append_block_scaled -- quantise the K/V rows of new tokens into their
+ * blocks.
+ *
+ * Row q_indptr[b] + i of k_new / v_new goes to position prefix_lens[b] + i of
+ * request b (the layout of the extend calls; one row per request is a decode
+ * step).  For every (block, kv head), K and V apart:
+ *   s = the smallest power of two >= 2^-126 with max |x| <= 448 s over the
+ *       finite new values x of the block (2^-126 if all are 0);
+ *   a block that holds positions before prefix_lens[b] keeps them: its scale
+ *       becomes the larger of s and its old scale (rounded up to a power of two
+ *       if the caller wrote another), and the kept codes c become
+ *       e4m3(c * old / new) (exact but where a code becomes subnormal);
+ *   any other block takes s, whatever it held before;
+ *   new codes are e4m3(x / scale): one rounding, to nearest even; infinities
+ *       become +-448 * scale, NaN stays NaN.
+ * Codes of positions at or after the request's new end are left as they were
+ * (they belong to no token); so are all other blocks.
+ * k_new, v_new:  [total_rows][num_kv_heads][head_dim] act dtype, 16-byte aligned.
+ * q_indptr:      int32 [batch+1], device, non-decreasing, q_indptr[0] = 0.
+ * prefix_lens:   int32 [batch], device: the tokens request b already holds.
+ * max_suffix_len: host bound of the rows per request; rows beyond it are not
+ *                written and set PKV_DEVERR_BAD_LENGTH.
+ * The blocks written must not be shared by two requests of the call (nor appear
+ * twice in a request's table): which of the two wins is then unspecified.  A
+ * request whose rows do not lie in [0, total_rows) or whose positions do not fit
+ * its table is not written (PKV_DEVERR_BAD_LENGTH), a block id outside the
+ * pool is skipped (PKV_DEVERR_BAD_SLOT).
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_kv_append_block_scaled(const pkv_cache_desc* desc, void* k_cache, void* v_cache,
+                                      float* k_scales, float* v_scales, const void* k_new,
+                                      const void* v_new, pkv_dtype act_dtype,
+                                      const int32_t* q_indptr, const int32_t* prefix_lens,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      int32_t batch, int32_t total_rows, int32_t max_suffix_len,
+                                      cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_kv_gather -- read tokens' K/V rows back out of a cache of any kind.
+ *
+ * Row row_indptr[b] + i of k_out / v_out is position start_positions[b] + i of
+ * request b, read through its block table: for moving a request to another
+ * pool, for swapping it out, or for looking at what a cache holds.
+ *   16-bit cache: the bits (act dtype == cache dtype).
+ *   fp8 cache:    act(code * k_scale) (resp. v_scale), rounded once; with
+ *                 k_scales and v_scales (not null, together) code * scale of the
+ *                 code's block and head, and for f16 outputs finite values
+ *                 beyond the type's range become its largest (the code of a
+ *                 value near 65504 may stand for a larger one).
+ * k_out, v_out:  [total_rows][num_kv_heads][head_dim] act dtype, 16-byte
+ *                aligned, not overlapping the cache.
+ * row_indptr:    int32 [batch+1], device, non-decreasing; rows that no request
+ *                owns are left as they were.
+ * A position outside the request's table gives zeros (PKV_DEVERR_BAD_LENGTH), a
+ * block id outside the pool too (PKV_DEVERR_BAD_BLOCK).
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_kv_gather(const pkv_cache_desc* desc, const void* k_cache, const void* v_cache,
+                         const float* k_scales, const float* v_scales, void* k_out, void* v_out,
+                         pkv_dtype act_dtype, const int32_t* row_indptr,
+                         const int32_t* start_positions, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, int32_t batch, int32_t total_rows,
+                         cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention with a sliding window and a few first tokens that stay visible.
+ *
+ * A query at position p sees the keys j <= p with j > p - window (the last
+ * `window` tokens, its own included) or j < sink_tokens.  A block that no query
+ * of the call sees is not read and its block table entry is not looked up: a
+ * caller may have given it back (entry -1, or now another request's).  Blocks
+ * that hold a visible token stay valid as a whole.
+ * window:       >= 1 (pkv_..._window); pkv_..._block_scaled take 0 for "every
+ *               token", whatever sink_tokens.  sink_tokens: >= 0.
+ *
+ * pkv_paged_decode_attn_window -- pkv_paged_decode_attn under a window: the
+ * query is at position seq_lens[b] - 1.  A long sequence costs what its visible
+ * tokens cost.  max_seq_len bounds seq_lens as there, and the workspace is
+ * pkv_decode_window_workspace_bytes() (window 0: as without one).
+ * ------------------------------------------------------------------------- */
+size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                         int32_t num_q_heads, int32_t max_seq_len, int32_t window,
+                                         int32_t sink_tokens, int32_t num_splits);
+
+pkv_status pkv_paged_decode_attn_window(const pkv_cache_desc* desc, const void* k_cache,
+                                        const void* v_cache, const void* q, void* out,
+                                        pkv_dtype act_dtype, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                        int32_t batch, int32_t num_q_heads, float sm_scale,
+                                        int32_t max_seq_len, int32_t window, int32_t sink_tokens,
+                                        int32_t num_splits, float* lse_out, void* workspace,
+                                        size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_paged_decode_attn_block_scaled -- pkv_paged_decode_attn over a cache with
+ * a scale per block and kv head (pkv_kv_append_block_scaled), optionally under
+ * a window (0: none).  The scales may be any finite positive values; they are
+ * applied in fp32 (K's to the scores, V's as each block's part is added up).
+ * A block id outside the pool reads zeros (PKV_DEVERR_BAD_BLOCK).  The
+ * workspace is pkv_decode_window_workspace_bytes().
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_paged_decode_attn_block_scaled(
+    const pkv_cache_desc* desc, const void* k_cache, const void* v_cache, const float* k_scales,
+    const float* v_scales, const void* q, void* out, pkv_dtype act_dtype,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    int32_t batch, int32_t num_q_heads, float sm_scale, int32_t max_seq_len, int32_t window,
+    int32_t sink_tokens, int32_t num_splits, float* lse_out, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_paged_extend_attn_window -- pkv_paged_extend_attn under a window: row i
+ * of request b is at position prefix_lens[b] + i.  The workspace is optional
+ * as there (pkv_extend_widen_workspace_bytes()).  A request whose prefix is
+ * negative or whose keys do not fit its table is not computed
+ * (PKV_DEVERR_BAD_LENGTH).  V of a key that no row of a work item (two 128-row
+ * tiles) sees does not touch its outputs, whatever it holds; a key that some of
+ * those rows see must be finite for all of them, as in the plain call.
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_paged_extend_attn_window(const pkv_cache_desc* desc, const void* k_cache,
+                                        const void* v_cache, const void* q, void* out,
+                                        pkv_dtype act_dtype, const int32_t* q_indptr,
+                                        const int32_t* prefix_lens, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, int32_t batch,
+                                        int32_t num_q_heads, float sm_scale, int32_t total_q_rows,
+                                        int32_t max_suffix_len, int32_t max_total_len,
+                                        int32_t window, int32_t sink_tokens, float* lse_out,
+                                        void* workspace, size_t workspace_bytes,
+                                        cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_paged_extend_attn_block_scaled -- pkv_paged_extend_attn over a cache with
+ * a scale per block and kv head, optionally under a window (0: none).
+ * workspace:    required: pkv_extend_block_scaled_workspace_bytes() bytes or
+ *               more, 256-byte aligned, any contents (else PKV_ERR_WORKSPACE).
+ *               The call first widens each block that its rows see, once,
+ *               into 16-bit copies there: K as code * scale in the act dtype,
+ *               V as code * scale in f16.  With powers of two as scales (what
+ *               the append writes) K is exact in bf16, and K and V in f16 within
+ *               that type's range (finite values beyond it become its largest,
+ *               values below 2^-14 lose bits); other scales round to nearest.
+ *               Calls that run at the same time need workspaces of their own.
+ * At most 65,535 requests (else PKV_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------- */
+size_t pkv_extend_block_scaled_workspace_bytes(const pkv_cache_desc* desc);
+
+pkv_status pkv_paged_extend_attn_block_scaled(
+    const pkv_cache_desc* desc, const void* k_cache, const void* v_cache, const float* k_scales,
+    const float* v_scales, const void* q, void* out, pkv_dtype act_dtype, const int32_t* q_indptr,
+    const int32_t* prefix_lens, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    int32_t batch, int32_t num_q_heads, float sm_scale, int32_t total_q_rows,
+    int32_t max_suffix_len, int32_t max_total_len, int32_t window, int32_t sink_tokens,
+    float* lse_out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Prefix index (host): radix tree over token ids with leaf-first LRU eviction.
  *
  * "PagedAttention과 RadixAttention으로 LLM KV 캐시 최적화", section 03: the KV

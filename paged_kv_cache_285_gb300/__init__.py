@@ -18,6 +18,13 @@ kernel itself), paged_decode_attn_shared_prefix
 group), RadixIndex (the host prefix index that hands out block tables and
 prefix lengths; host int32 arrays in, host arrays out) and chain_hash (salted
 chain hashes of full blocks, as block identifiers).
+
+A cache of fp8 codes with a scale per block and kv head: kv_append_block_scaled
+(quantised as it is written), paged_decode_attn_block_scaled and
+paged_extend_attn_block_scaled; kv_gather reads rows back out of any cache.
+paged_decode_attn_window and paged_extend_attn_window: attention with a
+sliding window and a few first tokens that stay visible (the block-scaled calls
+take a window too).
 """
 from __future__ import annotations
 
@@ -33,7 +40,11 @@ __all__ = ["F16", "BF16", "FP8_E4M3", "PkvError", "CacheDesc", "lib_path", "load
            "paged_decode_attn_append", "RadixIndex", "NO_SPACE", "chain_hash",
            "paged_decode_attn_shared_prefix", "shared_prefix_decode_workspace_bytes",
            "paged_extend_attn_append", "paged_extend_attn_shared_prefix",
-           "extend_shared_prefix_workspace_bytes", "extend_widen_workspace_bytes"]
+           "extend_shared_prefix_workspace_bytes", "extend_widen_workspace_bytes",
+           "kv_append_block_scaled", "kv_gather", "decode_window_workspace_bytes",
+           "paged_decode_attn_window", "paged_decode_attn_block_scaled",
+           "paged_extend_attn_window", "extend_block_scaled_workspace_bytes",
+           "paged_extend_attn_block_scaled"]
 
 F16, BF16, FP8_E4M3 = 0, 1, 2
 NO_SPACE = 5  # PKV_ERR_NO_SPACE
@@ -121,6 +132,29 @@ def load():
         lib.pkv_paged_decode_attn_shared_prefix.restype = ctypes.c_int
         lib.pkv_chain_hash.argtypes = [P, P, I32, I32, P, P, I32, P]
         lib.pkv_chain_hash.restype = ctypes.c_int
+        I = ctypes.c_int
+        lib.pkv_kv_append_block_scaled.argtypes = [D, P, P, P, P, P, P, I, P, P, P, I32, I32, I32,
+                                                   I32, P]
+        lib.pkv_kv_append_block_scaled.restype = I
+        lib.pkv_kv_gather.argtypes = [D, P, P, P, P, P, P, I, P, P, P, I32, I32, I32, P]
+        lib.pkv_kv_gather.restype = I
+        lib.pkv_decode_window_workspace_bytes.argtypes = [D, I32, I32, I32, I32, I32, I32]
+        lib.pkv_decode_window_workspace_bytes.restype = SZ
+        lib.pkv_paged_decode_attn_window.argtypes = [D, P, P, P, P, I, P, I32, P, I32, I32, F, I32,
+                                                     I32, I32, I32, P, P, SZ, P]
+        lib.pkv_paged_decode_attn_window.restype = I
+        lib.pkv_paged_decode_attn_block_scaled.argtypes = [D, P, P, P, P, P, P, I, P, I32, P, I32,
+                                                           I32, F, I32, I32, I32, I32, P, P, SZ, P]
+        lib.pkv_paged_decode_attn_block_scaled.restype = I
+        lib.pkv_paged_extend_attn_window.argtypes = [D, P, P, P, P, I, P, P, P, I32, I32, I32, F,
+                                                     I32, I32, I32, I32, I32, P, P, SZ, P]
+        lib.pkv_paged_extend_attn_window.restype = I
+        lib.pkv_extend_block_scaled_workspace_bytes.argtypes = [D]
+        lib.pkv_extend_block_scaled_workspace_bytes.restype = SZ
+        lib.pkv_paged_extend_attn_block_scaled.argtypes = [D, P, P, P, P, P, P, I, P, P, P, I32, I32,
+                                                           I32, F, I32, I32, I32, I32, I32, P, P,
+                                                           SZ, P]
+        lib.pkv_paged_extend_attn_block_scaled.restype = I
         VP = ctypes.c_void_p
         lib.pkv_radix_create.argtypes = [I32, I32, ctypes.POINTER(VP)]
         lib.pkv_radix_create.restype = ctypes.c_int
@@ -481,6 +515,191 @@ def paged_extend_attn_append(k_cache, v_cache, k_new, v_new, q, out, q_indptr, p
                                           hq, float(sm_scale), rows, int(max_suffix_len),
                                           int(max_total_len), _ptr(lse_out), _stream(stream))
     _check(st, "pkv_paged_extend_attn_append")
+
+
+def _pointers(device, *tensors):
+    """Data pointers of contiguous tensors (or None) that all lie on `device`."""
+    if device.type != "cuda":
+        raise ValueError("libpkv takes device tensors")
+    ptrs = []
+    for t in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.device != device:
+            raise ValueError(f"every tensor of the call must be on {device}, got one on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("libpkv takes contiguous tensors")
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _run(what, device, stream, *args):
+    """Call a C entry point whose last argument is the stream (None: the current one of
+    `device`), with `device` current."""
+    fn = getattr(load(), what)
+    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, s)
+    _check(st, what)
+
+
+def _scales(k_cache, k_scales, v_scales):
+    """Scales per block and kv head of a cache of fp8 codes."""
+    want = (int(k_cache.shape[0]), int(k_cache.shape[1]))
+    _shape("k_scales", k_scales, want, torch.float32)
+    _shape("v_scales", v_scales, want, torch.float32)
+
+
+def _ws_bytes(workspace):
+    return workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def kv_append_block_scaled(k_cache, v_cache, k_scales, v_scales, k_new, v_new, q_indptr,
+                           prefix_lens, block_tables, max_suffix_len, stream=None):
+    """pkv_kv_append_block_scaled: k_new/v_new [rows, Hkv, D] act dtype; row q_indptr[b] + i goes
+    to position prefix_lens[b] + i of request b, quantised with a power-of-two scale per block
+    and kv head.  k_scales/v_scales float32 [num_blocks, Hkv]; q_indptr int32 [B+1]; prefix_lens
+    int32 [B]; max_suffix_len bounds the rows per request."""
+    _need(torch.int32, q_indptr=q_indptr, prefix_lens=prefix_lens, block_tables=block_tables)
+    hkv, d = _cache_pair(k_cache, v_cache)
+    _scales(k_cache, k_scales, v_scales)
+    rows, _ = _rows("k_new", k_new, d)
+    _shape("k_new", k_new, (rows, hkv, d))
+    _shape("v_new", v_new, (rows, hkv, d), k_new.dtype)
+    if prefix_lens.dim() != 1:
+        raise ValueError("prefix_lens must be [batch]")
+    batch = int(prefix_lens.shape[0])
+    _shape("q_indptr", q_indptr, (batch + 1,))
+    _table("block_tables", block_tables, batch)
+    desc = _desc(k_cache, 1.0, 1.0)
+    kc, vc, ks, vs, kn, vn, qi, pl, bt = _pointers(
+        k_cache.device, k_cache, v_cache, k_scales, v_scales, k_new, v_new, q_indptr, prefix_lens,
+        block_tables)
+    _run("pkv_kv_append_block_scaled", k_cache.device, stream, ctypes.byref(desc), kc, vc, ks, vs,
+         kn, vn, _dtype_code(k_new), qi, pl, bt, int(block_tables.shape[1]), batch, rows,
+         int(max_suffix_len))
+
+
+def kv_gather(k_cache, v_cache, k_out, v_out, row_indptr, start_positions, block_tables,
+              k_scale=1.0, v_scale=1.0, k_scales=None, v_scales=None, stream=None):
+    """pkv_kv_gather: rows row_indptr[b] .. row_indptr[b+1]-1 of k_out/v_out [rows, Hkv, D] (f16
+    or bf16) are positions start_positions[b] ... of request b.  k_scale/v_scale: an fp8 cache's
+    scales per tensor; k_scales/v_scales float32 [num_blocks, Hkv]: scales per block and head."""
+    _need(torch.int32, row_indptr=row_indptr, start_positions=start_positions,
+          block_tables=block_tables)
+    hkv, d = _cache_pair(k_cache, v_cache)
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales come together")
+    _scales(k_cache, k_scales, v_scales)
+    rows, _ = _rows("k_out", k_out, d)
+    _shape("k_out", k_out, (rows, hkv, d))
+    _shape("v_out", v_out, (rows, hkv, d), k_out.dtype)
+    if start_positions.dim() != 1:
+        raise ValueError("start_positions must be [batch]")
+    batch = int(start_positions.shape[0])
+    _shape("row_indptr", row_indptr, (batch + 1,))
+    _table("block_tables", block_tables, batch)
+    desc = _desc(k_cache, k_scale, v_scale)
+    kc, vc, ks, vs, ko, vo, ri, sp, bt = _pointers(
+        k_cache.device, k_cache, v_cache, k_scales, v_scales, k_out, v_out, row_indptr,
+        start_positions, block_tables)
+    _run("pkv_kv_gather", k_cache.device, stream, ctypes.byref(desc), kc, vc, ks, vs, ko, vo,
+         _dtype_code(k_out), ri, sp, bt, int(block_tables.shape[1]), batch, rows)
+
+
+def decode_window_workspace_bytes(k_cache, batch, num_q_heads, max_seq_len, window=0,
+                                  sink_tokens=0, num_splits=0) -> int:
+    """pkv_decode_window_workspace_bytes: the workspace of paged_decode_attn_window and
+    paged_decode_attn_block_scaled."""
+    desc = _desc(k_cache, 1.0, 1.0)
+    return int(load().pkv_decode_window_workspace_bytes(ctypes.byref(desc), batch, num_q_heads,
+                                                        max_seq_len, window, sink_tokens,
+                                                        num_splits))
+
+
+def paged_decode_attn_window(k_cache, v_cache, q, out, block_tables, seq_lens, sm_scale,
+                             max_seq_len, window, sink_tokens=0, k_scale=1.0, v_scale=1.0,
+                             num_splits=0, lse_out=None, workspace=None, stream=None):
+    """pkv_paged_decode_attn_window: paged_decode_attn where each request's query sees its last
+    `window` tokens and its first `sink_tokens`.  ``workspace`` is a uint8 device tensor of at
+    least decode_window_workspace_bytes() bytes."""
+    _need(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
+    b, hq = _decode_shapes(k_cache, v_cache, q, out, block_tables, seq_lens, lse_out)
+    desc = _desc(k_cache, k_scale, v_scale)
+    kc, vc, qp, op, bt, sl, lse, ws = _pointers(q.device, k_cache, v_cache, q, out, block_tables,
+                                                seq_lens, lse_out, workspace)
+    _run("pkv_paged_decode_attn_window", q.device, stream, ctypes.byref(desc), kc, vc, qp, op,
+         _dtype_code(q), bt, int(block_tables.shape[1]), sl, b, hq, float(sm_scale),
+         int(max_seq_len), int(window), int(sink_tokens), int(num_splits), lse, ws,
+         _ws_bytes(workspace))
+
+
+def paged_decode_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out, block_tables,
+                                   seq_lens, sm_scale, max_seq_len, window=0, sink_tokens=0,
+                                   num_splits=0, lse_out=None, workspace=None, stream=None):
+    """pkv_paged_decode_attn_block_scaled: paged_decode_attn over fp8 codes with k_scales/v_scales
+    float32 [num_blocks, Hkv]; window 0: every token, else as paged_decode_attn_window (the same
+    workspace)."""
+    _need(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
+    b, hq = _decode_shapes(k_cache, v_cache, q, out, block_tables, seq_lens, lse_out)
+    _scales(k_cache, k_scales, v_scales)
+    desc = _desc(k_cache, 1.0, 1.0)
+    kc, vc, ks, vs, qp, op, bt, sl, lse, ws = _pointers(
+        q.device, k_cache, v_cache, k_scales, v_scales, q, out, block_tables, seq_lens, lse_out,
+        workspace)
+    _run("pkv_paged_decode_attn_block_scaled", q.device, stream, ctypes.byref(desc), kc, vc, ks, vs,
+         qp, op, _dtype_code(q), bt, int(block_tables.shape[1]), sl, b, hq, float(sm_scale),
+         int(max_seq_len), int(window), int(sink_tokens), int(num_splits), lse, ws,
+         _ws_bytes(workspace))
+
+
+def paged_extend_attn_window(k_cache, v_cache, q, out, q_indptr, prefix_lens, block_tables,
+                             sm_scale, max_suffix_len, max_total_len, window, sink_tokens=0,
+                             k_scale=1.0, v_scale=1.0, lse_out=None, workspace=None, stream=None):
+    """pkv_paged_extend_attn_window: paged_extend_attn where the row at position p sees keys
+    p - window + 1 .. p and the first `sink_tokens`.  workspace: optional, as there."""
+    _need(torch.int32, q_indptr=q_indptr, prefix_lens=prefix_lens, block_tables=block_tables)
+    rows, hq, batch = _extend_shapes(k_cache, v_cache, q, out, q_indptr, prefix_lens,
+                                     block_tables, lse_out)
+    desc = _desc(k_cache, k_scale, v_scale)
+    kc, vc, qp, op, qi, pl, bt, lse, ws = _pointers(q.device, k_cache, v_cache, q, out, q_indptr,
+                                                    prefix_lens, block_tables, lse_out, workspace)
+    _run("pkv_paged_extend_attn_window", q.device, stream, ctypes.byref(desc), kc, vc, qp, op,
+         _dtype_code(q), qi, pl, bt, int(block_tables.shape[1]), batch, hq, float(sm_scale), rows,
+         int(max_suffix_len), int(max_total_len), int(window), int(sink_tokens), lse, ws,
+         _ws_bytes(workspace))
+
+
+def extend_block_scaled_workspace_bytes(k_cache) -> int:
+    """pkv_extend_block_scaled_workspace_bytes: the workspace that paged_extend_attn_block_scaled
+    needs (16-bit copies of the K and V pools, and the per-block claims)."""
+    desc = _desc(k_cache, 1.0, 1.0)
+    return int(load().pkv_extend_block_scaled_workspace_bytes(ctypes.byref(desc)))
+
+
+def paged_extend_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out, q_indptr,
+                                   prefix_lens, block_tables, sm_scale, max_suffix_len,
+                                   max_total_len, window=0, sink_tokens=0, lse_out=None,
+                                   workspace=None, stream=None):
+    """pkv_paged_extend_attn_block_scaled: paged_extend_attn over fp8 codes with k_scales/v_scales
+    float32 [num_blocks, Hkv]; window 0: every key, else as paged_extend_attn_window.
+    workspace: a uint8 device tensor of extend_block_scaled_workspace_bytes() bytes or more."""
+    _need(torch.int32, q_indptr=q_indptr, prefix_lens=prefix_lens, block_tables=block_tables)
+    rows, hq, batch = _extend_shapes(k_cache, v_cache, q, out, q_indptr, prefix_lens,
+                                     block_tables, lse_out)
+    _scales(k_cache, k_scales, v_scales)
+    desc = _desc(k_cache, 1.0, 1.0)
+    kc, vc, ks, vs, qp, op, qi, pl, bt, lse, ws = _pointers(
+        q.device, k_cache, v_cache, k_scales, v_scales, q, out, q_indptr, prefix_lens, block_tables,
+        lse_out, workspace)
+    _run("pkv_paged_extend_attn_block_scaled", q.device, stream, ctypes.byref(desc), kc, vc, ks, vs,
+         qp, op, _dtype_code(q), qi, pl, bt, int(block_tables.shape[1]), batch, hq,
+         float(sm_scale), rows, int(max_suffix_len), int(max_total_len), int(window),
+         int(sink_tokens), lse, ws, _ws_bytes(workspace))
 
 
 def chain_hash(tokens, token_indptr, block_size, hashes, salts=None, stream=None):

@@ -515,8 +515,47 @@ pkv_status pkv_paged_decode_attn_shared_prefix(
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// What a decode or extend call sees: scales per block and kv head (null:
+// none), and a window with sink tokens (window 0: every token).
+struct AttnView {
+  const float* k_scales;
+  const float* v_scales;
+  int32_t window;
+  int32_t sink_tokens;
+};
+
+static pkv_status check_view(const pkv_cache_desc* desc, const AttnView& w, bool scaled) {
+  if (w.window < 0 || w.sink_tokens < 0) return PKV_ERR_INVALID_ARG;
+  if (!scaled) return PKV_OK;
+  if (desc->cache_dtype != PKV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
+}
+static pkv_status check_scales(const float* k_scales, const float* v_scales) {
+  if (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4))
+    return PKV_ERR_INVALID_ARG;
+  return PKV_OK;
+}
+
+// The desc of a block-scaled cache: its per-tensor scales are not used.
+static pkv_cache_desc scaled_desc(const pkv_cache_desc* desc) {
+  pkv_cache_desc d = *desc;
+  d.k_scale = d.v_scale = 1.f;
+  return d;
+}
+
+// Most tokens that the decode kernel goes over for a query that sees
+// max_seq_len tokens under a window: whole 16-token tiles of the sinks and of
+// the window (which may begin and end inside a tile).
+static int visible_bound(int max_seq_len, int window, int sink_tokens) {
+  if (window <= 0) return max_seq_len;
+  const int64_t tiles = ((int64_t)window + kSubTokens - 1) / kSubTokens + 1 +
+                        ((int64_t)sink_tokens + kSubTokens - 1) / kSubTokens;
+  return (int)std::min<int64_t>(max_seq_len, tiles * kSubTokens);
+}
+
 // Decode, optionally with the current token's K/V (k_new/v_new, [B][Hkv][D]
-// act dtype) appended to position seq_len-1 inside the decode kernel.
+// act dtype) appended to position seq_len-1 inside the decode kernel, or
+// through a view (a window and / or scales per block).
 static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
                                 const void* v_cache, const void* k_new, const void* v_new,
                                 const void* q, void* out, pkv_dtype act_dtype,
@@ -524,7 +563,7 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
                                 const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
                                 float sm_scale, int32_t max_seq_len, int32_t num_splits,
                                 float* lse_out, void* workspace, size_t workspace_bytes,
-                                cudaStream_t stream) {
+                                cudaStream_t stream, const AttnView* view = nullptr) {
   pkv_status st = check_desc(desc);
   if (st != PKV_OK) return st;
   if ((st = check_act(desc, act_dtype)) != PKV_OK) return st;
@@ -544,7 +583,8 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
   cudaError_t e;
   DeviceState* ds = device_state(&e);
   if (!ds) return PKV_ERR_CUDA;
-  const DecodePlan pl = plan_decode(desc, batch, num_q_heads, max_seq_len, num_splits, ds->sm_count);
+  const int plan_len = view ? visible_bound(max_seq_len, view->window, view->sink_tokens) : max_seq_len;
+  const DecodePlan pl = plan_decode(desc, batch, num_q_heads, plan_len, num_splits, ds->sm_count);
   if (pl.ws_bytes > 0 && (!workspace || workspace_bytes < pl.ws_bytes || !aligned(workspace, 256)))
     return PKV_ERR_WORKSPACE;
   if (pl.splits > 65535) return PKV_ERR_UNSUPPORTED;
@@ -581,6 +621,15 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
   ap.v_scale = desc->v_scale;
   ap.k_rcp = (float)(1.0 / (double)desc->k_scale);
   ap.v_rcp = (float)(1.0 / (double)desc->v_scale);
+  if (view) {
+    ap.window = view->window;
+    ap.sink_tokens = view->sink_tokens;
+    ap.k_scales = view->k_scales;
+    ap.v_scales = view->v_scales;
+    e = launch_decode_window(kmap, vmap, p, ap, desc->head_dim, (int)desc->cache_dtype,
+                             (int)act_dtype, stream);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  }
   e = launch_decode(kmap, vmap, p, ap, desc->head_dim, (int)desc->cache_dtype, (int)act_dtype,
                     stream);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
@@ -610,6 +659,139 @@ pkv_status pkv_paged_decode_attn_append(const pkv_cache_desc* desc, void* k_cach
   return decode_common(desc, k_cache, v_cache, k_new, v_new, q, out, act_dtype, block_tables,
                        max_blocks_per_seq, seq_lens, batch, num_q_heads, sm_scale, max_seq_len,
                        num_splits, lse_out, workspace, workspace_bytes, stream);
+}
+
+size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                         int32_t num_q_heads, int32_t max_seq_len, int32_t window,
+                                         int32_t sink_tokens, int32_t num_splits) {
+  if (max_seq_len < 0 || window < 0 || sink_tokens < 0) return 0;
+  return pkv_decode_workspace_bytes(desc, batch, num_q_heads,
+                                    visible_bound(max_seq_len, window, sink_tokens), num_splits);
+}
+
+pkv_status pkv_paged_decode_attn_window(const pkv_cache_desc* desc, const void* k_cache,
+                                        const void* v_cache, const void* q, void* out,
+                                        pkv_dtype act_dtype, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                        int32_t batch, int32_t num_q_heads, float sm_scale,
+                                        int32_t max_seq_len, int32_t window, int32_t sink_tokens,
+                                        int32_t num_splits, float* lse_out, void* workspace,
+                                        size_t workspace_bytes, cudaStream_t stream) {
+  const AttnView view{nullptr, nullptr, window, sink_tokens};
+  pkv_status st = check_desc(desc);
+  if (st == PKV_OK) st = check_view(desc, view, false);
+  if (st != PKV_OK) return st;
+  if (window == 0) return PKV_ERR_INVALID_ARG;
+  return decode_common(desc, k_cache, v_cache, nullptr, nullptr, q, out, act_dtype, block_tables,
+                       max_blocks_per_seq, seq_lens, batch, num_q_heads, sm_scale, max_seq_len,
+                       num_splits, lse_out, workspace, workspace_bytes, stream, &view);
+}
+
+pkv_status pkv_paged_decode_attn_block_scaled(
+    const pkv_cache_desc* desc, const void* k_cache, const void* v_cache, const float* k_scales,
+    const float* v_scales, const void* q, void* out, pkv_dtype act_dtype,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    int32_t batch, int32_t num_q_heads, float sm_scale, int32_t max_seq_len, int32_t window,
+    int32_t sink_tokens, int32_t num_splits, float* lse_out, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream) {
+  const AttnView view{k_scales, v_scales, window, sink_tokens};
+  pkv_status st = check_desc(desc);
+  if (st == PKV_OK) st = check_view(desc, view, true);
+  if (st == PKV_OK && batch > 0) st = check_scales(k_scales, v_scales);
+  if (st != PKV_OK) return st;
+  const pkv_cache_desc d = scaled_desc(desc);
+  return decode_common(&d, k_cache, v_cache, nullptr, nullptr, q, out, act_dtype, block_tables,
+                       max_blocks_per_seq, seq_lens, batch, num_q_heads, sm_scale, max_seq_len,
+                       num_splits, lse_out, workspace, workspace_bytes, stream, &view);
+}
+
+pkv_status pkv_kv_append_block_scaled(const pkv_cache_desc* desc, void* k_cache, void* v_cache,
+                                      float* k_scales, float* v_scales, const void* k_new,
+                                      const void* v_new, pkv_dtype act_dtype,
+                                      const int32_t* q_indptr, const int32_t* prefix_lens,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      int32_t batch, int32_t total_rows, int32_t max_suffix_len,
+                                      cudaStream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if ((st = check_act(desc, act_dtype)) != PKV_OK) return st;
+  if (desc->cache_dtype != PKV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
+  if (batch < 0 || max_blocks_per_seq <= 0 || total_rows < 0 || max_suffix_len < 0)
+    return PKV_ERR_INVALID_ARG;
+  if (batch == 0 || total_rows == 0 || max_suffix_len == 0) return PKV_OK;
+  if ((st = check_scales(k_scales, v_scales)) != PKV_OK) return st;
+  if (!k_cache || !v_cache || !k_new || !v_new || !q_indptr || !prefix_lens || !block_tables)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return PKV_ERR_INVALID_ARG;
+  cudaError_t e;
+  DeviceState* ds = device_state(&e);
+  if (!ds) return PKV_ERR_CUDA;
+  AppendScaledParams p{};
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.q_indptr = q_indptr;
+  p.prefix_lens = prefix_lens;
+  p.block_tables = block_tables;
+  p.err = ds->err;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = desc->num_blocks;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.batch = batch;
+  p.total_rows = total_rows;
+  p.max_suffix_len = max_suffix_len;
+  e = launch_append_scaled(p, (int)act_dtype, desc->head_dim, desc->block_size, stream);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_gather(const pkv_cache_desc* desc, const void* k_cache, const void* v_cache,
+                         const float* k_scales, const float* v_scales, void* k_out, void* v_out,
+                         pkv_dtype act_dtype, const int32_t* row_indptr,
+                         const int32_t* start_positions, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, int32_t batch, int32_t total_rows,
+                         cudaStream_t stream) {
+  pkv_status st = check_desc(desc);
+  if (st != PKV_OK) return st;
+  if ((st = check_act(desc, act_dtype)) != PKV_OK) return st;
+  if (batch < 0 || max_blocks_per_seq <= 0 || total_rows < 0) return PKV_ERR_INVALID_ARG;
+  if ((k_scales == nullptr) != (v_scales == nullptr)) return PKV_ERR_INVALID_ARG;
+  if (k_scales) {
+    if (desc->cache_dtype != PKV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
+    if ((st = check_scales(k_scales, v_scales)) != PKV_OK) return st;
+  }
+  if (batch == 0 || total_rows == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !k_out || !v_out || !row_indptr || !start_positions || !block_tables)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return PKV_ERR_INVALID_ARG;
+  cudaError_t e;
+  DeviceState* ds = device_state(&e);
+  if (!ds) return PKV_ERR_CUDA;
+  GatherParams p{};
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.row_indptr = row_indptr;
+  p.start_positions = start_positions;
+  p.block_tables = block_tables;
+  p.err = ds->err;
+  p.total_rows = total_rows;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = desc->num_blocks;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.batch = batch;
+  p.bs_shift = desc->block_size == 16 ? 4 : 5;
+  p.k_scale = desc->k_scale;
+  p.v_scale = desc->v_scale;
+  e = launch_gather(p, (int)desc->cache_dtype, (int)act_dtype, desc->head_dim, stream);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 size_t pkv_extend_workspace_bytes(const pkv_cache_desc* desc, int32_t batch, int32_t num_q_heads,
@@ -661,7 +843,8 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
                                 int32_t total_q_rows, int32_t max_suffix_len,
                                 int32_t max_total_len, float* lse_out, void* workspace,
                                 size_t workspace_bytes, cudaStream_t stream,
-                                const ExtendGroups* groups = nullptr) {
+                                const ExtendGroups* groups = nullptr,
+                                const AttnView* view = nullptr) {
   pkv_status st = check_desc(desc);
   if (st != PKV_OK) return st;
   if ((st = check_act(desc, act_dtype)) != PKV_OK) return st;
@@ -679,6 +862,9 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   const bool widen_plain = !groups && workspace != nullptr && plain_bytes > 0 &&
                            workspace_bytes >= plain_bytes && aligned(workspace, 256) &&
                            batch <= 65535;
+  // a block-scaled cache is read through its widened pages only
+  const bool scaled = view && view->k_scales;
+  if (scaled && batch > 65535) return PKV_ERR_UNSUPPORTED;
   const size_t widen_bytes = groups ? shared_prefix_widen_bytes(desc) : 0;
   // (the widening pass takes one CTA row per request: larger batches keep the
   // per-tile conversion)
@@ -691,6 +877,7 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   }
   const int32_t rows_hint = groups ? groups->max_group_rows : max_suffix_len;
   if (batch == 0 || total_q_rows == 0 || rows_hint == 0) return PKV_OK;
+  if (scaled && !widen_plain) return PKV_ERR_WORKSPACE;
   if (!k_cache || !v_cache || !q || !out || !block_tables || !q_indptr || !prefix_lens)
     return PKV_ERR_INVALID_ARG;
   if (groups && (!groups->group_indptr || !groups->group_shared)) return PKV_ERR_INVALID_ARG;
@@ -728,6 +915,8 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   p.total_rows = total_q_rows;
   p.scale_log2 = score_scale_log2(desc, sm_scale);
   p.out_scale = output_scale(desc);
+  p.window = view ? view->window : 0;
+  p.sink_tokens = view ? view->sink_tokens : 0;
   // work items per (request or group, kv head): pairs of row tiles
   if (!plan_extend(p, groups ? groups->num_groups : batch, desc->num_kv_heads, group, rows_hint,
                    ds->sm_count))
@@ -795,13 +984,22 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     int32_t* claims = reinterpret_cast<int32_t*>(base + shared_prefix_widen_bytes(desc));
     if (fp8 && (st = make_page_map(&kmap, k16, &d16)) != PKV_OK) return st;
     if ((st = make_page_map(&vmap, v16, &d16)) != PKV_OK) return st;
-    e = launch_widen_claim(fp8 ? DT_E4M3 : DT_BF16, (int)act_dtype, k_cache, v_cache, k16, v16,
-                           claims, p, desc->head_dim, desc->block_size, max_total_len,
-                           ds->sm_count, stream);
+    if (scaled)
+      e = launch_widen_scaled((int)act_dtype, k_cache, v_cache, view->k_scales, view->v_scales, k16,
+                              v16, claims, p, desc->head_dim, desc->block_size, max_total_len,
+                              ds->sm_count, stream);
+    else
+      e = launch_widen_claim(fp8 ? DT_E4M3 : DT_BF16, (int)act_dtype, k_cache, v_cache, k16, v16,
+                             claims, p, desc->head_dim, desc->block_size, max_total_len,
+                             ds->sm_count, stream);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     cache_dt = act_dtype == PKV_BF16 ? DT_BF16_V16 : DT_F16;
   }
-  e = launch_extend(kmap, vmap, qmap, omap, p, desc->head_dim, cache_dt, (int)act_dtype, stream);
+  if (p.window > 0)
+    e = launch_extend_window(kmap, vmap, qmap, omap, p, desc->head_dim, cache_dt, (int)act_dtype,
+                             stream);
+  else
+    e = launch_extend(kmap, vmap, qmap, omap, p, desc->head_dim, cache_dt, (int)act_dtype, stream);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -819,6 +1017,51 @@ pkv_status pkv_paged_extend_attn(const pkv_cache_desc* desc, const void* k_cache
                        prefix_lens, block_tables, max_blocks_per_seq, batch, num_q_heads,
                        sm_scale, total_q_rows, max_suffix_len, max_total_len, lse_out, workspace,
                        workspace_bytes, stream);
+}
+
+pkv_status pkv_paged_extend_attn_window(const pkv_cache_desc* desc, const void* k_cache,
+                                        const void* v_cache, const void* q, void* out,
+                                        pkv_dtype act_dtype, const int32_t* q_indptr,
+                                        const int32_t* prefix_lens, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, int32_t batch,
+                                        int32_t num_q_heads, float sm_scale, int32_t total_q_rows,
+                                        int32_t max_suffix_len, int32_t max_total_len,
+                                        int32_t window, int32_t sink_tokens, float* lse_out,
+                                        void* workspace, size_t workspace_bytes,
+                                        cudaStream_t stream) {
+  const AttnView view{nullptr, nullptr, window, sink_tokens};
+  pkv_status st = check_desc(desc);
+  if (st == PKV_OK) st = check_view(desc, view, false);
+  if (st != PKV_OK) return st;
+  if (window == 0) return PKV_ERR_INVALID_ARG;
+  return extend_common(desc, k_cache, v_cache, nullptr, nullptr, q, out, act_dtype, q_indptr,
+                       prefix_lens, block_tables, max_blocks_per_seq, batch, num_q_heads,
+                       sm_scale, total_q_rows, max_suffix_len, max_total_len, lse_out, workspace,
+                       workspace_bytes, stream, nullptr, &view);
+}
+
+size_t pkv_extend_block_scaled_workspace_bytes(const pkv_cache_desc* desc) {
+  if (check_desc(desc) != PKV_OK || desc->cache_dtype != PKV_FP8_E4M3) return 0;
+  return plain_widen_bytes(desc);
+}
+
+pkv_status pkv_paged_extend_attn_block_scaled(
+    const pkv_cache_desc* desc, const void* k_cache, const void* v_cache, const float* k_scales,
+    const float* v_scales, const void* q, void* out, pkv_dtype act_dtype, const int32_t* q_indptr,
+    const int32_t* prefix_lens, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    int32_t batch, int32_t num_q_heads, float sm_scale, int32_t total_q_rows,
+    int32_t max_suffix_len, int32_t max_total_len, int32_t window, int32_t sink_tokens,
+    float* lse_out, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const AttnView view{k_scales, v_scales, window, sink_tokens};
+  pkv_status st = check_desc(desc);
+  if (st == PKV_OK) st = check_view(desc, view, true);
+  if (st == PKV_OK && batch > 0) st = check_scales(k_scales, v_scales);
+  if (st != PKV_OK) return st;
+  const pkv_cache_desc d = scaled_desc(desc);
+  return extend_common(&d, k_cache, v_cache, nullptr, nullptr, q, out, act_dtype, q_indptr,
+                       prefix_lens, block_tables, max_blocks_per_seq, batch, num_q_heads,
+                       sm_scale, total_q_rows, max_suffix_len, max_total_len, lse_out, workspace,
+                       workspace_bytes, stream, nullptr, &view);
 }
 
 size_t pkv_extend_widen_workspace_bytes(const pkv_cache_desc* desc) {

@@ -29,6 +29,18 @@
 //     the softmax scale and v_scale into the output scale.
 //   * online softmax in base 2 (running max and sum per head column, max
 //     reduced over the 8 lanes that hold a column with xor-shuffles).
+//   * a window with sink tokens (WIN): the query at position n - 1 sees the
+//     first `sink_tokens` tokens and the last `window`.  The 16-token tiles
+//     that hold a visible token are numbered without the gap between the two
+//     runs; splits, pipelines and merges work on that numbering, so that the
+//     hidden tiles (and their block ids) are never read, and hidden tokens of
+//     the tiles at a run's edge are masked (score -inf, V zeroed).
+//   * scales per block and kv head (BSC, fp8 codes): a 16-token tile lies in
+//     one block, so its K scale multiplies the tile's scores and its V scale
+//     the tile's PV product as it is added to the fp32 accumulators
+//     (O = al O + s_v (V^T P^T)): scales of any size keep P in f16's range.
+//     The lane that holds a tile's block id holds its scales too, issues the
+//     tile's copies and leaves the scales in the stage's slot.
 //   * warps are combined through shared memory with their (max, sum); a split
 //     either writes the final output (single-split requests) or a normalised
 //     partial plus its log-sum-exp, merged by merge_kernel.
@@ -58,6 +70,7 @@ struct DecodeCfg {
   static constexpr int COMB_BYTES = NW * 8 * HD * 4 + NW * 8 * 2 * 4;
   static constexpr int AREA = STAGE_AREA > COMB_BYTES ? STAGE_AREA : COMB_BYTES;
   static constexpr int SMEM = 1024 /*align slack*/ + AREA + NW * NS * 8;
+  static constexpr int SMEM_BSC = SMEM + NW * NS * 8;  // and a tile's two scales per stage
 };
 
 // Byte offset of (token t, row byte x) inside a staged tile, matching the TMA
@@ -126,12 +139,33 @@ __device__ __forceinline__ int group_prefix_len(const DecodeExtraParams& ap, int
   return __ldg(ap.group_prefix_lens + lo);
 }
 
+// The tokens of request b that its query sees under a window (length n,
+// clamped by the caller): tokens 0 .. sv - 1 of the compact numbering are the
+// first tokens, later ones lie `skip` further on (sv and skip multiples of
+// 16); nv of them in all; tokens before w0 and not below `sinks` are hidden.
+struct WinSpan {
+  int w0, sinks, sv, skip, nv;
+};
+__device__ __forceinline__ WinSpan win_span(int n, int window, int sinks) {
+  WinSpan s;
+  s.w0 = max(n - window, 0);
+  s.sinks = sinks;
+  const int wt = s.w0 & ~(kSubTokens - 1);  // start of the window's first tile
+  const int se = min(sinks, n);
+  s.sv = min((se + kSubTokens - 1) & ~(kSubTokens - 1), wt);
+  s.skip = wt - s.sv;
+  s.nv = n - s.skip;
+  return s;
+}
+
 // CASC: a cascade launch (tokens from the group's shared prefix on; partials
-// in the workspace slots after the prefix's chunks, always merged).
-template <int HD, int CT, int AT, int NW, int NS, bool CASC>
+// in the workspace slots after the prefix's chunks, always merged).  WIN: a
+// window with sink tokens.  BSC: fp8 codes with scales per block and kv head.
+template <int HD, int CT, int AT, int NW, int NS, bool CASC, bool WIN, bool BSC>
 __global__ void __launch_bounds__(NW * 32)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const DecodeParams p, const DecodeExtraParams ap) {
+  static_assert(!(CASC && (WIN || BSC)) && (!BSC || CT == DT_E4M3), "unsupported combination");
   using C = DecodeCfg<HD, CT, NW, NS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -153,7 +187,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   int n = p.seq_lens[b];
   int tb = 0;  // first token of this launch (cascade: the end of the shared prefix)
   if constexpr (CASC) tb = group_prefix_len(ap, b);
-  const int cap = min(p.max_blocks * bs, (tb > 0 ? tb : 0) + p.num_splits * p.chunk);
+  const int cap = WIN ? p.max_blocks * bs
+                      : min(p.max_blocks * bs, (tb > 0 ? tb : 0) + p.num_splits * p.chunk);
   if (n < 0 || n > cap) {
     if (threadIdx.x == 0 && split == 0) set_err(p.err, 3);
     n = n < 0 ? 0 : cap;
@@ -166,6 +201,16 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     tb = (tb >> p.bs_shift) << p.bs_shift;  // only whole blocks are shared
     // the merge reads the request's span from here instead of searching again
     if (split == 0 && blockIdx.x == 0 && threadIdx.x == 0) ap.ws_span[b] = make_int2(tb, n);
+  }
+  // WIN: from here on `n` and token numbers are compact (hidden tiles left out)
+  WinSpan ws{};
+  if constexpr (WIN) {
+    ws = win_span(n, ap.window, ap.sink_tokens);
+    if (ws.nv > p.num_splits * p.chunk) {  // longer than the call's hint
+      if (threadIdx.x == 0 && split == 0) set_err(p.err, 3);
+      ws = win_span(p.num_splits * p.chunk, ap.window, ap.sink_tokens);
+    }
+    n = ws.nv;
   }
   const int t0 = tb + split * p.chunk;
   if (t0 >= n) {
@@ -274,39 +319,56 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
   // ---- block ids of this warp's tiles, 32 at a time in registers ------------
   const int32_t* bt_row = p.block_tables + (int64_t)b * p.max_blocks;
+  float2 sc_cur = make_float2(1.f, 1.f), sc_next = sc_cur;  // BSC: the tiles' K and V scales
   auto fetch = [&](int win) -> int {
     const int i = win * 32 + lane;
     int blk = -1;
     if (i < cnt) {
-      const int tok = t0 + kSubTokens * (warp + i * NW);
+      int tok = t0 + kSubTokens * (warp + i * NW);
+      if constexpr (WIN) tok += tok >= ws.sv ? ws.skip : 0;
       blk = bt_row[tok >> p.bs_shift];
       if (blk < 0 || blk >= p.num_blocks) {
         set_err(p.err, 1);
         blk = -1;  // TMA fills out-of-range tiles with zeros
       }
     }
+    if constexpr (BSC) {
+      sc_next = make_float2(1.f, 1.f);
+      if (blk >= 0) {
+        const int64_t at = (int64_t)blk * p.num_kv_heads + g;
+        sc_next = make_float2(__ldg(ap.k_scales + at), __ldg(ap.v_scales + at));
+      }
+    }
     return blk;
   };
   int win_cur = 0;
-  int bw_cur = fetch(0), bw_next = fetch(1);
-  auto blk_of = [&](int i) -> int {  // called by all lanes with a warp-uniform, rising i
+  int bw_cur = fetch(0);
+  if constexpr (BSC) sc_cur = sc_next;
+  int bw_next = fetch(1);
+  auto window_of = [&](int i) {  // called by all lanes with a warp-uniform, rising i
     while ((i >> 5) > win_cur) {
       bw_cur = bw_next;
+      if constexpr (BSC) sc_cur = sc_next;
       ++win_cur;
       bw_next = fetch(win_cur + 1);
     }
+  };
+  auto blk_of = [&](int i) -> int {
+    window_of(i);
     return __shfl_sync(kFull, bw_cur, i & 31);
   };
 
   uint8_t* wstage = smem + warp * NS * C::STAGEB;
   const uint32_t wstage_s = smem_u32(wstage);
   const uint32_t wbar_s = smem_u32(&bars[warp * NS]);
-  auto issue = [&](int i, int blk) {  // lane 0 only
+  float2* wscale = reinterpret_cast<float2*>(bars + NW * NS) + warp * NS;  // BSC
+  auto issue = [&](int i, int blk) {  // one lane only
     const int s = i % NS;
     const uint32_t bar = wbar_s + 8 * s;
     const uint32_t kdst = wstage_s + s * C::STAGEB;
     const uint32_t vdst = kdst + C::TILEB;
-    const int tok = t0 + kSubTokens * (warp + i * NW);
+    int tok = t0 + kSubTokens * (warp + i * NW);
+    if constexpr (WIN) tok += tok >= ws.sv ? ws.skip : 0;
     const int row = tok & (bs - 1);
     const int page = blk < 0 ? -1 : blk * p.num_kv_heads + g;
     mbar_arrive_expect_tx(bar, C::STAGEB);
@@ -318,12 +380,23 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       tma_load_3d(vdst + ch * kSubTokens * C::CHUNKB, &vmap, bar, ch * (C::CHUNKB / C::ELEM), row, page);
   };
 
-  {
-    const int pre = cnt < NS ? cnt : NS;
-    for (int i = 0; i < pre; ++i) {
+  auto load_tile = [&](int i) {  // the whole warp
+    if constexpr (BSC) {
+      // the scales are in place before the stage's barrier can complete
+      window_of(i);
+      if (lane == (i & 31)) {
+        wscale[i % NS] = sc_cur;
+        issue(i, bw_cur);
+      }
+    } else {
       const int blk = blk_of(i);
       if (lane == 0) issue(i, blk);
     }
+  };
+
+  {
+    const int pre = cnt < NS ? cnt : NS;
+    for (int i = 0; i < pre; ++i) load_tile(i);
   }
 
   float acc[C::MT][4];
@@ -344,6 +417,18 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint32_t vb = kb + C::TILEB;
     const int tok0 = t0 + kSubTokens * (warp + i * NW);
     const int nvalid = min(kSubTokens, t1 - tok0);
+    // WIN: rows below w_lo of the tile are hidden unless below w_sk
+    int w_lo = 0, w_sk = 0;
+    if constexpr (WIN) {
+      const int at = tok0 + (tok0 >= ws.sv ? ws.skip : 0);
+      w_lo = ws.w0 - at;
+      w_sk = ws.sinks - at;
+    }
+    auto hidden = [&](int row) -> bool {
+      return row >= nvalid || (WIN && row < w_lo && row >= w_sk);
+    };
+    float2 bsc = make_float2(1.f, 1.f);
+    if constexpr (BSC) bsc = wscale[s];
 
     // ---- S^T (16 tokens x 8 heads) = K_tile . q^T --------------------------
     float sc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -380,10 +465,11 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
 
     // ---- online softmax (base 2) over this tile, per head column --------------
-    float s0 = sc[0] * p.scale_log2, s1 = sc[1] * p.scale_log2;
-    float s2 = sc[2] * p.scale_log2, s3 = sc[3] * p.scale_log2;
-    if (gid >= nvalid) { s0 = -INFINITY; s1 = -INFINITY; }
-    if (gid + 8 >= nvalid) { s2 = -INFINITY; s3 = -INFINITY; }
+    const float sl2 = BSC ? p.scale_log2 * bsc.x : p.scale_log2;
+    float s0 = sc[0] * sl2, s1 = sc[1] * sl2;
+    float s2 = sc[2] * sl2, s3 = sc[3] * sl2;
+    if (hidden(gid)) { s0 = -INFINITY; s1 = -INFINITY; }
+    if (hidden(gid + 8)) { s2 = -INFINITY; s3 = -INFINITY; }
     float mx_e = fmaxf(s0, s2), mx_o = fmaxf(s1, s3);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -423,8 +509,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
     // Zero the V values of tokens past the sequence end (they may hold
     // anything, and 0 * inf would poison the sum).
-    const uint32_t mlo = (2 * tig < nvalid ? 0x0000FFFFu : 0u) | (2 * tig + 1 < nvalid ? 0xFFFF0000u : 0u);
-    const uint32_t mhi = (2 * tig + 8 < nvalid ? 0x0000FFFFu : 0u) | (2 * tig + 9 < nvalid ? 0xFFFF0000u : 0u);
+    const uint32_t mlo = (hidden(2 * tig) ? 0u : 0x0000FFFFu) | (hidden(2 * tig + 1) ? 0u : 0xFFFF0000u);
+    const uint32_t mhi = (hidden(2 * tig + 8) ? 0u : 0x0000FFFFu) | (hidden(2 * tig + 9) ? 0u : 0xFFFF0000u);
 
     // ---- O^T[dim][head] += V^T . P^T -----------------------------------------
     {
@@ -459,17 +545,22 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             a[1] = e4m3x2_to_f16x2(e ? (r[1] >> 16) : (r[1] & 0xFFFFu));
             a[2] = e4m3x2_to_f16x2(e ? (r[2] >> 16) : (r[2] & 0xFFFFu));
             a[3] = e4m3x2_to_f16x2(e ? (r[3] >> 16) : (r[3] & 0xFFFFu));
-            mma16816<false>(acc[2 * pp + e], a, bh0, bh1);
+            if constexpr (BSC) {
+              float pv[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<false>(pv, a, bh0, bh1);
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4)
+                acc[2 * pp + e][q4] = fmaf(pv[q4], bsc.y, acc[2 * pp + e][q4]);
+            } else {
+              mma16816<false>(acc[2 * pp + e], a, bh0, bh1);
+            }
           }
         }
       }
     }
 
     __syncwarp();
-    if (i + NS < cnt) {
-      const int blk = blk_of(i + NS);
-      if (lane == 0) issue(i + NS, blk);
-    }
+    if (i + NS < cnt) load_tile(i + NS);
   }
 
   if (timed_out) {
@@ -540,7 +631,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 //   lse* = log2 sum_s 2^lse_s,  out = sum_s 2^(lse_s - lse*) o_s.
 // Cascade: the shared prefix's chunks (slots 0 .. npc-1, when the group has a
 // prefix) and the request's own splits (slots prefix_slots ..).
-template <int HD, int AT, bool CASC>
+template <int HD, int AT, bool CASC, bool WIN>
 __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, const DecodeExtraParams ap) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t bh = (int64_t)blockIdx.x * 4 + warp;
@@ -580,8 +671,13 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, const 
   } else {
     const int bs = 1 << p.bs_shift;
     n = p.seq_lens[b];
-    const int cap = min(p.max_blocks * bs, p.num_splits * p.chunk);
+    const int cap = WIN ? p.max_blocks * bs : min(p.max_blocks * bs, p.num_splits * p.chunk);
     n = n < 0 ? 0 : (n > cap ? cap : n);
+    if constexpr (WIN) {  // the compact length, clamped as the split kernel does
+      n = win_span(n, ap.window, ap.sink_tokens).nv;
+      if (n > p.num_splits * p.chunk)
+        n = win_span(p.num_splits * p.chunk, ap.window, ap.sink_tokens).nv;
+    }
   }
   const int ns = (n - tb + p.chunk - 1) / p.chunk;
   if (!CASC && ns <= 1) return;  // written directly by the split kernel
@@ -668,23 +764,25 @@ constexpr int stages_for() {
 }
 
 // NSO > 0 overrides the pipeline depth (stages per warp), NW the warps per CTA.
-template <int HD, int CT, int AT, bool CASC, int NSO = 0, int NW = kNW>
+template <int HD, int CT, int AT, bool CASC, int NSO = 0, int NW = kNW, bool WIN = false,
+          bool BSC = false>
 cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const DecodeParams& p, const DecodeExtraParams& ap,
                             cudaStream_t stream, cudaEvent_t merge_after = nullptr) {
   constexpr int NS = NSO > 0 ? NSO : stages_for<HD, CT>();
   using C = DecodeCfg<HD, CT, NW, NS>;
-  auto kern = decode_kernel<HD, CT, AT, NW, NS, CASC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  auto kern = decode_kernel<HD, CT, AT, NW, NS, CASC, WIN, BSC>;
+  constexpr int smem = BSC ? C::SMEM_BSC : C::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.num_kv_heads * ((p.group + 7) / 8), p.batch, p.num_splits);
-  kern<<<grid, NW * 32, C::SMEM, stream>>>(kmap, vmap, p, ap);
+  kern<<<grid, NW * 32, smem, stream>>>(kmap, vmap, p, ap);
   e = cudaGetLastError();
   if (e != cudaSuccess || (!CASC && p.num_splits <= 1)) return e;
   if (merge_after != nullptr && (e = cudaStreamWaitEvent(stream, merge_after, 0)) != cudaSuccess)
     return e;
   const int64_t pairs = (int64_t)p.batch * p.num_q_heads;
-  merge_kernel<HD, AT, CASC><<<(unsigned)((pairs + 3) / 4), 128, 0, stream>>>(p, ap);
+  merge_kernel<HD, AT, CASC, WIN><<<(unsigned)((pairs + 3) / 4), 128, 0, stream>>>(p, ap);
   return cudaGetLastError();
 }
 

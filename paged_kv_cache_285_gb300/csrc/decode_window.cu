@@ -1,0 +1,38 @@
+// Launches of the paged decode kernel (decode_kernel.cuh) under a window with
+// sink tokens, and over fp8 codes with scales per block and kv head.
+#include "decode_kernel.cuh"
+
+namespace pkv {
+
+cudaError_t launch_decode_window(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
+                                 int cache_dt, int act_dt, cudaStream_t stream) {
+  const bool scaled = ap.k_scales != nullptr;
+  if (scaled && (!ap.v_scales || cache_dt != DT_E4M3)) return cudaErrorInvalidValue;
+  if (!scaled && ap.window <= 0) return cudaErrorInvalidValue;
+#define PKV_WIN(HD, CT, AT)                                                              \
+  if (head_dim == HD && cache_dt == CT && act_dt == AT && !scaled)                       \
+    return launch_decode_t<HD, CT, AT, false, 0, kNW, true, false>(kmap, vmap, p, ap, stream);
+#define PKV_BSC(HD, AT)                                                                  \
+  if (head_dim == HD && act_dt == AT && scaled)                                          \
+    return ap.window > 0                                                                 \
+               ? launch_decode_t<HD, DT_E4M3, AT, false, 0, kNW, true, true>(kmap, vmap, p, ap, stream) \
+               : launch_decode_t<HD, DT_E4M3, AT, false, 0, kNW, false, true>(kmap, vmap, p, ap, stream);
+  PKV_WIN(64, DT_F16, DT_F16)
+  PKV_WIN(64, DT_BF16, DT_BF16)
+  PKV_WIN(64, DT_E4M3, DT_F16)
+  PKV_WIN(64, DT_E4M3, DT_BF16)
+  PKV_WIN(128, DT_F16, DT_F16)
+  PKV_WIN(128, DT_BF16, DT_BF16)
+  PKV_WIN(128, DT_E4M3, DT_F16)
+  PKV_WIN(128, DT_E4M3, DT_BF16)
+  PKV_BSC(64, DT_F16)
+  PKV_BSC(64, DT_BF16)
+  PKV_BSC(128, DT_F16)
+  PKV_BSC(128, DT_BF16)
+#undef PKV_WIN
+#undef PKV_BSC
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pkv

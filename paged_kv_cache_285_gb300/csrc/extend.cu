@@ -131,11 +131,15 @@ __global__ void __launch_bounds__(256) claim_kernel(int* claims, const ExtendPar
   const int r = blockIdx.y;
   const int total = __ldg(p.prefix_lens + r) + (__ldg(p.q_indptr + r + 1) - __ldg(p.q_indptr + r));
   const int nb = min(p.max_blocks, (max(total, 0) + (1 << p.bs_shift) - 1) >> p.bs_shift);
+  const int w0 = p.window > 0 ? max(__ldg(p.prefix_lens + r), 0) - p.window + 1 : 0;
   // the grid is sized from the call's length hint; a request past it loops
   for (int base = blockIdx.x * 256; base < nb; base += gridDim.x * 256) {
     const int i = base + threadIdx.x;
     int blk = -1;
-    if (i < nb) blk = __ldg(p.block_tables + (int64_t)r * p.max_blocks + i);
+    // a block that a window hides from every row is not read
+    const bool unseen = p.window > 0 && (i << p.bs_shift) >= p.sink_tokens &&
+                        ((i + 1) << p.bs_shift) <= w0;
+    if (i < nb && !unseen) blk = __ldg(p.block_tables + (int64_t)r * p.max_blocks + i);
     const bool won = blk >= 0 && blk < p.num_blocks && atomicCAS(claims + 1 + blk, 0, 1) == 0;
     // one list slot reservation per warp
     const unsigned m = __ballot_sync(0xffffffffu, won);
@@ -146,6 +150,72 @@ __global__ void __launch_bounds__(256) claim_kernel(int* claims, const ExtendPar
       slot = __shfl_sync(0xffffffffu, slot, leader);
       if (won) claims[1 + p.num_blocks + slot + __popc(m & ((1u << lane) - 1))] = blk;
     }
+  }
+}
+
+// 16 codes -> 16 OUT values code * s.  OUT f16: finite values are kept inside
+// its range (+-65504); bf16 and f16 round to nearest where code * s does not
+// fit (powers of two as scales: exact but for f16's subnormals).
+template <int OUT>
+__device__ __forceinline__ uint32_t widen2_scaled(uint32_t two, float s) {
+  const uint32_t h = e4m3x2_to_f16x2(two);
+  float a = lo_f32<false>(h) * s, b = hi_f32<false>(h) * s;
+  if constexpr (OUT == DT_BF16) {
+    return pack2<true>(a, b);
+  } else {
+    // (a NaN code stays NaN: the comparison is false)
+    if (fabsf(a) > 65504.f) a = copysignf(65504.f, a);
+    if (fabsf(b) > 65504.f) b = copysignf(65504.f, b);
+    return pack2<false>(a, b);
+  }
+}
+
+// One block's page [num_kv_heads][head_vec 16-code vectors] widened with a
+// scale per head.
+template <int OUT>
+__device__ __forceinline__ void widen_block_scaled(const uint4* __restrict__ src,
+                                                   uint4* __restrict__ dst,
+                                                   const float* __restrict__ scales, int in_vec,
+                                                   int head_shift) {
+  for (int u0 = threadIdx.x; u0 < in_vec; u0 += 4 * 256) {
+    uint4 x[4];
+    float s[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (u0 + e * 256 < in_vec) {
+        x[e] = __ldg(src + u0 + e * 256);
+        s[e] = __ldg(scales + ((u0 + e * 256) >> head_shift));
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int u = u0 + e * 256;
+      if (u < in_vec) {
+        const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          o[2 * q] = widen2_scaled<OUT>(w[q] & 0xFFFFu, s[e]);
+          o[2 * q + 1] = widen2_scaled<OUT>(w[q] >> 16, s[e]);
+        }
+        dst[2 * u] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    }
+  }
+}
+
+template <int KOUT>
+__global__ void __launch_bounds__(256) widen_scaled_list_kernel(
+    const uint4* __restrict__ k, const uint4* __restrict__ v, const float* __restrict__ k_scales,
+    const float* __restrict__ v_scales, uint4* __restrict__ k16, uint4* __restrict__ v16,
+    const int* __restrict__ claims, int num_blocks, int num_kv_heads, int in_vec, int head_shift) {
+  const int n = min(claims[0], num_blocks);
+  const int* list = claims + 1 + num_blocks;
+  for (int j = blockIdx.x; j < n; j += gridDim.x) {
+    const int blk = list[j];
+    const int64_t at = (int64_t)blk * in_vec, sc = (int64_t)blk * num_kv_heads;
+    widen_block_scaled<KOUT>(k + at, k16 + 2 * at, k_scales + sc, in_vec, head_shift);
+    widen_block_scaled<DT_F16>(v + at, v16 + 2 * at, v_scales + sc, in_vec, head_shift);
   }
 }
 
@@ -199,6 +269,35 @@ cudaError_t launch_widen_claim(int cache_dt, int act_dt, const void* k_cache,
   else
     widen_list_kernel<DT_E4M3, DT_F16><<<ctas, 256, 0, stream>>>(k, v, k16v, v16v, claims,
                                                                    p.num_blocks, in_vec);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_widen_scaled(int act_dt, const void* k_cache, const void* v_cache,
+                                const float* k_scales, const float* v_scales, void* k16, void* v16,
+                                int* claims, const ExtendParams& p, int head_dim, int block_size,
+                                int max_total_len, int sm_count, cudaStream_t stream) {
+  if (!k_cache || !v_cache || !k_scales || !v_scales || !k16 || !v16 || !claims || p.batch <= 0 ||
+      p.num_blocks <= 0 || sm_count <= 0 || p.batch > 65535)
+    return cudaErrorInvalidValue;
+  const int head_vec = block_size * head_dim / 16;  // a power of two
+  int head_shift = 0;
+  while ((1 << head_shift) < head_vec) ++head_shift;
+  const int in_vec = p.num_kv_heads * head_vec;
+  const int max_nb = std::min(p.max_blocks, (std::max(max_total_len, 1) + block_size - 1) / block_size);
+  cudaError_t e = cudaMemsetAsync(claims, 0, (size_t)(1 + p.num_blocks) * sizeof(int), stream);
+  if (e != cudaSuccess) return e;
+  claim_kernel<<<dim3((unsigned)((max_nb + 255) / 256), (unsigned)p.batch), 256, 0, stream>>>(claims, p);
+  const int ctas = std::min(8 * sm_count, p.num_blocks);
+  const uint4* k = static_cast<const uint4*>(k_cache);
+  const uint4* v = static_cast<const uint4*>(v_cache);
+  uint4* k16v = static_cast<uint4*>(k16);
+  uint4* v16v = static_cast<uint4*>(v16);
+  if (act_dt == DT_BF16)
+    widen_scaled_list_kernel<DT_BF16><<<ctas, 256, 0, stream>>>(
+        k, v, k_scales, v_scales, k16v, v16v, claims, p.num_blocks, p.num_kv_heads, in_vec, head_shift);
+  else
+    widen_scaled_list_kernel<DT_F16><<<ctas, 256, 0, stream>>>(
+        k, v, k_scales, v_scales, k16v, v16v, claims, p.num_blocks, p.num_kv_heads, in_vec, head_shift);
   return cudaGetLastError();
 }
 

@@ -67,6 +67,14 @@
 // item each (so that a few groups still fill the GPU), and each row's result
 // over a chunk leaves as an fp32 partial (O / l and the base-2 LSE) in the
 // chunk's slot, for an LSE merge with the member's own tokens.
+//
+// Window (WIN = true): row i at position p = prefix + i sees keys j <= p with
+// j > p - window, and the first sink_tokens keys.  An item's key tiles are
+// the tiles of the sink keys, then those from the oldest key of its first
+// row's window on (one run if they meet); the 16-key sub-tiles that no row of
+// the item sees are neither read nor looked up (zeros stand for them), V of
+// every key that no row sees is zeroed, and tiles at an edge of some row's
+// window are masked.
 #pragma once
 
 #include "internal.h"
@@ -186,8 +194,10 @@ __device__ __forceinline__ void conv_q_tile(uint8_t* tile, int ct) {
   }
 }
 
-template <int HD, bool CVT, bool TAIL>
-__device__ __forceinline__ void conv_tile16(uint8_t* tile, int ct, int key0, int kv_end) {
+// WIN: keys h0 .. h1 - 1 become zeros too (with TAIL).
+template <int HD, bool CVT, bool TAIL, bool WIN = false>
+__device__ __forceinline__ void conv_tile16(uint8_t* tile, int ct, int key0, int kv_end, int h0 = 0,
+                                            int h1 = 0) {
   constexpr int PER = BN * HD * 2 / 16 / NCONV;  // 16-byte units per thread
   uint4* v4 = reinterpret_cast<uint4*>(tile);
   if constexpr (TAIL) {
@@ -195,7 +205,8 @@ __device__ __forceinline__ void conv_tile16(uint8_t* tile, int ct, int key0, int
     for (int i = 0; i < PER; ++i) {
       const int uu = ct + i * NCONV;
       uint4 v = v4[uu];
-      if (key0 + ((uu * 16) % CHUNK) / 128 >= kv_end) {
+      const int key = key0 + ((uu * 16) % CHUNK) / 128;
+      if (key >= kv_end || (WIN && key >= h0 && key < h1)) {
         v = make_uint4(0u, 0u, 0u, 0u);
       } else if (CVT) {
         v.x = to_f16x2<true>(v.x);
@@ -289,6 +300,22 @@ struct ItemRaw {
 struct Item {
   int b, g, i0, ntok[2], P, S, row0, kv_total, k_lo, k_hi, T, slot, Tsh, r_lo, r_hi;
 };
+// Ts, wlo, w0 (WIN): the sink keys' tiles, the first key of the tiles after
+// them (a multiple of 16) and the oldest key of the first row's window.
+struct WinItem : Item {
+  int Ts, wlo, w0;
+};
+template <bool WIN>
+struct ItemOf { using T = Item; };
+template <>
+struct ItemOf<true> { using T = WinItem; };
+
+// First key of key tile kt of a plain, prefix-pass or window item.
+template <bool WIN>
+__device__ __forceinline__ int tile_key(const typename ItemOf<WIN>::T& it, int kt) {
+  if constexpr (WIN) return kt < it.Ts ? kt * BN : it.wlo + (kt - it.Ts) * BN;
+  else return it.k_lo + kt * BN;
+}
 
 template <bool SX>
 __device__ __forceinline__ ItemRaw load_raw(const ExtendParams& p, int item) {
@@ -415,8 +442,11 @@ __device__ __forceinline__ void seg_advance(const ExtendParams& p, const Item& i
 // rows are not valid, or a request in the item whose prefix is shorter than
 // the group's shared prefix or whose keys do not fit its block table, is not
 // computed and is reported as a length error.
-template <bool PP, bool SX>
-__device__ __forceinline__ bool derive(const ExtendParams& p, int item, const ItemRaw& r, Item& it) {
+// WIN: a request whose prefix is negative or whose keys do not fit its block
+// table is not computed and is reported as a length error.
+template <bool PP, bool SX, bool WIN>
+__device__ __forceinline__ bool derive(const ExtendParams& p, int item, const ItemRaw& r,
+                                       typename ItemOf<WIN>::T& it) {
   const uint32_t rest = p.div_pairs.div((uint32_t)item);
   int pair = item - (int)(rest * p.div_pairs.d);
   int kc = 0;  // prefix pass: the item's key chunk
@@ -492,6 +522,21 @@ __device__ __forceinline__ bool derive(const ExtendParams& p, int item, const It
     it.kv_total = it.P + it.S;
     it.k_hi = it.P + it.i0 + it.ntok[0] + it.ntok[1];  // keys the pair needs
   }
+  if constexpr (WIN) {
+    if (it.P < 0 || it.P > cap - it.S) {
+      set_err(p.err, 3);
+      return false;
+    }
+    it.w0 = max(it.P + it.i0 - p.window + 1, 0);
+    it.wlo = it.w0 & ~15;
+    it.Ts = (min(p.sink_tokens, it.k_hi) + BN - 1) / BN;
+    if (it.Ts * BN >= it.wlo) {  // the sinks' tiles reach the window's
+      if (it.Ts > 0) it.wlo = 0;
+      it.Ts = 0;
+    }
+    it.T = it.Ts + (it.k_hi - it.wlo + BN - 1) / BN;
+    return true;
+  }
   if (it.P < 0 || it.kv_total > cap) {
     set_err(p.err, 3);
     it.kv_total = min(max(it.kv_total, 0), cap);
@@ -504,12 +549,13 @@ __device__ __forceinline__ bool derive(const ExtendParams& p, int item, const It
 
 // HD: head dim (64 or 128); CT: cache dtype (f16, bf16 or e4m3); AT: the
 // activation dtype of q and out (equal to CT for 16-bit caches); PP: the
-// prefix pass; SX: shared-prefix extend.
-template <int HD, int CT, int AT, bool PP, bool SX>
+// prefix pass; SX: shared-prefix extend; WIN: a window with sink tokens.
+template <int HD, int CT, int AT, bool PP, bool SX, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
 extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
               const ExtendParams p, const ExtendPartialParams pp) {
+  static_assert(!(WIN && (PP || SX)), "unsupported combination");
   using C = ExtCfg<HD, CT, AT>;
   constexpr int NST = C::NST;
   extern __shared__ uint8_t smem_raw[];
@@ -524,6 +570,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const int G = p.group;
   const int TOK = p.tok;
   const int item0 = blockIdx.x, stride = gridDim.x;
+  // WIN: no row of the item sees keys key .. key + count - 1
+  auto unseen = [&](const auto& it, int key, int count) -> bool {
+    return key >= p.sink_tokens && key + count <= it.w0;
+  };
 
   if (threadIdx.x == 0) {
     prefetch_tensormap(&kmap);
@@ -582,8 +632,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     for (int item = item0; ok && item < p.num_items; item += stride) {
       const ItemRaw raw = nxt_raw;
       nxt_raw = load_raw<SX>(p, item + stride);
-      Item it;
-      if (!derive<PP, SX>(p, item, raw, it)) continue;
+      typename ItemOf<WIN>::T it;
+      if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
       const int i0x = it.i0 + x * TOK;  // first token of this tile
       // a row's last visible key is kdiag + its token (prefix pass: the chunk's
       // last key for all)
@@ -604,7 +654,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int kt = 0; kt < it.T; ++kt, ++n, seg_advance<SX>(p, it, si)) {
         if (!mbar_wait(bar(C::B_SDONE + x), n & 1)) { ok = false; break; }
         tc_fence_after();
-        const int key0 = SX ? si.sg.k_lo + si.st * BN : it.k_lo + kt * BN;
+        const int key0 = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN>(it, kt);
         // keys key0 .. key0 + nvis of the tile are visible to this row
         int nvis;
         bool masked;
@@ -617,7 +667,18 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         } else {
           nvis = kdiag + (PP ? 0 : rtok) - key0;
           masked = key0 + BN - 1 > kdiag;
+          // WIN: or some row's window starts after the tile's first key, in
+          // a tile that is not all sink keys
+          if (WIN) masked |= key0 <= kdiag + TOK - 1 - p.window && key0 + BN > p.sink_tokens;
         }
+        // WIN: bit q set where key 32 c + q of the tile is visible to this row
+        auto win_bits = [&](int c) -> uint32_t {
+          auto below = [](int n) -> uint32_t {  // bits 0 .. n - 1
+            return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+          };
+          const int k0 = key0 + 32 * c;
+          return below(nvis + 1 - 32 * c) & (~below(key0 + nvis - p.window + 1 - k0) | below(p.sink_tokens - k0));
+        };
         // Scores past a row's limit become -inf.  Plain 16-bit kernels mask the
         // loaded row in registers (~130 cycles); the fp8, prefix-pass and
         // shared-prefix kernels, whose hot loops already fill the instruction
@@ -632,9 +693,15 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             uint32_t t[32];
             tmem_ld32(srow + c * 32, t);
             tmem_wait_ld();
-            const int lc = nvis - c * 32;
+            if constexpr (WIN) {
+              const uint32_t wb = win_bits(c);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) t[q] = (q > lc) ? ninf : t[q];
+              for (int q = 0; q < 32; ++q) t[q] = ((wb >> q) & 1u) ? t[q] : ninf;
+            } else {
+              const int lc = nvis - c * 32;
+#pragma unroll
+              for (int q = 0; q < 32; ++q) t[q] = (q > lc) ? ninf : t[q];
+            }
             tmem_st32(srow + c * 32, t);
           }
           tmem_wait_st();
@@ -646,9 +713,12 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         tmem_wait_ld();
         if (kRegMask && masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t wb = WIN ? win_bits(c) : 0u;
 #pragma unroll
-            for (int q = 0; q < 32; ++q) sr[c][q] = (c * 32 + q > nvis) ? ninf : sr[c][q];
+            for (int q = 0; q < 32; ++q)
+              sr[c][q] = (WIN ? ((wb >> q) & 1u) == 0u : c * 32 + q > nvis) ? ninf : sr[c][q];
+          }
         }
         // row max: three-input max over 8 independent accumulators
         float mx[8];
@@ -663,9 +733,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                                fmaxf(mx[6], mx[7])) * p.scale_log2;
         float m_new = m_run;
         if (mt > m_run + 8.f) m_new = mt;
-        // SX: a row that has seen no key yet keeps m = -inf and takes 0 as
+        // SX, WIN: a row that has seen no key yet keeps m = -inf and takes 0 as
         // the exponent's base, so its masked scores give exact zeros
-        const float m_base = (SX && m_new == -INFINITY) ? 0.f : m_new;
+        const float m_base = ((SX || WIN) && m_new == -INFINITY) ? 0.f : m_new;
         const float alpha = fast_exp2(m_run - m_base);
         const bool mine = (m_new != m_run);
         if (kt >= 1 && __any_sync(0xFFFFFFFFu, mine)) {
@@ -851,17 +921,23 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = item0; ok && item < p.num_items; item += stride) {
         const ItemRaw raw = nxt_raw;
         nxt_raw = load_raw<SX>(p, item + stride);
-        Item it;
-        if (!derive<PP, SX>(p, item, raw, it)) continue;
+        typename ItemOf<WIN>::T it;
+        if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
         if (is_k && !load_q(it, j, 0)) { ok = false; break; }
         SegIter si;
         seg_begin<SX>(p, it, si);
         const int32_t* bt = p.block_tables;
         int sk_lo = 0, sk_hi = 0;  // the segment's keys
         auto fetch = [&](int wi) -> int {
-          const int key0 = sk_lo + (wi * 32 + lane) * 16;  // sub-tile = 16 keys
+          const int st16 = wi * 32 + lane;  // sub-tile = 16 keys
+          int key0 = sk_lo + st16 * 16;
+          bool read = key0 < sk_hi;
+          if constexpr (WIN) {
+            if (st16 >= it.Ts * 8) key0 = it.wlo + (st16 - it.Ts * 8) * 16;
+            read = key0 < sk_hi && !unseen(it, key0, 16);
+          }
           int page = -1;
-          if (key0 < sk_hi) {
+          if (read) {
             const int blk = bt[key0 >> p.bs_shift];
             if (blk < 0 || blk >= p.num_blocks) set_err(p.err, 1);  // TMA zero-fills page -1
             else page = blk * p.num_kv_heads + it.g;
@@ -879,7 +955,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             // for it are the group's
             const int breq = SX ? (si.sg.req < 0 ? it.r_lo : si.sg.req) : (PP ? it.row0 : it.b);
             bt = p.block_tables + (int64_t)breq * p.max_blocks;
-            sk_lo = SX ? si.sg.k_lo : it.k_lo;
+            sk_lo = SX ? si.sg.k_lo : it.k_lo;  // WIN: 0
             sk_hi = SX ? si.sg.k_hi : it.k_hi;
             win = 0;
             cur = fetch(0);
@@ -901,7 +977,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               mbar_arrive_expect_tx(fb, C::T8);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const int rip = (sk_lo + st * BN + 16 * q) & ((1 << p.bs_shift) - 1);
+                const int rip = ((WIN ? tile_key<WIN>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
                 tma_load_3d(dst + q * 16 * HD, map, fb, 0, rip, pg[q]);
               }
             } else {
@@ -909,7 +985,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               mbar_arrive_expect_tx(fb, C::T16);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const int rip = (sk_lo + st * BN + 16 * q) & ((1 << p.bs_shift) - 1);
+                const int rip = ((WIN ? tile_key<WIN>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
 #pragma unroll
                 for (int c = 0; c < C::NCH; ++c)
                   tma_load_3d(dst + c * CHUNK + q * 2048, map, fb, c * 64, rip, pg[q]);
@@ -935,8 +1011,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = item0; ok && item < p.num_items; item += stride) {
         const ItemRaw raw = nxt_raw;
         nxt_raw = load_raw<SX>(p, item + stride);
-        Item it;
-        if (!derive<PP, SX>(p, item, raw, it)) continue;
+        typename ItemOf<WIN>::T it;
+        if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
         const uint32_t stg = s_base + C::OFF_Q + ((2 * js + 1) % NQB) * C::T16;
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
@@ -1014,8 +1090,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = item0; ok && item < p.num_items; item += stride) {
         const ItemRaw raw = nxt_raw;
         nxt_raw = load_raw<SX>(p, item + stride);
-        Item it;
-        if (!derive<PP, SX>(p, item, raw, it)) continue;
+        typename ItemOf<WIN>::T it;
+        if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
         const int qa = (2 * j) % NQB, qb = (2 * j + 1) % NQB;
         for (int kt = 0; kt < it.T; ++kt, ++n) {
           if constexpr (C::FP8 && HD == 128) {
@@ -1095,8 +1171,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = item0; ok && item < p.num_items; item += stride) {
         const ItemRaw raw = nxt_raw;
         nxt_raw = load_raw<SX>(p, item + stride);
-        Item it;
-        if (!derive<PP, SX>(p, item, raw, it)) continue;
+        typename ItemOf<WIN>::T it;
+        if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
         SegIter si;
         seg_begin<SX>(p, it, si);
         for (int kt = 0; kt < it.T; ++kt, ++n, seg_advance<SX>(p, it, si)) {
@@ -1121,15 +1197,24 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           // keys at or past the segment's end are zeroed (a shared prefix's
           // last tile reaches into one member's own keys, which no row of the
           // segment sees)
-          const int kbase = SX ? si.sg.k_lo + si.st * BN : it.k_lo + kt * BN;
+          const int kbase = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN>(it, kt);
           const int kv_end = SX ? si.sg.kv_total : it.kv_total;
-          const bool zero = kbase + t >= kv_end;
+          // WIN: keys between the sinks and the first row's window too
+          bool zero = kbase + t >= kv_end, hole = false;
+          if constexpr (WIN) {
+            zero |= unseen(it, kbase + t, 1);
+            hole = kbase + BN > p.sink_tokens && kbase < it.w0;
+          }
           uint8_t* vt = smem + C::OFF_V + s * C::T16;
           if constexpr (C::FP8) {
             widen_row<HD, DT_F16>(smem + C::src8(true, s), vt, t, zero);
             fence_async_smem();
-          } else if (kbase + BN > kv_end) {  // tail tile: zero the keys past the end
-            conv_tile16<HD, CT == DT_BF16, true>(vt, t, kbase, kv_end);
+          } else if (kbase + BN > kv_end || hole) {
+            // tail tile: zero the keys past the end (and those no row sees)
+            if constexpr (WIN)
+              conv_tile16<HD, CT == DT_BF16, true, true>(vt, t, kbase, kv_end, p.sink_tokens, it.w0);
+            else
+              conv_tile16<HD, CT == DT_BF16, true>(vt, t, kbase, kv_end);
             fence_async_smem();
           } else if constexpr (CT == DT_BF16) {
             conv_tile16<HD, true, false>(vt, t, kbase, kv_end);
@@ -1152,11 +1237,11 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 }
 
-template <int HD, int CT, int AT, bool PP, bool SX>
+template <int HD, int CT, int AT, bool PP, bool SX, bool WIN = false>
 cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                             const CUtensorMap& omap, const ExtendParams& p,
                             const ExtendPartialParams& pp, cudaStream_t stream) {
-  auto k = extend_kernel<HD, CT, AT, PP, SX>;
+  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN>;
   constexpr int smem = ExtCfg<HD, CT, AT>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

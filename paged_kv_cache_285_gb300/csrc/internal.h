@@ -72,6 +72,13 @@ struct DecodeExtraParams {
   int prefix_slots;
   int prefix_chunk;
   int prefix_chunks;  // chunks the prefix pass computes (<= prefix_slots)
+  //  - window launches: the query of length n sees tokens [0, sink_tokens) and
+  //    [n - window, n) (window > 0);
+  //  - block-scaled launches: fp32 scales [num_blocks][num_kv_heads] of the codes.
+  int window;
+  int sink_tokens;
+  const float* k_scales;
+  const float* v_scales;
 };
 
 // Division of unsigned n < 2^31 by a divisor fixed for a launch, as a
@@ -131,6 +138,58 @@ struct AppendParams {
   FastDiv div_hkv;    // by num_kv_heads
 };
 
+// Append into a cache of e4m3 codes with scales per block and kv head.
+struct AppendScaledParams {
+  void* k_cache;
+  void* v_cache;
+  float* k_scales;             // [num_blocks][num_kv_heads]
+  float* v_scales;
+  const void* k_new;           // [total_rows][num_kv_heads][head_dim]
+  const void* v_new;
+  const int32_t* q_indptr;     // [batch + 1]
+  const int32_t* prefix_lens;  // [batch]
+  const int32_t* block_tables;
+  int32_t* err;
+  int max_blocks;
+  int num_blocks;
+  int num_kv_heads;
+  int batch;
+  int total_rows;
+  int max_suffix_len;
+  // set by the launcher
+  int bs_shift;
+  int units_per_request;       // 0: a unit's request is searched
+  uint32_t num_tasks;          // units x kv heads x (K, V)
+  FastDiv div_units;
+  FastDiv div_hkv;
+};
+
+// Rows out of a cache: request b's rows row_indptr[b] .. row_indptr[b+1]-1 are
+// its positions start_positions[b] ...
+struct GatherParams {
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;       // [num_blocks][num_kv_heads], or null
+  const float* v_scales;
+  void* k_out;                 // [total_rows][num_kv_heads][head_dim]
+  void* v_out;
+  const int32_t* row_indptr;
+  const int32_t* start_positions;
+  const int32_t* block_tables;
+  int32_t* err;
+  int64_t total_rows;
+  int max_blocks;
+  int num_blocks;
+  int num_kv_heads;
+  int batch;
+  int bs_shift;
+  float k_scale;               // an fp8 cache's scales without k_scales
+  float v_scale;
+  // set by the launcher
+  int rows_per_cta;
+  FastDiv div_hkv;
+};
+
 struct ExtendParams {
   const int32_t* q_indptr;
   const int32_t* prefix_lens;
@@ -165,6 +224,8 @@ struct ExtendParams {
   FastDiv div_req;      // by ceil(tiles_per_head / 2) * num_kv_heads (items per request)
   float scale_log2;
   float out_scale;
+  int window;           // window launches: keys j > p - window are visible to position p ...
+  int sink_tokens;      // ... and keys j < sink_tokens (window 0: every key j <= p)
 };
 
 // Partial output of the extend kernel's prefix pass: row q (request b, head h:
@@ -190,8 +251,18 @@ cudaError_t launch_decode_cascade(const CUtensorMap& kmap, const CUtensorMap& vm
                                   const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
                                   int cache_dt, int act_dt, cudaStream_t stream,
                                   cudaEvent_t merge_after);
+// Decode of fp8 codes with scales per block and kv head (ap.k_scales and
+// ap.v_scales not null) and / or under a window with sink tokens (ap.window
+// > 0); p's splits count the tokens that a query can see.
+cudaError_t launch_decode_window(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
+                                 int cache_dt, int act_dt, cudaStream_t stream);
 size_t decode_smem_bytes(int head_dim, int cache_dt);
 cudaError_t launch_append(const AppendParams& p, int cache_dt, int act_dt, cudaStream_t stream);
+cudaError_t launch_append_scaled(const AppendScaledParams& p, int act_dt, int head_dim,
+                                 int block_size, cudaStream_t stream);
+cudaError_t launch_gather(const GatherParams& p, int cache_dt, int act_dt, int head_dim,
+                          cudaStream_t stream);
 // Chain hashes of the full blocks of each request's token ids.
 struct ChainHashParams {
   const int32_t* tokens;        // [token_indptr[batch]]
@@ -224,6 +295,11 @@ cudaError_t launch_extend_shared(const CUtensorMap& kmap, const CUtensorMap& vma
                                  const CUtensorMap& qmap, const CUtensorMap& omap,
                                  const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
                                  cudaStream_t stream);
+// Extend under a window with sink tokens (p.window > 0).
+cudaError_t launch_extend_window(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 const CUtensorMap& qmap, const CUtensorMap& omap,
+                                 const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
+                                 cudaStream_t stream);
 bool extend_supported(int head_dim, int cache_dt, int act_dt, int group);
 // The pages a shared-prefix extend reads (each group's shared blocks through
 // its first member's table, every request's own blocks through its own),
@@ -244,5 +320,11 @@ cudaError_t launch_widen_claim(int cache_dt, int act_dt, const void* k_cache,
                                const void* v_cache, void* k16, void* v16, int* claims,
                                const ExtendParams& p, int head_dim, int block_size,
                                int max_total_len, int sm_count, cudaStream_t stream);
+// The same for fp8 codes with fp32 scales [num_blocks][num_kv_heads]: the pools
+// hold code * scale, K in the queries' type and V as f16.
+cudaError_t launch_widen_scaled(int act_dt, const void* k_cache, const void* v_cache,
+                                const float* k_scales, const float* v_scales, void* k16, void* v16,
+                                int* claims, const ExtendParams& p, int head_dim, int block_size,
+                                int max_total_len, int sm_count, cudaStream_t stream);
 
 }  // namespace pkv
