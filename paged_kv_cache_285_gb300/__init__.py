@@ -29,6 +29,7 @@ take a window too).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -517,45 +518,102 @@ def paged_extend_attn_append(k_cache, v_cache, k_new, v_new, q, out, q_indptr, p
     _check(st, "pkv_paged_extend_attn_append")
 
 
-def _pointers(device, *tensors):
-    """Data pointers of contiguous tensors (or None) that all lie on `device`."""
-    if device.type != "cuda":
-        raise ValueError("libpkv takes device tensors")
-    ptrs = []
-    for t in tensors:
-        if t is None:
-            ptrs.append(None)
-            continue
-        if t.device != device:
-            raise ValueError(f"every tensor of the call must be on {device}, got one on {t.device}")
-        if not t.is_contiguous():
-            raise ValueError("libpkv takes contiguous tensors")
-        ptrs.append(t.data_ptr())
-    return ptrs
+# ---- calls over tensors of one device, checked in one pass (a decode step's host time is mostly
+# these checks, so each tensor is looked at once and the C struct of a pool is kept by its values)
+
+@functools.lru_cache(maxsize=256)
+def _desc_ref(num_blocks, num_kv_heads, block_size, head_dim, code, k_scale, v_scale):
+    return ctypes.byref(CacheDesc(num_blocks, block_size, num_kv_heads, head_dim, code, k_scale,
+                                  v_scale))
+
+
+def _refuse(name, t, shape, dtype, device):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} like the call's other tensors, got {t.device}")
+    raise ValueError(f"libpkv takes contiguous tensors: {name} is not")
+
+
+def _arg(name, t, shape, dtype, device):
+    """Data pointer of a tensor argument of this shape, dtype and device, contiguous."""
+    if (t is None or t.shape != shape or t.dtype is not dtype or t.device != device or
+            not t.is_contiguous()):
+        _refuse(name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _opt(name, t, shape, dtype, device):
+    return None if t is None else _arg(name, t, shape, dtype, device)
+
+
+def _workspace(t, device):
+    """(pointer, bytes) of a workspace tensor of any shape and dtype, or of none."""
+    if t is None:
+        return None, 0
+    if t.device != device:
+        raise ValueError(f"workspace must be on {device} like the call's other tensors, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("libpkv takes contiguous tensors: workspace is not")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _dim(name, t, dims, what):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be {what}")
+    return t.shape
+
+
+def _pools(k_cache, v_cache, k_scale, v_scale):
+    """The desc of a pair of pools, their pointers, [num_blocks, Hkv] and head dim."""
+    shape = _dim("cache", k_cache, 4, "[num_blocks, num_kv_heads, block_size, head_dim]")
+    nb, hkv, bs, d = shape
+    dev = k_cache.device
+    kc = _arg("k_cache", k_cache, shape, k_cache.dtype, dev)
+    vc = _arg("v_cache", v_cache, shape, k_cache.dtype, dev)
+    return (_desc_ref(nb, hkv, bs, d, _dtype_code(k_cache), float(k_scale), float(v_scale)), kc, vc,
+            (nb, hkv), d)
+
+
+def _block_scales(k_scales, v_scales, pages, device):
+    return (_arg("k_scales", k_scales, pages, torch.float32, device),
+            _arg("v_scales", v_scales, pages, torch.float32, device))
+
+
+try:
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _run(what, device, stream, *args):
     """Call a C entry point whose last argument is the stream (None: the current one of
     `device`), with `device` current."""
-    fn = getattr(load(), what)
-    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.type != "cuda":
+        raise ValueError("libpkv takes device tensors")
+    fn = getattr(_lib or load(), what)
+    s = _raw_stream(device.index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == device.index:
         st = fn(*args, s)
     else:
         with torch.cuda.device(device):
             st = fn(*args, s)
-    _check(st, what)
+    if st != 0:
+        raise PkvError(st, what)
 
 
-def _scales(k_cache, k_scales, v_scales):
-    """Scales per block and kv head of a cache of fp8 codes."""
-    want = (int(k_cache.shape[0]), int(k_cache.shape[1]))
-    _shape("k_scales", k_scales, want, torch.float32)
-    _shape("v_scales", v_scales, want, torch.float32)
-
-
-def _ws_bytes(workspace):
-    return workspace.numel() * workspace.element_size() if workspace is not None else 0
+def _layout(indptr_name, indptr, start_name, starts, block_tables, device):
+    """Pointers of a call's row layout: indptr [B+1], starts [B], block_tables [B, W]; then B, W."""
+    batch, = _dim(start_name, starts, 1, "[batch]")
+    width = _dim("block_tables", block_tables, 2, "[batch, max_blocks_per_seq]")[1]
+    return (_arg(indptr_name, indptr, (batch + 1,), torch.int32, device),
+            _arg(start_name, starts, (batch,), torch.int32, device),
+            _arg("block_tables", block_tables, (batch, width), torch.int32, device), batch, width)
 
 
 def kv_append_block_scaled(k_cache, v_cache, k_scales, v_scales, k_new, v_new, q_indptr,
@@ -564,24 +622,16 @@ def kv_append_block_scaled(k_cache, v_cache, k_scales, v_scales, k_new, v_new, q
     to position prefix_lens[b] + i of request b, quantised with a power-of-two scale per block
     and kv head.  k_scales/v_scales float32 [num_blocks, Hkv]; q_indptr int32 [B+1]; prefix_lens
     int32 [B]; max_suffix_len bounds the rows per request."""
-    _need(torch.int32, q_indptr=q_indptr, prefix_lens=prefix_lens, block_tables=block_tables)
-    hkv, d = _cache_pair(k_cache, v_cache)
-    _scales(k_cache, k_scales, v_scales)
-    rows, _ = _rows("k_new", k_new, d)
-    _shape("k_new", k_new, (rows, hkv, d))
-    _shape("v_new", v_new, (rows, hkv, d), k_new.dtype)
-    if prefix_lens.dim() != 1:
-        raise ValueError("prefix_lens must be [batch]")
-    batch = int(prefix_lens.shape[0])
-    _shape("q_indptr", q_indptr, (batch + 1,))
-    _table("block_tables", block_tables, batch)
-    desc = _desc(k_cache, 1.0, 1.0)
-    kc, vc, ks, vs, kn, vn, qi, pl, bt = _pointers(
-        k_cache.device, k_cache, v_cache, k_scales, v_scales, k_new, v_new, q_indptr, prefix_lens,
-        block_tables)
-    _run("pkv_kv_append_block_scaled", k_cache.device, stream, ctypes.byref(desc), kc, vc, ks, vs,
-         kn, vn, _dtype_code(k_new), qi, pl, bt, int(block_tables.shape[1]), batch, rows,
-         int(max_suffix_len))
+    dev = k_cache.device
+    desc, kc, vc, pages, d = _pools(k_cache, v_cache, 1.0, 1.0)
+    ks, vs = _block_scales(k_scales, v_scales, pages, dev)
+    rows = _dim("k_new", k_new, 3, "[rows, num_kv_heads, head_dim]")[0]
+    kn = _arg("k_new", k_new, (rows, pages[1], d), k_new.dtype, dev)
+    vn = _arg("v_new", v_new, (rows, pages[1], d), k_new.dtype, dev)
+    qi, pl, bt, batch, width = _layout("q_indptr", q_indptr, "prefix_lens", prefix_lens,
+                                       block_tables, dev)
+    _run("pkv_kv_append_block_scaled", dev, stream, desc, kc, vc, ks, vs, kn, vn,
+         _dtype_code(k_new), qi, pl, bt, width, batch, rows, int(max_suffix_len))
 
 
 def kv_gather(k_cache, v_cache, k_out, v_out, row_indptr, start_positions, block_tables,
@@ -589,26 +639,18 @@ def kv_gather(k_cache, v_cache, k_out, v_out, row_indptr, start_positions, block
     """pkv_kv_gather: rows row_indptr[b] .. row_indptr[b+1]-1 of k_out/v_out [rows, Hkv, D] (f16
     or bf16) are positions start_positions[b] ... of request b.  k_scale/v_scale: an fp8 cache's
     scales per tensor; k_scales/v_scales float32 [num_blocks, Hkv]: scales per block and head."""
-    _need(torch.int32, row_indptr=row_indptr, start_positions=start_positions,
-          block_tables=block_tables)
-    hkv, d = _cache_pair(k_cache, v_cache)
+    dev = k_cache.device
+    desc, kc, vc, pages, d = _pools(k_cache, v_cache, k_scale, v_scale)
     if (k_scales is None) != (v_scales is None):
         raise ValueError("k_scales and v_scales come together")
-    _scales(k_cache, k_scales, v_scales)
-    rows, _ = _rows("k_out", k_out, d)
-    _shape("k_out", k_out, (rows, hkv, d))
-    _shape("v_out", v_out, (rows, hkv, d), k_out.dtype)
-    if start_positions.dim() != 1:
-        raise ValueError("start_positions must be [batch]")
-    batch = int(start_positions.shape[0])
-    _shape("row_indptr", row_indptr, (batch + 1,))
-    _table("block_tables", block_tables, batch)
-    desc = _desc(k_cache, k_scale, v_scale)
-    kc, vc, ks, vs, ko, vo, ri, sp, bt = _pointers(
-        k_cache.device, k_cache, v_cache, k_scales, v_scales, k_out, v_out, row_indptr,
-        start_positions, block_tables)
-    _run("pkv_kv_gather", k_cache.device, stream, ctypes.byref(desc), kc, vc, ks, vs, ko, vo,
-         _dtype_code(k_out), ri, sp, bt, int(block_tables.shape[1]), batch, rows)
+    ks, vs = (None, None) if k_scales is None else _block_scales(k_scales, v_scales, pages, dev)
+    rows = _dim("k_out", k_out, 3, "[rows, num_kv_heads, head_dim]")[0]
+    ko = _arg("k_out", k_out, (rows, pages[1], d), k_out.dtype, dev)
+    vo = _arg("v_out", v_out, (rows, pages[1], d), k_out.dtype, dev)
+    ri, sp, bt, batch, width = _layout("row_indptr", row_indptr, "start_positions", start_positions,
+                                       block_tables, dev)
+    _run("pkv_kv_gather", dev, stream, desc, kc, vc, ks, vs, ko, vo, _dtype_code(k_out), ri, sp, bt,
+         width, batch, rows)
 
 
 def decode_window_workspace_bytes(k_cache, batch, num_q_heads, max_seq_len, window=0,
@@ -621,21 +663,30 @@ def decode_window_workspace_bytes(k_cache, batch, num_q_heads, max_seq_len, wind
                                                         num_splits))
 
 
+def _decode_args(q, out, block_tables, seq_lens, lse_out, head_dim, device):
+    """Pointers of q, out, block_tables, seq_lens and lse_out, then batch, heads, table width."""
+    b, hq, d = _dim("q", q, 3, f"[batch, num_q_heads, {head_dim}]")
+    width = _dim("block_tables", block_tables, 2, "[batch, max_blocks_per_seq]")[1]
+    return (_arg("q", q, (b, hq, head_dim), q.dtype, device),
+            _arg("out", out, (b, hq, head_dim), q.dtype, device),
+            _arg("block_tables", block_tables, (b, width), torch.int32, device),
+            _arg("seq_lens", seq_lens, (b,), torch.int32, device),
+            _opt("lse_out", lse_out, (b, hq), torch.float32, device), b, hq, width)
+
+
 def paged_decode_attn_window(k_cache, v_cache, q, out, block_tables, seq_lens, sm_scale,
                              max_seq_len, window, sink_tokens=0, k_scale=1.0, v_scale=1.0,
                              num_splits=0, lse_out=None, workspace=None, stream=None):
     """pkv_paged_decode_attn_window: paged_decode_attn where each request's query sees its last
     `window` tokens and its first `sink_tokens`.  ``workspace`` is a uint8 device tensor of at
     least decode_window_workspace_bytes() bytes."""
-    _need(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
-    b, hq = _decode_shapes(k_cache, v_cache, q, out, block_tables, seq_lens, lse_out)
-    desc = _desc(k_cache, k_scale, v_scale)
-    kc, vc, qp, op, bt, sl, lse, ws = _pointers(q.device, k_cache, v_cache, q, out, block_tables,
-                                                seq_lens, lse_out, workspace)
-    _run("pkv_paged_decode_attn_window", q.device, stream, ctypes.byref(desc), kc, vc, qp, op,
-         _dtype_code(q), bt, int(block_tables.shape[1]), sl, b, hq, float(sm_scale),
-         int(max_seq_len), int(window), int(sink_tokens), int(num_splits), lse, ws,
-         _ws_bytes(workspace))
+    dev = q.device
+    desc, kc, vc, _, d = _pools(k_cache, v_cache, k_scale, v_scale)
+    qp, op, bt, sl, lse, b, hq, width = _decode_args(q, out, block_tables, seq_lens, lse_out, d,
+                                                     k_cache.device)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run("pkv_paged_decode_attn_window", dev, stream, desc, kc, vc, qp, op, _dtype_code(q), bt,
+         width, sl, b, hq, sm_scale, max_seq_len, window, sink_tokens, num_splits, lse, ws, ws_bytes)
 
 
 def paged_decode_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out, block_tables,
@@ -644,17 +695,24 @@ def paged_decode_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out,
     """pkv_paged_decode_attn_block_scaled: paged_decode_attn over fp8 codes with k_scales/v_scales
     float32 [num_blocks, Hkv]; window 0: every token, else as paged_decode_attn_window (the same
     workspace)."""
-    _need(torch.int32, block_tables=block_tables, seq_lens=seq_lens)
-    b, hq = _decode_shapes(k_cache, v_cache, q, out, block_tables, seq_lens, lse_out)
-    _scales(k_cache, k_scales, v_scales)
-    desc = _desc(k_cache, 1.0, 1.0)
-    kc, vc, ks, vs, qp, op, bt, sl, lse, ws = _pointers(
-        q.device, k_cache, v_cache, k_scales, v_scales, q, out, block_tables, seq_lens, lse_out,
-        workspace)
-    _run("pkv_paged_decode_attn_block_scaled", q.device, stream, ctypes.byref(desc), kc, vc, ks, vs,
-         qp, op, _dtype_code(q), bt, int(block_tables.shape[1]), sl, b, hq, float(sm_scale),
-         int(max_seq_len), int(window), int(sink_tokens), int(num_splits), lse, ws,
-         _ws_bytes(workspace))
+    dev = q.device
+    desc, kc, vc, pages, d = _pools(k_cache, v_cache, 1.0, 1.0)
+    ks, vs = _block_scales(k_scales, v_scales, pages, k_cache.device)
+    qp, op, bt, sl, lse, b, hq, width = _decode_args(q, out, block_tables, seq_lens, lse_out, d,
+                                                     k_cache.device)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run("pkv_paged_decode_attn_block_scaled", dev, stream, desc, kc, vc, ks, vs, qp, op,
+         _dtype_code(q), bt, width, sl, b, hq, sm_scale, max_seq_len, window, sink_tokens,
+         num_splits, lse, ws, ws_bytes)
+
+
+def _extend_args(q, out, q_indptr, prefix_lens, block_tables, lse_out, head_dim, device):
+    rows, hq, _ = _dim("q", q, 3, f"[rows, num_q_heads, {head_dim}]")
+    qi, pl, bt, batch, width = _layout("q_indptr", q_indptr, "prefix_lens", prefix_lens,
+                                       block_tables, device)
+    return (_arg("q", q, (rows, hq, head_dim), q.dtype, device),
+            _arg("out", out, (rows, hq, head_dim), q.dtype, device), qi, pl, bt,
+            _opt("lse_out", lse_out, (rows, hq), torch.float32, device), rows, hq, batch, width)
 
 
 def paged_extend_attn_window(k_cache, v_cache, q, out, q_indptr, prefix_lens, block_tables,
@@ -662,16 +720,14 @@ def paged_extend_attn_window(k_cache, v_cache, q, out, q_indptr, prefix_lens, bl
                              k_scale=1.0, v_scale=1.0, lse_out=None, workspace=None, stream=None):
     """pkv_paged_extend_attn_window: paged_extend_attn where the row at position p sees keys
     p - window + 1 .. p and the first `sink_tokens`.  workspace: optional, as there."""
-    _need(torch.int32, q_indptr=q_indptr, prefix_lens=prefix_lens, block_tables=block_tables)
-    rows, hq, batch = _extend_shapes(k_cache, v_cache, q, out, q_indptr, prefix_lens,
-                                     block_tables, lse_out)
-    desc = _desc(k_cache, k_scale, v_scale)
-    kc, vc, qp, op, qi, pl, bt, lse, ws = _pointers(q.device, k_cache, v_cache, q, out, q_indptr,
-                                                    prefix_lens, block_tables, lse_out, workspace)
-    _run("pkv_paged_extend_attn_window", q.device, stream, ctypes.byref(desc), kc, vc, qp, op,
-         _dtype_code(q), qi, pl, bt, int(block_tables.shape[1]), batch, hq, float(sm_scale), rows,
-         int(max_suffix_len), int(max_total_len), int(window), int(sink_tokens), lse, ws,
-         _ws_bytes(workspace))
+    dev = q.device
+    desc, kc, vc, _, d = _pools(k_cache, v_cache, k_scale, v_scale)
+    qp, op, qi, pl, bt, lse, rows, hq, batch, width = _extend_args(
+        q, out, q_indptr, prefix_lens, block_tables, lse_out, d, k_cache.device)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run("pkv_paged_extend_attn_window", dev, stream, desc, kc, vc, qp, op, _dtype_code(q), qi, pl,
+         bt, width, batch, hq, sm_scale, rows, max_suffix_len, max_total_len, window, sink_tokens,
+         lse, ws, ws_bytes)
 
 
 def extend_block_scaled_workspace_bytes(k_cache) -> int:
@@ -688,18 +744,15 @@ def paged_extend_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out,
     """pkv_paged_extend_attn_block_scaled: paged_extend_attn over fp8 codes with k_scales/v_scales
     float32 [num_blocks, Hkv]; window 0: every key, else as paged_extend_attn_window.
     workspace: a uint8 device tensor of extend_block_scaled_workspace_bytes() bytes or more."""
-    _need(torch.int32, q_indptr=q_indptr, prefix_lens=prefix_lens, block_tables=block_tables)
-    rows, hq, batch = _extend_shapes(k_cache, v_cache, q, out, q_indptr, prefix_lens,
-                                     block_tables, lse_out)
-    _scales(k_cache, k_scales, v_scales)
-    desc = _desc(k_cache, 1.0, 1.0)
-    kc, vc, ks, vs, qp, op, qi, pl, bt, lse, ws = _pointers(
-        q.device, k_cache, v_cache, k_scales, v_scales, q, out, q_indptr, prefix_lens, block_tables,
-        lse_out, workspace)
-    _run("pkv_paged_extend_attn_block_scaled", q.device, stream, ctypes.byref(desc), kc, vc, ks, vs,
-         qp, op, _dtype_code(q), qi, pl, bt, int(block_tables.shape[1]), batch, hq,
-         float(sm_scale), rows, int(max_suffix_len), int(max_total_len), int(window),
-         int(sink_tokens), lse, ws, _ws_bytes(workspace))
+    dev = q.device
+    desc, kc, vc, pages, d = _pools(k_cache, v_cache, 1.0, 1.0)
+    ks, vs = _block_scales(k_scales, v_scales, pages, k_cache.device)
+    qp, op, qi, pl, bt, lse, rows, hq, batch, width = _extend_args(
+        q, out, q_indptr, prefix_lens, block_tables, lse_out, d, k_cache.device)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run("pkv_paged_extend_attn_block_scaled", dev, stream, desc, kc, vc, ks, vs, qp, op,
+         _dtype_code(q), qi, pl, bt, width, batch, hq, sm_scale, rows, max_suffix_len,
+         max_total_len, window, sink_tokens, lse, ws, ws_bytes)
 
 
 def chain_hash(tokens, token_indptr, block_size, hashes, salts=None, stream=None):
