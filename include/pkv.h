@@ -593,7 +593,9 @@ pkv_status pkv_paged_decode_attn_block_scaled(
  * negative or whose keys do not fit its table is not computed
  * (PKV_DEVERR_BAD_LENGTH).  V of a key that no row of a work item (two 128-row
  * tiles) sees does not touch its outputs, whatever it holds; a key that some of
- * those rows see must be finite for all of them, as in the plain call.
+ * those rows see must be finite for all of them, as in the plain call.  A call
+ * with few rows and many visible keys is computed in parts that are added up
+ * (clusters of up to 8 CTAs; no workspace): the same up to rounding.
  * ------------------------------------------------------------------------- */
 pkv_status pkv_paged_extend_attn_window(const pkv_cache_desc* desc, const void* k_cache,
                                         const void* v_cache, const void* q, void* out,
@@ -609,16 +611,18 @@ pkv_status pkv_paged_extend_attn_window(const pkv_cache_desc* desc, const void* 
 /* ---------------------------------------------------------------------------
  * pkv_paged_extend_attn_block_scaled -- pkv_paged_extend_attn over a cache with
  * a scale per block and kv head, optionally under a window (0: none).
- * workspace:    required: pkv_extend_block_scaled_workspace_bytes() bytes or
- *               more, 256-byte aligned, any contents (else PKV_ERR_WORKSPACE).
- *               The call first widens each block that its rows see, once,
- *               into 16-bit copies there: K as code * scale in the act dtype,
- *               V as code * scale in f16.  With powers of two as scales (what
- *               the append writes) K is exact in bf16, and K and V in f16 within
- *               that type's range (finite values beyond it become its largest,
- *               values below 2^-14 lose bits); other scales round to nearest.
+ * The kernel reads the codes: K's scales multiply the scores in fp32 (bf16
+ * queries are taken as f16, as over the fp8 cache above), V takes part as
+ * f16(code * scale) (finite values beyond f16's range become its largest, values
+ * below 2^-14 lose bits).
+ * workspace:    optional, as for pkv_paged_extend_attn: given
+ *               pkv_extend_block_scaled_workspace_bytes() bytes or more, 256-byte
+ *               aligned, any contents, a call with many rows per request first
+ *               widens each block that its rows see, once, into 16-bit copies
+ *               there: K as code * scale in the act dtype (exact in bf16 for
+ *               powers of two as scales, what the append writes; in f16 within
+ *               its range, as V; other scales round to nearest), V as above.
  *               Calls that run at the same time need workspaces of their own.
- * At most 65,535 requests (else PKV_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 size_t pkv_extend_block_scaled_workspace_bytes(const pkv_cache_desc* desc);
 

@@ -731,8 +731,9 @@ def paged_extend_attn_window(k_cache, v_cache, q, out, q_indptr, prefix_lens, bl
 
 
 def extend_block_scaled_workspace_bytes(k_cache) -> int:
-    """pkv_extend_block_scaled_workspace_bytes: the workspace that paged_extend_attn_block_scaled
-    needs (16-bit copies of the K and V pools, and the per-block claims)."""
+    """pkv_extend_block_scaled_workspace_bytes: the optional workspace of
+    paged_extend_attn_block_scaled (16-bit copies of the K and V pools, and the per-block
+    claims)."""
     desc = _desc(k_cache, 1.0, 1.0)
     return int(load().pkv_extend_block_scaled_workspace_bytes(ctypes.byref(desc)))
 
@@ -743,7 +744,8 @@ def paged_extend_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out,
                                    workspace=None, stream=None):
     """pkv_paged_extend_attn_block_scaled: paged_extend_attn over fp8 codes with k_scales/v_scales
     float32 [num_blocks, Hkv]; window 0: every key, else as paged_extend_attn_window.
-    workspace: a uint8 device tensor of extend_block_scaled_workspace_bytes() bytes or more."""
+    workspace: None, or a uint8 device tensor of extend_block_scaled_workspace_bytes() bytes or
+    more (calls with many rows per request then widen the pages they read once per block)."""
     dev = q.device
     desc, kc, vc, pages, d = _pools(k_cache, v_cache, 1.0, 1.0)
     ks, vs = _block_scales(k_scales, v_scales, pages, k_cache.device)

@@ -173,6 +173,35 @@ bool plan_extend(ExtendParams& p, int batch, int num_kv_heads, int group, int ma
   return true;
 }
 
+// CTAs per item of an extend call with a window and / or block scales: its key
+// tiles are split over a cluster when the items are too few to fill the GPU and
+// their key ranges long.  The estimate is in key tiles (1.9 us each at 128 dims,
+// both row tiles): a CTA costs its tiles and a fixed part, 3 tiles, or 7 in a
+// cluster (writing and adding up the parts); 152 SMs hold 152, 152, 144 and 120
+// CTAs in clusters of 1, 2, 4 and 8.  Measured (us at 1 / 2 / 4 / 8 CTAs): 8
+// items of 64 tiles 123 / 75 / 44 / 30, 64 of 254 tiles 458 / 261 / 278 / 365,
+// 128 of up to 21 tiles 43 / 53 / 62 / 107, 32 of 35 tiles 62 / 43 / 31 / 65.
+int plan_key_splits(const ExtendParams& p, int max_total_len, int sm_count) {
+  int64_t tiles = ((int64_t)max_total_len + 127) / 128;
+  if (p.window > 0)
+    tiles = std::min<int64_t>(tiles, ((int64_t)p.window + 2 * p.tok + 15 + 127) / 128 + 1 +
+                                         ((int64_t)p.sink_tokens + 127) / 128);
+  const double sms = sm_count > 0 ? sm_count : 152;
+  int best = 1;
+  double best_cost = 1e30;
+  for (int c = 1; c <= 8; c *= 2) {
+    if ((int64_t)p.num_items * c > INT32_MAX || (c > 1 && tiles < c)) break;
+    const double slots = c == 8 ? sms * 120 / 152 : c == 4 ? sms * 144 / 152 : sms;
+    const double cost = std::ceil(p.num_items * c / slots) *
+                        ((double)((tiles + c - 1) / c) + (c > 1 ? 7.0 : 3.0));
+    if (cost < 0.9 * best_cost) {  // (not for less than a tenth)
+      best_cost = cost;
+      best = c;
+    }
+  }
+  return best;
+}
+
 // Softmax scale in base 2 with an fp8 cache's k_scale folded in (scores are
 // computed on the codes), and the output scale (v_scale for fp8, else 1).
 float score_scale_log2(const pkv_cache_desc* d, float sm_scale) {
@@ -862,9 +891,7 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   const bool widen_plain = !groups && workspace != nullptr && plain_bytes > 0 &&
                            workspace_bytes >= plain_bytes && aligned(workspace, 256) &&
                            batch <= 65535;
-  // a block-scaled cache is read through its widened pages only
   const bool scaled = view && view->k_scales;
-  if (scaled && batch > 65535) return PKV_ERR_UNSUPPORTED;
   const size_t widen_bytes = groups ? shared_prefix_widen_bytes(desc) : 0;
   // (the widening pass takes one CTA row per request: larger batches keep the
   // per-tile conversion)
@@ -877,7 +904,6 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   }
   const int32_t rows_hint = groups ? groups->max_group_rows : max_suffix_len;
   if (batch == 0 || total_q_rows == 0 || rows_hint == 0) return PKV_OK;
-  if (scaled && !widen_plain) return PKV_ERR_WORKSPACE;
   if (!k_cache || !v_cache || !q || !out || !block_tables || !q_indptr || !prefix_lens)
     return PKV_ERR_INVALID_ARG;
   if (groups && (!groups->group_indptr || !groups->group_shared)) return PKV_ERR_INVALID_ARG;
@@ -972,7 +998,22 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     if (e != cudaSuccess) return PKV_ERR_CUDA;
   }
   int cache_dt = (int)desc->cache_dtype;
-  if (widen_plain) {
+  bool widen_pages = widen_plain;
+  if (view) {
+    p.splits = plan_key_splits(p, max_total_len, ds->sm_count);
+    if (p.splits > 1) p.out_tma = 0;  // (every row leaves with the cluster's sum)
+    // Widening pays where many pairs of row tiles would convert the same pages:
+    // one pair per key tile costs 15 % (4 requests of 1,900 rows x 4 heads, 59
+    // pairs: 804 against 957 us), the pass itself three launches and three
+    // times the pages' bytes (300 rows, 10 pairs: 140 against 132; 16 rows: 123
+    // against 68).
+    if (p.splits > 1 || (p.tiles_per_head + 1) / 2 < 16) widen_pages = false;
+    if (scaled && !widen_pages) {
+      p.k_scales = view->k_scales;
+      p.v_scales = view->v_scales;
+    }
+  }
+  if (widen_pages) {
     // the pages the call reads, each block widened once (claimed in the
     // workspace) into 16-bit pools read through maps over them
     pkv_cache_desc d16 = *desc;
@@ -995,9 +1036,9 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     cache_dt = act_dtype == PKV_BF16 ? DT_BF16_V16 : DT_F16;
   }
-  if (p.window > 0)
-    e = launch_extend_window(kmap, vmap, qmap, omap, p, desc->head_dim, cache_dt, (int)act_dtype,
-                             stream);
+  if (view)
+    e = launch_extend_view(kmap, vmap, qmap, omap, p, desc->head_dim, cache_dt, (int)act_dtype,
+                           stream);
   else
     e = launch_extend(kmap, vmap, qmap, omap, p, desc->head_dim, cache_dt, (int)act_dtype, stream);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

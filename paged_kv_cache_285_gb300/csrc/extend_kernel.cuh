@@ -68,6 +68,24 @@
 // over a chunk leaves as an fp32 partial (O / l and the base-2 LSE) in the
 // chunk's slot, for an LSE merge with the member's own tokens.
 //
+// Scales per block and kv head (BSC = true, fp8 codes): K stays as codes (exact
+// in f16) and its scales multiply the scores, 16 keys of one block at a time
+// (the row max, and the factor of the exponent's FFMA, which is a constant
+// otherwise); V's scale is applied as the converter thread that owns the key
+// row widens it, V = f16(code * scale), one rounding.  The producer lanes that
+// look a sub-tile's block up load its scales too and leave them beside the
+// ring.
+//
+// Split (CL = true), for calls with few items and long key ranges: the key tiles
+// of one item are cut into runs, one per CTA of a cluster (item =
+// blockIdx.x / cluster size), each with a softmax of its own.  At the end each
+// CTA combines a share of the rows: once every CTA is done with its rings, the
+// rows' unnormalised O (fp32, from TMEM) and (max, sum) are written straight
+// into the rings of the CTA that owns them, and
+// O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c.  No workspace, no second
+// launch.  (Writing to the owner, not reading from the others: a remote load is
+// waited for, a remote store is not.)
+//
 // Window (WIN = true): row i at position p = prefix + i sees keys j <= p with
 // j > p - window, and the first sink_tokens keys.  An item's key tiles are
 // the tiles of the sink keys, then those from the oldest key of its first
@@ -136,6 +154,20 @@ struct ExtCfg {
   static constexpr int OFF_TMEMSLOT = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_TMEMSLOT + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory per CTA");
+  // BSC: the scales of a tile's eight 16-key sub-tiles, K's and V's, in rings of
+  // four tiles.  Tile m's K scales replace those of tile m - 4, whose softmax is
+  // done: the K stage of tile m is free once S_B(m - NST) is done, which was
+  // issued after P_A and P_B of tile m - NST - 1.
+  static constexpr int NSC = 4;
+  static_assert(NSC >= NST + 1, "scale ring");
+  static constexpr int OFF_SCALE = (OFF_TMEMSLOT + 16 + 15) / 16 * 16;  // read 16 bytes at a time
+  static constexpr int SMEM_BSC = OFF_SCALE + 2 * NSC * 8 * 4 + 1024;
+  static_assert(SMEM_BSC <= 232448, "shared memory per CTA");
+  // CL: the fp32 parts of the CTA's share of the rows over the rings, their
+  // (max, sum) and the softmax warps' buffers (4 KB each) over the Q tiles
+  static constexpr int OFF_CO = OFF_K;
+  static_assert(4096 + 8 * 4096 <= NQB * T16, "buffers fit the Q tiles");
+  static_assert(2 * BM * HD * 4 <= 2 * NST * T16, "O rows fit the rings");
   // where the fp8 codes of stage s of the K (isv false) or V ring are loaded
   __host__ __device__ static constexpr int src8(bool isv, int s) {
     return STAGE8 ? (isv ? OFF_V8 : OFF_K8) + s * T8 : (isv ? OFF_V : OFF_K) + s * T16;
@@ -288,6 +320,70 @@ __device__ __forceinline__ void widen_row(const uint8_t* src, uint8_t* dst, int 
   }
 }
 
+// A finite value beyond f16's range becomes its largest (NaN stays NaN).
+__device__ __forceinline__ float clamp_f16(float a) {
+  return fabsf(a) > 65504.f ? copysignf(65504.f, a) : a;
+}
+
+// widen_row for V codes under a scale s: f16(code * s), rounded once, finite
+// values kept inside f16's range.  A scale that f16 holds, and that keeps 448 s
+// inside, is applied in f16 (one rounding of the exact product, the same bits);
+// any other in fp32.
+template <int HD>
+__device__ __forceinline__ void widen_row_scaled(const uint8_t* src, uint8_t* dst, int t, bool zero,
+                                                 float s) {
+  const __half hs = __float2half_rn(s);
+  const __half2 hs2 = __half2half2(hs);
+  const uint32_t sbase = (HD == 128) ? ((uint32_t)t * 128u) | (((uint32_t)t & 7u) << 4)
+                                     : ((uint32_t)t * 64u) | ((((uint32_t)t >> 1) & 3u) << 4);
+  const uint32_t dbase = ((uint32_t)t * 128u) | (((uint32_t)t & 7u) << 4);
+  auto put = [&](int u, const uint4& lo, const uint4& hi) {
+    uint8_t* blk = dst + (u >> 2) * CHUNK;
+    *reinterpret_cast<uint4*>(blk + (dbase ^ (uint32_t)((2 * (u & 3)) << 4))) = lo;
+    *reinterpret_cast<uint4*>(blk + (dbase ^ (uint32_t)((2 * (u & 3) + 1) << 4))) = hi;
+  };
+  auto mul = [&](uint32_t w) -> uint32_t {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&w), hs2);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  };
+  if (zero || (__half2float(hs) == s && s <= 146.f)) {
+#pragma unroll
+    for (int pr = HD / 32 - 1; pr >= 0; --pr) {  // unit pairs, highest first, as widen_row
+      uint4 a[2];
+      if (!zero) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          a[j] = *reinterpret_cast<const uint4*>(src + (sbase ^ (uint32_t)((2 * pr + j) << 4)));
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+        if (!zero) {
+          widen16<DT_F16>(a[j], lo, hi);
+          lo = make_uint4(mul(lo.x), mul(lo.y), mul(lo.z), mul(lo.w));
+          hi = make_uint4(mul(hi.x), mul(hi.y), mul(hi.z), mul(hi.w));
+        }
+        put(2 * pr + j, lo, hi);
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int u = HD / 16 - 1; u >= 0; --u) {
+      const uint4 a = *reinterpret_cast<const uint4*>(src + (sbase ^ (uint32_t)(u << 4)));
+      uint4 w[2];
+      widen16<DT_F16>(a, w[0], w[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t* q[4] = {&w[j].x, &w[j].y, &w[j].z, &w[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *q[e] = pack2<false>(clamp_f16(lo_f32<false>(*q[e]) * s), clamp_f16(hi_f32<false>(*q[e]) * s));
+      }
+      put(u, w[0], w[1]);
+    }
+  }
+}
+
 // Per-request values an item needs, loaded one item ahead.  Shared-prefix
 // extend (SX): per-group values (rows r0 .. r1-1 of requests ga .. gb-1,
 // `prefix` = the group's shared prefix length).
@@ -305,17 +401,11 @@ struct Item {
 struct WinItem : Item {
   int Ts, wlo, w0;
 };
-template <bool WIN>
+template <bool WIN, bool CL>
 struct ItemOf { using T = Item; };
 template <>
-struct ItemOf<true> { using T = WinItem; };
+struct ItemOf<true, false> { using T = WinItem; };
 
-// First key of key tile kt of a plain, prefix-pass or window item.
-template <bool WIN>
-__device__ __forceinline__ int tile_key(const typename ItemOf<WIN>::T& it, int kt) {
-  if constexpr (WIN) return kt < it.Ts ? kt * BN : it.wlo + (kt - it.Ts) * BN;
-  else return it.k_lo + kt * BN;
-}
 
 template <bool SX>
 __device__ __forceinline__ ItemRaw load_raw(const ExtendParams& p, int item) {
@@ -341,6 +431,17 @@ __device__ __forceinline__ ItemRaw load_raw(const ExtendParams& p, int item) {
   }
   return r;
 }
+
+// The cluster's share of an item's key tiles (CL): kt0 is the CTA's first tile;
+// `rows` is set where the item has rows, whether or not the CTA has a tile.
+struct SplitItem : WinItem {
+  int kt0;
+  bool rows;
+};
+template <>
+struct ItemOf<true, true> { using T = SplitItem; };
+template <>
+struct ItemOf<false, true> { using T = SplitItem; };
 
 // A run of key tiles that the same rows may see through the same block
 // table: the whole key range of a plain or prefix-pass item, or (SX) the
@@ -395,6 +496,16 @@ __device__ __forceinline__ int find_req_warp(const int32_t* q_indptr, int lo, in
 
 // The key tiles of an item walked in order, segment by segment; every role
 // walks them the same way.
+
+// First key of key tile kt (of the CTA's share) of a plain, prefix-pass or
+// window item.
+template <bool WIN, bool CL>
+__device__ __forceinline__ int tile_key(const typename ItemOf<WIN, CL>::T& it, int kt) {
+  if constexpr (CL) kt += it.kt0;
+  if constexpr (WIN) return kt < it.Ts ? kt * BN : it.wlo + (kt - it.Ts) * BN;
+  else return it.k_lo + kt * BN;
+}
+
 struct SegIter {
   Seg sg;
   int st;  // tile within the segment
@@ -446,7 +557,7 @@ __device__ __forceinline__ void seg_advance(const ExtendParams& p, const Item& i
 // table is not computed and is reported as a length error.
 template <bool PP, bool SX, bool WIN>
 __device__ __forceinline__ bool derive(const ExtendParams& p, int item, const ItemRaw& r,
-                                       typename ItemOf<WIN>::T& it) {
+                                       typename ItemOf<WIN, false>::T& it) {
   const uint32_t rest = p.div_pairs.div((uint32_t)item);
   int pair = item - (int)(rest * p.div_pairs.d);
   int kc = 0;  // prefix pass: the item's key chunk
@@ -547,15 +658,96 @@ __device__ __forceinline__ bool derive(const ExtendParams& p, int item, const It
   return true;
 }
 
+// derive for any kernel; CL: then the CTA's share of the item's key tiles.
+template <bool PP, bool SX, bool WIN, bool CL>
+__device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, const ItemRaw& r,
+                                           typename ItemOf<WIN, CL>::T& it) {
+  if constexpr (CL) {
+    it.kt0 = 0;
+    it.rows = false;
+    if (!derive<PP, SX, WIN>(p, item, r, it)) return false;
+    it.rows = true;
+    const int per = (it.T + p.splits - 1) / p.splits;
+    it.kt0 = (int)cluster_rank() * per;
+    it.T = min(per, it.T - it.kt0);
+    return it.T > 0;
+  } else {
+    return derive<PP, SX, WIN>(p, item, r, it);
+  }
+}
+
+// CL: this CTA's share of the item's 2 x 128 rows (row R belongs to CTA R mod
+// splits, as its row R / splits) out of the parts that the cluster's CTAs left at
+// co [splits][share][HD] (fp32) and ml [splits][share] (max, sum).  The softmax
+// threads, tid 0 .. 255 = splits x share: each first turns one (max, sum) into
+// its part's weight (in place), then they add the rows up.
+template <int HD, int AT, bool WIN>
+__device__ __forceinline__ void combine_parts(const ExtendParams& p, int item, const uint8_t* co,
+                                              float2* ml, int tid) {
+  typename ItemOf<WIN, true>::T it;
+  const ItemRaw raw = load_raw<false>(p, item);
+  derive_any<false, false, WIN, true>(p, item, raw, it);
+  if (!it.rows) return;
+  const int C = p.splits, share = 2 * BM / C, rank = (int)cluster_rank();
+  // row lr of the share: its output row, or -1
+  auto out_row = [&](int lr) -> int64_t {
+    const int row = lr * C + rank, x = row / BM, r = row % BM;
+    const int rtok = r / p.group;
+    if (rtok >= it.ntok[x]) return -1;
+    return (int64_t)(it.row0 + it.i0 + x * p.tok + rtok) * p.num_q_heads + it.g * p.group + (r - rtok * p.group);
+  };
+  {
+    const int c = tid / share, lr = tid - c * share;
+    float m = -INFINITY, l = 0.f;
+    for (int k = 0; k < C; ++k) m = fmaxf(m, ml[k * share + lr].x);
+    for (int k = 0; k < C; ++k) {
+      const float2 s = ml[k * share + lr];
+      if (s.x != -INFINITY) l += fast_exp2(s.x - m) * s.y;
+    }
+    const float mine = ml[tid].x;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    // (a part without a key has weight 0 and was not written)
+    ml[tid].x = mine != -INFINITY ? fast_exp2(mine - m) * (p.out_scale / l) : 0.f;
+    const int64_t q = p.lse_out && c == 0 ? out_row(lr) : -1;
+    if (q >= 0) p.lse_out[q] = (m + log2f(l)) * kLn2f;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+  }
+  constexpr int UPR = HD / 8;  // a task is 8 values of a row
+#pragma unroll 1
+  for (int task = tid; task < share * UPR; task += 256) {
+    const int lr = task / UPR, u = task % UPR;
+    const int64_t q = out_row(lr);
+    if (q < 0) continue;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int c = 0; c < C; ++c) {
+      const float w = ml[c * share + lr].x;
+      if (w == 0.f) continue;
+      const float4* at = reinterpret_cast<const float4*>(co + (c * share + lr) * (HD * 4)) + 2 * u;
+      const float4 a = at[0], b = at[1];
+      o[0] += w * a.x; o[1] += w * a.y; o[2] += w * a.z; o[3] += w * a.w;
+      o[4] += w * b.x; o[5] += w * b.y; o[6] += w * b.z; o[7] += w * b.w;
+    }
+    uint4 w4;
+    w4.x = pack2<AT == DT_BF16>(o[0], o[1]);
+    w4.y = pack2<AT == DT_BF16>(o[2], o[3]);
+    w4.z = pack2<AT == DT_BF16>(o[4], o[5]);
+    w4.w = pack2<AT == DT_BF16>(o[6], o[7]);
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + q * HD + u * 8) = w4;
+  }
+}
+
 // HD: head dim (64 or 128); CT: cache dtype (f16, bf16 or e4m3); AT: the
 // activation dtype of q and out (equal to CT for 16-bit caches); PP: the
-// prefix pass; SX: shared-prefix extend; WIN: a window with sink tokens.
-template <int HD, int CT, int AT, bool PP, bool SX, bool WIN>
+// prefix pass; SX: shared-prefix extend; WIN: a window with sink tokens; BSC:
+// fp8 codes with scales per block and kv head; CL: key tiles split over a cluster.
+template <int HD, int CT, int AT, bool PP, bool SX, bool WIN, bool BSC, bool CL>
 __global__ void __launch_bounds__(NTHREADS, 1)
 extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
               const ExtendParams p, const ExtendPartialParams pp) {
-  static_assert(!(WIN && (PP || SX)), "unsupported combination");
+  static_assert(!((WIN || BSC || CL) && (PP || SX)) && (!BSC || CT == DT_E4M3),
+                "unsupported combination");
   using C = ExtCfg<HD, CT, AT>;
   constexpr int NST = C::NST;
   extern __shared__ uint8_t smem_raw[];
@@ -569,7 +761,17 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
   const int TOK = p.tok;
-  const int item0 = blockIdx.x, stride = gridDim.x;
+  // CL: one item per cluster, the first pair of tiles of every (request, head)
+  // before any second one (later pairs of short requests are empty); else a
+  // persistent CTA
+  int item0 = blockIdx.x, stride = gridDim.x;
+  if constexpr (CL) {
+    const int pairs = (int)p.div_pairs.d, heads = p.num_items / pairs, j = blockIdx.x / p.splits;
+    item0 = (j % heads) * pairs + j / heads;
+    stride = p.num_items;
+  }
+  float* kscale = reinterpret_cast<float*>(smem + C::OFF_SCALE);  // BSC: [NSC][8]
+  float* vscale = kscale + C::NSC * 8;
   // WIN: no row of the item sees keys key .. key + count - 1
   auto unseen = [&](const auto& it, int key, int count) -> bool {
     return key >= p.sink_tokens && key + count <= it.w0;
@@ -614,7 +816,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // MMA warpgroup (0-3) lowers its to 96 and the converters (12-15) to 48
   // (fp8 caches, whose converters widen K and V: 88 and 56); the shares add up
   // to the launch budget, 4 x 128.
-  constexpr int kRegsProd = C::FP8 ? 88 : 96, kRegsConv = C::FP8 ? 56 : 48;
+  // (BSC: 80 and 64; the converters hold a scale)
+  constexpr int kRegsProd = BSC ? 80 : C::FP8 ? 88 : 96, kRegsConv = BSC ? 64 : C::FP8 ? 56 : 48;
   static_assert(2 * 184 + kRegsProd + kRegsConv == 4 * 128,
                 "register split must equal the launch budget");
   if (warp >= 4 && warp < 12) {
@@ -628,12 +831,14 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint32_t srow = tmem + lane_addr + tm_s(x);
     const uint32_t orow = tmem + lane_addr + tm_o<HD>(x);
     int n = 0, js = 0;
+    float m_fin = -INFINITY, l_fin = 0.f;  // CL
+    int nrows = 0;
     ItemRaw nxt_raw = load_raw<SX>(p, item0);
     for (int item = item0; ok && item < p.num_items; item += stride) {
       const ItemRaw raw = nxt_raw;
       nxt_raw = load_raw<SX>(p, item + stride);
-      typename ItemOf<WIN>::T it;
-      if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
+      typename ItemOf<WIN, CL>::T it;
+      if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
       const int i0x = it.i0 + x * TOK;  // first token of this tile
       // a row's last visible key is kdiag + its token (prefix pass: the chunk's
       // last key for all)
@@ -654,7 +859,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int kt = 0; kt < it.T; ++kt, ++n, seg_advance<SX>(p, it, si)) {
         if (!mbar_wait(bar(C::B_SDONE + x), n & 1)) { ok = false; break; }
         tc_fence_after();
-        const int key0 = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN>(it, kt);
+        const int key0 = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, CL>(it, kt);
         // keys key0 .. key0 + nvis of the tile are visible to this row
         int nvis;
         bool masked;
@@ -720,22 +925,39 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               sr[c][q] = (WIN ? ((wb >> q) & 1u) == 0u : c * 32 + q > nvis) ? ninf : sr[c][q];
           }
         }
-        // row max: three-input max over 8 independent accumulators
+        // BSC: the factors of the tile's eight groups of 16 keys (at least the
+        // smallest normal number, so that a masked score stays -inf)
+        float sg[8];
+        if constexpr (BSC) {
+          const float4* ks4 = reinterpret_cast<const float4*>(kscale + (n % C::NSC) * 8);
+          const float4 ka = ks4[0], kb = ks4[1];
+          const float kk[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int a = 0; a < 8; ++a) sg[a] = fmaxf(kk[a] * p.scale_log2, 1.17549435e-38f);
+        }
+        // row max: three-input max over 8 independent accumulators (BSC: one
+        // per group, scaled afterwards)
         float mx[8];
 #pragma unroll
         for (int a = 0; a < 8; ++a) mx[a] = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int q = 0; q < 16; ++q)
-            mx[q & 7] = fmax3(mx[q & 7], __uint_as_float(sr[c][2 * q]), __uint_as_float(sr[c][2 * q + 1]));
+          for (int q = 0; q < 16; ++q) {
+            const int a = BSC ? 2 * c + (q >> 3) : q & 7;
+            mx[a] = fmax3(mx[a], __uint_as_float(sr[c][2 * q]), __uint_as_float(sr[c][2 * q + 1]));
+          }
+        if constexpr (BSC) {
+#pragma unroll
+          for (int a = 0; a < 8; ++a) mx[a] *= sg[a];
+        }
         const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                               fmaxf(mx[6], mx[7])) * p.scale_log2;
+                               fmaxf(mx[6], mx[7])) * (BSC ? 1.f : p.scale_log2);
         float m_new = m_run;
         if (mt > m_run + 8.f) m_new = mt;
-        // SX, WIN: a row that has seen no key yet keeps m = -inf and takes 0 as
+        // SX, WIN, CL: a row that has seen no key yet keeps m = -inf and takes 0 as
         // the exponent's base, so its masked scores give exact zeros
-        const float m_base = ((SX || WIN) && m_new == -INFINITY) ? 0.f : m_new;
+        const float m_base = ((SX || WIN || CL) && m_new == -INFINITY) ? 0.f : m_new;
         const float alpha = fast_exp2(m_run - m_base);
         const bool mine = (m_new != m_run);
         if (kt >= 1 && __any_sync(0xFFFFFFFFu, mine)) {
@@ -764,8 +986,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           uint32_t pk[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
+            const float2 f2 = BSC ? make_float2(sg[2 * c + (q >> 3)], sg[2 * c + (q >> 3)]) : sc2;
             const float2 xv = __ffma2_rn(
-                make_float2(__uint_as_float(sr[c][2 * q]), __uint_as_float(sr[c][2 * q + 1])), sc2, nm2);
+                make_float2(__uint_as_float(sr[c][2 * q]), __uint_as_float(sr[c][2 * q + 1])), f2, nm2);
             const float2 pe = make_float2(fast_exp2(xv.x), fast_exp2(xv.y));
             sm[q & 3] = __fadd2_rn(sm[q & 3], pe);
             pk[q] = pack2<false>(pe.x, pe.y);
@@ -791,7 +1014,12 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // each thread)
       const bool staged = out_tma_for<HD, CT, SX>() && !PP && p.out_tma && it.ntok[x] == TOK;
       const float osc = p.out_scale / l_run;
-      if constexpr (PP) {
+      if constexpr (CL) {
+        // O stays in TMEM until the whole cluster is done with its rings
+        m_fin = m_run;
+        l_fin = l_run;
+        nrows = it.ntok[x];
+      } else if constexpr (PP) {
         // fp32 O / l straight from TMEM (the whole row before one wait), then
         // the LSE
         const int req = it.row0 + i0x + rtok;  // the group member of this row
@@ -881,6 +1109,50 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
       ++js;
     }
+    if constexpr (CL) {
+      // every CTA of the cluster is done with its rings: the rows go to the CTA
+      // that combines them, unnormalised, with their (max, sum)
+      cluster_sync();
+      // (row R to CTA R mod splits; 32 columns of the warp's rows at a time
+      // through shared memory, so that eight lanes write 128 bytes of a row: a
+      // row per lane took 3 to 6 us more)
+      const int C_ = p.splits, share = 2 * BM / C_, row = x * BM + r;
+      const uint32_t rank = cluster_rank();
+      {
+        const uint32_t lr = row / C_, owner = row - lr * C_;
+        cluster_st2(cluster_map(s_base + C::OFF_Q + (rank * share + lr) * 8, owner), make_float2(m_fin, l_fin));
+      }
+      const uint32_t send = __ballot_sync(0xFFFFFFFFu, m_fin != -INFINITY && rtok < nrows);
+      if (send != 0u) {
+        uint8_t* stg = smem + C::OFF_Q + 4096 + (x * 4 + qw) * 4096;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(orow + c * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4*>(stg + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 4 * k + (lane >> 3), u = lane & 7;
+            if ((send >> rr) & 1u) {
+              const uint32_t R = x * BM + qw * 32 + rr, lr = R / C_, owner = R - lr * C_;
+              const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * 128 + ((u ^ (rr & 7)) << 4));
+              cluster_st4(cluster_map(s_base + C::OFF_CO + (rank * share + lr) * (HD * 4) + c * 128 + u * 16, owner),
+                          v.x, v.y, v.z, v.w);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      cluster_sync();
+      combine_parts<HD, AT, WIN>(p, item0, smem + C::OFF_CO,
+                                 reinterpret_cast<float2*>(smem + C::OFF_Q), row);
+    }
   } else if (warp < 4) {
     regs_dec<kRegsProd>();
     if (warp == 0 || warp == 2) {
@@ -921,27 +1193,27 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = item0; ok && item < p.num_items; item += stride) {
         const ItemRaw raw = nxt_raw;
         nxt_raw = load_raw<SX>(p, item + stride);
-        typename ItemOf<WIN>::T it;
-        if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
+        typename ItemOf<WIN, CL>::T it;
+        if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
         if (is_k && !load_q(it, j, 0)) { ok = false; break; }
         SegIter si;
         seg_begin<SX>(p, it, si);
         const int32_t* bt = p.block_tables;
+        float scale_cur = 1.f, scale_nxt = 1.f;  // BSC: of the lane's sub-tile in the two windows
         int sk_lo = 0, sk_hi = 0;  // the segment's keys
         auto fetch = [&](int wi) -> int {
           const int st16 = wi * 32 + lane;  // sub-tile = 16 keys
           int key0 = sk_lo + st16 * 16;
+          if constexpr (WIN || CL) key0 = tile_key<WIN, CL>(it, st16 >> 3) + (st16 & 7) * 16;
           bool read = key0 < sk_hi;
-          if constexpr (WIN) {
-            if (st16 >= it.Ts * 8) key0 = it.wlo + (st16 - it.Ts * 8) * 16;
-            read = key0 < sk_hi && !unseen(it, key0, 16);
-          }
+          if constexpr (WIN) read = read && !unseen(it, key0, 16);
           int page = -1;
           if (read) {
             const int blk = bt[key0 >> p.bs_shift];
             if (blk < 0 || blk >= p.num_blocks) set_err(p.err, 1);  // TMA zero-fills page -1
             else page = blk * p.num_kv_heads + it.g;
           }
+          if constexpr (BSC) scale_nxt = page >= 0 ? __ldg((is_k ? p.k_scales : p.v_scales) + page) : 1.f;
           return page;
         };
         int win = 0, cur = -1, nxt = -1;
@@ -959,9 +1231,11 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             sk_hi = SX ? si.sg.k_hi : it.k_hi;
             win = 0;
             cur = fetch(0);
+            scale_cur = scale_nxt;
             nxt = fetch(1);
           } else if ((st >> 2) > win) {  // 4 tiles x 8 sub-tiles per window
             cur = nxt;
+            scale_cur = scale_nxt;
             ++win;
             nxt = fetch(win + 1);
           }
@@ -969,6 +1243,11 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
           for (int q = 0; q < 8; ++q) pg[q] = __shfl_sync(0xFFFFFFFFu, cur, (st & 3) * 8 + q);
           if (n >= NST && !mbar_wait(bar(free0 + s), (uint32_t)((n / NST - 1) & 1))) { ok = false; break; }
+          if constexpr (BSC) {
+            // the tile's eight scales, ordered before its barrier completes
+            if ((lane >> 3) == (st & 3)) (is_k ? kscale : vscale)[(n % C::NSC) * 8 + (lane & 7)] = scale_cur;
+            __syncwarp();
+          }
           if (lane == 0) {
             const uint32_t fb = bar(full0 + s);
             if constexpr (C::FP8) {
@@ -977,7 +1256,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               mbar_arrive_expect_tx(fb, C::T8);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const int rip = ((WIN ? tile_key<WIN>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
+                const int rip = ((WIN || CL ? tile_key<WIN, CL>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
                 tma_load_3d(dst + q * 16 * HD, map, fb, 0, rip, pg[q]);
               }
             } else {
@@ -985,7 +1264,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               mbar_arrive_expect_tx(fb, C::T16);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const int rip = ((WIN ? tile_key<WIN>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
+                const int rip = ((WIN || CL ? tile_key<WIN, CL>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
 #pragma unroll
                 for (int c = 0; c < C::NCH; ++c)
                   tma_load_3d(dst + c * CHUNK + q * 2048, map, fb, c * 64, rip, pg[q]);
@@ -1011,8 +1290,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = item0; ok && item < p.num_items; item += stride) {
         const ItemRaw raw = nxt_raw;
         nxt_raw = load_raw<SX>(p, item + stride);
-        typename ItemOf<WIN>::T it;
-        if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
+        typename ItemOf<WIN, CL>::T it;
+        if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
         const uint32_t stg = s_base + C::OFF_Q + ((2 * js + 1) % NQB) * C::T16;
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
@@ -1090,8 +1369,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = item0; ok && item < p.num_items; item += stride) {
         const ItemRaw raw = nxt_raw;
         nxt_raw = load_raw<SX>(p, item + stride);
-        typename ItemOf<WIN>::T it;
-        if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
+        typename ItemOf<WIN, CL>::T it;
+        if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
         const int qa = (2 * j) % NQB, qb = (2 * j + 1) % NQB;
         for (int kt = 0; kt < it.T; ++kt, ++n) {
           if constexpr (C::FP8 && HD == 128) {
@@ -1171,8 +1450,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = item0; ok && item < p.num_items; item += stride) {
         const ItemRaw raw = nxt_raw;
         nxt_raw = load_raw<SX>(p, item + stride);
-        typename ItemOf<WIN>::T it;
-        if (!derive<PP, SX, WIN>(p, item, raw, it)) continue;
+        typename ItemOf<WIN, CL>::T it;
+        if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
         SegIter si;
         seg_begin<SX>(p, it, si);
         for (int kt = 0; kt < it.T; ++kt, ++n, seg_advance<SX>(p, it, si)) {
@@ -1197,7 +1476,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           // keys at or past the segment's end are zeroed (a shared prefix's
           // last tile reaches into one member's own keys, which no row of the
           // segment sees)
-          const int kbase = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN>(it, kt);
+          const int kbase = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, CL>(it, kt);
           const int kv_end = SX ? si.sg.kv_total : it.kv_total;
           // WIN: keys between the sinks and the first row's window too
           bool zero = kbase + t >= kv_end, hole = false;
@@ -1207,7 +1486,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
           uint8_t* vt = smem + C::OFF_V + s * C::T16;
           if constexpr (C::FP8) {
-            widen_row<HD, DT_F16>(smem + C::src8(true, s), vt, t, zero);
+            if constexpr (BSC)
+              widen_row_scaled<HD>(smem + C::src8(true, s), vt, t, zero, vscale[(n % C::NSC) * 8 + (t >> 4)]);
+            else
+              widen_row<HD, DT_F16>(smem + C::src8(true, s), vt, t, zero);
             fence_async_smem();
           } else if (kbase + BN > kv_end || hole) {
             // tail tile: zero the keys past the end (and those no row sees)
@@ -1229,6 +1511,14 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 
   if (!ok) set_err(p.err, 4);
+  if constexpr (CL) {
+    // the softmax warps' two barriers (no CTA leaves before all have written
+    // what they owe the others)
+    if (warp < 4 || warp >= 12) {
+      cluster_sync();
+      cluster_sync();
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1237,16 +1527,41 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 }
 
-template <int HD, int CT, int AT, bool PP, bool SX, bool WIN = false>
+template <int HD, int CT, int AT, bool PP, bool SX, bool WIN = false, bool BSC = false>
 cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                             const CUtensorMap& omap, const ExtendParams& p,
                             const ExtendPartialParams& pp, cudaStream_t stream) {
-  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN>;
-  constexpr int smem = ExtCfg<HD, CT, AT>::SMEM;
+  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN, BSC, false>;
+  constexpr int smem = BSC ? ExtCfg<HD, CT, AT>::SMEM_BSC : ExtCfg<HD, CT, AT>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   k<<<dim3(p.num_ctas), NTHREADS, smem, stream>>>(kmap, vmap, qmap, omap, p, pp);
   return cudaGetLastError();
+}
+
+// One item per cluster of p.splits CTAs (1, 2, 4 or 8), its key tiles split over them.
+template <int HD, int CT, int AT, bool WIN, bool BSC>
+cudaError_t launch_extend_split_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                  const CUtensorMap& qmap, const CUtensorMap& omap,
+                                  const ExtendParams& p, cudaStream_t stream) {
+  auto k = extend_kernel<HD, CT, AT, false, false, WIN, BSC, true>;
+  constexpr int smem = BSC ? ExtCfg<HD, CT, AT>::SMEM_BSC : ExtCfg<HD, CT, AT>::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.splits;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p.num_items * (unsigned)p.splits);
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const ExtendPartialParams pp{};
+  return cudaLaunchKernelEx(&cfg, k, kmap, vmap, qmap, omap, p, pp);
 }
 
 }  // namespace

@@ -8,11 +8,6 @@ cudaError_t launch_extend_window(const CUtensorMap& kmap, const CUtensorMap& vma
                                  const CUtensorMap& qmap, const CUtensorMap& omap,
                                  const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
                                  cudaStream_t stream) {
-  const int checked_dt = cache_dt == DT_BF16_V16 ? DT_BF16 : cache_dt;
-  if (!extend_supported(head_dim, checked_dt, act_dt, p.group)) return cudaErrorInvalidValue;
-  if (p.num_items <= 0 || p.num_ctas <= 0 || p.tok != BM / p.group || p.window <= 0 ||
-      p.sink_tokens < 0)
-    return cudaErrorInvalidValue;
   const ExtendPartialParams pp{};
 #define PKV_EXT(HD, CT, AT)                             \
   if (head_dim == HD && cache_dt == CT && act_dt == AT) \

@@ -226,6 +226,9 @@ struct ExtendParams {
   float out_scale;
   int window;           // window launches: keys j > p - window are visible to position p ...
   int sink_tokens;      // ... and keys j < sink_tokens (window 0: every key j <= p)
+  const float* k_scales;  // block-scaled launches: [num_blocks][num_kv_heads]
+  const float* v_scales;
+  int splits;           // split launches: CTAs per item (its key tiles split over them)
 };
 
 // Partial output of the extend kernel's prefix pass: row q (request b, head h:
@@ -295,7 +298,17 @@ cudaError_t launch_extend_shared(const CUtensorMap& kmap, const CUtensorMap& vma
                                  const CUtensorMap& qmap, const CUtensorMap& omap,
                                  const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
                                  cudaStream_t stream);
-// Extend under a window with sink tokens (p.window > 0).
+// Extend under a window with sink tokens (p.window > 0), or of fp8 codes with
+// scales per block and kv head (p.k_scales, p.v_scales; read as codes), or
+// both; p.splits > 1: the key tiles of every item split over a cluster of CTAs.
+cudaError_t launch_extend_view(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const CUtensorMap& qmap, const CUtensorMap& omap,
+                               const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
+                               cudaStream_t stream);
+cudaError_t launch_extend_split(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                const CUtensorMap& qmap, const CUtensorMap& omap,
+                                const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
+                                cudaStream_t stream);
 cudaError_t launch_extend_window(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  const CUtensorMap& qmap, const CUtensorMap& omap,
                                  const ExtendParams& p, int head_dim, int cache_dt, int act_dt,

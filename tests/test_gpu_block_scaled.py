@@ -230,7 +230,9 @@ def test_decode_ignores_what_lies_past_the_end():
 def run_extend(c, q, hq, rows, prefix, window=0, sinks=0, fill=0xFF):
     out = torch.full((q.shape[0], hq, c.d), float("nan"), dtype=TDT[c.act], device="cuda")
     lse = torch.full((q.shape[0], hq), float("nan"), device="cuda")
-    ws = torch.full((pkv.extend_block_scaled_workspace_bytes(c.k),), fill, dtype=torch.uint8, device="cuda")
+    ws = None
+    if fill is not None:
+        ws = torch.full((pkv.extend_block_scaled_workspace_bytes(c.k),), fill, dtype=torch.uint8, device="cuda")
     pkv.paged_extend_attn_block_scaled(c.k, c.v, c.ks, c.vs, q, out, ints(indptr(rows)), ints(prefix), c.bt,
                                        1 / c.d ** 0.5, max(rows), max(p + n for p, n in zip(prefix, rows)),
                                        window=window, sink_tokens=sinks, lse_out=lse, workspace=ws)
@@ -257,6 +259,43 @@ def test_extend(cfg, window, sinks):
     ref = R.attention(*c.values(), to_f64(q), indptr(rows), prefix, c.tables, hq, 1 / d ** 0.5, window, sinks)
     check_attention(out, lse, ref, act, d, f"{cfg} {window}")
     assert pkv.get_device_error() == 0
+
+
+# (rows, prefix, heads, window, sinks): many rows per request (pages widened into the workspace, or
+# not without one), few rows over many keys (split over clusters of 2, 4 and 8), some of whose parts
+# hold no key that a row sees
+REGIMES = [([40, 530], [100, 3], 8, 0, 0), ([530], [60], 16, 200, 4), ([9, 0, 33], [700, 50, 300], 4, 0, 0),
+           ([3], [2100], 4, 0, 0), ([70], [900], 4, 600, 130), ([200], [520], 2, 300, 0)]
+
+
+@pytest.mark.parametrize("cfg", REGIMES, ids=lambda c: f"r{max(c[0])}-p{max(c[1])}-h{c[2]}-w{c[3]}")
+@pytest.mark.parametrize("d,bs,act", [(64, 32, F16), (128, 16, BF16)])
+def test_extend_regimes(cfg, d, bs, act):
+    rows, prefix, hq, window, sinks = cfg
+    c = Case(SCALED, act, 1, d, bs, [p + n for p, n in zip(prefix, rows)], seed=sum(rows)).cuda()
+    q = c.rows(sum(rows), hq).cuda()
+    ref = R.attention(*c.values(), to_f64(q), indptr(rows), prefix, c.tables, hq, 1 / d ** 0.5, window, sinks)
+    for fill in (0xFF, None):
+        out, lse = run_extend(c, q, hq, rows, prefix, window, sinks, fill)
+        check_attention(out, lse, ref, act, d, f"{cfg} {fill}")
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("rows,prefix", [([16], [16]), ([20], [1500]), ([140], [0])])
+def test_extend_scales_of_any_size(rows, prefix):
+    # V scales that f16 does not hold, K scales far apart, and pages of zeros under the least scale
+    c = Case(SCALED, BF16, 2, 128, 16, [rows[0] + prefix[0]], seed=rows[0])
+    c.vs = torch.from_numpy(np.exp2(c.rng.integers(-20, 5, c.vs.shape)).astype(np.float32)) * 1.37
+    c.ks = torch.from_numpy(np.exp2(c.rng.integers(-30, -4, c.ks.shape)).astype(np.float32))
+    blk = c.tables[0, 0]
+    c.k[blk], c.v[blk], c.ks[blk], c.vs[blk] = 0, 0, 2.0 ** -126, 2.0 ** -126
+    c.cuda()
+    q = c.rows(rows[0], 8).cuda()
+    vals = c.values()
+    vals[1] = to_f64(torch.from_numpy(vals[1]).float().half())  # V takes part as f16(code * scale)
+    ref = R.attention(*vals, to_f64(q), [0, rows[0]], prefix, c.tables, 8, 1 / 128 ** 0.5)
+    out, lse = run_extend(c, q, 8, rows, prefix, fill=None)
+    check_attention(out, lse, ref, BF16, 128)
 
 
 def test_extend_with_shared_blocks_and_dirty_tail():

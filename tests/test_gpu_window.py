@@ -162,7 +162,9 @@ def test_extend_of_a_whole_window_is_the_plain_extend(cache, act):
                           k_scale=c.k_scale, v_scale=c.v_scale)
     for window, sinks in ((390, 0), (2**31 - 1, 9)):
         out, _ = run_extend(c, q, 8, rows, prefix, window, sinks)
-        assert torch.equal(out, plain)
+        # (its keys may be split: both round their weights, by 2^-11 of the values, and the output)
+        vmax = float(np.abs(c.values()[1]).max())
+        assert torch.allclose(out.float(), plain.float(), rtol=torch.finfo(TDT[act]).eps, atol=2 * 2.0 ** -11 * vmax)
 
 
 def test_extend_reports_and_leaves_alone():

@@ -88,11 +88,8 @@ def test_extend_refusals(lib):
     need = lib.pkv_extend_block_scaled_workspace_bytes(ctypes.byref(fp8()))
     assert need == 2 * 8 * 2 * 16 * 128 * 2 + 256       # two 16-bit pools and the claims
     assert lib.pkv_extend_block_scaled_workspace_bytes(ctypes.byref(_desc())) == 0
-    assert scaled() == 3 and scaled(ws=FAKE, ws_bytes=need - 1) == 3
-    assert scaled(ws=ctypes.c_void_p(0x10010), ws_bytes=need) == 3
     assert scaled(desc=_desc()) == 2 and scaled(ks=None) == 1 and scaled(w=-1) == 1
-    assert scaled(batch=65536, ws=FAKE, ws_bytes=need) == 2
-    assert scaled(batch=0) == 0
+    assert scaled(sinks=-1) == 1 and scaled(batch=-1) == 1 and scaled(batch=0) == 0
 
 
 def test_decode_window_workspace_plan(lib):
