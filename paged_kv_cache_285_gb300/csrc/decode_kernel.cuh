@@ -165,6 +165,7 @@ template <int HD, int CT, int AT, int NW, int NS, bool CASC, bool WIN, bool BSC>
 __global__ void __launch_bounds__(NW * 32)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const DecodeParams p, const DecodeExtraParams ap) {
+  constexpr bool LEAN = WIN || BSC;  // a leaner inner loop than the plain and cascade forms
   static_assert(!(CASC && (WIN || BSC)) && (!BSC || CT == DT_E4M3), "unsupported combination");
   using C = DecodeCfg<HD, CT, NW, NS>;
   extern __shared__ uint8_t smem_raw[];
@@ -427,6 +428,22 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     auto hidden = [&](int row) -> bool {
       return row >= nvalid || (WIN && row < w_lo && row >= w_sk);
     };
+    // LEAN: a tile with hidden tokens gets their V rows zeroed in shared memory,
+    // so that the other tiles carry no masks
+    const bool edge = nvalid < kSubTokens || (WIN && w_lo > 0 && w_sk < kSubTokens);
+    if constexpr (LEAN) {
+      if (edge) {
+        constexpr int UPR = C::ROWB / 16;
+        for (int e = lane; e < kSubTokens * UPR; e += 32) {
+          const int row = e / UPR;
+          if (hidden(row))
+            *reinterpret_cast<uint4*>(wstage + s * C::STAGEB + C::TILEB +
+                                      tile_off<C::CHUNKB>(row, (e % UPR) * 16)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_shared();  // before the next copy into this stage
+        __syncwarp();
+      }
+    }
     float2 bsc = make_float2(1.f, 1.f);
     if constexpr (BSC) bsc = wscale[s];
 
@@ -450,16 +467,25 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           uint32_t r[4];
           ldsm_x4(kb + tile_off<C::CHUNKB>(t, (2 * kp + (lane >> 4)) * 16), r);
           uint32_t a[4];
-          a[0] = e4m3x2_to_f16x2(r[0] & 0xFFFFu);
-          a[2] = e4m3x2_to_f16x2(r[0] >> 16);
-          a[1] = e4m3x2_to_f16x2(r[1] & 0xFFFFu);
-          a[3] = e4m3x2_to_f16x2(r[1] >> 16);
-          mma16816<false>(sc, a, qf[2 * kp][0], qf[2 * kp][1]);
-          a[0] = e4m3x2_to_f16x2(r[2] & 0xFFFFu);
-          a[2] = e4m3x2_to_f16x2(r[2] >> 16);
-          a[1] = e4m3x2_to_f16x2(r[3] & 0xFFFFu);
-          a[3] = e4m3x2_to_f16x2(r[3] >> 16);
-          mma16816<false>(sc, a, qf[2 * kp + 1][0], qf[2 * kp + 1][1]);
+          if constexpr (LEAN) {
+            e4m3x4_to_f16x4(r[0], a[0], a[2]);
+            e4m3x4_to_f16x4(r[1], a[1], a[3]);
+            mma16816<false>(sc, a, qf[2 * kp][0], qf[2 * kp][1]);
+            e4m3x4_to_f16x4(r[2], a[0], a[2]);
+            e4m3x4_to_f16x4(r[3], a[1], a[3]);
+            mma16816<false>(sc, a, qf[2 * kp + 1][0], qf[2 * kp + 1][1]);
+          } else {
+            a[0] = e4m3x2_to_f16x2(r[0] & 0xFFFFu);
+            a[2] = e4m3x2_to_f16x2(r[0] >> 16);
+            a[1] = e4m3x2_to_f16x2(r[1] & 0xFFFFu);
+            a[3] = e4m3x2_to_f16x2(r[1] >> 16);
+            mma16816<false>(sc, a, qf[2 * kp][0], qf[2 * kp][1]);
+            a[0] = e4m3x2_to_f16x2(r[2] & 0xFFFFu);
+            a[2] = e4m3x2_to_f16x2(r[2] >> 16);
+            a[1] = e4m3x2_to_f16x2(r[3] & 0xFFFFu);
+            a[3] = e4m3x2_to_f16x2(r[3] >> 16);
+            mma16816<false>(sc, a, qf[2 * kp + 1][0], qf[2 * kp + 1][1]);
+          }
         }
       }
     }
@@ -468,28 +494,46 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const float sl2 = BSC ? p.scale_log2 * bsc.x : p.scale_log2;
     float s0 = sc[0] * sl2, s1 = sc[1] * sl2;
     float s2 = sc[2] * sl2, s3 = sc[3] * sl2;
-    if (hidden(gid)) { s0 = -INFINITY; s1 = -INFINITY; }
-    if (hidden(gid + 8)) { s2 = -INFINITY; s3 = -INFINITY; }
+    if (!LEAN || edge) {
+      if (hidden(gid)) { s0 = -INFINITY; s1 = -INFINITY; }
+      if (hidden(gid + 8)) { s2 = -INFINITY; s3 = -INFINITY; }
+    }
     float mx_e = fmaxf(s0, s2), mx_o = fmaxf(s1, s3);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       mx_e = fmaxf(mx_e, __shfl_xor_sync(kFull, mx_e, off));
       mx_o = fmaxf(mx_o, __shfl_xor_sync(kFull, mx_o, off));
     }
-    const float mn_e = fmaxf(m_e, mx_e), mn_o = fmaxf(m_o, mx_o);
-    const float al_e = fast_exp2(m_e - mn_e), al_o = fast_exp2(m_o - mn_o);
+    // LEAN: the base of the exponents moves only when a maximum grows by more
+    // than 2^8 (weights of up to 2^8 are as exact in f16 as those below 1), so
+    // that most tiles rescale nothing
+    bool grow = true;
+    float mn_e = fmaxf(m_e, mx_e), mn_o = fmaxf(m_o, mx_o);
+    if constexpr (LEAN) {
+      if (!(mx_e > m_e + 8.f)) mn_e = m_e;
+      if (!(mx_o > m_o + 8.f)) mn_o = m_o;
+      grow = __any_sync(kFull, mn_e != m_e || mn_o != m_o);
+    }
+    float al_e = 1.f, al_o = 1.f;
+    if (grow) {
+      // (m == mn == -inf: nothing summed so far)
+      al_e = LEAN && mn_e == m_e ? 1.f : fast_exp2(m_e - mn_e);
+      al_o = LEAN && mn_o == m_o ? 1.f : fast_exp2(m_o - mn_o);
+    }
     m_e = mn_e;
     m_o = mn_o;
     const float p0 = fast_exp2(s0 - mn_e), p1 = fast_exp2(s1 - mn_o);
     const float p2 = fast_exp2(s2 - mn_e), p3 = fast_exp2(s3 - mn_o);
     l_e = l_e * al_e + (p0 + p2);
     l_o = l_o * al_o + (p1 + p3);
+    if (grow) {
 #pragma unroll
-    for (int u = 0; u < C::MT; ++u) {
-      acc[u][0] *= al_e;
-      acc[u][1] *= al_o;
-      acc[u][2] *= al_e;
-      acc[u][3] *= al_o;
+      for (int u = 0; u < C::MT; ++u) {
+        acc[u][0] *= al_e;
+        acc[u][1] *= al_o;
+        acc[u][2] *= al_e;
+        acc[u][3] *= al_o;
+      }
     }
 
     // ---- P^T as the B operand: transpose the S^T accumulator layout ----------
@@ -521,7 +565,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int u = 0; u < C::MT; ++u) {
           uint32_t a[4];
           ldsm_x4_t(vb + tile_off<C::CHUNKB>(t, (u * 16 + (j & 1) * 8) * 2), a);
-          a[0] &= mlo; a[1] &= mlo; a[2] &= mhi; a[3] &= mhi;
+          if constexpr (!LEAN) { a[0] &= mlo; a[1] &= mlo; a[2] &= mhi; a[3] &= mhi; }
           mma16816<MMA_BF16>(acc[u], a, bh0, bh1);
           if constexpr (MMA_BF16) mma16816<true>(acc[u], a, bl0, bl1);
         }
@@ -534,17 +578,28 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int pp = 0; pp < HD / 32; ++pp) {
           uint32_t r[4];
           ldsm_x4_t(vb + tile_off<C::CHUNKB>(t, (2 * pp + (j & 1)) * 16), r);
-          r[0] = __byte_perm(r[0] & mlo, 0, 0x3120);
-          r[1] = __byte_perm(r[1] & mlo, 0, 0x3120);
-          r[2] = __byte_perm(r[2] & mhi, 0, 0x3120);
-          r[3] = __byte_perm(r[3] & mhi, 0, 0x3120);
+          uint32_t w[2][4];  // LEAN: the two products' operands
+          if constexpr (LEAN) {
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              e4m3x4_to_f16x4(__byte_perm(r[q4], 0, 0x3120), w[0][q4], w[1][q4]);
+          } else {
+            r[0] = __byte_perm(r[0] & mlo, 0, 0x3120);
+            r[1] = __byte_perm(r[1] & mlo, 0, 0x3120);
+            r[2] = __byte_perm(r[2] & mhi, 0, 0x3120);
+            r[3] = __byte_perm(r[3] & mhi, 0, 0x3120);
+          }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t a[4];
-            a[0] = e4m3x2_to_f16x2(e ? (r[0] >> 16) : (r[0] & 0xFFFFu));
-            a[1] = e4m3x2_to_f16x2(e ? (r[1] >> 16) : (r[1] & 0xFFFFu));
-            a[2] = e4m3x2_to_f16x2(e ? (r[2] >> 16) : (r[2] & 0xFFFFu));
-            a[3] = e4m3x2_to_f16x2(e ? (r[3] >> 16) : (r[3] & 0xFFFFu));
+            if constexpr (LEAN) {
+              a[0] = w[e][0]; a[1] = w[e][1]; a[2] = w[e][2]; a[3] = w[e][3];
+            } else {
+              a[0] = e4m3x2_to_f16x2(e ? (r[0] >> 16) : (r[0] & 0xFFFFu));
+              a[1] = e4m3x2_to_f16x2(e ? (r[1] >> 16) : (r[1] & 0xFFFFu));
+              a[2] = e4m3x2_to_f16x2(e ? (r[2] >> 16) : (r[2] & 0xFFFFu));
+              a[3] = e4m3x2_to_f16x2(e ? (r[3] >> 16) : (r[3] & 0xFFFFu));
+            }
             if constexpr (BSC) {
               float pv[4] = {0.f, 0.f, 0.f, 0.f};
               mma16816<false>(pv, a, bh0, bh1);

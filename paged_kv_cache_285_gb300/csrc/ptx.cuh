@@ -239,6 +239,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes_in_low16)
   return r;
 }
 
+// Four e4m3 codes to two f16 pairs (codes 0, 1 and 2, 3); exact.  The halves of
+// the register are named as such, so that the converts can take them in place.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(c));
+}
+
 // f16/bf16 pair (as stored, low half first) -> f16 pair.  bf16 values beyond
 // the f16 range become +-inf; values below 2^-24 in magnitude become 0.
 template <bool SRC_BF16>
@@ -261,6 +270,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // async-proxy (TMA) reads that are ordered after it (by a barrier).
 __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
+// Orders this thread's earlier generic-proxy shared-memory accesses before later
+// async-proxy ones that are ordered after it.
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // 32 bytes to global memory in one store; `p` must be 32-byte aligned.
