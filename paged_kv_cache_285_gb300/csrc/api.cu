@@ -218,6 +218,7 @@ struct DecodePlan {
   size_t ws_bytes = 0;
   size_t ws_lse_offset = 0;
   size_t ws_span_offset = 0;  // cascade: int2 (first own token, length) per request
+  bool cluster = false;       // window / block-scaled: the splits form clusters, no workspace
 };
 
 // Split plan: the sequence is cut into runs of `chunk` tokens (a multiple of
@@ -582,6 +583,62 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
   return (int)std::min<int64_t>(max_seq_len, tiles * kSubTokens);
 }
 
+// Split plan of a decode call through a view, from what a CTA and an SM do (us;
+// four CTAs fit an SM): a CTA alone goes through r1 tokens per us (100 at 128
+// dims, 160 at 64: the latency of its four warps' tiles), an SM through its
+// share of the bandwidth, whatever its CTAs.  A launch costs its full rounds of
+// CTAs, then the last round (2.5 more each), and a fixed part: 5, 6 for splits
+// joined in a cluster, 8 with a merge launch (and more for long rows of
+// partials).  Under a window the sequences are taken as all of the bound's
+// length, else half as that, half as spread evenly up to it.  Measured against plain runs of 128 to 4,096 tokens aimed at
+// six rounds: block-scaled, 16 x 4,096 tokens 39.2 -> 31, 1 x 100,000 69 -> 45,
+// 128 x 100-300 tokens 27.5 -> 21; windows: 32 x 1,024 (bf16) 37.6 -> 26.8,
+// 128 x 4,096 (fp8) 179 -> 169.
+static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_seq_len, int window,
+                            int sink_tokens, int forced, int sm_count) {
+  const int len = visible_bound(max_seq_len, window, sink_tokens);
+  const int tiles = std::max(1, ceil_div(len, kSubTokens));
+  if (forced > 0 || tiles <= 4) return plan_decode(d, batch, hq, len, forced > 0 ? forced : 1, sm_count);
+  const int sms = sm_count > 0 ? sm_count : 152;
+  const double items = (double)batch * d->num_kv_heads * ((hq / d->num_kv_heads + 7) / 8);
+  const double r1 = d->head_dim == 128 ? 100.0 : 160.0;
+  const double sm_rate = 44600.0 / (2.0 * d->head_dim * elem_bytes(d->cache_dtype));
+  const double slots = 4.0 * sms;
+  double best = 1e30;
+  int best_s = 1;
+  bool best_cluster = false;
+  // at most about two rounds of CTAs beyond one per item, of 64 tokens at least
+  const int most = (int)std::min<double>(std::max(1, tiles / 4), 2.0 * slots / items + 8.0);
+  for (int s = 1; s <= most; ++s) {
+    const int chunk = ceil_div(tiles, s);
+    if (s > 1 && ceil_div(tiles, chunk) != s) continue;  // the same plan as a smaller s
+    const double tokens = 16.0 * chunk;
+    const double ctas = items * s, full = std::floor(ctas / slots), rest = ctas - full * slots;
+    double cost = full * (tokens * 4 / sm_rate + 2.5);
+    if (rest > 0) cost += tokens / std::min(r1, sm_rate / std::ceil(rest / sms)) + 2.5;
+    if (window <= 0) {
+      const double some = items * (s + 1) * 0.5, k = std::min(4.0, std::ceil(some / sms));
+      const double one = tokens / std::min(r1, sm_rate / k);
+      const double spread = std::max(one, items * len * 0.5 / (sm_rate * sms) + 0.5 * one) +
+                            2.0 * some / slots;
+      cost = 0.5 * (cost + spread);
+    }
+    const bool cl = s >= 2 && s <= 8 && (s & (s - 1)) == 0 && items * s <= 0.75 * slots;
+    cost += s == 1 ? 5.0 : cl ? 6.0 : 8.0 + 0.2 * std::max(0, s - 8);
+    if (cost < best) {
+      best = cost;
+      best_s = s;
+      best_cluster = cl;
+    }
+  }
+  DecodePlan pl = plan_decode(d, batch, hq, len, best_s, sm_count);
+  if (best_cluster && pl.splits >= 2) {
+    pl.cluster = true;
+    pl.ws_bytes = 0;
+  }
+  return pl;
+}
+
 // Decode, optionally with the current token's K/V (k_new/v_new, [B][Hkv][D]
 // act dtype) appended to position seq_len-1 inside the decode kernel, or
 // through a view (a window and / or scales per block).
@@ -612,8 +669,10 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
   cudaError_t e;
   DeviceState* ds = device_state(&e);
   if (!ds) return PKV_ERR_CUDA;
-  const int plan_len = view ? visible_bound(max_seq_len, view->window, view->sink_tokens) : max_seq_len;
-  const DecodePlan pl = plan_decode(desc, batch, num_q_heads, plan_len, num_splits, ds->sm_count);
+  const DecodePlan pl =
+      view ? plan_view(desc, batch, num_q_heads, max_seq_len, view->window, view->sink_tokens,
+                       num_splits, ds->sm_count)
+           : plan_decode(desc, batch, num_q_heads, max_seq_len, num_splits, ds->sm_count);
   if (pl.ws_bytes > 0 && (!workspace || workspace_bytes < pl.ws_bytes || !aligned(workspace, 256)))
     return PKV_ERR_WORKSPACE;
   if (pl.splits > 65535) return PKV_ERR_UNSUPPORTED;
@@ -655,6 +714,7 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
     ap.sink_tokens = view->sink_tokens;
     ap.k_scales = view->k_scales;
     ap.v_scales = view->v_scales;
+    ap.join_cluster = pl.cluster ? 1 : 0;
     e = launch_decode_window(kmap, vmap, p, ap, desc->head_dim, (int)desc->cache_dtype,
                              (int)act_dtype, stream);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
@@ -693,9 +753,14 @@ pkv_status pkv_paged_decode_attn_append(const pkv_cache_desc* desc, void* k_cach
 size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
                                          int32_t num_q_heads, int32_t max_seq_len, int32_t window,
                                          int32_t sink_tokens, int32_t num_splits) {
-  if (max_seq_len < 0 || window < 0 || sink_tokens < 0) return 0;
-  return pkv_decode_workspace_bytes(desc, batch, num_q_heads,
-                                    visible_bound(max_seq_len, window, sink_tokens), num_splits);
+  if (check_desc(desc) != PKV_OK || batch <= 0 || num_q_heads <= 0 || max_seq_len < 0 ||
+      window < 0 || sink_tokens < 0 || num_splits < 0)
+    return 0;
+  cudaError_t e;
+  DeviceState* ds = device_state(&e);
+  return plan_view(desc, batch, num_q_heads, max_seq_len, window, sink_tokens, num_splits,
+                   ds ? ds->sm_count : 0)
+      .ws_bytes;
 }
 
 pkv_status pkv_paged_decode_attn_window(const pkv_cache_desc* desc, const void* k_cache,

@@ -41,6 +41,11 @@
 //     (O = al O + s_v (V^T P^T)): scales of any size keep P in f16's range.
 //     The lane that holds a tile's block id holds its scales too, issues the
 //     tile's copies and leaves the scales in the stage's slot.
+//   * splits joined in a cluster (CLM, few requests): the splits of one (request,
+//     head chunk) are the CTAs of a cluster.  Each leaves its heads' (max, sum,
+//     unnormalised O) in shared memory, and after a cluster barrier each adds up
+//     its share of the outputs, reading the others' over the cluster: no
+//     workspace and no second launch.
 //   * warps are combined through shared memory with their (max, sum); a split
 //     either writes the final output (single-split requests) or a normalised
 //     partial plus its log-sum-exp, merged by merge_kernel.
@@ -161,11 +166,13 @@ __device__ __forceinline__ WinSpan win_span(int n, int window, int sinks) {
 // CASC: a cascade launch (tokens from the group's shared prefix on; partials
 // in the workspace slots after the prefix's chunks, always merged).  WIN: a
 // window with sink tokens.  BSC: fp8 codes with scales per block and kv head.
-template <int HD, int CT, int AT, int NW, int NS, bool CASC, bool WIN, bool BSC>
+// CLM: the splits of a (request, head chunk) form a cluster that joins them.
+template <int HD, int CT, int AT, int NW, int NS, bool CASC, bool WIN, bool BSC, bool CLM>
 __global__ void __launch_bounds__(NW * 32)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const DecodeParams p, const DecodeExtraParams ap) {
   constexpr bool LEAN = WIN || BSC;  // a leaner inner loop than the plain and cascade forms
+  static_assert(!(CASC && CLM), "unsupported combination");
   static_assert(!(CASC && (WIN || BSC)) && (!BSC || CT == DT_E4M3), "unsupported combination");
   using C = DecodeCfg<HD, CT, NW, NS>;
   extern __shared__ uint8_t smem_raw[];
@@ -214,6 +221,49 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     n = ws.nv;
   }
   const int t0 = tb + split * p.chunk;
+  // CLM: this CTA's share of the outputs from the parts of the cluster's active
+  // CTAs, [8][HD] O and [2][8] (max, sum) at the start of their shared memory
+  auto join_cluster = [&]() {
+    cluster_sync();
+    const int active = (n + p.chunk - 1) / p.chunk, S = p.num_splits;
+    const uint32_t o_at = smem_u32(smem), ml_at = o_at + 8 * HD * 4;
+    for (int idx = split * (NW * 32) + (int)threadIdx.x; idx < GC * HD; idx += S * NW * 32) {
+      const int jh = idx / HD, d = idx % HD;
+      constexpr int MAXC = 8;
+      float m[MAXC], l[MAXC], o[MAXC], mstar = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < MAXC; ++c) {
+        m[c] = -INFINITY;
+        l[c] = o[c] = 0.f;
+        if (c < active) {
+          m[c] = cluster_ld(cluster_map(ml_at + jh * 4, c));
+          l[c] = cluster_ld(cluster_map(ml_at + 32 + jh * 4, c));
+          o[c] = cluster_ld(cluster_map(o_at + idx * 4, c));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < MAXC; ++c) mstar = fmaxf(mstar, m[c]);
+      float L = 0.f, O = 0.f;
+#pragma unroll
+      for (int c = 0; c < MAXC; ++c) {
+        if (c < active) {
+          const float f = fast_exp2(m[c] - mstar);
+          L += f * l[c];
+          O += f * o[c];
+        }
+      }
+      const int64_t bh = (int64_t)b * p.num_q_heads + hb + jh;
+      store_act<AT>(p.out, bh * HD + d, (O / L) * p.out_scale);
+      if (p.lse_out && d == 0) p.lse_out[bh] = (mstar + log2f(L)) * kLn2;
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  };
+  if constexpr (CLM) {
+    if (t0 >= n && n > p.chunk) {  // nothing here, but the cluster has more than one part
+      join_cluster();
+      return;
+    }
+  }
   if (t0 >= n) {
     if constexpr (CASC) {
       // nothing after the prefix; the current token cannot be appended there
@@ -652,6 +702,37 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
   __syncthreads();
 
+  if constexpr (CLM) {
+    if (nsplit_b > 1) {
+      // (an element's sums over the warps are read by the thread that replaces them)
+      float* sm_ml = sm_o + 8 * HD;  // over warp 1's rows: read before it is written
+      for (int idx = threadIdx.x; idx < 8 * HD; idx += NW * 32) {
+        const int jh = idx / HD;
+        float mstar = -INFINITY, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) mstar = fmaxf(mstar, sm_m[w * 8 + jh]);
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          O += fast_exp2(sm_m[w * 8 + jh] - mstar) * sm_o[w * 8 * HD + idx];
+        sm_o[idx] = O;
+      }
+      float mstar = -INFINITY, L = 0.f;
+      if (threadIdx.x < 8) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) mstar = fmaxf(mstar, sm_m[w * 8 + threadIdx.x]);
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          L += fast_exp2(sm_m[w * 8 + threadIdx.x] - mstar) * sm_l[w * 8 + threadIdx.x];
+      }
+      __syncthreads();
+      if (threadIdx.x < 8) {
+        sm_ml[threadIdx.x] = mstar;
+        sm_ml[8 + threadIdx.x] = L;
+      }
+      join_cluster();
+      return;
+    }
+  }
   const bool direct = !CASC && (nsplit_b == 1);
   // cascade: the shared prefix's chunks hold the first slots
   const int kSlot0 = CASC ? ap.prefix_slots : 0;
@@ -820,17 +901,32 @@ constexpr int stages_for() {
 
 // NSO > 0 overrides the pipeline depth (stages per warp), NW the warps per CTA.
 template <int HD, int CT, int AT, bool CASC, int NSO = 0, int NW = kNW, bool WIN = false,
-          bool BSC = false>
+          bool BSC = false, bool CLM = false>
 cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const DecodeParams& p, const DecodeExtraParams& ap,
                             cudaStream_t stream, cudaEvent_t merge_after = nullptr) {
   constexpr int NS = NSO > 0 ? NSO : stages_for<HD, CT>();
   using C = DecodeCfg<HD, CT, NW, NS>;
-  auto kern = decode_kernel<HD, CT, AT, NW, NS, CASC, WIN, BSC>;
+  auto kern = decode_kernel<HD, CT, AT, NW, NS, CASC, WIN, BSC, CLM>;
   constexpr int smem = BSC ? C::SMEM_BSC : C::SMEM;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.num_kv_heads * ((p.group + 7) / 8), p.batch, p.num_splits);
+  if constexpr (CLM) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = (unsigned)p.num_splits;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, ap);
+  }
   kern<<<grid, NW * 32, smem, stream>>>(kmap, vmap, p, ap);
   e = cudaGetLastError();
   if (e != cudaSuccess || (!CASC && p.num_splits <= 1)) return e;

@@ -4,20 +4,34 @@
 
 namespace pkv {
 
+namespace {
+
+template <int HD, int AT, bool WIN>
+cudaError_t launch_scaled(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
+                          const DecodeExtraParams& ap, cudaStream_t stream) {
+  return ap.join_cluster
+             ? launch_decode_t<HD, DT_E4M3, AT, false, 0, kNW, WIN, true, true>(kmap, vmap, p, ap, stream)
+             : launch_decode_t<HD, DT_E4M3, AT, false, 0, kNW, WIN, true>(kmap, vmap, p, ap, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_decode_window(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
                                  int cache_dt, int act_dt, cudaStream_t stream) {
   const bool scaled = ap.k_scales != nullptr;
   if (scaled && (!ap.v_scales || cache_dt != DT_E4M3)) return cudaErrorInvalidValue;
   if (!scaled && ap.window <= 0) return cudaErrorInvalidValue;
+  if (ap.join_cluster && (p.num_splits < 2 || p.num_splits > 8)) return cudaErrorInvalidValue;
 #define PKV_WIN(HD, CT, AT)                                                              \
   if (head_dim == HD && cache_dt == CT && act_dt == AT && !scaled)                       \
-    return launch_decode_t<HD, CT, AT, false, 0, kNW, true, false>(kmap, vmap, p, ap, stream);
+    return ap.join_cluster                                                               \
+               ? launch_decode_t<HD, CT, AT, false, 0, kNW, true, false, true>(kmap, vmap, p, ap, stream) \
+               : launch_decode_t<HD, CT, AT, false, 0, kNW, true, false>(kmap, vmap, p, ap, stream);
 #define PKV_BSC(HD, AT)                                                                  \
   if (head_dim == HD && act_dt == AT && scaled)                                          \
-    return ap.window > 0                                                                 \
-               ? launch_decode_t<HD, DT_E4M3, AT, false, 0, kNW, true, true>(kmap, vmap, p, ap, stream) \
-               : launch_decode_t<HD, DT_E4M3, AT, false, 0, kNW, false, true>(kmap, vmap, p, ap, stream);
+    return ap.window > 0 ? launch_scaled<HD, AT, true>(kmap, vmap, p, ap, stream)        \
+                         : launch_scaled<HD, AT, false>(kmap, vmap, p, ap, stream);
   PKV_WIN(64, DT_F16, DT_F16)
   PKV_WIN(64, DT_BF16, DT_BF16)
   PKV_WIN(64, DT_E4M3, DT_F16)

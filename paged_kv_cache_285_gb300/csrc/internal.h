@@ -79,6 +79,7 @@ struct DecodeExtraParams {
   int sink_tokens;
   const float* k_scales;
   const float* v_scales;
+  int join_cluster;  // window / block-scaled launches: the splits (2 .. 8) form clusters
 };
 
 // Division of unsigned n < 2^31 by a divisor fixed for a launch, as a
