@@ -188,6 +188,7 @@ struct GatherParams {
   float v_scale;
   // set by the launcher
   int rows_per_cta;
+  int out_32b;                 // both outputs are 32-byte aligned
   FastDiv div_hkv;
 };
 
