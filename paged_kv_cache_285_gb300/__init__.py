@@ -527,93 +527,97 @@ def _desc_ref(num_blocks, num_kv_heads, block_size, head_dim, code, k_scale, v_s
                                   v_scale))
 
 
-def _refuse(name, t, shape, dtype, device):
+def _refuse(name, t, shape, dtype, index):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} like the call's other tensors, got {t.device}")
+    if t.get_device() != index or not (t.is_cuda or index < 0):
+        raise ValueError(f"{name} must be on the device of the call's other tensors, got {t.device}")
     raise ValueError(f"libpkv takes contiguous tensors: {name} is not")
 
 
-def _arg(name, t, shape, dtype, device):
-    """Data pointer of a tensor argument of this shape, dtype and device, contiguous."""
-    if (t is None or t.shape != shape or t.dtype is not dtype or t.device != device or
+def _arg(name, t, shape, dtype, index):
+    """Data pointer of a tensor argument of this shape and dtype on the device of this index
+    (-1: the CPU, refused by _run), contiguous."""
+    if (t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != index or
             not t.is_contiguous()):
-        _refuse(name, t, shape, dtype, device)
+        _refuse(name, t, shape, dtype, index)
     return t.data_ptr()
 
 
-def _opt(name, t, shape, dtype, device):
-    return None if t is None else _arg(name, t, shape, dtype, device)
-
-
-def _workspace(t, device):
+def _workspace(t, index):
     """(pointer, bytes) of a workspace tensor of any shape and dtype, or of none."""
     if t is None:
         return None, 0
-    if t.device != device:
-        raise ValueError(f"workspace must be on {device} like the call's other tensors, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError("libpkv takes contiguous tensors: workspace is not")
+    if t.get_device() != index or not t.is_contiguous():
+        _refuse("workspace", t, t.shape, t.dtype, index)
     return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _dim(name, t, dims, what):
+    """The shape of a tensor of so many dimensions."""
     if not isinstance(t, torch.Tensor) or t.dim() != dims:
         raise ValueError(f"{name} must be {what}")
     return t.shape
 
 
+_CODES = {torch.float16: F16, torch.bfloat16: BF16, torch.uint8: FP8_E4M3,
+          getattr(torch, "float8_e4m3fn", torch.uint8): FP8_E4M3}
+
+
+def _code(t):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported tensor dtype {t.dtype}")
+    return code
+
+
 def _pools(k_cache, v_cache, k_scale, v_scale):
-    """The desc of a pair of pools, their pointers, [num_blocks, Hkv] and head dim."""
+    """The desc of a pair of pools, their pointers, [num_blocks, Hkv], head dim, device index."""
     shape = _dim("cache", k_cache, 4, "[num_blocks, num_kv_heads, block_size, head_dim]")
     nb, hkv, bs, d = shape
-    dev = k_cache.device
-    kc = _arg("k_cache", k_cache, shape, k_cache.dtype, dev)
-    vc = _arg("v_cache", v_cache, shape, k_cache.dtype, dev)
-    return (_desc_ref(nb, hkv, bs, d, _dtype_code(k_cache), float(k_scale), float(v_scale)), kc, vc,
-            (nb, hkv), d)
-
-
-def _block_scales(k_scales, v_scales, pages, device):
-    return (_arg("k_scales", k_scales, pages, torch.float32, device),
-            _arg("v_scales", v_scales, pages, torch.float32, device))
+    dtype, index = k_cache.dtype, k_cache.get_device()
+    return (_desc_ref(nb, hkv, bs, d, _code(k_cache), float(k_scale), float(v_scale)),
+            _arg("k_cache", k_cache, shape, dtype, index),
+            _arg("v_cache", v_cache, shape, dtype, index), (nb, hkv), d, index)
 
 
 try:
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 except AttributeError:
+    _current_device = torch.cuda.current_device
+
     def _raw_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
 
 
-def _run(what, device, stream, *args):
-    """Call a C entry point whose last argument is the stream (None: the current one of
-    `device`), with `device` current."""
-    if device.type != "cuda":
+def _run(what, index, stream, *args):
+    """Call a C entry point whose last argument is the stream (None: the current one of device
+    `index`), with that device current."""
+    if index < 0:
         raise ValueError("libpkv takes device tensors")
     fn = getattr(_lib or load(), what)
-    s = _raw_stream(device.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
         st = fn(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, s)
     if st != 0:
         raise PkvError(st, what)
 
 
-def _layout(indptr_name, indptr, start_name, starts, block_tables, device):
+def _layout(indptr_name, indptr, start_name, starts, block_tables, index):
     """Pointers of a call's row layout: indptr [B+1], starts [B], block_tables [B, W]; then B, W."""
     batch, = _dim(start_name, starts, 1, "[batch]")
-    width = _dim("block_tables", block_tables, 2, "[batch, max_blocks_per_seq]")[1]
-    return (_arg(indptr_name, indptr, (batch + 1,), torch.int32, device),
-            _arg(start_name, starts, (batch,), torch.int32, device),
-            _arg("block_tables", block_tables, (batch, width), torch.int32, device), batch, width)
+    table = _dim("block_tables", block_tables, 2, "[batch, max_blocks_per_seq]")
+    width = table[1]
+    return (_arg(indptr_name, indptr, (batch + 1,), torch.int32, index),
+            _arg(start_name, starts, (batch,), torch.int32, index),
+            _arg("block_tables", block_tables, (batch, width), torch.int32, index), batch, width)
 
 
 def kv_append_block_scaled(k_cache, v_cache, k_scales, v_scales, k_new, v_new, q_indptr,
@@ -622,16 +626,17 @@ def kv_append_block_scaled(k_cache, v_cache, k_scales, v_scales, k_new, v_new, q
     to position prefix_lens[b] + i of request b, quantised with a power-of-two scale per block
     and kv head.  k_scales/v_scales float32 [num_blocks, Hkv]; q_indptr int32 [B+1]; prefix_lens
     int32 [B]; max_suffix_len bounds the rows per request."""
-    dev = k_cache.device
-    desc, kc, vc, pages, d = _pools(k_cache, v_cache, 1.0, 1.0)
-    ks, vs = _block_scales(k_scales, v_scales, pages, dev)
+    desc, kc, vc, pages, d, dev = _pools(k_cache, v_cache, 1.0, 1.0)
+    ks = _arg("k_scales", k_scales, pages, torch.float32, dev)
+    vs = _arg("v_scales", v_scales, pages, torch.float32, dev)
     rows = _dim("k_new", k_new, 3, "[rows, num_kv_heads, head_dim]")[0]
-    kn = _arg("k_new", k_new, (rows, pages[1], d), k_new.dtype, dev)
-    vn = _arg("v_new", v_new, (rows, pages[1], d), k_new.dtype, dev)
+    shape, dtype = (rows, pages[1], d), k_new.dtype
+    kn = _arg("k_new", k_new, shape, dtype, dev)
+    vn = _arg("v_new", v_new, shape, dtype, dev)
     qi, pl, bt, batch, width = _layout("q_indptr", q_indptr, "prefix_lens", prefix_lens,
                                        block_tables, dev)
     _run("pkv_kv_append_block_scaled", dev, stream, desc, kc, vc, ks, vs, kn, vn,
-         _dtype_code(k_new), qi, pl, bt, width, batch, rows, int(max_suffix_len))
+         _code(k_new), qi, pl, bt, width, batch, rows, int(max_suffix_len))
 
 
 def kv_gather(k_cache, v_cache, k_out, v_out, row_indptr, start_positions, block_tables,
@@ -639,17 +644,20 @@ def kv_gather(k_cache, v_cache, k_out, v_out, row_indptr, start_positions, block
     """pkv_kv_gather: rows row_indptr[b] .. row_indptr[b+1]-1 of k_out/v_out [rows, Hkv, D] (f16
     or bf16) are positions start_positions[b] ... of request b.  k_scale/v_scale: an fp8 cache's
     scales per tensor; k_scales/v_scales float32 [num_blocks, Hkv]: scales per block and head."""
-    dev = k_cache.device
-    desc, kc, vc, pages, d = _pools(k_cache, v_cache, k_scale, v_scale)
+    desc, kc, vc, pages, d, dev = _pools(k_cache, v_cache, k_scale, v_scale)
     if (k_scales is None) != (v_scales is None):
         raise ValueError("k_scales and v_scales come together")
-    ks, vs = (None, None) if k_scales is None else _block_scales(k_scales, v_scales, pages, dev)
+    ks = vs = None
+    if k_scales is not None:
+        ks = _arg("k_scales", k_scales, pages, torch.float32, dev)
+        vs = _arg("v_scales", v_scales, pages, torch.float32, dev)
     rows = _dim("k_out", k_out, 3, "[rows, num_kv_heads, head_dim]")[0]
-    ko = _arg("k_out", k_out, (rows, pages[1], d), k_out.dtype, dev)
-    vo = _arg("v_out", v_out, (rows, pages[1], d), k_out.dtype, dev)
+    shape, dtype = (rows, pages[1], d), k_out.dtype
+    ko = _arg("k_out", k_out, shape, dtype, dev)
+    vo = _arg("v_out", v_out, shape, dtype, dev)
     ri, sp, bt, batch, width = _layout("row_indptr", row_indptr, "start_positions", start_positions,
                                        block_tables, dev)
-    _run("pkv_kv_gather", dev, stream, desc, kc, vc, ks, vs, ko, vo, _dtype_code(k_out), ri, sp, bt,
+    _run("pkv_kv_gather", dev, stream, desc, kc, vc, ks, vs, ko, vo, _code(k_out), ri, sp, bt,
          width, batch, rows)
 
 
@@ -663,15 +671,16 @@ def decode_window_workspace_bytes(k_cache, batch, num_q_heads, max_seq_len, wind
                                                         num_splits))
 
 
-def _decode_args(q, out, block_tables, seq_lens, lse_out, head_dim, device):
+def _decode_args(q, out, block_tables, seq_lens, lse_out, head_dim, index):
     """Pointers of q, out, block_tables, seq_lens and lse_out, then batch, heads, table width."""
-    b, hq, d = _dim("q", q, 3, f"[batch, num_q_heads, {head_dim}]")
+    b, hq, _ = _dim("q", q, 3, "[batch, num_q_heads, head_dim]")
     width = _dim("block_tables", block_tables, 2, "[batch, max_blocks_per_seq]")[1]
-    return (_arg("q", q, (b, hq, head_dim), q.dtype, device),
-            _arg("out", out, (b, hq, head_dim), q.dtype, device),
-            _arg("block_tables", block_tables, (b, width), torch.int32, device),
-            _arg("seq_lens", seq_lens, (b,), torch.int32, device),
-            _opt("lse_out", lse_out, (b, hq), torch.float32, device), b, hq, width)
+    shape, dtype = (b, hq, head_dim), q.dtype
+    return (_arg("q", q, shape, dtype, index), _arg("out", out, shape, dtype, index),
+            _arg("block_tables", block_tables, (b, width), torch.int32, index),
+            _arg("seq_lens", seq_lens, (b,), torch.int32, index),
+            None if lse_out is None else _arg("lse_out", lse_out, (b, hq), torch.float32, index),
+            b, hq, width)
 
 
 def paged_decode_attn_window(k_cache, v_cache, q, out, block_tables, seq_lens, sm_scale,
@@ -680,13 +689,12 @@ def paged_decode_attn_window(k_cache, v_cache, q, out, block_tables, seq_lens, s
     """pkv_paged_decode_attn_window: paged_decode_attn where each request's query sees its last
     `window` tokens and its first `sink_tokens`.  ``workspace`` is a uint8 device tensor of at
     least decode_window_workspace_bytes() bytes."""
-    dev = q.device
-    desc, kc, vc, _, d = _pools(k_cache, v_cache, k_scale, v_scale)
-    qp, op, bt, sl, lse, b, hq, width = _decode_args(q, out, block_tables, seq_lens, lse_out, d,
-                                                     k_cache.device)
+    desc, kc, vc, _, d, dev = _pools(k_cache, v_cache, k_scale, v_scale)
+    qp, op, bt, sl, lse, b, hq, width = _decode_args(q, out, block_tables, seq_lens, lse_out, d, dev)
     ws, ws_bytes = _workspace(workspace, dev)
-    _run("pkv_paged_decode_attn_window", dev, stream, desc, kc, vc, qp, op, _dtype_code(q), bt,
-         width, sl, b, hq, sm_scale, max_seq_len, window, sink_tokens, num_splits, lse, ws, ws_bytes)
+    _run("pkv_paged_decode_attn_window", dev, stream, desc, kc, vc, qp, op, _code(q), bt,
+         width, sl, b, hq, float(sm_scale), int(max_seq_len), int(window), int(sink_tokens),
+         int(num_splits), lse, ws, ws_bytes)
 
 
 def paged_decode_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out, block_tables,
@@ -695,24 +703,25 @@ def paged_decode_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out,
     """pkv_paged_decode_attn_block_scaled: paged_decode_attn over fp8 codes with k_scales/v_scales
     float32 [num_blocks, Hkv]; window 0: every token, else as paged_decode_attn_window (the same
     workspace)."""
-    dev = q.device
-    desc, kc, vc, pages, d = _pools(k_cache, v_cache, 1.0, 1.0)
-    ks, vs = _block_scales(k_scales, v_scales, pages, k_cache.device)
-    qp, op, bt, sl, lse, b, hq, width = _decode_args(q, out, block_tables, seq_lens, lse_out, d,
-                                                     k_cache.device)
+    desc, kc, vc, pages, d, dev = _pools(k_cache, v_cache, 1.0, 1.0)
+    ks = _arg("k_scales", k_scales, pages, torch.float32, dev)
+    vs = _arg("v_scales", v_scales, pages, torch.float32, dev)
+    qp, op, bt, sl, lse, b, hq, width = _decode_args(q, out, block_tables, seq_lens, lse_out, d, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _run("pkv_paged_decode_attn_block_scaled", dev, stream, desc, kc, vc, ks, vs, qp, op,
-         _dtype_code(q), bt, width, sl, b, hq, sm_scale, max_seq_len, window, sink_tokens,
-         num_splits, lse, ws, ws_bytes)
+         _code(q), bt, width, sl, b, hq, float(sm_scale), int(max_seq_len), int(window),
+         int(sink_tokens), int(num_splits), lse, ws, ws_bytes)
 
 
-def _extend_args(q, out, q_indptr, prefix_lens, block_tables, lse_out, head_dim, device):
-    rows, hq, _ = _dim("q", q, 3, f"[rows, num_q_heads, {head_dim}]")
+def _extend_args(q, out, q_indptr, prefix_lens, block_tables, lse_out, head_dim, index):
+    """Pointers of q, out, the layout and lse_out, then rows, heads, batch, table width."""
+    rows, hq, _ = _dim("q", q, 3, "[rows, num_q_heads, head_dim]")
     qi, pl, bt, batch, width = _layout("q_indptr", q_indptr, "prefix_lens", prefix_lens,
-                                       block_tables, device)
-    return (_arg("q", q, (rows, hq, head_dim), q.dtype, device),
-            _arg("out", out, (rows, hq, head_dim), q.dtype, device), qi, pl, bt,
-            _opt("lse_out", lse_out, (rows, hq), torch.float32, device), rows, hq, batch, width)
+                                       block_tables, index)
+    shape, dtype = (rows, hq, head_dim), q.dtype
+    return (_arg("q", q, shape, dtype, index), _arg("out", out, shape, dtype, index), qi, pl, bt,
+            None if lse_out is None else _arg("lse_out", lse_out, (rows, hq), torch.float32, index),
+            rows, hq, batch, width)
 
 
 def paged_extend_attn_window(k_cache, v_cache, q, out, q_indptr, prefix_lens, block_tables,
@@ -720,14 +729,13 @@ def paged_extend_attn_window(k_cache, v_cache, q, out, q_indptr, prefix_lens, bl
                              k_scale=1.0, v_scale=1.0, lse_out=None, workspace=None, stream=None):
     """pkv_paged_extend_attn_window: paged_extend_attn where the row at position p sees keys
     p - window + 1 .. p and the first `sink_tokens`.  workspace: optional, as there."""
-    dev = q.device
-    desc, kc, vc, _, d = _pools(k_cache, v_cache, k_scale, v_scale)
+    desc, kc, vc, _, d, dev = _pools(k_cache, v_cache, k_scale, v_scale)
     qp, op, qi, pl, bt, lse, rows, hq, batch, width = _extend_args(
-        q, out, q_indptr, prefix_lens, block_tables, lse_out, d, k_cache.device)
+        q, out, q_indptr, prefix_lens, block_tables, lse_out, d, dev)
     ws, ws_bytes = _workspace(workspace, dev)
-    _run("pkv_paged_extend_attn_window", dev, stream, desc, kc, vc, qp, op, _dtype_code(q), qi, pl,
-         bt, width, batch, hq, sm_scale, rows, max_suffix_len, max_total_len, window, sink_tokens,
-         lse, ws, ws_bytes)
+    _run("pkv_paged_extend_attn_window", dev, stream, desc, kc, vc, qp, op, _code(q), qi, pl,
+         bt, width, batch, hq, float(sm_scale), rows, int(max_suffix_len), int(max_total_len),
+         int(window), int(sink_tokens), lse, ws, ws_bytes)
 
 
 def extend_block_scaled_workspace_bytes(k_cache) -> int:
@@ -746,15 +754,15 @@ def paged_extend_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out,
     float32 [num_blocks, Hkv]; window 0: every key, else as paged_extend_attn_window.
     workspace: None, or a uint8 device tensor of extend_block_scaled_workspace_bytes() bytes or
     more (calls with many rows per request then widen the pages they read once per block)."""
-    dev = q.device
-    desc, kc, vc, pages, d = _pools(k_cache, v_cache, 1.0, 1.0)
-    ks, vs = _block_scales(k_scales, v_scales, pages, k_cache.device)
+    desc, kc, vc, pages, d, dev = _pools(k_cache, v_cache, 1.0, 1.0)
+    ks = _arg("k_scales", k_scales, pages, torch.float32, dev)
+    vs = _arg("v_scales", v_scales, pages, torch.float32, dev)
     qp, op, qi, pl, bt, lse, rows, hq, batch, width = _extend_args(
-        q, out, q_indptr, prefix_lens, block_tables, lse_out, d, k_cache.device)
+        q, out, q_indptr, prefix_lens, block_tables, lse_out, d, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _run("pkv_paged_extend_attn_block_scaled", dev, stream, desc, kc, vc, ks, vs, qp, op,
-         _dtype_code(q), qi, pl, bt, width, batch, hq, sm_scale, rows, max_suffix_len,
-         max_total_len, window, sink_tokens, lse, ws, ws_bytes)
+         _code(q), qi, pl, bt, width, batch, hq, float(sm_scale), rows,
+         int(max_suffix_len), int(max_total_len), int(window), int(sink_tokens), lse, ws, ws_bytes)
 
 
 def chain_hash(tokens, token_indptr, block_size, hashes, salts=None, stream=None):
