@@ -176,7 +176,7 @@ bool plan_extend(ExtendParams& p, int batch, int num_kv_heads, int group, int ma
 // CTAs per item of an extend call with a window and / or block scales: its key
 // tiles are split over a cluster when the items are too few to fill the GPU and
 // their key ranges long.  The estimate is in key tiles (1.9 us each at 128 dims,
-// both row tiles): a CTA costs its tiles and a fixed part, 3 tiles, or 7 in a
+// both row tiles): a CTA costs its tiles and a fixed part, 3 tiles, or 5.5 in a
 // cluster (writing and adding up the parts); 152 SMs hold 152, 152, 144 and 120
 // CTAs in clusters of 1, 2, 4 and 8.  Measured (us at 1 / 2 / 4 / 8 CTAs): 8
 // items of 64 tiles 123 / 75 / 44 / 30, 64 of 254 tiles 458 / 261 / 278 / 365,
@@ -193,7 +193,7 @@ int plan_key_splits(const ExtendParams& p, int max_total_len, int sm_count) {
     if ((int64_t)p.num_items * c > INT32_MAX || (c > 1 && tiles < c)) break;
     const double slots = c == 8 ? sms * 120 / 152 : c == 4 ? sms * 144 / 152 : sms;
     const double cost = std::ceil(p.num_items * c / slots) *
-                        ((double)((tiles + c - 1) / c) + (c > 1 ? 7.0 : 3.0));
+                        ((double)((tiles + c - 1) / c) + (c > 1 ? 5.5 : 3.0));
     if (cost < 0.9 * best_cost) {  // (not for less than a tenth)
       best_cost = cost;
       best = c;

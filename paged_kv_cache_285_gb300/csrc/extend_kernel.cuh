@@ -682,22 +682,22 @@ __device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, cons
 // threads, tid 0 .. 255 = splits x share: each first turns one (max, sum) into
 // its part's weight (in place), then they add the rows up.
 template <int HD, int AT, bool WIN>
-__device__ __forceinline__ void combine_parts(const ExtendParams& p, int item, const uint8_t* co,
-                                              float2* ml, int tid) {
-  typename ItemOf<WIN, true>::T it;
-  const ItemRaw raw = load_raw<false>(p, item);
-  derive_any<false, false, WIN, true>(p, item, raw, it);
+__device__ __forceinline__ void combine_parts(const ExtendParams& p, const SplitItem& it,
+                                              const uint8_t* co, float2* ml, int tid) {
   if (!it.rows) return;
-  const int C = p.splits, share = 2 * BM / C, rank = (int)cluster_rank();
+  const int C = p.splits, sh = 31 - __clz(C), share = (2 * BM) >> sh, rank = (int)cluster_rank();
+  // r / group for r < 128 as a multiply: the quotient's error, below 128 / 2^16,
+  // is less than 1 / group
+  const uint32_t gmul = 65536u / (uint32_t)p.group + 1u;
   // row lr of the share: its output row, or -1
   auto out_row = [&](int lr) -> int64_t {
-    const int row = lr * C + rank, x = row / BM, r = row % BM;
-    const int rtok = r / p.group;
+    const int row = (lr << sh) + rank, x = row / BM, r = row % BM;
+    const int rtok = (int)(((uint32_t)r * gmul) >> 16);
     if (rtok >= it.ntok[x]) return -1;
     return (int64_t)(it.row0 + it.i0 + x * p.tok + rtok) * p.num_q_heads + it.g * p.group + (r - rtok * p.group);
   };
   {
-    const int c = tid / share, lr = tid - c * share;
+    const int c = tid >> (8 - sh), lr = tid & (share - 1);
     float m = -INFINITY, l = 0.f;
     for (int k = 0; k < C; ++k) m = fmaxf(m, ml[k * share + lr].x);
     for (int k = 0; k < C; ++k) {
@@ -832,7 +832,6 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint32_t orow = tmem + lane_addr + tm_o<HD>(x);
     int n = 0, js = 0;
     float m_fin = -INFINITY, l_fin = 0.f;  // CL
-    int nrows = 0;
     ItemRaw nxt_raw = load_raw<SX>(p, item0);
     for (int item = item0; ok && item < p.num_items; item += stride) {
       const ItemRaw raw = nxt_raw;
@@ -1018,7 +1017,6 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // O stays in TMEM until the whole cluster is done with its rings
         m_fin = m_run;
         l_fin = l_run;
-        nrows = it.ntok[x];
       } else if constexpr (PP) {
         // fp32 O / l straight from TMEM (the whole row before one wait), then
         // the LSE
@@ -1110,19 +1108,21 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       ++js;
     }
     if constexpr (CL) {
+      // the item once more, whether or not the CTA has a key tile of it (kept
+      // through the key loop it would take the registers of that loop)
+      SplitItem fin;
+      derive_any<PP, SX, WIN, CL>(p, item0, load_raw<SX>(p, item0), fin);
       // every CTA of the cluster is done with its rings: the rows go to the CTA
       // that combines them, unnormalised, with their (max, sum)
       cluster_sync();
       // (row R to CTA R mod splits; 32 columns of the warp's rows at a time
       // through shared memory, so that eight lanes write 128 bytes of a row: a
       // row per lane took 3 to 6 us more)
-      const int C_ = p.splits, share = 2 * BM / C_, row = x * BM + r;
-      const uint32_t rank = cluster_rank();
-      {
-        const uint32_t lr = row / C_, owner = row - lr * C_;
-        cluster_st2(cluster_map(s_base + C::OFF_Q + (rank * share + lr) * 8, owner), make_float2(m_fin, l_fin));
-      }
-      const uint32_t send = __ballot_sync(0xFFFFFFFFu, m_fin != -INFINITY && rtok < nrows);
+      const uint32_t sh = 31 - __clz(p.splits), share = (2 * BM) >> sh, row = x * BM + r;
+      const uint32_t rank = cluster_rank(), cmask = p.splits - 1;
+      cluster_st2(cluster_map(s_base + C::OFF_Q + (rank * share + (row >> sh)) * 8, row & cmask),
+                  make_float2(m_fin, l_fin));
+      const uint32_t send = __ballot_sync(0xFFFFFFFFu, m_fin != -INFINITY && rtok < fin.ntok[x]);
       if (send != 0u) {
         uint8_t* stg = smem + C::OFF_Q + 4096 + (x * 4 + qw) * 4096;
 #pragma unroll 1
@@ -1139,9 +1139,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           for (int k = 0; k < 8; ++k) {
             const int rr = 4 * k + (lane >> 3), u = lane & 7;
             if ((send >> rr) & 1u) {
-              const uint32_t R = x * BM + qw * 32 + rr, lr = R / C_, owner = R - lr * C_;
+              const uint32_t R = x * BM + qw * 32 + rr;
               const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * 128 + ((u ^ (rr & 7)) << 4));
-              cluster_st4(cluster_map(s_base + C::OFF_CO + (rank * share + lr) * (HD * 4) + c * 128 + u * 16, owner),
+              cluster_st4(cluster_map(s_base + C::OFF_CO + (rank * share + (R >> sh)) * (HD * 4) + c * 128 + u * 16,
+                                      R & cmask),
                           v.x, v.y, v.z, v.w);
             }
           }
@@ -1150,7 +1151,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
       tc_fence_before();
       cluster_sync();
-      combine_parts<HD, AT, WIN>(p, item0, smem + C::OFF_CO,
+      combine_parts<HD, AT, WIN>(p, fin, smem + C::OFF_CO,
                                  reinterpret_cast<float2*>(smem + C::OFF_Q), row);
     }
   } else if (warp < 4) {
