@@ -197,8 +197,7 @@ __device__ __forceinline__ void widen_block_scaled(const uint4* __restrict__ src
           o[2 * q] = widen2_scaled<OUT>(w[q] & 0xFFFFu, s[e]);
           o[2 * q + 1] = widen2_scaled<OUT>(w[q] >> 16, s[e]);
         }
-        dst[2 * u] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        st_global_v8(dst + 2 * u, o);  // (the workspace is 256-byte aligned)
       }
     }
   }
