@@ -76,6 +76,16 @@
 // look a sub-tile's block up load its scales too and leave them beside the
 // ring.
 //
+// Items taken as they come (DYN = true; the kernels of calls with a window or
+// block scales): the grid has a CTA per item, one fits an SM, and a running CTA
+// takes over blocks that have not started (cluster launch control) instead of
+// walking a fixed stride: items differ by their key tiles, and the pairs past a
+// short request's rows are empty.  The K producer asks for the next block when
+// it is three tiles from its item's end, looks the item up and passes both on to
+// the other roles through a two-slot ring.  Later pairs of a (request, head),
+// which see more keys, come first.  (1,760 items of 34 tiles on 152 SMs: 700
+// against 752 us with the stride.)
+//
 // Split (CL = true), for calls with few items and long key ranges: the key tiles
 // of one item are cut into runs, one per CTA of a cluster (item =
 // blockIdx.x / cluster size), each with a softmax of its own.  At the end each
@@ -163,6 +173,11 @@ struct ExtCfg {
   static constexpr int OFF_SCALE = (OFF_TMEMSLOT + 16 + 15) / 16 * 16;  // read 16 bytes at a time
   static constexpr int SMEM_BSC = OFF_SCALE + 2 * NSC * 8 * 4 + 1024;
   static_assert(SMEM_BSC <= 232448, "shared memory per CTA");
+  // DYN: the ring of items (two int4), the answer to a request, and barriers
+  enum { B_ASK = 0, B_ITEM = 1, B_ITAKEN = 3, NSCHED = 5 };
+  static constexpr int OFF_SCHED = OFF_SCALE + 2 * NSC * 8 * 4;
+  static constexpr int SMEM_DYN = OFF_SCHED + 3 * 16 + NSCHED * 8 + 1024;
+  static_assert(OFF_SCHED % 16 == 0 && SMEM_DYN <= 232448, "shared memory per CTA");
   // CL: the fp32 parts of the CTA's share of the rows over the rings, their
   // (max, sum) and the softmax warps' buffers (4 KB each) over the Q tiles
   static constexpr int OFF_CO = OFF_K;
@@ -740,13 +755,14 @@ __device__ __forceinline__ void combine_parts(const ExtendParams& p, const Split
 // HD: head dim (64 or 128); CT: cache dtype (f16, bf16 or e4m3); AT: the
 // activation dtype of q and out (equal to CT for 16-bit caches); PP: the
 // prefix pass; SX: shared-prefix extend; WIN: a window with sink tokens; BSC:
-// fp8 codes with scales per block and kv head; CL: key tiles split over a cluster.
-template <int HD, int CT, int AT, bool PP, bool SX, bool WIN, bool BSC, bool CL>
+// fp8 codes with scales per block and kv head; CL: key tiles split over a
+// cluster; DYN: items taken as they come.
+template <int HD, int CT, int AT, bool PP, bool SX, bool WIN, bool BSC, bool CL, bool DYN>
 __global__ void __launch_bounds__(NTHREADS, 1)
 extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
               const ExtendParams p, const ExtendPartialParams pp) {
-  static_assert(!((WIN || BSC || CL) && (PP || SX)) && (!BSC || CT == DT_E4M3),
+  static_assert(!((WIN || BSC || CL || DYN) && (PP || SX)) && !(CL && DYN) && (!BSC || CT == DT_E4M3),
                 "unsupported combination");
   using C = ExtCfg<HD, CT, AT>;
   constexpr int NST = C::NST;
@@ -770,6 +786,14 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     item0 = (j % heads) * pairs + j / heads;
     stride = p.num_items;
   }
+  // DYN: block j's item (a head's later pairs first)
+  auto item_of = [&](int j) -> int {
+    const int q = (int)p.div_pairs.div((uint32_t)j), pairs = (int)p.div_pairs.d;
+    return q * pairs + (pairs - 1 - (j - q * pairs));
+  };
+  if constexpr (DYN) item0 = item_of(blockIdx.x);
+  int4* sched = reinterpret_cast<int4*>(smem + C::OFF_SCHED);
+  auto sbar = [&](int i) -> uint32_t { return s_base + C::OFF_SCHED + 48 + 8 * i; };
   float* kscale = reinterpret_cast<float*>(smem + C::OFF_SCALE);  // BSC: [NSC][8]
   float* vscale = kscale + C::NSC * 8;
   // WIN: no row of the item sees keys key .. key + count - 1
@@ -802,6 +826,13 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       mbar_init(bar(C::B_EFREE + x), 1);
     }
     mbar_init(bar(C::B_ODONE), 1);
+    if constexpr (DYN) {
+      mbar_init(sbar(C::B_ASK), 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(sbar(C::B_ITEM + x), 1);
+        mbar_init(sbar(C::B_ITAKEN + x), NTHREADS / 32 - 1);
+      }
+    }
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
@@ -810,6 +841,25 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
+
+  // DYN: the CTA's next item and its request's values, from the K producer
+  // (past the last: num_items); the seq-th (from 1) is in slot seq & 1
+  int seq = 0;
+  auto next_item = [&](ItemRaw& raw) -> int {
+    ++seq;
+    const int slot = seq & 1;
+    if (!mbar_wait(sbar(C::B_ITEM + slot), ((seq - 1) >> 1) & 1)) {
+      ok = false;
+      return p.num_items;
+    }
+    const int4 v = sched[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sbar(C::B_ITAKEN + slot));
+    raw.r0 = v.y;
+    raw.r1 = v.z;
+    raw.prefix = v.w;
+    return v.x;
+  };
 
   // registers: launched with 128 per thread (512 x 128); the two softmax
   // warpgroups (warps 4-7 and 8-11) raise their budget to 184, the producer /
@@ -833,9 +883,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     int n = 0, js = 0;
     float m_fin = -INFINITY, l_fin = 0.f;  // CL
     ItemRaw nxt_raw = load_raw<SX>(p, item0);
-    for (int item = item0; ok && item < p.num_items; item += stride) {
+    for (int item = item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
       const ItemRaw raw = nxt_raw;
-      nxt_raw = load_raw<SX>(p, item + stride);
+      if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
       typename ItemOf<WIN, CL>::T it;
       if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
       const int i0x = it.i0 + x * TOK;  // first token of this tile
@@ -1189,11 +1239,54 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         return __shfl_sync(0xFFFFFFFFu, good, 0) != 0;
       };
+      // DYN, the K producer: ask for the next block, and pass its item on
+      bool asked = false;
+      int asks = 0;
+      auto ask = [&]() {
+        fence_proxy_async_shared();  // the last answer has been read
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(sbar(C::B_ASK), 16);
+          next_block_request(s_base + C::OFF_SCHED + 32, sbar(C::B_ASK));
+        }
+        asked = true;
+      };
+      auto ask_item = [&](ItemRaw& raw) -> int {
+        ++seq;
+        const int slot = seq & 1, use = (seq - 1) >> 1;
+        // items without work are passed over here: a role that waited for the
+        // item after them would hold up the MMA warp, which issues an item's
+        // last O += P V when it has the next one
+        int nxt = p.num_items;
+        for (bool more = true; more;) {
+          if (!asked) ask();
+          if (!mbar_wait(sbar(C::B_ASK), asks++ & 1)) {
+            ok = false;
+            nxt = p.num_items;
+            break;
+          }
+          asked = false;
+          const int blk = next_block_answer(s_base + C::OFF_SCHED + 32);
+          nxt = blk >= 0 ? item_of(blk) : p.num_items;
+          raw = load_raw<SX>(p, nxt);
+          typename ItemOf<WIN, CL>::T it;
+          more = nxt < p.num_items && !derive_any<PP, SX, WIN, CL>(p, nxt, raw, it);
+        }
+        if (use > 0 && !mbar_wait(sbar(C::B_ITAKEN + slot), (use - 1) & 1)) ok = false;
+        if (ok) {
+          if (lane == 0) {
+            sched[slot] = make_int4(nxt, raw.r0, raw.r1, raw.prefix);
+            mbar_arrive(sbar(C::B_ITEM + slot));
+          }
+          __syncwarp();
+        }
+        return nxt;
+      };
       int n = 0, j = 0;
       ItemRaw nxt_raw = load_raw<SX>(p, item0);
-      for (int item = item0; ok && item < p.num_items; item += stride) {
+      for (int item = item0; ok && item < p.num_items; item = DYN ? (is_k ? ask_item(nxt_raw) : next_item(nxt_raw)) : item + stride) {
         const ItemRaw raw = nxt_raw;
-        nxt_raw = load_raw<SX>(p, item + stride);
+        if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
         if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
         if (is_k && !load_q(it, j, 0)) { ok = false; break; }
@@ -1272,10 +1365,17 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               }
             }
           }
+          if constexpr (DYN) {
+            if (is_k && !asked && kt >= it.T - 3) ask();
+          }
           // Q of tile B once tile A of the previous item is done with its buffer
           if (is_k && kt == min(1, it.T - 1) && !load_q(it, j, 1)) { ok = false; break; }
         }
         ++j;
+      }
+      // a failed wait ended the loop: the request under way still writes its answer
+      if constexpr (DYN) {
+        if (asked) (void)mbar_wait(sbar(C::B_ASK), asks & 1);
       }
     } else if (warp == 3) {
       if constexpr (out_tma_for<HD, CT, SX>()) {
@@ -1288,9 +1388,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // softmax warps off the TMA engine's queue.
       int js = 0;
       ItemRaw nxt_raw = load_raw<SX>(p, item0);
-      for (int item = item0; ok && item < p.num_items; item += stride) {
+      for (int item = item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
-        nxt_raw = load_raw<SX>(p, item + stride);
+        if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
         if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
         const uint32_t stg = s_base + C::OFF_Q + ((2 * js + 1) % NQB) * C::T16;
@@ -1367,9 +1467,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       bool have_prev = false, prev_first = false, prev_last = false;
       int prev_n = 0, prev_j = 0;
       ItemRaw nxt_raw = load_raw<SX>(p, item0);
-      for (int item = item0; ok && item < p.num_items; item += stride) {
+      for (int item = item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
-        nxt_raw = load_raw<SX>(p, item + stride);
+        if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
         if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
         const int qa = (2 * j) % NQB, qb = (2 * j + 1) % NQB;
@@ -1448,9 +1548,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         return true;
       };
       ItemRaw nxt_raw = load_raw<SX>(p, item0);
-      for (int item = item0; ok && item < p.num_items; item += stride) {
+      for (int item = item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
-        nxt_raw = load_raw<SX>(p, item + stride);
+        if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
         if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
         SegIter si;
@@ -1528,15 +1628,17 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 }
 
-template <int HD, int CT, int AT, bool PP, bool SX, bool WIN = false, bool BSC = false>
+template <int HD, int CT, int AT, bool PP, bool SX, bool WIN = false, bool BSC = false,
+          bool DYN = false>
 cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                             const CUtensorMap& omap, const ExtendParams& p,
                             const ExtendPartialParams& pp, cudaStream_t stream) {
-  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN, BSC, false>;
-  constexpr int smem = BSC ? ExtCfg<HD, CT, AT>::SMEM_BSC : ExtCfg<HD, CT, AT>::SMEM;
+  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN, BSC, false, DYN>;
+  using C = ExtCfg<HD, CT, AT>;
+  constexpr int smem = DYN ? C::SMEM_DYN : BSC ? C::SMEM_BSC : C::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k<<<dim3(p.num_ctas), NTHREADS, smem, stream>>>(kmap, vmap, qmap, omap, p, pp);
+  k<<<dim3(DYN ? p.num_items : p.num_ctas), NTHREADS, smem, stream>>>(kmap, vmap, qmap, omap, p, pp);
   return cudaGetLastError();
 }
 
@@ -1545,7 +1647,7 @@ template <int HD, int CT, int AT, bool WIN, bool BSC>
 cudaError_t launch_extend_split_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                   const CUtensorMap& qmap, const CUtensorMap& omap,
                                   const ExtendParams& p, cudaStream_t stream) {
-  auto k = extend_kernel<HD, CT, AT, false, false, WIN, BSC, true>;
+  auto k = extend_kernel<HD, CT, AT, false, false, WIN, BSC, true, false>;
   constexpr int smem = BSC ? ExtCfg<HD, CT, AT>::SMEM_BSC : ExtCfg<HD, CT, AT>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

@@ -13,8 +13,19 @@ cudaError_t launch_scaled_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const ExtendParams& p, cudaStream_t stream) {
   const ExtendPartialParams pp{};
   return p.window > 0
-             ? launch_extend_t<HD, DT_E4M3, AT, false, false, true, true>(kmap, vmap, qmap, omap, p, pp, stream)
-             : launch_extend_t<HD, DT_E4M3, AT, false, false, false, true>(kmap, vmap, qmap, omap, p, pp, stream);
+             ? launch_extend_t<HD, DT_E4M3, AT, false, false, true, true, true>(kmap, vmap, qmap, omap, p, pp, stream)
+             : launch_extend_t<HD, DT_E4M3, AT, false, false, false, true, true>(kmap, vmap, qmap, omap, p, pp, stream);
+}
+
+// Pages widened beforehand, every key seen: K in the queries' type, V as f16.
+template <int HD>
+cudaError_t launch_widened_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                             const CUtensorMap& qmap, const CUtensorMap& omap,
+                             const ExtendParams& p, int act_dt, cudaStream_t stream) {
+  const ExtendPartialParams pp{};
+  return act_dt == DT_BF16
+             ? launch_extend_t<HD, DT_BF16_V16, DT_BF16, false, false, false, false, true>(kmap, vmap, qmap, omap, p, pp, stream)
+             : launch_extend_t<HD, DT_F16, DT_F16, false, false, false, false, true>(kmap, vmap, qmap, omap, p, pp, stream);
 }
 
 }  // namespace
@@ -32,8 +43,11 @@ cudaError_t launch_extend_view(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (p.splits > 1)
     return launch_extend_split(kmap, vmap, qmap, omap, p, head_dim, cache_dt, act_dt, stream);
   if (!p.k_scales) {
-    if (p.window <= 0)
-      return launch_extend(kmap, vmap, qmap, omap, p, head_dim, cache_dt, act_dt, stream);
+    if (p.window <= 0) {
+      if (cache_dt != DT_BF16_V16 && cache_dt != DT_F16) return cudaErrorInvalidValue;
+      return head_dim == 128 ? launch_widened_t<128>(kmap, vmap, qmap, omap, p, act_dt, stream)
+                             : launch_widened_t<64>(kmap, vmap, qmap, omap, p, act_dt, stream);
+    }
     return launch_extend_window(kmap, vmap, qmap, omap, p, head_dim, cache_dt, act_dt, stream);
   }
   if (head_dim == 128)

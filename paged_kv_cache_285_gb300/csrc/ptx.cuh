@@ -99,6 +99,28 @@ __device__ __forceinline__ void cluster_st2(uint32_t a, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
+// ---- work taken from the launch ------------------------------------------------
+// Ask for the next block of this grid that has not started (it then never
+// starts): 16 bytes at `resp` (16-byte aligned), counted on `bar`.
+__device__ __forceinline__ void next_block_request(uint32_t resp, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+      ::"r"(resp), "r"(bar)
+      : "memory");
+}
+// The answer: its blockIdx.x, or -1 where no block was left (then no more may be asked for).
+__device__ __forceinline__ int next_block_answer(uint32_t resp) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tmov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+      : "=r"(x)
+      : "r"(resp)
+      : "memory");
+  return x;
+}
+
 // ---- TMA --------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int32_t c0, int32_t c1, int32_t c2) {

@@ -281,6 +281,19 @@ def test_extend_regimes(cfg, d, bs, act):
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("d,bs,act", [(64, 32, F16), (128, 16, BF16)])
+def test_extend_of_more_items_than_sms(d, bs, act):
+    # widened pages (the workspace given) and codes; rows from none to many, several items per SM
+    rows, prefix, hq = [0, 1100, 1, 0, 70, 2, 900], [9, 30, 40, 0, 200, 64, 0], 8
+    c = Case(SCALED, act, 8, d, bs, [p + n for p, n in zip(prefix, rows)], seed=12).cuda()
+    q = c.rows(sum(rows), hq).cuda()
+    ref = R.attention(*c.values(), to_f64(q), indptr(rows), prefix, c.tables, hq, 1 / d ** 0.5)
+    for fill in (0xFF, None):
+        out, lse = run_extend(c, q, hq, rows, prefix, fill=fill)
+        check_attention(out, lse, ref, act, d, f"{fill}")
+    assert pkv.get_device_error() == 0
+
+
 @pytest.mark.parametrize("rows,prefix", [([16], [16]), ([20], [1500]), ([140], [0])])
 def test_extend_scales_of_any_size(rows, prefix):
     # V scales that f16 does not hold, K scales far apart, and pages of zeros under the least scale

@@ -152,6 +152,23 @@ def test_extend_over_many_tiles():
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("cache,act,d", [(BF16, BF16, 128), (E4M3, BF16, 64), (F16, F16, 128)])
+def test_extend_of_more_items_than_sms(cache, act, d):
+    # several items per SM, taken as they come: requests of one row beside requests of many, empty
+    # requests, and pairs past a short request's rows in between
+    rows = [0, 1, 330, 0, 0, 2, 700, 1, 64, 65, 0, 500, 3, 1, 129, 0]
+    prefix = [9, 40, 0, 5, 0, 33, 100, 0, 70, 5, 1, 260, 0, 300, 16, 0]
+    hq, hkv = 8, 8
+    c = Case(cache, act, hkv, d, 16, [p + n for p, n in zip(prefix, rows)], seed=11).cuda()
+    q = c.rows(sum(rows), hq).cuda()
+    out, lse = run_extend(c, q, hq, rows, prefix, 150, 5)
+    ref = R.attention(*c.values(), to_f64(q), indptr(rows), prefix, c.tables, hq, 1 / d ** 0.5, 150, 5)
+    check_attention(out, lse, ref, act, d)
+    again, _ = run_extend(c, q, hq, rows, prefix, 150, 5)
+    assert torch.equal(again, out)
+    assert pkv.get_device_error() == 0
+
+
 @pytest.mark.parametrize("cache,act", [(F16, F16), (E4M3, BF16)])
 def test_extend_of_a_whole_window_is_the_plain_extend(cache, act):
     prefix, rows = [300, 0], [90, 200]
