@@ -1642,6 +1642,18 @@ cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, co
   return cudaGetLastError();
 }
 
+// A call with a window and / or block scales: one CTA per item where they fit the
+// GPU at once, else items taken as they come (which costs an item 0.4 us).
+template <int HD, int CT, int AT, bool WIN, bool BSC>
+cudaError_t launch_extend_view_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 const CUtensorMap& qmap, const CUtensorMap& omap,
+                                 const ExtendParams& p, cudaStream_t stream) {
+  const ExtendPartialParams pp{};
+  return p.num_items > p.num_ctas
+             ? launch_extend_t<HD, CT, AT, false, false, WIN, BSC, true>(kmap, vmap, qmap, omap, p, pp, stream)
+             : launch_extend_t<HD, CT, AT, false, false, WIN, BSC, false>(kmap, vmap, qmap, omap, p, pp, stream);
+}
+
 // One item per cluster of p.splits CTAs (1, 2, 4 or 8), its key tiles split over them.
 template <int HD, int CT, int AT, bool WIN, bool BSC>
 cudaError_t launch_extend_split_t(const CUtensorMap& kmap, const CUtensorMap& vmap,

@@ -11,10 +11,8 @@ template <int HD, int AT>
 cudaError_t launch_scaled_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const CUtensorMap& qmap, const CUtensorMap& omap,
                             const ExtendParams& p, cudaStream_t stream) {
-  const ExtendPartialParams pp{};
-  return p.window > 0
-             ? launch_extend_t<HD, DT_E4M3, AT, false, false, true, true, true>(kmap, vmap, qmap, omap, p, pp, stream)
-             : launch_extend_t<HD, DT_E4M3, AT, false, false, false, true, true>(kmap, vmap, qmap, omap, p, pp, stream);
+  return p.window > 0 ? launch_extend_view_t<HD, DT_E4M3, AT, true, true>(kmap, vmap, qmap, omap, p, stream)
+                      : launch_extend_view_t<HD, DT_E4M3, AT, false, true>(kmap, vmap, qmap, omap, p, stream);
 }
 
 // Pages widened beforehand, every key seen: K in the queries' type, V as f16.
@@ -22,10 +20,9 @@ template <int HD>
 cudaError_t launch_widened_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                              const CUtensorMap& qmap, const CUtensorMap& omap,
                              const ExtendParams& p, int act_dt, cudaStream_t stream) {
-  const ExtendPartialParams pp{};
   return act_dt == DT_BF16
-             ? launch_extend_t<HD, DT_BF16_V16, DT_BF16, false, false, false, false, true>(kmap, vmap, qmap, omap, p, pp, stream)
-             : launch_extend_t<HD, DT_F16, DT_F16, false, false, false, false, true>(kmap, vmap, qmap, omap, p, pp, stream);
+             ? launch_extend_view_t<HD, DT_BF16_V16, DT_BF16, false, false>(kmap, vmap, qmap, omap, p, stream)
+             : launch_extend_view_t<HD, DT_F16, DT_F16, false, false>(kmap, vmap, qmap, omap, p, stream);
 }
 
 }  // namespace

@@ -8,11 +8,9 @@ cudaError_t launch_extend_window(const CUtensorMap& kmap, const CUtensorMap& vma
                                  const CUtensorMap& qmap, const CUtensorMap& omap,
                                  const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
                                  cudaStream_t stream) {
-  const ExtendPartialParams pp{};
 #define PKV_EXT(HD, CT, AT)                             \
   if (head_dim == HD && cache_dt == CT && act_dt == AT) \
-    return launch_extend_t<HD, CT, AT, false, false, true, false, true>(kmap, vmap, qmap, omap, p, pp, \
-                                                                        stream);
+    return launch_extend_view_t<HD, CT, AT, true, false>(kmap, vmap, qmap, omap, p, stream);
   PKV_EXT(128, DT_BF16_V16, DT_BF16)
   PKV_EXT(64, DT_BF16_V16, DT_BF16)
   PKV_EXT(128, DT_F16, DT_F16)
