@@ -1067,6 +1067,14 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   if (view) {
     p.splits = plan_key_splits(p, max_total_len, ds->sm_count);
     if (p.splits > 1) p.out_tma = 0;  // (every row leaves with the cluster's sum)
+    const int64_t units = total_q_rows / (2 * p.tok) + (int64_t)batch;
+    p.num_blocks_dyn = p.num_items;
+    p.div_rows = make_fastdiv((uint32_t)(2 * p.tok));
+    if (units * desc->num_kv_heads * 2 < p.num_items) {
+      p.by_rows = 1;
+      p.num_units = (int)units;
+      p.num_blocks_dyn = (int)(units * desc->num_kv_heads);
+    }
     // Widening pays where many pairs of row tiles would convert the same pages:
     // one pair per key tile costs 15 % (4 requests of 1,900 rows x 4 heads, 59
     // pairs: 804 against 957 us), the pass itself three launches and three

@@ -83,7 +83,9 @@
 // short request's rows are empty.  The K producer asks for the next block when
 // it is three tiles from its item's end, looks the item up and passes both on to
 // the other roles through a two-slot ring.  Later pairs of a (request, head),
-// which see more keys, come first.  (1,760 items of 34 tiles on 152 SMs: 700
+// which see more keys, come first.  Where the requests' lengths differ so much
+// that most pairs up to the length hint would be empty (a prompt among single
+// tokens), blocks are counted by rows and their requests searched.  (1,760 items of 34 tiles on 152 SMs: 700
 // against 752 us with the stride.)
 //
 // Split (CL = true), for calls with few items and long key ranges: the key tiles
@@ -673,6 +675,27 @@ __device__ __forceinline__ bool derive(const ExtendParams& p, int item, const It
   return true;
 }
 
+// DYN with blocks counted by rows: block j is (unit, head), and unit u is pair
+// u - key(b) of the last request b with key(b) = q_indptr[b] / rows + b <= u
+// (rows = 2 tok, the rows of a pair), units from the last on.  The whole warp.
+__device__ __forceinline__ int item_by_rows(const int32_t* q_indptr, int batch, int heads, int units,
+                                         int rows, int pairs, int num_items, int j) {
+  const int lane = threadIdx.x & 31;
+  const int v = j / heads, g = j - v * heads, u = units - 1 - v;
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5;
+    const int idx = lo + lane * step;
+    const int key = idx < hi ? max(__ldg(q_indptr + idx), 0) / rows + idx : INT_MAX;
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, key <= u);
+    const int k = m ? 31 - __clz(m) : 0;
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  const int pair = u - (max(__ldg(q_indptr + lo), 0) / rows + lo);
+  return pair >= 0 && pair < pairs ? (lo * heads + g) * pairs + pair : num_items;
+}
+
 // derive for any kernel; CL: then the CTA's share of the item's key tiles.
 template <bool PP, bool SX, bool WIN, bool CL>
 __device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, const ItemRaw& r,
@@ -756,12 +779,14 @@ __device__ __forceinline__ void combine_parts(const ExtendParams& p, const Split
 // activation dtype of q and out (equal to CT for 16-bit caches); PP: the
 // prefix pass; SX: shared-prefix extend; WIN: a window with sink tokens; BSC:
 // fp8 codes with scales per block and kv head; CL: key tiles split over a
-// cluster; DYN: items taken as they come.
-template <int HD, int CT, int AT, bool PP, bool SX, bool WIN, bool BSC, bool CL, bool DYN>
+// cluster; TAKE: items taken as they come (DYN), from blocks counted by the
+// length hint (1) or by rows (2).
+template <int HD, int CT, int AT, bool PP, bool SX, bool WIN, bool BSC, bool CL, int TAKE>
 __global__ void __launch_bounds__(NTHREADS, 1)
 extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
               const ExtendParams p, const ExtendPartialParams pp) {
+  constexpr bool DYN = TAKE != 0;
   static_assert(!((WIN || BSC || CL || DYN) && (PP || SX)) && !(CL && DYN) && (!BSC || CT == DT_E4M3),
                 "unsupported combination");
   using C = ExtCfg<HD, CT, AT>;
@@ -786,12 +811,16 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     item0 = (j % heads) * pairs + j / heads;
     stride = p.num_items;
   }
-  // DYN: block j's item (a head's later pairs first)
+  // DYN: block j's item (the whole warp; a head's later pairs first), or
+  // num_items where it has none
   auto item_of = [&](int j) -> int {
-    const int q = (int)p.div_pairs.div((uint32_t)j), pairs = (int)p.div_pairs.d;
+    const int pairs = (int)p.div_pairs.d;
+    if constexpr (TAKE == 2)
+      return item_by_rows(p.q_indptr, p.batch, p.num_kv_heads, p.num_units, (int)p.div_rows.d, pairs,
+                          p.num_items, j);
+    const int q = (int)p.div_pairs.div((uint32_t)j);
     return q * pairs + (pairs - 1 - (j - q * pairs));
   };
-  if constexpr (DYN) item0 = item_of(blockIdx.x);
   int4* sched = reinterpret_cast<int4*>(smem + C::OFF_SCHED);
   auto sbar = [&](int i) -> uint32_t { return s_base + C::OFF_SCHED + 48 + 8 * i; };
   float* kscale = reinterpret_cast<float*>(smem + C::OFF_SCALE);  // BSC: [NSC][8]
@@ -843,7 +872,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   bool ok = true;
 
   // DYN: the CTA's next item and its request's values, from the K producer
-  // (past the last: num_items); the seq-th (from 1) is in slot seq & 1
+  // (past the last: num_items); the seq-th (from 1) is in slot seq & 1.  (The
+  // code that finds an item stands once, there, and the search by rows only in
+  // the kernels that use it: in the others, or twice, it cost 3 % of a call.)
   int seq = 0;
   auto next_item = [&](ItemRaw& raw) -> int {
     ++seq;
@@ -882,8 +913,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint32_t orow = tmem + lane_addr + tm_o<HD>(x);
     int n = 0, js = 0;
     float m_fin = -INFINITY, l_fin = 0.f;  // CL
-    ItemRaw nxt_raw = load_raw<SX>(p, item0);
-    for (int item = item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
+    ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+    for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
       const ItemRaw raw = nxt_raw;
       if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
       typename ItemOf<WIN, CL>::T it;
@@ -1240,7 +1271,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         return __shfl_sync(0xFFFFFFFFu, good, 0) != 0;
       };
       // DYN, the K producer: ask for the next block, and pass its item on
-      bool asked = false;
+      bool asked = false, first = true;  // the first item is this block's own
       int asks = 0;
       auto ask = [&]() {
         fence_proxy_async_shared();  // the last answer has been read
@@ -1259,18 +1290,25 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // last O += P V when it has the next one
         int nxt = p.num_items;
         for (bool more = true; more;) {
-          if (!asked) ask();
-          if (!mbar_wait(sbar(C::B_ASK), asks++ & 1)) {
-            ok = false;
-            nxt = p.num_items;
-            break;
+          int blk = blockIdx.x;
+          if (!first) {
+            if (!asked) ask();
+            blk = -1;
+            if (mbar_wait(sbar(C::B_ASK), asks & 1)) {
+              ++asks;
+              asked = false;
+              blk = next_block_answer(s_base + C::OFF_SCHED + 32);
+            } else {
+              ok = false;
+            }
           }
-          asked = false;
-          const int blk = next_block_answer(s_base + C::OFF_SCHED + 32);
-          nxt = blk >= 0 ? item_of(blk) : p.num_items;
+          first = false;
+          nxt = p.num_items;
+          if (blk < 0) break;
+          nxt = item_of(blk);
           raw = load_raw<SX>(p, nxt);
           typename ItemOf<WIN, CL>::T it;
-          more = nxt < p.num_items && !derive_any<PP, SX, WIN, CL>(p, nxt, raw, it);
+          more = nxt >= p.num_items || !derive_any<PP, SX, WIN, CL>(p, nxt, raw, it);
         }
         if (use > 0 && !mbar_wait(sbar(C::B_ITAKEN + slot), (use - 1) & 1)) ok = false;
         if (ok) {
@@ -1283,8 +1321,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         return nxt;
       };
       int n = 0, j = 0;
-      ItemRaw nxt_raw = load_raw<SX>(p, item0);
-      for (int item = item0; ok && item < p.num_items; item = DYN ? (is_k ? ask_item(nxt_raw) : next_item(nxt_raw)) : item + stride) {
+      ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+      for (int item = DYN ? (is_k ? ask_item(nxt_raw) : next_item(nxt_raw)) : item0; ok && item < p.num_items; item = DYN ? (is_k ? ask_item(nxt_raw) : next_item(nxt_raw)) : item + stride) {
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
@@ -1387,8 +1425,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // two items on waits for tile B's release).  Waiting here keeps the
       // softmax warps off the TMA engine's queue.
       int js = 0;
-      ItemRaw nxt_raw = load_raw<SX>(p, item0);
-      for (int item = item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
+      ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+      for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
@@ -1466,8 +1504,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       int n = 0, j = 0;
       bool have_prev = false, prev_first = false, prev_last = false;
       int prev_n = 0, prev_j = 0;
-      ItemRaw nxt_raw = load_raw<SX>(p, item0);
-      for (int item = item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
+      ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+      for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
@@ -1547,8 +1585,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (lane == 0) mbar_arrive(bar(C::B_QCONV + 2 * xq + (j & 1)));
         return true;
       };
-      ItemRaw nxt_raw = load_raw<SX>(p, item0);
-      for (int item = item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
+      ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+      for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
@@ -1629,29 +1667,31 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 }
 
 template <int HD, int CT, int AT, bool PP, bool SX, bool WIN = false, bool BSC = false,
-          bool DYN = false>
+          int TAKE = 0>
 cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                             const CUtensorMap& omap, const ExtendParams& p,
                             const ExtendPartialParams& pp, cudaStream_t stream) {
-  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN, BSC, false, DYN>;
+  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN, BSC, false, TAKE>;
   using C = ExtCfg<HD, CT, AT>;
+  constexpr bool DYN = TAKE != 0;
   constexpr int smem = DYN ? C::SMEM_DYN : BSC ? C::SMEM_BSC : C::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k<<<dim3(DYN ? p.num_items : p.num_ctas), NTHREADS, smem, stream>>>(kmap, vmap, qmap, omap, p, pp);
+  k<<<dim3(DYN ? p.num_blocks_dyn : p.num_ctas), NTHREADS, smem, stream>>>(kmap, vmap, qmap, omap, p, pp);
   return cudaGetLastError();
 }
 
 // A call with a window and / or block scales: one CTA per item where they fit the
-// GPU at once, else items taken as they come (which costs an item 0.4 us).
+// GPU at once, else items taken as they come (which costs an item 0.4 us).  The
+// by-rows kernels are compiled in translation units of their own.
 template <int HD, int CT, int AT, bool WIN, bool BSC>
 cudaError_t launch_extend_view_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  const CUtensorMap& qmap, const CUtensorMap& omap,
                                  const ExtendParams& p, cudaStream_t stream) {
   const ExtendPartialParams pp{};
-  return p.num_items > p.num_ctas
-             ? launch_extend_t<HD, CT, AT, false, false, WIN, BSC, true>(kmap, vmap, qmap, omap, p, pp, stream)
-             : launch_extend_t<HD, CT, AT, false, false, WIN, BSC, false>(kmap, vmap, qmap, omap, p, pp, stream);
+  return p.num_blocks_dyn > p.num_ctas
+             ? launch_extend_t<HD, CT, AT, false, false, WIN, BSC, 1>(kmap, vmap, qmap, omap, p, pp, stream)
+             : launch_extend_t<HD, CT, AT, false, false, WIN, BSC, 0>(kmap, vmap, qmap, omap, p, pp, stream);
 }
 
 // One item per cluster of p.splits CTAs (1, 2, 4 or 8), its key tiles split over them.
@@ -1659,7 +1699,7 @@ template <int HD, int CT, int AT, bool WIN, bool BSC>
 cudaError_t launch_extend_split_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                   const CUtensorMap& qmap, const CUtensorMap& omap,
                                   const ExtendParams& p, cudaStream_t stream) {
-  auto k = extend_kernel<HD, CT, AT, false, false, WIN, BSC, true, false>;
+  auto k = extend_kernel<HD, CT, AT, false, false, WIN, BSC, true, 0>;
   constexpr int smem = BSC ? ExtCfg<HD, CT, AT>::SMEM_BSC : ExtCfg<HD, CT, AT>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

@@ -39,6 +39,8 @@ cudaError_t launch_extend_view(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (p.k_scales && (!p.v_scales || cache_dt != DT_E4M3)) return cudaErrorInvalidValue;
   if (p.splits > 1)
     return launch_extend_split(kmap, vmap, qmap, omap, p, head_dim, cache_dt, act_dt, stream);
+  if (p.by_rows)
+    return launch_extend_by_rows(kmap, vmap, qmap, omap, p, head_dim, cache_dt, act_dt, stream);
   if (!p.k_scales) {
     if (p.window <= 0) {
       if (cache_dt != DT_BF16_V16 && cache_dt != DT_F16) return cudaErrorInvalidValue;

@@ -231,6 +231,13 @@ struct ExtendParams {
   const float* k_scales;  // block-scaled launches: [num_blocks][num_kv_heads]
   const float* v_scales;
   int splits;           // split launches: CTAs per item (its key tiles split over them)
+  // window / block-scaled launches that take items as they come: blocks of the
+  // grid, one per item, or (by_rows) num_kv_heads x num_units, units being
+  // total_rows / (2 tok) + batch candidates for pairs of row tiles
+  int num_blocks_dyn;
+  int by_rows;
+  int num_units;
+  FastDiv div_rows;     // by 2 tok
 };
 
 // Partial output of the extend kernel's prefix pass: row q (request b, head h:
@@ -307,6 +314,10 @@ cudaError_t launch_extend_view(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const CUtensorMap& qmap, const CUtensorMap& omap,
                                const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
                                cudaStream_t stream);
+cudaError_t launch_extend_by_rows(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                  const CUtensorMap& qmap, const CUtensorMap& omap,
+                                  const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
+                                  cudaStream_t stream);
 cudaError_t launch_extend_split(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                 const CUtensorMap& qmap, const CUtensorMap& omap,
                                 const ExtendParams& p, int head_dim, int cache_dt, int act_dt,

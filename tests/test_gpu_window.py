@@ -169,6 +169,21 @@ def test_extend_of_more_items_than_sms(cache, act, d):
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("at", [0, 37, 69])
+def test_extend_of_a_prompt_among_single_tokens(at):
+    # one long request among many of a row or none: blocks are counted by rows
+    rows, prefix = [1] * 70, [(7 * i) % 90 for i in range(70)]
+    for i in (3, 4, 36, 38):
+        rows[i] = 0
+    rows[at], prefix[at] = 600, 40
+    c = Case(BF16, BF16, 2, 64, 16, [p + n for p, n in zip(prefix, rows)], seed=13).cuda()
+    q = c.rows(sum(rows), 8).cuda()
+    out, lse = run_extend(c, q, 8, rows, prefix, 100, 3)
+    ref = R.attention(*c.values(), to_f64(q), indptr(rows), prefix, c.tables, 8, 1 / 8, 100, 3)
+    check_attention(out, lse, ref, BF16, 64)
+    assert pkv.get_device_error() == 0
+
+
 @pytest.mark.parametrize("cache,act", [(F16, F16), (E4M3, BF16)])
 def test_extend_of_a_whole_window_is_the_plain_extend(cache, act):
     prefix, rows = [300, 0], [90, 200]
