@@ -173,33 +173,37 @@ bool plan_extend(ExtendParams& p, int batch, int num_kv_heads, int group, int ma
   return true;
 }
 
-// CTAs per item of an extend call with a window and / or block scales: its key
-// tiles are split over a cluster when the items are too few to fill the GPU and
-// their key ranges long.  The estimate is in key tiles (1.9 us each at 128 dims,
-// both row tiles): a CTA costs its tiles and a fixed part, 3 tiles, or 5.5 in a
-// cluster (writing and adding up the parts); 152 SMs hold 152, 152, 144 and 120
-// CTAs in clusters of 1, 2, 4 and 8.  Measured (us at 1 / 2 / 4 / 8 CTAs): 8
-// items of 64 tiles 123 / 75 / 44 / 30, 64 of 254 tiles 458 / 261 / 278 / 365,
-// 128 of up to 21 tiles 43 / 53 / 62 / 107, 32 of 35 tiles 62 / 43 / 31 / 65.
-int plan_key_splits(const ExtendParams& p, int max_total_len, int sm_count) {
+// How an extend call with a window and / or block scales takes its items: in
+// whole tiles or, where every request's rows fit one row tile, in half tiles; and
+// with its key tiles split over a cluster of `splits` CTAs when the items are too
+// few to fill the GPU.  The estimate, in us, at 128 dims: a key tile costs 1.80
+// (half tiles: 1.43), a CTA a fixed part of 5.5, or 9.5 where parts are combined
+// (clusters and half tiles); 152 SMs hold 152, 152, 144 and 120 CTAs in clusters
+// of 1, 2, 4 and 8.  Measured (us at 1 / 2 / 4 / 8 CTAs): whole tiles, 64 items of
+// 254 tiles 458 / 259 / 278 / 365, 128 of up to 21 tiles 43 / 53 / 62 / 107, 8 of
+// 63 tiles 115 / 66 / 39 / 25; the last in half tiles 100 / 55 / 33 / 22.5, and
+// 512 of 1 to 4 tiles 44 whole, 56 in half tiles.
+void plan_view_items(ExtendParams& p, int max_total_len, int sm_count) {
   int64_t tiles = ((int64_t)max_total_len + 127) / 128;
   if (p.window > 0)
     tiles = std::min<int64_t>(tiles, ((int64_t)p.window + 2 * p.tok + 15 + 127) / 128 + 1 +
                                          ((int64_t)p.sink_tokens + 127) / 128);
   const double sms = sm_count > 0 ? sm_count : 152;
-  int best = 1;
-  double best_cost = 1e30;
-  for (int c = 1; c <= 8; c *= 2) {
-    if ((int64_t)p.num_items * c > INT32_MAX || (c > 1 && tiles < c)) break;
-    const double slots = c == 8 ? sms * 120 / 152 : c == 4 ? sms * 144 / 152 : sms;
-    const double cost = std::ceil(p.num_items * c / slots) *
-                        ((double)((tiles + c - 1) / c) + (c > 1 ? 5.5 : 3.0));
-    if (cost < 0.9 * best_cost) {  // (not for less than a tenth)
-      best_cost = cost;
-      best = c;
+  double best = 1e30;
+  for (int half = 0; half <= (p.tiles_per_head <= 1 ? 1 : 0); ++half) {
+    for (int c = 1; c <= 8; c *= 2) {
+      if ((int64_t)p.num_items * c > INT32_MAX || (c > 1 && tiles < c)) break;
+      const double slots = c == 8 ? sms * 120 / 152 : c == 4 ? sms * 144 / 152 : sms;
+      const double cost = std::ceil(p.num_items * c / slots) *
+                          ((double)((tiles + c - 1) / c) * (half ? 1.43 : 1.80) +
+                           (c > 1 || half ? 9.5 : 5.5));
+      if (cost < 0.93 * best) {  // (not for less than a few per cent)
+        best = cost;
+        p.splits = c;
+        p.half = half;
+      }
     }
   }
-  return best;
 }
 
 // Softmax scale in base 2 with an fp8 cache's k_scale folded in (scores are
@@ -1065,8 +1069,8 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   int cache_dt = (int)desc->cache_dtype;
   bool widen_pages = widen_plain;
   if (view) {
-    p.splits = plan_key_splits(p, max_total_len, ds->sm_count);
-    if (p.splits > 1) p.out_tma = 0;  // (every row leaves with the cluster's sum)
+    plan_view_items(p, max_total_len, ds->sm_count);
+    if (p.splits > 1 || p.half) p.out_tma = 0;  // (every row leaves with its parts' sum)
     const int64_t units = total_q_rows / (2 * p.tok) + (int64_t)batch;
     p.num_blocks_dyn = p.num_items;
     p.div_rows = make_fastdiv((uint32_t)(2 * p.tok));
@@ -1080,7 +1084,7 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     // pairs: 804 against 957 us), the pass itself three launches and three
     // times the pages' bytes (300 rows, 10 pairs: 140 against 132; 16 rows: 123
     // against 68).
-    if (p.splits > 1 || (p.tiles_per_head + 1) / 2 < 16) widen_pages = false;
+    if (p.splits > 1 || p.half || (p.tiles_per_head + 1) / 2 < 16) widen_pages = false;
     if (scaled && !widen_pages) {
       p.k_scales = view->k_scales;
       p.v_scales = view->v_scales;

@@ -98,6 +98,11 @@
 // launch.  (Writing to the owner, not reading from the others: a remote load is
 // waited for, a remote store is not.)
 //
+// Half tiles (HALF = true, with CL): where every request's rows fit one row tile,
+// tile B would be empty.  Both tiles then hold the same rows and share the keys
+// of each key tile, A its first 64, B its last: S, softmax and P V of half the
+// width, still in ping-pong, and two parts per CTA to combine.
+//
 // Window (WIN = true): row i at position p = prefix + i sees keys j <= p with
 // j > p - window, and the first sink_tokens keys.  An item's key tiles are
 // the tiles of the sink keys, then those from the oldest key of its first
@@ -697,7 +702,7 @@ __device__ __forceinline__ int item_by_rows(const int32_t* q_indptr, int batch, 
 }
 
 // derive for any kernel; CL: then the CTA's share of the item's key tiles.
-template <bool PP, bool SX, bool WIN, bool CL>
+template <bool PP, bool SX, bool WIN, bool CL, bool HALF = false>
 __device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, const ItemRaw& r,
                                            typename ItemOf<WIN, CL>::T& it) {
   if constexpr (CL) {
@@ -705,6 +710,7 @@ __device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, cons
     it.rows = false;
     if (!derive<PP, SX, WIN>(p, item, r, it)) return false;
     it.rows = true;
+    if constexpr (HALF) it.ntok[1] = it.ntok[0];
     const int per = (it.T + p.splits - 1) / p.splits;
     it.kt0 = (int)cluster_rank() * per;
     it.T = min(per, it.T - it.kt0);
@@ -716,14 +722,16 @@ __device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, cons
 
 // CL: this CTA's share of the item's 2 x 128 rows (row R belongs to CTA R mod
 // splits, as its row R / splits) out of the parts that the cluster's CTAs left at
-// co [splits][share][HD] (fp32) and ml [splits][share] (max, sum).  The softmax
-// threads, tid 0 .. 255 = splits x share: each first turns one (max, sum) into
+// co [parts][share][HD] (fp32) and ml [parts][share] (max, sum): one part per CTA,
+// or (HALF) 128 rows and two parts per CTA.  The softmax threads, tid 0 .. 255 =
+// parts x share: each first turns one (max, sum) into
 // its part's weight (in place), then they add the rows up.
-template <int HD, int AT, bool WIN>
+template <int HD, int AT, bool HALF>
 __device__ __forceinline__ void combine_parts(const ExtendParams& p, const SplitItem& it,
                                               const uint8_t* co, float2* ml, int tid) {
   if (!it.rows) return;
-  const int C = p.splits, sh = 31 - __clz(C), share = (2 * BM) >> sh, rank = (int)cluster_rank();
+  const int sh = 31 - __clz(p.splits), rank = (int)cluster_rank();
+  const int C = HALF ? 2 * p.splits : p.splits, share = (HALF ? BM : 2 * BM) >> sh;
   // r / group for r < 128 as a multiply: the quotient's error, below 128 / 2^16,
   // is less than 1 / group
   const uint32_t gmul = 65536u / (uint32_t)p.group + 1u;
@@ -735,7 +743,7 @@ __device__ __forceinline__ void combine_parts(const ExtendParams& p, const Split
     return (int64_t)(it.row0 + it.i0 + x * p.tok + rtok) * p.num_q_heads + it.g * p.group + (r - rtok * p.group);
   };
   {
-    const int c = tid >> (8 - sh), lr = tid & (share - 1);
+    const int c = tid >> ((HALF ? 7 : 8) - sh), lr = tid & (share - 1);
     float m = -INFINITY, l = 0.f;
     for (int k = 0; k < C; ++k) m = fmaxf(m, ml[k * share + lr].x);
     for (int k = 0; k < C; ++k) {
@@ -780,13 +788,16 @@ __device__ __forceinline__ void combine_parts(const ExtendParams& p, const Split
 // prefix pass; SX: shared-prefix extend; WIN: a window with sink tokens; BSC:
 // fp8 codes with scales per block and kv head; CL: key tiles split over a
 // cluster; TAKE: items taken as they come (DYN), from blocks counted by the
-// length hint (1) or by rows (2).
-template <int HD, int CT, int AT, bool PP, bool SX, bool WIN, bool BSC, bool CL, int TAKE>
+// length hint (1) or by rows (2); HALF: both tiles hold the same rows and half of
+// each key tile.
+template <int HD, int CT, int AT, bool PP, bool SX, bool WIN, bool BSC, bool CL, int TAKE, bool HALF>
 __global__ void __launch_bounds__(NTHREADS, 1)
 extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
               const ExtendParams p, const ExtendPartialParams pp) {
   constexpr bool DYN = TAKE != 0;
+  static_assert(!HALF || CL, "half tiles are combined as parts");
+  constexpr int SN = HALF ? BN / 2 : BN;  // keys of a key tile that one row tile takes
   static_assert(!((WIN || BSC || CL || DYN) && (PP || SX)) && !(CL && DYN) && (!BSC || CT == DT_E4M3),
                 "unsupported combination");
   using C = ExtCfg<HD, CT, AT>;
@@ -918,8 +929,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const ItemRaw raw = nxt_raw;
       if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
       typename ItemOf<WIN, CL>::T it;
-      if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
-      const int i0x = it.i0 + x * TOK;  // first token of this tile
+      if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
+      const int i0x = it.i0 + (HALF ? 0 : x * TOK);  // first token of this tile
       // a row's last visible key is kdiag + its token (prefix pass: the chunk's
       // last key for all)
       const int kdiag = PP ? it.kv_total - 1 : it.P + i0x;
@@ -939,7 +950,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int kt = 0; kt < it.T; ++kt, ++n, seg_advance<SX>(p, it, si)) {
         if (!mbar_wait(bar(C::B_SDONE + x), n & 1)) { ok = false; break; }
         tc_fence_after();
-        const int key0 = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, CL>(it, kt);
+        const int key0 = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, CL>(it, kt) + (HALF ? x * SN : 0);
         // keys key0 .. key0 + nvis of the tile are visible to this row
         int nvis;
         bool masked;
@@ -951,10 +962,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           masked = __any_sync(0xFFFFFFFFu, nvis < BN - 1);
         } else {
           nvis = kdiag + (PP ? 0 : rtok) - key0;
-          masked = key0 + BN - 1 > kdiag;
+          masked = key0 + SN - 1 > kdiag;
           // WIN: or some row's window starts after the tile's first key, in
           // a tile that is not all sink keys
-          if (WIN) masked |= key0 <= kdiag + TOK - 1 - p.window && key0 + BN > p.sink_tokens;
+          if (WIN) masked |= key0 <= kdiag + TOK - 1 - p.window && key0 + SN > p.sink_tokens;
         }
         // WIN: bit q set where key 32 c + q of the tile is visible to this row
         auto win_bits = [&](int c) -> uint32_t {
@@ -974,7 +985,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const uint32_t ninf = __float_as_uint(-INFINITY);
         if (!kRegMask && masked) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < SN / 32; ++c) {
             uint32_t t[32];
             tmem_ld32(srow + c * 32, t);
             tmem_wait_ld();
@@ -992,13 +1003,13 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           tmem_wait_st();
         }
         // the whole S row: four 32-column loads, one wait
-        uint32_t sr[4][32];
+        uint32_t sr[SN / 32][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(srow + c * 32, sr[c]);
+        for (int c = 0; c < SN / 32; ++c) tmem_ld32(srow + c * 32, sr[c]);
         tmem_wait_ld();
         if (kRegMask && masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < SN / 32; ++c) {
             const uint32_t wb = WIN ? win_bits(c) : 0u;
 #pragma unroll
             for (int q = 0; q < 32; ++q)
@@ -1010,7 +1021,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         float sg[8];
         if constexpr (BSC) {
           const float4* ks4 = reinterpret_cast<const float4*>(kscale + (n % C::NSC) * 8);
-          const float4 ka = ks4[0], kb = ks4[1];
+          const float4 ka = ks4[HALF ? x : 0], kb = ks4[1];  // HALF: four groups
           const float kk[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
           for (int a = 0; a < 8; ++a) sg[a] = fmaxf(kk[a] * p.scale_log2, 1.17549435e-38f);
@@ -1021,7 +1032,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
         for (int a = 0; a < 8; ++a) mx[a] = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < SN / 32; ++c)
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             const int a = BSC ? 2 * c + (q >> 3) : q & 7;
@@ -1062,7 +1073,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         const float2 nm2 = make_float2(-m_base, -m_base);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < SN / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
@@ -1192,16 +1203,17 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // the item once more, whether or not the CTA has a key tile of it (kept
       // through the key loop it would take the registers of that loop)
       SplitItem fin;
-      derive_any<PP, SX, WIN, CL>(p, item0, load_raw<SX>(p, item0), fin);
+      derive_any<PP, SX, WIN, CL, HALF>(p, item0, load_raw<SX>(p, item0), fin);
       // every CTA of the cluster is done with its rings: the rows go to the CTA
       // that combines them, unnormalised, with their (max, sum)
       cluster_sync();
       // (row R to CTA R mod splits; 32 columns of the warp's rows at a time
       // through shared memory, so that eight lanes write 128 bytes of a row: a
       // row per lane took 3 to 6 us more)
-      const uint32_t sh = 31 - __clz(p.splits), share = (2 * BM) >> sh, row = x * BM + r;
-      const uint32_t rank = cluster_rank(), cmask = p.splits - 1;
-      cluster_st2(cluster_map(s_base + C::OFF_Q + (rank * share + (row >> sh)) * 8, row & cmask),
+      const uint32_t sh = 31 - __clz(p.splits), share = (HALF ? BM : 2 * BM) >> sh;
+      const uint32_t xrow = HALF ? 0u : x * BM, row = xrow + r, cmask = p.splits - 1;
+      const uint32_t part = HALF ? cluster_rank() * 2 + x : cluster_rank();
+      cluster_st2(cluster_map(s_base + C::OFF_Q + (part * share + (row >> sh)) * 8, row & cmask),
                   make_float2(m_fin, l_fin));
       const uint32_t send = __ballot_sync(0xFFFFFFFFu, m_fin != -INFINITY && rtok < fin.ntok[x]);
       if (send != 0u) {
@@ -1220,9 +1232,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           for (int k = 0; k < 8; ++k) {
             const int rr = 4 * k + (lane >> 3), u = lane & 7;
             if ((send >> rr) & 1u) {
-              const uint32_t R = x * BM + qw * 32 + rr;
+              const uint32_t R = xrow + qw * 32 + rr;
               const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * 128 + ((u ^ (rr & 7)) << 4));
-              cluster_st4(cluster_map(s_base + C::OFF_CO + (rank * share + (R >> sh)) * (HD * 4) + c * 128 + u * 16,
+              cluster_st4(cluster_map(s_base + C::OFF_CO + (part * share + (R >> sh)) * (HD * 4) + c * 128 + u * 16,
                                       R & cmask),
                           v.x, v.y, v.z, v.w);
             }
@@ -1232,8 +1244,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
       tc_fence_before();
       cluster_sync();
-      combine_parts<HD, AT, WIN>(p, fin, smem + C::OFF_CO,
-                                 reinterpret_cast<float2*>(smem + C::OFF_Q), row);
+      combine_parts<HD, AT, HALF>(p, fin, smem + C::OFF_CO,
+                                  reinterpret_cast<float2*>(smem + C::OFF_Q), x * BM + r);
     }
   } else if (warp < 4) {
     regs_dec<kRegsProd>();
@@ -1265,7 +1277,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             mbar_arrive_expect_tx(fb, qbytes);
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c)
-              tma_load_3d(dst + c * CHUNK, &qmap, fb, c * 64, it.g * G, it.row0 + it.i0 + xq * TOK);
+              tma_load_3d(dst + c * CHUNK, &qmap, fb, c * 64, it.g * G,
+                          it.row0 + it.i0 + (HALF ? 0 : xq * TOK));
           }
         }
         return __shfl_sync(0xFFFFFFFFu, good, 0) != 0;
@@ -1308,7 +1321,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           nxt = item_of(blk);
           raw = load_raw<SX>(p, nxt);
           typename ItemOf<WIN, CL>::T it;
-          more = nxt >= p.num_items || !derive_any<PP, SX, WIN, CL>(p, nxt, raw, it);
+          more = nxt >= p.num_items || !derive_any<PP, SX, WIN, CL, HALF>(p, nxt, raw, it);
         }
         if (use > 0 && !mbar_wait(sbar(C::B_ITAKEN + slot), (use - 1) & 1)) ok = false;
         if (ok) {
@@ -1326,7 +1339,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
-        if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
+        if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
         if (is_k && !load_q(it, j, 0)) { ok = false; break; }
         SegIter si;
         seg_begin<SX>(p, it, si);
@@ -1430,7 +1443,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
-        if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
+        if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
         const uint32_t stg = s_base + C::OFF_Q + ((2 * js + 1) % NQB) * C::T16;
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
@@ -1461,7 +1474,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // O_A += P_A(n-1) V(n-1), S_A(n), O_B += P_B(n-1) V(n-1), S_B(n): each
       // S_x(n) overwrites P_x(n-1) after the PV that reads it.
       constexpr uint32_t qk_fmt = C::QK_BF16 ? 1u : 0u;
-      constexpr uint32_t idesc_qk = umma_idesc_f16(qk_fmt, qk_fmt, BM, BN);
+      constexpr uint32_t idesc_qk = umma_idesc_f16(qk_fmt, qk_fmt, BM, SN);
       constexpr uint32_t idesc_pv = umma_idesc_f16(0u, 0u, BM, HD) | (1u << 16);
       // K is ready for the MMA once loaded, or, for fp8 codes, once widened;
       // Q once loaded, or once converted to f16
@@ -1474,10 +1487,12 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (xx == 0 && !mbar_wait(bar(C::B_VCONV + u % NST), (u / NST) & 1)) return false;
         if (first && ju >= 1 && !mbar_wait(bar(C::B_OFREE + xx), (ju - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t vdesc = umma_desc_sw128_mn(s_base + C::OFF_V + (u % NST) * C::T16, CHUNK);
+        // (HALF: keys 64 xx .. of the tile, 128 bytes a key row)
+        const uint64_t vdesc =
+            umma_desc_sw128_mn(s_base + C::OFF_V + (u % NST) * C::T16 + (HALF ? xx * SN * 128 : 0), CHUNK);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
+          for (int kk = 0; kk < SN / 16; ++kk)
             umma_f16_ts(tmem + tm_o<HD>(xx), tmem + tm_s(xx) + kk * 8, vdesc + (uint64_t)(kk * 2048 >> 4),
                         idesc_pv, (!first || kk > 0) ? 1u : 0u);
         }
@@ -1485,7 +1500,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         return true;
       };
       auto issue_qk = [&](int xx, int nn, int qbuf) {
-        const uint64_t kdesc = umma_desc_sw128(s_base + C::OFF_K + (nn % NST) * C::T16);
+        const uint64_t kdesc =
+            umma_desc_sw128(s_base + C::OFF_K + (nn % NST) * C::T16 + (HALF ? xx * SN * 128 : 0));
         const uint64_t qdesc = umma_desc_sw128(s_base + C::OFF_Q + qbuf * C::T16);
         if (elect_one()) {
 #pragma unroll
@@ -1509,7 +1525,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
-        if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
+        if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
         const int qa = (2 * j) % NQB, qb = (2 * j + 1) % NQB;
         for (int kt = 0; kt < it.T; ++kt, ++n) {
           if constexpr (C::FP8 && HD == 128) {
@@ -1590,7 +1606,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
-        if (!derive_any<PP, SX, WIN, CL>(p, item, raw, it)) continue;
+        if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
         SegIter si;
         seg_begin<SX>(p, it, si);
         for (int kt = 0; kt < it.T; ++kt, ++n, seg_advance<SX>(p, it, si)) {
@@ -1671,7 +1687,7 @@ template <int HD, int CT, int AT, bool PP, bool SX, bool WIN = false, bool BSC =
 cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                             const CUtensorMap& omap, const ExtendParams& p,
                             const ExtendPartialParams& pp, cudaStream_t stream) {
-  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN, BSC, false, TAKE>;
+  auto k = extend_kernel<HD, CT, AT, PP, SX, WIN, BSC, false, TAKE, false>;
   using C = ExtCfg<HD, CT, AT>;
   constexpr bool DYN = TAKE != 0;
   constexpr int smem = DYN ? C::SMEM_DYN : BSC ? C::SMEM_BSC : C::SMEM;
@@ -1695,11 +1711,11 @@ cudaError_t launch_extend_view_t(const CUtensorMap& kmap, const CUtensorMap& vma
 }
 
 // One item per cluster of p.splits CTAs (1, 2, 4 or 8), its key tiles split over them.
-template <int HD, int CT, int AT, bool WIN, bool BSC>
+template <int HD, int CT, int AT, bool WIN, bool BSC, bool HALF>
 cudaError_t launch_extend_split_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                   const CUtensorMap& qmap, const CUtensorMap& omap,
                                   const ExtendParams& p, cudaStream_t stream) {
-  auto k = extend_kernel<HD, CT, AT, false, false, WIN, BSC, true, 0>;
+  auto k = extend_kernel<HD, CT, AT, false, false, WIN, BSC, true, 0, HALF>;
   constexpr int smem = BSC ? ExtCfg<HD, CT, AT>::SMEM_BSC : ExtCfg<HD, CT, AT>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

@@ -37,6 +37,7 @@ cudaError_t launch_extend_view(const CUtensorMap& kmap, const CUtensorMap& vmap,
       p.sink_tokens < 0)
     return cudaErrorInvalidValue;
   if (p.k_scales && (!p.v_scales || cache_dt != DT_E4M3)) return cudaErrorInvalidValue;
+  if (p.half) return launch_extend_half(kmap, vmap, qmap, omap, p, head_dim, cache_dt, act_dt, stream);
   if (p.splits > 1)
     return launch_extend_split(kmap, vmap, qmap, omap, p, head_dim, cache_dt, act_dt, stream);
   if (p.by_rows)

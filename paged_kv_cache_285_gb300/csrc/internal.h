@@ -231,6 +231,7 @@ struct ExtendParams {
   const float* k_scales;  // block-scaled launches: [num_blocks][num_kv_heads]
   const float* v_scales;
   int splits;           // split launches: CTAs per item (its key tiles split over them)
+  int half;             // half tiles: every request's rows fit one row tile
   // window / block-scaled launches that take items as they come: blocks of the
   // grid, one per item, or (by_rows) num_kv_heads x num_units, units being
   // total_rows / (2 tok) + batch candidates for pairs of row tiles
@@ -311,6 +312,10 @@ cudaError_t launch_extend_shared(const CUtensorMap& kmap, const CUtensorMap& vma
 // scales per block and kv head (p.k_scales, p.v_scales; read as codes), or
 // both; p.splits > 1: the key tiles of every item split over a cluster of CTAs.
 cudaError_t launch_extend_view(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const CUtensorMap& qmap, const CUtensorMap& omap,
+                               const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
+                               cudaStream_t stream);
+cudaError_t launch_extend_half(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const CUtensorMap& qmap, const CUtensorMap& omap,
                                const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
                                cudaStream_t stream);

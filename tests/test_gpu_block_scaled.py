@@ -281,6 +281,20 @@ def test_extend_regimes(cfg, d, bs, act):
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d,bs,act", [(8, 2, 128, 16, BF16), (5, 1, 64, 32, F16), (2, 2, 64, 16, BF16),
+                                             (12, 1, 128, 32, F16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 5)])
+def test_extend_of_few_rows(hq, hkv, d, bs, act, window, sinks):
+    # requests whose rows fit one row tile, alone and many, over short and long prefixes
+    for rows, prefix in (([1, 5, 0, 9], [300, 0, 17, 640]), ([10], [1500]), ([3] * 12, list(range(0, 480, 40)))):
+        c = Case(SCALED, act, hkv, d, bs, [p + n for p, n in zip(prefix, rows)], seed=sum(rows)).cuda()
+        q = c.rows(sum(rows), hq).cuda()
+        ref = R.attention(*c.values(), to_f64(q), indptr(rows), prefix, c.tables, hq, 1 / d ** 0.5, window, sinks)
+        out, lse = run_extend(c, q, hq, rows, prefix, window, sinks, None)
+        check_attention(out, lse, ref, act, d, f"{rows} {window}")
+    assert pkv.get_device_error() == 0
+
+
 @pytest.mark.parametrize("d,bs,act", [(64, 32, F16), (128, 16, BF16)])
 def test_extend_of_more_items_than_sms(d, bs, act):
     # widened pages (the workspace given) and codes; rows from none to many, several items per SM

@@ -169,6 +169,27 @@ def test_extend_of_more_items_than_sms(cache, act, d):
     assert pkv.get_device_error() == 0
 
 
+FEW = [
+    # cache, act, hq, hkv, d, bs: requests whose rows fit one row tile (128 / group tokens)
+    (BF16, BF16, 8, 2, 128, 16), (F16, F16, 3, 1, 64, 32), (E4M3, BF16, 2, 2, 128, 32), (E4M3, F16, 24, 2, 64, 16),
+]
+
+
+@pytest.mark.parametrize("cfg", FEW, ids=lambda c: f"c{c[0]}a{c[1]}h{c[2]}x{c[3]}d{c[4]}bs{c[5]}")
+@pytest.mark.parametrize("window,sinks", [(1, 0), (64, 1), (70, 130), (300, 0), (5000, 7)])
+def test_extend_of_few_rows(cfg, window, sinks):
+    cache, act, hq, hkv, d, bs = cfg
+    for rows, prefix in (([1, 5, 0, 9], [300, 0, 17, 640]), ([10], [1500]), ([3] * 12, list(range(0, 480, 40)))):
+        c = Case(cache, act, hkv, d, bs, [p + n for p, n in zip(prefix, rows)], seed=sum(rows) + window)
+        q = c.rows(sum(rows), hq).cuda()
+        give_back(c, prefix, window, sinks)
+        c.cuda()
+        out, lse = run_extend(c, q, hq, rows, prefix, window, sinks)
+        assert pkv.get_device_error() == 0
+        ref = R.attention(*c.values(), to_f64(q), indptr(rows), prefix, c.tables, hq, 1 / d ** 0.5, window, sinks)
+        check_attention(out, lse, ref, act, d, f"{cfg} {window} {sinks} {rows}")
+
+
 @pytest.mark.parametrize("at", [0, 37, 69])
 def test_extend_of_a_prompt_among_single_tokens(at):
     # one long request among many of a row or none: blocks are counted by rows
