@@ -613,7 +613,7 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   bool best_cluster = false;
   // at most about two rounds of CTAs beyond one per item, of 64 tokens at least
   const int most = (int)std::min<double>(std::max(1, tiles / 4), 2.0 * slots / items + 8.0);
-  for (int s = 1; s <= most; ++s) {
+  for (int s = 1; s <= most; s += s < 16 ? 1 : s / 8) {
     const int chunk = ceil_div(tiles, s);
     if (s > 1 && ceil_div(tiles, chunk) != s) continue;  // the same plan as a smaller s
     const double tokens = 16.0 * chunk;

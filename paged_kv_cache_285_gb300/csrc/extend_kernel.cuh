@@ -846,8 +846,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     prefetch_tensormap(&vmap);
     prefetch_tensormap(&qmap);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(bar(C::B_KFULL + i), 1);
-      mbar_init(bar(C::B_VFULL + i), 1);
+      mbar_init(bar(C::B_KFULL + i), BSC ? 2 : 1);  // BSC: the copy, and the tile's scales
+      mbar_init(bar(C::B_VFULL + i), BSC ? 2 : 1);
       mbar_init(bar(C::B_KCONV + i), NCONV / 32);
       mbar_init(bar(C::B_VCONV + i), NCONV / 32);
       mbar_init(bar(C::B_KFREE + i), 1);
@@ -1388,11 +1388,6 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
           for (int q = 0; q < 8; ++q) pg[q] = __shfl_sync(0xFFFFFFFFu, cur, (st & 3) * 8 + q);
           if (n >= NST && !mbar_wait(bar(free0 + s), (uint32_t)((n / NST - 1) & 1))) { ok = false; break; }
-          if constexpr (BSC) {
-            // the tile's eight scales, ordered before its barrier completes
-            if ((lane >> 3) == (st & 3)) (is_k ? kscale : vscale)[(n % C::NSC) * 8 + (lane & 7)] = scale_cur;
-            __syncwarp();
-          }
           if (lane == 0) {
             const uint32_t fb = bar(full0 + s);
             if constexpr (C::FP8) {
@@ -1415,6 +1410,13 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                   tma_load_3d(dst + c * CHUNK + q * 2048, map, fb, c * 64, rip, pg[q]);
               }
             }
+          }
+          if constexpr (BSC) {
+            // the tile's eight scales (after the copy is under way: the first
+            // tile's are still being loaded)
+            if ((lane >> 3) == (st & 3)) (is_k ? kscale : vscale)[(n % C::NSC) * 8 + (lane & 7)] = scale_cur;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(full0 + s));
           }
           if constexpr (DYN) {
             if (is_k && !asked && kt >= it.T - 3) ask();
