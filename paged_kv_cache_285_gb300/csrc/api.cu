@@ -591,13 +591,14 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
 // four CTAs fit an SM): a CTA alone goes through r1 tokens per us (100 at 128
 // dims, 160 at 64: the latency of its four warps' tiles), an SM through its
 // share of the bandwidth, whatever its CTAs.  A launch costs its full rounds of
-// CTAs, then the last round (2.5 more each), and a fixed part: 5, 6 for splits
+// CTAs, then the last round (5.5 more each), and a fixed part: 5, 7 for splits
 // joined in a cluster, 8 with a merge launch (and more for long rows of
 // partials).  Under a window the sequences are taken as all of the bound's
-// length, else half as that, half as spread evenly up to it.  Measured against plain runs of 128 to 4,096 tokens aimed at
-// six rounds: block-scaled, 16 x 4,096 tokens 39.2 -> 31, 1 x 100,000 69 -> 45,
-// 128 x 100-300 tokens 27.5 -> 21; windows: 32 x 1,024 (bf16) 37.6 -> 26.8,
-// 128 x 4,096 (fp8) 179 -> 169.
+// length, else for a third as that, for the rest as spread evenly up to it.
+// Against the plain plan's runs (128 to 4,096 tokens, six rounds): block-scaled,
+// 16 x 4,096 tokens 39 -> 31 us, 8 x 5,000-20,000 50 -> 47, 1 x 100,000 69 -> 45,
+// 128 x 100-300 27.5 -> 21; windows: 32 x 1,024 (bf16) 37.6 -> 26.7, 128 x 4,096
+// (fp8) 179 -> 168.
 static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_seq_len, int window,
                             int sink_tokens, int forced, int sm_count) {
   const int len = visible_bound(max_seq_len, window, sink_tokens);
@@ -618,17 +619,17 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
     if (s > 1 && ceil_div(tiles, chunk) != s) continue;  // the same plan as a smaller s
     const double tokens = 16.0 * chunk;
     const double ctas = items * s, full = std::floor(ctas / slots), rest = ctas - full * slots;
-    double cost = full * (tokens * 4 / sm_rate + 2.5);
-    if (rest > 0) cost += tokens / std::min(r1, sm_rate / std::ceil(rest / sms)) + 2.5;
+    double cost = full * (tokens * 4 / sm_rate + 5.5);
+    if (rest > 0) cost += tokens / std::min(r1, sm_rate / std::ceil(rest / sms)) + 5.5;
     if (window <= 0) {
       const double some = items * (s + 1) * 0.5, k = std::min(4.0, std::ceil(some / sms));
       const double one = tokens / std::min(r1, sm_rate / k);
       const double spread = std::max(one, items * len * 0.5 / (sm_rate * sms) + 0.5 * one) +
                             2.0 * some / slots;
-      cost = 0.5 * (cost + spread);
+      cost = 0.35 * cost + 0.65 * spread;
     }
     const bool cl = s >= 2 && s <= 8 && (s & (s - 1)) == 0 && items * s <= 0.75 * slots;
-    cost += s == 1 ? 5.0 : cl ? 6.0 : 8.0 + 0.2 * std::max(0, s - 8);
+    cost += s == 1 ? 5.0 : cl ? 7.0 : 8.0 + 0.2 * std::max(0, s - 8);
     if (cost < best) {
       best = cost;
       best_s = s;
