@@ -332,7 +332,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   if (threadIdx.x == 0) {
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
-    for (int i = 0; i < NW * NS; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    // BSC: two arrivals, the copies and the tile's scales
+    for (int i = 0; i < NW * NS; ++i) mbar_init(smem_u32(&bars[i]), BSC ? 2 : 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -431,14 +432,16 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       tma_load_3d(vdst + ch * kSubTokens * C::CHUNKB, &vmap, bar, ch * (C::CHUNKB / C::ELEM), row, page);
   };
 
+  auto give_scales = [&](int i) {  // BSC: in place before the stage's barrier completes
+    if (lane == (i & 31)) {
+      wscale[i % NS] = sc_cur;
+      mbar_arrive(wbar_s + 8 * (i % NS));
+    }
+  };
   auto load_tile = [&](int i) {  // the whole warp
     if constexpr (BSC) {
-      // the scales are in place before the stage's barrier can complete
       window_of(i);
-      if (lane == (i & 31)) {
-        wscale[i % NS] = sc_cur;
-        issue(i, bw_cur);
-      }
+      if (lane == (i & 31)) issue(i, bw_cur);
     } else {
       const int blk = blk_of(i);
       if (lane == 0) issue(i, blk);
@@ -448,6 +451,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   {
     const int pre = cnt < NS ? cnt : NS;
     for (int i = 0; i < pre; ++i) load_tile(i);
+    // (the first copies do not wait for the scales, one more dependent load)
+    if constexpr (BSC)
+      for (int i = 0; i < pre; ++i) give_scales(i);
   }
 
   float acc[C::MT][4];
@@ -651,8 +657,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               a[3] = e4m3x2_to_f16x2(e ? (r[3] >> 16) : (r[3] & 0xFFFFu));
             }
             if constexpr (BSC) {
-              float pv[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816<false>(pv, a, bh0, bh1);
+              float pv[4];
+              mma16816_f16_zero(pv, a, bh0, bh1);
 #pragma unroll
               for (int q4 = 0; q4 < 4; ++q4)
                 acc[2 * pp + e][q4] = fmaf(pv[q4], bsc.y, acc[2 * pp + e][q4]);
@@ -665,7 +671,10 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
 
     __syncwarp();
-    if (i + NS < cnt) load_tile(i + NS);
+    if (i + NS < cnt) {
+      load_tile(i + NS);
+      if constexpr (BSC) give_scales(i + NS);
+    }
   }
 
   if (timed_out) {
