@@ -710,7 +710,10 @@ __device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, cons
     it.rows = false;
     if (!derive<PP, SX, WIN>(p, item, r, it)) return false;
     it.rows = true;
-    if constexpr (HALF) it.ntok[1] = it.ntok[0];
+    if constexpr (HALF) {
+      it.ntok[1] = it.ntok[0];
+      if (it.S > p.tok) set_err(p.err, 3);  // rows beyond the length hint
+    }
     const int per = (it.T + p.splits - 1) / p.splits;
     it.kt0 = (int)cluster_rank() * per;
     it.T = min(per, it.T - it.kt0);

@@ -190,6 +190,23 @@ def test_extend_of_few_rows(cfg, window, sinks):
         check_attention(out, lse, ref, act, d, f"{cfg} {window} {sinks} {rows}")
 
 
+@pytest.mark.parametrize("rows,hint", [(40, 20), (200, 20), (200, 64), (3, 2)])
+def test_extend_reports_rows_beyond_the_hint(rows, hint):
+    # 4 heads per kv head: row tiles of 32 tokens.  Rows beyond the hint are reported or computed,
+    # never left out silently; the other request is computed
+    c = Case(BF16, BF16, 1, 64, 16, [10 + rows, 60], seed=14).cuda()
+    q = c.rows(rows + 2, 4).cuda()
+    out = torch.full_like(q, float("nan"))
+    pkv.paged_extend_attn_window(c.k, c.v, q, out, ints([0, rows, rows + 2]), ints([10, 58]), c.bt, 0.125, hint,
+                                 10 + rows, 30, 2)
+    err = pkv.get_device_error()
+    done = ~torch.isnan(out).any(-1).any(-1)
+    assert bool(done[:hint].all()) and bool(done[rows:].all())
+    assert err == (0 if bool(done.all()) else 3)
+    ref = R.attention(*c.values(), to_f64(q), [0, rows, rows + 2], [10, 58], c.tables, 4, 0.125, 30, 2)[0]
+    assert np.abs(to_f64(out) - ref)[done.cpu().numpy()].max() < 0.05
+
+
 @pytest.mark.parametrize("at", [0, 37, 69])
 def test_extend_of_a_prompt_among_single_tokens(at):
     # one long request among many of a row or none: blocks are counted by rows
