@@ -295,6 +295,22 @@ def test_extend_of_few_rows(hq, hkv, d, bs, act, window, sinks):
     assert pkv.get_device_error() == 0
 
 
+# requests of different lengths, few enough to fit the GPU at once: the long ones are split
+UNEVEN = [([70, 3, 40, 0, 1], [900, 10, 300, 77, 1500]), ([1, 90], [2000, 0]), ([33] * 9, [1000] * 9),
+          ([2, 100, 5] + [1] * 30, [800, 790, 0] + [50] * 30)]
+
+
+@pytest.mark.parametrize("rows,prefix", UNEVEN, ids=lambda v: f"{len(v)}x{max(v)}")
+@pytest.mark.parametrize("d,bs,act,window,sinks", [(64, 32, F16, 0, 0), (128, 16, BF16, 0, 0), (128, 16, BF16, 850, 9)])
+def test_extend_of_uneven_requests(rows, prefix, d, bs, act, window, sinks):
+    c = Case(SCALED, act, 2, d, bs, [p + n for p, n in zip(prefix, rows)], seed=sum(rows)).cuda()
+    q = c.rows(sum(rows), 8).cuda()
+    ref = R.attention(*c.values(), to_f64(q), indptr(rows), prefix, c.tables, 8, 1 / d ** 0.5, window, sinks)
+    out, lse = run_extend(c, q, 8, rows, prefix, window, sinks, None)
+    check_attention(out, lse, ref, act, d)
+    assert pkv.get_device_error() == 0
+
+
 @pytest.mark.parametrize("d,bs,act", [(64, 32, F16), (128, 16, BF16)])
 def test_extend_of_more_items_than_sms(d, bs, act):
     # widened pages (the workspace given) and codes; rows from none to many, several items per SM
