@@ -339,6 +339,7 @@ def run_decode_bench(args, world, rank, local):
     }
     traffic = profiled_traffic("decode_kernel_llama3_8b_layer.md",
                                ["paged_kv_cache_285_gb300/csrc/decode.cu",
+                                "paged_kv_cache_285_gb300/csrc/decode_kernel.cuh",
                                 "paged_kv_cache_285_gb300/csrc/ptx.cuh",
                                 "paged_kv_cache_285_gb300/csrc/internal.h"
                                 "#DecodeParams,DecodeExtraParams"]) \
@@ -669,6 +670,7 @@ def run_extend_bench(args, dev, bf16, bf16_sus, peak_src):
                         "traffic": profiled_traffic(
                             "extend_kernel_shared_prefix_extend.md",
                             ["paged_kv_cache_285_gb300/csrc/extend.cu",
+                             "paged_kv_cache_285_gb300/csrc/extend_kernel.cuh",
                              "paged_kv_cache_285_gb300/csrc/ptx.cuh",
                              "paged_kv_cache_285_gb300/csrc/tcgen05.cuh",
                              "paged_kv_cache_285_gb300/csrc/internal.h"
@@ -678,7 +680,8 @@ def run_extend_bench(args, dev, bf16, bf16_sus, peak_src):
         # the widened kernel's DRAM bytes per launch (the widening pass not included)
         ww["traffic"] = profiled_traffic(
             "extend_kernel_shared_prefix_extend.md",
-            ["paged_kv_cache_285_gb300/csrc/extend.cu", "paged_kv_cache_285_gb300/csrc/ptx.cuh",
+            ["paged_kv_cache_285_gb300/csrc/extend.cu",
+             "paged_kv_cache_285_gb300/csrc/extend_kernel.cuh", "paged_kv_cache_285_gb300/csrc/ptx.cuh",
              "paged_kv_cache_285_gb300/csrc/tcgen05.cuh",
              "paged_kv_cache_285_gb300/csrc/internal.h#ExtendParams,ExtendPartialParams,FastDiv"],
             key="dram_bytes_per_launch_workspace")
@@ -757,7 +760,8 @@ def run_extend_bench(args, dev, bf16, bf16_sus, peak_src):
             "frac_of_nominal": ww["frac_of_nominal"], "nominal_peak": NOMINAL_BF16_TFLOPS,
             "traffic": profiled_traffic(
                 "extend_kernel_shared_prefix_extend.md",
-                ["paged_kv_cache_285_gb300/csrc/extend.cu", "paged_kv_cache_285_gb300/csrc/ptx.cuh",
+                ["paged_kv_cache_285_gb300/csrc/extend.cu",
+             "paged_kv_cache_285_gb300/csrc/extend_kernel.cuh", "paged_kv_cache_285_gb300/csrc/ptx.cuh",
                  "paged_kv_cache_285_gb300/csrc/tcgen05.cuh",
                  "paged_kv_cache_285_gb300/csrc/internal.h#ExtendParams,ExtendPartialParams,FastDiv"],
                 key="dram_bytes_per_launch_shared_prefix_workspace")}

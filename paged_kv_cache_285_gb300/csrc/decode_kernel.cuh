@@ -34,13 +34,17 @@
 //     that hold a visible token are numbered without the gap between the two
 //     runs; splits, pipelines and merges work on that numbering, so that the
 //     hidden tiles (and their block ids) are never read, and hidden tokens of
-//     the tiles at a run's edge are masked (score -inf, V zeroed).
+//     the tiles at a run's edge are masked (score -inf, V zeroed).  128 requests
+//     of 1,000-32,000 tokens in a window of 4,096 with 64 sinks (fp8, 64 / 8
+//     heads): 167 us = 6.38 TB/s, 94 % of the measured copy.
 //   * scales per block and kv head (BSC, fp8 codes): a 16-token tile lies in
 //     one block, so its K scale multiplies the tile's scores and its V scale
 //     the tile's PV product as it is added to the fp32 accumulators
 //     (O = al O + s_v (V^T P^T)): scales of any size keep P in f16's range.
 //     The lane that holds a tile's block id holds its scales too, issues the
-//     tile's copies and leaves the scales in the stage's slot.
+//     tile's copies and leaves the scales in the stage's slot.  64 requests of
+//     512-4,096 tokens: 64 us = 4.8 TB/s, 71 % (the scales of one tensor: 61 us):
+//     bound by the latency of the CTAs' first tiles and by their uneven ends.
 //   * splits joined in a cluster (CLM, few requests): the splits of one (request,
 //     head chunk) are the CTAs of a cluster.  Each leaves its heads' (max, sum,
 //     unnormalised O) in shared memory, and after a cluster barrier each adds up
