@@ -32,6 +32,7 @@ import ctypes
 import functools
 import os
 import threading
+import warnings
 
 import torch
 
@@ -52,6 +53,7 @@ NO_SPACE = 5  # PKV_ERR_NO_SPACE
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libpkv.so")
 _lib = None
+_direct = None  # _calls.so, the compiled binding of the small calls (set by load())
 _lock = threading.Lock()
 
 
@@ -81,7 +83,7 @@ def lib_path() -> str:
 
 def load():
     """Load libpkv.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _direct
     with _lock:
         if _lib is not None:
             return _lib
@@ -175,6 +177,13 @@ def load():
         lib.pkv_radix_evict.restype = ctypes.c_int
         lib.pkv_radix_stats.argtypes = [VP, ctypes.POINTER(RadixStats)]
         lib.pkv_radix_stats.restype = ctypes.c_int
+        # Tensors straight to the C ABI: without it (a build for another torch) the same calls
+        # go through ctypes, 5 to 7 us more host time each.
+        try:
+            from . import _calls
+            _direct = _calls
+        except ImportError as e:
+            warnings.warn(f"_calls.so does not load ({e}): rebuild with build.build()")
         _lib = lib
         return lib
 
@@ -626,6 +635,12 @@ def kv_append_block_scaled(k_cache, v_cache, k_scales, v_scales, k_new, v_new, q
     to position prefix_lens[b] + i of request b, quantised with a power-of-two scale per block
     and kv head.  k_scales/v_scales float32 [num_blocks, Hkv]; q_indptr int32 [B+1]; prefix_lens
     int32 [B]; max_suffix_len bounds the rows per request."""
+    if _direct is not None:
+        st = _direct.append_block_scaled(k_cache, v_cache, k_scales, v_scales, k_new, v_new,
+                                         q_indptr, prefix_lens, block_tables, max_suffix_len,
+                                         stream)
+        if st is not None:
+            return _check(st, "pkv_kv_append_block_scaled")
     desc, kc, vc, pages, d, dev = _pools(k_cache, v_cache, 1.0, 1.0)
     ks = _arg("k_scales", k_scales, pages, torch.float32, dev)
     vs = _arg("v_scales", v_scales, pages, torch.float32, dev)
@@ -644,6 +659,11 @@ def kv_gather(k_cache, v_cache, k_out, v_out, row_indptr, start_positions, block
     """pkv_kv_gather: rows row_indptr[b] .. row_indptr[b+1]-1 of k_out/v_out [rows, Hkv, D] (f16
     or bf16) are positions start_positions[b] ... of request b.  k_scale/v_scale: an fp8 cache's
     scales per tensor; k_scales/v_scales float32 [num_blocks, Hkv]: scales per block and head."""
+    if _direct is not None:
+        st = _direct.gather(k_cache, v_cache, k_out, v_out, row_indptr, start_positions,
+                            block_tables, k_scale, v_scale, k_scales, v_scales, stream)
+        if st is not None:
+            return _check(st, "pkv_kv_gather")
     desc, kc, vc, pages, d, dev = _pools(k_cache, v_cache, k_scale, v_scale)
     if (k_scales is None) != (v_scales is None):
         raise ValueError("k_scales and v_scales come together")
@@ -689,6 +709,12 @@ def paged_decode_attn_window(k_cache, v_cache, q, out, block_tables, seq_lens, s
     """pkv_paged_decode_attn_window: paged_decode_attn where each request's query sees its last
     `window` tokens and its first `sink_tokens`.  ``workspace`` is a uint8 device tensor of at
     least decode_window_workspace_bytes() bytes."""
+    if _direct is not None:
+        st = _direct.decode_window(k_cache, v_cache, k_scale, v_scale, q, out, block_tables,
+                                   seq_lens, sm_scale, max_seq_len, window, sink_tokens, num_splits,
+                                   lse_out, workspace, stream)
+        if st is not None:
+            return _check(st, "pkv_paged_decode_attn_window")
     desc, kc, vc, _, d, dev = _pools(k_cache, v_cache, k_scale, v_scale)
     qp, op, bt, sl, lse, b, hq, width = _decode_args(q, out, block_tables, seq_lens, lse_out, d, dev)
     ws, ws_bytes = _workspace(workspace, dev)
@@ -703,6 +729,12 @@ def paged_decode_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out,
     """pkv_paged_decode_attn_block_scaled: paged_decode_attn over fp8 codes with k_scales/v_scales
     float32 [num_blocks, Hkv]; window 0: every token, else as paged_decode_attn_window (the same
     workspace)."""
+    if _direct is not None:
+        st = _direct.decode_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out, block_tables,
+                                         seq_lens, sm_scale, max_seq_len, window, sink_tokens,
+                                         num_splits, lse_out, workspace, stream)
+        if st is not None:
+            return _check(st, "pkv_paged_decode_attn_block_scaled")
     desc, kc, vc, pages, d, dev = _pools(k_cache, v_cache, 1.0, 1.0)
     ks = _arg("k_scales", k_scales, pages, torch.float32, dev)
     vs = _arg("v_scales", v_scales, pages, torch.float32, dev)
@@ -729,6 +761,12 @@ def paged_extend_attn_window(k_cache, v_cache, q, out, q_indptr, prefix_lens, bl
                              k_scale=1.0, v_scale=1.0, lse_out=None, workspace=None, stream=None):
     """pkv_paged_extend_attn_window: paged_extend_attn where the row at position p sees keys
     p - window + 1 .. p and the first `sink_tokens`.  workspace: optional, as there."""
+    if _direct is not None:
+        st = _direct.extend_window(k_cache, v_cache, k_scale, v_scale, q, out, q_indptr,
+                                   prefix_lens, block_tables, sm_scale, max_suffix_len,
+                                   max_total_len, window, sink_tokens, lse_out, workspace, stream)
+        if st is not None:
+            return _check(st, "pkv_paged_extend_attn_window")
     desc, kc, vc, _, d, dev = _pools(k_cache, v_cache, k_scale, v_scale)
     qp, op, qi, pl, bt, lse, rows, hq, batch, width = _extend_args(
         q, out, q_indptr, prefix_lens, block_tables, lse_out, d, dev)
@@ -754,6 +792,13 @@ def paged_extend_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out,
     float32 [num_blocks, Hkv]; window 0: every key, else as paged_extend_attn_window.
     workspace: None, or a uint8 device tensor of extend_block_scaled_workspace_bytes() bytes or
     more (calls with many rows per request then widen the pages they read once per block)."""
+    if _direct is not None:
+        st = _direct.extend_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out, q_indptr,
+                                         prefix_lens, block_tables, sm_scale, max_suffix_len,
+                                         max_total_len, window, sink_tokens, lse_out, workspace,
+                                         stream)
+        if st is not None:
+            return _check(st, "pkv_paged_extend_attn_block_scaled")
     desc, kc, vc, pages, d, dev = _pools(k_cache, v_cache, 1.0, 1.0)
     ks = _arg("k_scales", k_scales, pages, torch.float32, dev)
     vs = _arg("v_scales", v_scales, pages, torch.float32, dev)

@@ -1,7 +1,8 @@
 """Build libpkv.so in-tree with nvcc for sm_103a.
 
 Each .cu (and host-only .cpp) under csrc/ is compiled in parallel to an object under _build/, then
-linked (static CUDA runtime) into paged_kv_cache_285_gb300/libpkv.so.
+linked (static CUDA runtime) into paged_kv_cache_285_gb300/libpkv.so.  bind/calls.cpp, the binding
+of the small calls, becomes _calls.so against libpkv.so and the installed torch.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libpkv.so")
+CALLS_SRC = os.path.join(HERE, "bind", "calls.cpp")
+CALLS = os.path.join(HERE, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-diag-suppress", "177",
@@ -47,6 +51,20 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _calls_cmd():
+    """Object, compile command and torch's library folder for the binding; the object's name
+    carries the torch it is compiled for."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    toolkit = os.path.dirname(os.path.dirname(nvcc()))
+    obj = os.path.join(BUILD, f"calls-{torch.__version__}.o")
+    return obj, [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", f"-I{INCLUDE}",
+                 f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include",
+                 f"-I{toolkit}/include", f"-I{sysconfig.get_paths()['include']}",
+                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                 "-c", CALLS_SRC, "-o", obj], os.path.join(root, "lib")
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -59,12 +77,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(obj, [src] + headers):
             jobs.append([cc, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj])
 
+    calls_obj, calls_cmd, torch_lib = _calls_cmd()
+    if force or _stale(calls_obj, [CALLS_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        jobs.append(calls_cmd)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {cmd[-3]}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed on {cmd[-3]}")
 
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
@@ -73,6 +95,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if force or jobs or _stale(CALLS, [calls_obj, LIB]):
+        tmp = CALLS + f".tmp{os.getpid()}"
+        run([shutil.which("g++") or "g++", "-shared", calls_obj, "-o", tmp, f"-L{HERE}",
+             "-l:libpkv.so", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+             "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, CALLS)
     return LIB
 
 

@@ -1,0 +1,170 @@
+"""GPU checks of the compiled binding of the block-scaled, gather and window calls: the same results
+and refusals as through the Python checks, and which arguments it leaves to them."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_285_gb300 as pkv
+from tests.pkv_testlib import BF16
+from tests.scaled_testlib import SCALED, Case, ints
+
+pytestmark = pytest.mark.gpu
+HQ, HKV, D, BS, ROWS, PREFIX = 8, 2, 64, 16, [3, 40], [20, 5]
+NAMES = ["append_block_scaled", "gather", "decode_window", "decode_block_scaled", "extend_window",
+         "extend_block_scaled"]
+
+
+class Calls:
+    """The arguments of one call of each function, over one pair of pools."""
+
+    def __init__(self):
+        total = [p + n for p, n in zip(PREFIX, ROWS)]
+        self.c = c = Case(SCALED, BF16, HKV, D, BS, total, seed=3).cuda()
+        n = sum(ROWS)
+        self.kn, self.vn, self.q = c.rows(n, HKV).cuda(), c.rows(n, HKV).cuda(), c.rows(n, HQ).cuda()
+        self.qd = c.rows(2, HQ).cuda()
+        self.ip, self.at, self.lens = ints([0, 3, 43]), ints(PREFIX), ints(total)
+        self.ri, self.zero = ints([0, total[0], sum(total)]), ints([0, 0])
+        need = pkv.decode_window_workspace_bytes(c.k, 2, HQ, 64, 0, 0, 3)
+        self.ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def args(self, name, **kw):
+        """(function, positional, keyword arguments); kw replaces by name."""
+        c, scale = self.c, D ** -0.5
+        if name == "append_block_scaled":
+            a = dict(k_cache=c.k, v_cache=c.v, k_scales=c.ks, v_scales=c.vs, k_new=self.kn, v_new=self.vn,
+                     q_indptr=self.ip, prefix_lens=self.at, block_tables=c.bt, max_suffix_len=40)
+            fn = pkv.kv_append_block_scaled
+        elif name == "gather":
+            ko = torch.full((sum(PREFIX) + sum(ROWS), HKV, D), 7.0, dtype=self.kn.dtype, device="cuda")
+            a = dict(k_cache=c.k, v_cache=c.v, k_out=ko, v_out=ko.clone(), row_indptr=self.ri,
+                     start_positions=self.zero, block_tables=c.bt, k_scales=c.ks, v_scales=c.vs)
+            fn = pkv.kv_gather
+        else:
+            kind, form = name.split("_", 1)
+            q = self.qd if kind == "decode" else self.q
+            a = dict(k_cache=c.k, v_cache=c.v, q=q, out=torch.full_like(q, 7.0), block_tables=c.bt, sm_scale=scale, window=24,
+                     sink_tokens=2, lse_out=torch.full((q.shape[0], HQ), 7.0, device="cuda"))
+            if kind == "decode":
+                a.update(seq_lens=self.lens, max_seq_len=64, num_splits=3, workspace=self.ws)
+            else:
+                a.update(q_indptr=self.ip, prefix_lens=self.at, max_suffix_len=40, max_total_len=64)
+            a.update(dict(k_scales=c.ks, v_scales=c.vs) if form == "block_scaled" else dict(k_scale=0.5, v_scale=2.0))
+            fn = getattr(pkv, f"paged_{kind}_attn_{form}")
+        a.update(kw)
+        return fn, a
+
+    def run(self, name, **kw):
+        fn, a = self.args(name, **kw)
+        assert fn(**a) is None
+        torch.cuda.synchronize()
+        return [a[x] for x in ("k_cache", "v_cache", "k_scales", "v_scales", "k_out", "v_out", "out", "lse_out") if x in a]
+
+
+class Spy:
+    """Stands before the binding and counts the calls it took and the calls it left."""
+
+    def __init__(self):
+        self.took, self.left = 0, 0
+
+    def __getattr__(self, name):
+        assert name in NAMES
+        fn = getattr(pkv._calls, name)
+
+        def call(*a):
+            st = fn(*a)
+            self.took += st is not None
+            self.left += st is None
+            return st
+        return call
+
+
+@pytest.fixture(params=["compiled", "python"])
+def way(request, monkeypatch):
+    pkv.load()
+    spy = Spy() if request.param == "compiled" else None
+    monkeypatch.setattr(pkv, "_direct", spy)
+    return spy
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8).cpu()
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_the_same_results(name, monkeypatch):
+    pkv.load()
+    got = []
+    for spy in (Spy(), None):
+        monkeypatch.setattr(pkv, "_direct", spy)
+        got.append([bits(t) for t in Calls().run(name)])
+        assert spy is None or (spy.took, spy.left) == (1, 0)
+    assert len(got[0]) == len(got[1]) and all(torch.equal(x, y) for x, y in zip(*got))
+    assert pkv.get_device_error() == 0
+
+
+class Sub(torch.Tensor):
+    pass
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_arguments_of_other_kinds(name, monkeypatch):
+    # what the Python functions convert keeps working, through them
+    pkv.load()
+    calls = Calls()
+    monkeypatch.setattr(pkv, "_direct", None)
+    want = [bits(t) for t in calls.run(name)]
+    spy = Spy()
+    monkeypatch.setattr(pkv, "_direct", spy)
+    _, a = calls.args(name)
+    kinds = [dict(block_tables=a["block_tables"].as_subclass(Sub))]
+    if "window" in a:
+        kinds += [dict(window=np.int32(24)), dict(window=24.0), dict(sm_scale=np.float64(a["sm_scale"]))]
+    if name == "append_block_scaled":
+        kinds += [dict(max_suffix_len=np.int64(40))]
+    for kw in kinds:  # (appending the same rows again changes nothing)
+        assert all(torch.equal(bits(t), w) for t, w in zip(calls.run(name, **kw), want)), kw
+    assert (spy.took, spy.left) == (0, len(kinds))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert all(torch.equal(bits(t), w) for t, w in zip(calls.run(name, stream=side), want))
+    with torch.cuda.stream(side):
+        assert all(torch.equal(bits(t), w) for t, w in zip(calls.run(name), want))
+    assert spy.took == 2 and pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_refusals(name, way):
+    calls = Calls()
+    _, a = calls.args(name)
+    tensors = {k: v for k, v in a.items() if isinstance(v, torch.Tensor)}
+    before = {k: bits(v) for k, v in tensors.items()}
+    bad = []
+    for k, t in tensors.items():
+        what = "cache" if k == "k_cache" else k
+        if k != "k_cache":
+            bad += [(ValueError, k, {k: t.cpu()})]
+        if k == "workspace":
+            bad += [(ValueError, k, {k: t[::2]})]
+            continue
+        bad += [(ValueError, what, {k: t[0]}),
+                ((ValueError, TypeError), "", {k: t.double()}),
+                (ValueError, "contiguous", {k: torch.stack([t, t], -1)[..., 0]})]
+        if t.shape[0] > 1 and k not in ("k_cache", "q", "k_new", "k_out", "prefix_lens", "start_positions",
+                                        "block_tables"):
+            bad += [(ValueError, k, {k: t[:-1].clone()})]
+    bad += [(pkv.PkvError, "", {"block_tables": a["block_tables"][:, :0].contiguous()})]
+    if "window" in a:
+        bad += [(pkv.PkvError, "", dict(sink_tokens=-1)), (pkv.PkvError, "", dict(sm_scale=float("nan")))]
+    if "max_suffix_len" in a:
+        bad += [(pkv.PkvError, "", dict(max_suffix_len=-1))]
+    if name == "gather":
+        bad += [(ValueError, "together", dict(k_scales=None)), (ValueError, "together", dict(v_scales=None)),
+                (pkv.PkvError, "", dict(k_scale=0.0, k_scales=None, v_scales=None))]
+    if name == "decode_block_scaled":
+        bad += [(pkv.PkvError, "", dict(workspace=None)), (pkv.PkvError, "", dict(workspace=a["workspace"][:256]))]
+    for kind, match, kw in bad:
+        with pytest.raises(kind, match=match):
+            calls.run(name, **kw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(bits(v), before[k]) for k, v in tensors.items()) and pkv.get_device_error() == 0

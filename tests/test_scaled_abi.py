@@ -133,3 +133,17 @@ def test_binding_refusals(lib):
     for name, call in bad:
         with pytest.raises(ValueError, match=name):
             call()
+
+
+def test_compiled_binding(lib):
+    # built and loaded; what is not on a device is left to the Python functions, which refuse it
+    assert pkv._direct is not None
+    t = torch.zeros(3)
+    for name, n in [("append_block_scaled", 11), ("gather", 12), ("decode_window", 16), ("decode_block_scaled", 16),
+                    ("extend_window", 17), ("extend_block_scaled", 17)]:
+        fn = getattr(pkv._direct, name)
+        c = torch.zeros((4, 2, 16, 128), dtype=torch.uint8)
+        for args in ([t] * n, [None] * n, [c] * n, [c, c] + [1.0, 1.0] + [c] * (n - 4), [1 << 80] * n):
+            assert fn(*args) is None
+        with pytest.raises(TypeError):
+            fn(*([t] * (n - 1)))
