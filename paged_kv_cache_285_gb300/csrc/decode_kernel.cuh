@@ -180,6 +180,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   static_assert(!(CASC && (WIN || BSC)) && (!BSC || CT == DT_E4M3), "unsupported combination");
   using C = DecodeCfg<HD, CT, NW, NS>;
   extern __shared__ uint8_t smem_raw[];
+  if constexpr (LEAN) grid_dependency_wait();
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::AREA);
@@ -392,7 +393,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       sc_next = make_float2(1.f, 1.f);
       if (blk >= 0) {
         const int64_t at = (int64_t)blk * p.num_kv_heads + g;
-        sc_next = make_float2(__ldg(ap.k_scales + at), __ldg(ap.v_scales + at));
+        sc_next = make_float2(ap.k_scales[at], ap.v_scales[at]);
       }
     }
     return blk;
@@ -927,23 +928,27 @@ cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.num_kv_heads * ((p.group + 7) / 8), p.batch, p.num_splits);
-  if constexpr (CLM) {
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = (unsigned)p.num_splits;
+  if constexpr (WIN || BSC) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = (unsigned)p.num_splits;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, ap);
+    cfg.numAttrs = CLM ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, ap);
+    if (CLM) return e;
+  } else {
+    kern<<<grid, NW * 32, smem, stream>>>(kmap, vmap, p, ap);
+    e = cudaGetLastError();
   }
-  kern<<<grid, NW * 32, smem, stream>>>(kmap, vmap, p, ap);
-  e = cudaGetLastError();
   if (e != cudaSuccess || (!CASC && p.num_splits <= 1)) return e;
   if (merge_after != nullptr && (e = cudaStreamWaitEvent(stream, merge_after, 0)) != cudaSuccess)
     return e;

@@ -61,6 +61,23 @@ __device__ __forceinline__ uint32_t pow2_scale_bits(float a) {
   return (uint32_t)max(e, 1) << 23;
 }
 
+// The launch of a kernel that begins with grid_dependency_wait(): it is set up
+// while the launch before it in the stream still runs.
+template <typename P>
+cudaError_t launch_dependent(void (*kern)(P), unsigned ctas, unsigned threads, cudaStream_t stream,
+                             const P& p) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 // Four e4m3 codes times f (in fp32), as codes again (one rounding each).
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
   const uint32_t h0 = e4m3x2_to_f16x2(c & 0xFFFFu), h1 = e4m3x2_to_f16x2(c >> 16);
@@ -77,7 +94,7 @@ __device__ __forceinline__ int find_unit(const AppendScaledParams& p, int u) {
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) >> 5;
     const int idx = lo + lane * step;
-    const int64_t v = idx < hi ? (int64_t)(__ldg(p.q_indptr + idx) >> p.bs_shift) + 2 * (int64_t)idx
+    const int64_t v = idx < hi ? (int64_t)(*(p.q_indptr + idx) >> p.bs_shift) + 2 * (int64_t)idx
                                : INT64_MAX;
     const unsigned m = __ballot_sync(kFull, v <= u);
     const int k = m ? 31 - __clz(m) : 0;
@@ -91,6 +108,7 @@ template <int AT, int HD, int BS>
 __global__ void __launch_bounds__(128) append_scaled_kernel(const AppendScaledParams p) {
   constexpr int VPR = HD / 8;           // 16-byte input vectors per row
   constexpr int NV = BS * VPR / 32;     // per lane
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const uint32_t task = blockIdx.x * 4u + (threadIdx.x >> 5);
   if (task >= p.num_tasks) return;
@@ -105,10 +123,10 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const AppendScaledPa
     j = unit - b * p.units_per_request;
   } else {
     b = find_unit(p, unit);
-    j = unit - ((__ldg(p.q_indptr + b) >> p.bs_shift) + 2 * b);
+    j = unit - ((*(p.q_indptr + b) >> p.bs_shift) + 2 * b);
   }
-  const int r0 = __ldg(p.q_indptr + b), r1 = __ldg(p.q_indptr + b + 1);
-  const int P = __ldg(p.prefix_lens + b);
+  const int r0 = *(p.q_indptr + b), r1 = *(p.q_indptr + b + 1);
+  const int P = *(p.prefix_lens + b);
   int S = r1 - r0;
   if (S == 0 || j < 0 || j > (S >> p.bs_shift) + 2) return;
   const bool report = j == 0 && h == 0 && !isv && lane == 0;
@@ -125,7 +143,7 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const AppendScaledPa
   const int start = max(P - lb * BS, 0);                // rows [start, end) of the page are new
   const int end = min(P + S - lb * BS, BS);
   if (end <= start) return;  // (the last unit or two of a request may be empty)
-  const int blk = __ldg(p.block_tables + (int64_t)b * p.max_blocks + lb);
+  const int blk = *(p.block_tables + (int64_t)b * p.max_blocks + lb);
   if (blk < 0 || blk >= p.num_blocks) {
     if (h == 0 && !isv && lane == 0) set_err(p.err, 2);
     return;
@@ -139,7 +157,7 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const AppendScaledPa
     const int v = lane + 32 * i, row = v / VPR, col = (v % VPR) * 8;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     if (row >= start && row < end)
-      x[i] = __ldg(reinterpret_cast<const uint4*>(src + (first_row + row) * row_elems + col));
+      x[i] = *(reinterpret_cast<const uint4*>(src + (first_row + row) * row_elems + col));
   }
   const int64_t page = (int64_t)blk * p.num_kv_heads + h;
   float* scale_at = (isv ? p.v_scales : p.k_scales) + page;
@@ -212,8 +230,7 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const AppendScaledPa
 
 template <int AT, int HD, int BS>
 cudaError_t launch_append_scaled_t(const AppendScaledParams& p, cudaStream_t stream) {
-  append_scaled_kernel<AT, HD, BS><<<(p.num_tasks + 3) / 4, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(append_scaled_kernel<AT, HD, BS>, (p.num_tasks + 3) / 4, 128, stream, p);
 }
 
 // ---- read back --------------------------------------------------------------
@@ -258,6 +275,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
   constexpr int VPR = HD / EPV;                // vectors per (row, head)
   __shared__ int s_blk[kGatherRows];           // -1: no such block (zeros)
   __shared__ int s_off[kGatherRows];
+  grid_dependency_wait();
   const int64_t row0 = (int64_t)blockIdx.x * p.rows_per_cta;
   const int rows = (int)min((int64_t)p.rows_per_cta, p.total_rows - row0);
   if (threadIdx.x < rows) {
@@ -265,18 +283,18 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
     int lo = 0, hi = p.batch;  // the request of row t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(p.row_indptr + mid) <= t) lo = mid;
+      if (*(p.row_indptr + mid) <= t) lo = mid;
       else hi = mid;
     }
-    const int64_t pos = (int64_t)__ldg(p.start_positions + lo) + (t - __ldg(p.row_indptr + lo));
+    const int64_t pos = (int64_t)*(p.start_positions + lo) + (t - *(p.row_indptr + lo));
     int blk = -1;
     // rows that no request owns (before the first or after the last one's) are left alone
-    if (t < __ldg(p.row_indptr + lo) || t >= __ldg(p.row_indptr + lo + 1)) {
+    if (t < *(p.row_indptr + lo) || t >= *(p.row_indptr + lo + 1)) {
       blk = -2;
     } else if (pos < 0 || (pos >> p.bs_shift) >= p.max_blocks) {
       set_err(p.err, 3);
     } else {
-      blk = __ldg(p.block_tables + (int64_t)lo * p.max_blocks + (pos >> p.bs_shift));
+      blk = *(p.block_tables + (int64_t)lo * p.max_blocks + (pos >> p.bs_shift));
       if (blk < 0 || blk >= p.num_blocks) {
         set_err(p.err, 1);
         blk = -1;
@@ -307,11 +325,11 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
         if (blk[e] >= 0) {
           const int64_t page = (int64_t)blk[e] * p.num_kv_heads + h;
           const int64_t at = ((page << p.bs_shift) + s_off[r]) * VPR + c;
-          kx[e] = __ldg(static_cast<const uint4*>(p.k_cache) + at);
-          vx[e] = __ldg(static_cast<const uint4*>(p.v_cache) + at);
+          kx[e] = *(static_cast<const uint4*>(p.k_cache) + at);
+          vx[e] = *(static_cast<const uint4*>(p.v_cache) + at);
           if constexpr (BSC) {
-            ks[e] = __ldg(p.k_scales + page);
-            vs[e] = __ldg(p.v_scales + page);
+            ks[e] = *(p.k_scales + page);
+            vs[e] = *(p.v_scales + page);
           }
         }
       }
@@ -336,9 +354,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 
 template <int CT, int AT, bool BSC>
 cudaError_t launch_gather_t(const GatherParams& p, int head_dim, unsigned ctas, cudaStream_t stream) {
-  if (head_dim == 64) gather_kernel<CT, AT, 64, BSC><<<ctas, 256, 0, stream>>>(p);
-  else gather_kernel<CT, AT, 128, BSC><<<ctas, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return head_dim == 64 ? launch_dependent(gather_kernel<CT, AT, 64, BSC>, ctas, 256, stream, p)
+                        : launch_dependent(gather_kernel<CT, AT, 128, BSC>, ctas, 256, stream, p);
 }
 
 }  // namespace
