@@ -430,7 +430,15 @@ template <>
 struct ItemOf<true, false> { using T = WinItem; };
 
 
-template <bool SX>
+// DEP kernels begin while the launch before them still runs and wait for its end
+// before they read: plain loads, which stay behind the wait.
+template <bool DEP>
+__device__ __forceinline__ int load_i32(const int32_t* at) {
+  if constexpr (DEP) return *at;
+  else return __ldg(at);
+}
+
+template <bool SX, bool DEP>
 __device__ __forceinline__ ItemRaw load_raw(const ExtendParams& p, int item) {
   ItemRaw r{0, 0, 0, 0, 0};
   if (item < p.num_items) {
@@ -447,9 +455,9 @@ __device__ __forceinline__ ItemRaw load_raw(const ExtendParams& p, int item) {
       }
       r.prefix = __ldg(p.group_shared + b);
     } else {
-      r.r0 = __ldg(p.q_indptr + b);
-      r.r1 = __ldg(p.q_indptr + b + 1);
-      r.prefix = __ldg(p.prefix_lens + b);
+      r.r0 = load_i32<DEP>(p.q_indptr + b);
+      r.r1 = load_i32<DEP>(p.q_indptr + b + 1);
+      r.prefix = load_i32<DEP>(p.prefix_lens + b);
     }
   }
   return r;
@@ -692,13 +700,13 @@ __device__ __forceinline__ int item_by_rows(const int32_t* q_indptr, int batch, 
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) >> 5;
     const int idx = lo + lane * step;
-    const int key = idx < hi ? max(__ldg(q_indptr + idx), 0) / rows + idx : INT_MAX;
+    const int key = idx < hi ? max(q_indptr[idx], 0) / rows + idx : INT_MAX;
     const unsigned m = __ballot_sync(0xFFFFFFFFu, key <= u);
     const int k = m ? 31 - __clz(m) : 0;
     lo += k * step;
     hi = min(hi, lo + step);
   }
-  const int pair = u - (max(__ldg(q_indptr + lo), 0) / rows + lo);
+  const int pair = u - (max(q_indptr[lo], 0) / rows + lo);
   return pair >= 0 && pair < pairs ? (lo * heads + g) * pairs + pair : num_items;
 }
 
@@ -800,6 +808,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
               const ExtendParams p, const ExtendPartialParams pp) {
   constexpr bool DYN = TAKE != 0;
+  constexpr bool DEP = WIN || BSC || CL || DYN;
   static_assert(!HALF || CL, "half tiles are combined as parts");
   constexpr int SN = HALF ? BN / 2 : BN;  // keys of a key tile that one row tile takes
   static_assert(!((WIN || BSC || CL || DYN) && (PP || SX)) && !(CL && DYN) && (!BSC || CT == DT_E4M3),
@@ -885,6 +894,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
+  if constexpr (DEP) grid_dependency_wait();
 
   // DYN: the CTA's next item and its request's values, from the K producer
   // (past the last: num_items); the seq-th (from 1) is in slot seq & 1.  (The
@@ -928,10 +938,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint32_t orow = tmem + lane_addr + tm_o<HD>(x);
     int n = 0, js = 0;
     float m_fin = -INFINITY, l_fin = 0.f;  // CL
-    ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+    ItemRaw nxt_raw = load_raw<SX, DEP>(p, DYN ? p.num_items : item0);
     for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
       const ItemRaw raw = nxt_raw;
-      if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
+      if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
       typename ItemOf<WIN, CL>::T it;
       if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
       const int i0x = it.i0 + (HALF ? 0 : x * TOK);  // first token of this tile
@@ -1207,7 +1217,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // the item once more, whether or not the CTA has a key tile of it (kept
       // through the key loop it would take the registers of that loop)
       SplitItem fin;
-      derive_any<PP, SX, WIN, CL, HALF>(p, item0, load_raw<SX>(p, item0), fin);
+      derive_any<PP, SX, WIN, CL, HALF>(p, item0, load_raw<SX, DEP>(p, item0), fin);
       // every CTA of the cluster is done with its rings: the rows go to the CTA
       // that combines them, unnormalised, with their (max, sum)
       cluster_sync();
@@ -1323,7 +1333,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           nxt = p.num_items;
           if (blk < 0) break;
           nxt = item_of(blk);
-          raw = load_raw<SX>(p, nxt);
+          raw = load_raw<SX, DEP>(p, nxt);
           typename ItemOf<WIN, CL>::T it;
           more = nxt >= p.num_items || !derive_any<PP, SX, WIN, CL, HALF>(p, nxt, raw, it);
         }
@@ -1338,10 +1348,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         return nxt;
       };
       int n = 0, j = 0;
-      ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+      ItemRaw nxt_raw = load_raw<SX, DEP>(p, DYN ? p.num_items : item0);
       for (int item = DYN ? (is_k ? ask_item(nxt_raw) : next_item(nxt_raw)) : item0; ok && item < p.num_items; item = DYN ? (is_k ? ask_item(nxt_raw) : next_item(nxt_raw)) : item + stride) {
         const ItemRaw raw = nxt_raw;
-        if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
+        if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
         if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
         if (is_k && !load_q(it, j, 0)) { ok = false; break; }
@@ -1362,7 +1372,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             if (blk < 0 || blk >= p.num_blocks) set_err(p.err, 1);  // TMA zero-fills page -1
             else page = blk * p.num_kv_heads + it.g;
           }
-          if constexpr (BSC) scale_nxt = page >= 0 ? __ldg((is_k ? p.k_scales : p.v_scales) + page) : 1.f;
+          if constexpr (BSC) scale_nxt = page >= 0 ? (is_k ? p.k_scales : p.v_scales)[page] : 1.f;
           return page;
         };
         int win = 0, cur = -1, nxt = -1;
@@ -1444,10 +1454,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // two items on waits for tile B's release).  Waiting here keeps the
       // softmax warps off the TMA engine's queue.
       int js = 0;
-      ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+      ItemRaw nxt_raw = load_raw<SX, DEP>(p, DYN ? p.num_items : item0);
       for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
-        if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
+        if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
         if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
         const uint32_t stg = s_base + C::OFF_Q + ((2 * js + 1) % NQB) * C::T16;
@@ -1526,10 +1536,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       int n = 0, j = 0;
       bool have_prev = false, prev_first = false, prev_last = false;
       int prev_n = 0, prev_j = 0;
-      ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+      ItemRaw nxt_raw = load_raw<SX, DEP>(p, DYN ? p.num_items : item0);
       for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
-        if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
+        if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
         if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
         const int qa = (2 * j) % NQB, qb = (2 * j + 1) % NQB;
@@ -1607,10 +1617,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (lane == 0) mbar_arrive(bar(C::B_QCONV + 2 * xq + (j & 1)));
         return true;
       };
-      ItemRaw nxt_raw = load_raw<SX>(p, DYN ? p.num_items : item0);
+      ItemRaw nxt_raw = load_raw<SX, DEP>(p, DYN ? p.num_items : item0);
       for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
-        if constexpr (!DYN) nxt_raw = load_raw<SX>(p, item + stride);
+        if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
         typename ItemOf<WIN, CL>::T it;
         if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
         SegIter si;
@@ -1688,6 +1698,21 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 }
 
+// The launch of a DEP kernel; at[0] of the n attributes says so.
+inline cudaLaunchConfig_t dependent_launch(dim3 grid, int smem, cudaStream_t stream,
+                                           cudaLaunchAttribute* at, int n) {
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cfg;
+}
+
 template <int HD, int CT, int AT, bool PP, bool SX, bool WIN = false, bool BSC = false,
           int TAKE = 0>
 cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
@@ -1699,7 +1724,13 @@ cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, co
   constexpr int smem = DYN ? C::SMEM_DYN : BSC ? C::SMEM_BSC : C::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k<<<dim3(DYN ? p.num_blocks_dyn : p.num_ctas), NTHREADS, smem, stream>>>(kmap, vmap, qmap, omap, p, pp);
+  const dim3 grid(DYN ? p.num_blocks_dyn : p.num_ctas);
+  if constexpr (WIN || BSC || DYN) {
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = dependent_launch(grid, smem, stream, at, 1);
+    return cudaLaunchKernelEx(&cfg, k, kmap, vmap, qmap, omap, p, pp);
+  }
+  k<<<grid, NTHREADS, smem, stream>>>(kmap, vmap, qmap, omap, p, pp);
   return cudaGetLastError();
 }
 
@@ -1725,18 +1756,13 @@ cudaError_t launch_extend_split_t(const CUtensorMap& kmap, const CUtensorMap& vm
   constexpr int smem = BSC ? ExtCfg<HD, CT, AT>::SMEM_BSC : ExtCfg<HD, CT, AT>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.splits;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.num_items * (unsigned)p.splits);
-  cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = dependent_launch(dim3((unsigned)p.num_items * (unsigned)p.splits), smem,
+                                            stream, at, 2);
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)p.splits;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   const ExtendPartialParams pp{};
   return cudaLaunchKernelEx(&cfg, k, kmap, vmap, qmap, omap, p, pp);
 }

@@ -164,7 +164,88 @@ def test_refusals(name, way):
     if name == "decode_block_scaled":
         bad += [(pkv.PkvError, "", dict(workspace=None)), (pkv.PkvError, "", dict(workspace=a["workspace"][:256]))]
     for kind, match, kw in bad:
-        with pytest.raises(kind, match=match):
+        with pytest.raises(kind, match=match or None):
             calls.run(name, **kw)
     torch.cuda.synchronize()
     assert all(torch.equal(bits(v), before[k]) for k, v in tensors.items()) and pkv.get_device_error() == 0
+
+
+class Chain:
+    """Calls that depend on one another and on small copies between them, without a pause: each is
+    set up while the one before it still runs, and must not read before that has ended."""
+
+    def __init__(self, steps=12):
+        self.b = b = Calls()
+        self.steps = steps
+        gen = torch.Generator(device="cuda").manual_seed(5)
+        draw = lambda t: torch.randn((steps,) + t.shape, generator=gen, device="cuda").to(t.dtype)
+        self.kn, self.vn, self.q, self.qd = draw(b.kn), draw(b.vn), draw(b.q), draw(b.qd)
+        self.extra = torch.randint(0, 9, (steps, 2), generator=gen, device="cuda", dtype=torch.int32)
+        self.start = b.at.clone()
+        self.got_q = torch.zeros((steps,) + b.q.shape, dtype=b.q.dtype, device="cuda")
+        self.got_d = torch.zeros((steps,) + b.qd.shape, dtype=b.qd.dtype, device="cuda")
+        self.got_k = torch.zeros((steps, 60, HKV, D), dtype=b.q.dtype, device="cuda")
+        self.got_v = torch.zeros_like(self.got_k)
+        self.rest = ints([0, 25, 60])
+
+    def run(self, pause, side=None):
+        b, c, main = self.b, self.b.c, torch.cuda.current_stream()
+        for i in range(self.steps):
+            for to, frm in ((b.kn, self.kn), (b.vn, self.vn), (b.q, self.q), (b.qd, self.qd)):
+                to.copy_(frm[i])
+            b.at.copy_(self.start).sub_(self.extra[i])
+            b.lens.copy_(b.at)
+            b.lens[0].add_(3)
+            b.lens[1].add_(40)
+            pause()
+            pkv.kv_append_block_scaled(c.k, c.v, c.ks, c.vs, b.kn, b.vn, b.ip, b.at, c.bt, 40)
+            pause()
+            pkv.paged_extend_attn_block_scaled(c.k, c.v, c.ks, c.vs, b.q, self.got_q[i], b.ip, b.at, c.bt, 0.1, 40, 64)
+            pause()
+            if side is not None:  # the read back beside the decode
+                side.wait_stream(main)
+            with torch.cuda.stream(side or main):
+                pkv.kv_gather(c.k, c.v, self.got_k[i], self.got_v[i], self.rest, b.zero, c.bt, k_scales=c.ks,
+                              v_scales=c.vs)
+            pause()
+            for splits in (0, 3):
+                pkv.paged_decode_attn_block_scaled(c.k, c.v, c.ks, c.vs, b.qd, self.got_d[i], c.bt, b.lens, 0.1, 64,
+                                                   num_splits=splits, workspace=b.ws)
+                pause()
+                b.qd.copy_(self.got_d[i])
+            pkv.paged_decode_attn_window(c.k, c.v, b.qd, self.got_d[i], c.bt, b.lens, 0.1, 64, 20, 3)
+            pause()
+            b.q.copy_(self.got_q[i])
+            pkv.paged_extend_attn_window(c.k, c.v, b.q, self.got_q[i], b.ip, b.at, c.bt, 0.1, 40, 64, 20, 3)
+            pause()
+            if side is not None:
+                main.wait_stream(side)
+        return self
+
+    def results(self):
+        torch.cuda.synchronize()
+        c = self.b.c
+        return [bits(t) for t in (self.got_q, self.got_d, self.got_k, self.got_v, c.k, c.v, c.ks, c.vs)]
+
+
+def test_calls_one_after_another_without_a_pause():
+    want = Chain().run(torch.cuda.synchronize).results()
+    assert not torch.equal(want[0][0], want[0][1])
+    nothing = lambda: None
+    for side in (None, torch.cuda.Stream()):
+        for _ in range(3):
+            assert all(torch.equal(x, y) for x, y in zip(Chain().run(nothing, side).results(), want))
+    side = torch.cuda.Stream()
+    for beside in (None, torch.cuda.Stream()):
+        chain = Chain()
+        before = [t.clone() for t in (chain.b.c.k, chain.b.c.v, chain.b.c.ks, chain.b.c.vs)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            chain.run(nothing, beside)
+        for _ in range(3):
+            for t, f in zip((chain.b.c.k, chain.b.c.v, chain.b.c.ks, chain.b.c.vs), before):
+                t.copy_(f)
+            graph.replay()
+            assert all(torch.equal(x, y) for x, y in zip(chain.results(), want))
+    # some of the drawn starts of the second request lie below 0: reported, its rows left alone
+    assert bool((Chain().extra[:, 1] > PREFIX[1]).any()) and pkv.get_device_error() == 3
