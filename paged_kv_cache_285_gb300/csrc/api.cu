@@ -182,7 +182,8 @@ bool plan_extend(ExtendParams& p, int batch, int num_kv_heads, int group, int ma
 // of 1, 2, 4 and 8.  Measured (us at 1 / 2 / 4 / 8 CTAs): whole tiles, 64 items of
 // 254 tiles 458 / 259 / 278 / 365, 128 of up to 21 tiles 43 / 53 / 62 / 107, 8 of
 // 63 tiles 115 / 66 / 39 / 25; the last in half tiles 100 / 55 / 33 / 22.5, and
-// 512 of 1 to 4 tiles 44 whole, 56 in half tiles.
+// 512 of 1 to 4 tiles 44 whole, 56 in half tiles.  (Two of these at each end
+// again with launches set up early: 257, 42.8; the order is the same.)
 void plan_view_items(ExtendParams& p, int max_total_len, int sm_count) {
   int64_t tiles = ((int64_t)max_total_len + 127) / 128;
   if (p.window > 0)
@@ -598,7 +599,9 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
 // Against the plain plan's runs (128 to 4,096 tokens, six rounds): block-scaled,
 // 16 x 4,096 tokens 39 -> 31 us, 8 x 5,000-20,000 50 -> 47, 1 x 100,000 69 -> 45,
 // 128 x 100-300 27.5 -> 21; windows: 32 x 1,024 (bf16) 37.6 -> 26.7, 128 x 4,096
-// (fp8) 179 -> 168.
+// (fp8) 179 -> 168.  (Since launches are set up while the one before runs: 29.5,
+// 45.5, 42.9, 19.8; 26.3, 168.  The best split of a sweep is 0 to 7 % faster, 11 %
+// where all lengths are equal and one split would just fill the GPU.)
 static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_seq_len, int window,
                             int sink_tokens, int forced, int sm_count) {
   const int len = visible_bound(max_seq_len, window, sink_tokens);

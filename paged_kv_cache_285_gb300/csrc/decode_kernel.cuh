@@ -36,15 +36,21 @@
 //     hidden tiles (and their block ids) are never read, and hidden tokens of
 //     the tiles at a run's edge are masked (score -inf, V zeroed).  128 requests
 //     of 1,000-32,000 tokens in a window of 4,096 with 64 sinks (fp8, 64 / 8
-//     heads): 167 us = 6.38 TB/s, 94 % of the measured copy.
+//     heads): 166 us = 6.41 TB/s, 94 % of the measured copy.
 //   * scales per block and kv head (BSC, fp8 codes): a 16-token tile lies in
 //     one block, so its K scale multiplies the tile's scores and its V scale
 //     the tile's PV product as it is added to the fp32 accumulators
 //     (O = al O + s_v (V^T P^T)): scales of any size keep P in f16's range.
 //     The lane that holds a tile's block id holds its scales too, issues the
 //     tile's copies and leaves the scales in the stage's slot.  64 requests of
-//     512-4,096 tokens: 64 us = 4.8 TB/s, 71 % (the scales of one tensor: 61 us):
-//     bound by the latency of the CTAs' first tiles and by their uneven ends.
+//     512-4,096 tokens: 62 us = 5.0 TB/s, 74 %: of each doubling of the tokens the
+//     kernel takes 101 % of the copy's time; the other 10 to 15 us are the launches,
+//     the first tiles' latency and the CTAs' uneven ends.
+//   * WIN and BSC kernels are launched while the launch before them in the stream
+//     still runs and wait for its end before their first load (3 requests of up
+//     to 700 tokens, calls one after another: 8.2 -> 5.0 us).  Letting the next
+//     launch's CTAs in before this one's have ended gave nothing more (62.5
+//     against 62.1, 7.8 against 7.4).
 //   * splits joined in a cluster (CLM, few requests): the splits of one (request,
 //     head chunk) are the CTAs of a cluster.  Each leaves its heads' (max, sum,
 //     unnormalised O) in shared memory, and after a cluster barrier each adds up
@@ -955,8 +961,8 @@ cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
   const int64_t pairs = (int64_t)p.batch * p.num_q_heads;
   if constexpr (WIN || BSC) {
     // Its launch overlaps the splits' last CTAs (it waits for all of them before
-    // its first read).  Calls one after another, block-scaled: 128 requests of
-    // up to 2,048 tokens 67.7 -> 66.3 us, 16 x 4,096 33.5 -> 32.4, 1 x 100,000
+    // its first read).  Calls one after another, block-scaled: 64 requests of
+    // 512-4,096 tokens 67.7 -> 66.3 us, 16 x 4,096 33.5 -> 32.4, 1 x 100,000
     // 48.6 -> 45.7; in a graph the same within 0.5.
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

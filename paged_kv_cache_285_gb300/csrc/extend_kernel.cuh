@@ -86,8 +86,9 @@
 // the other roles through a two-slot ring.  Later pairs of a (request, head),
 // which see more keys, come first.  Where the requests' lengths differ so much
 // that most pairs up to the length hint would be empty (a prompt among single
-// tokens), blocks are counted by rows and their requests searched.  (1,760 items of 34 tiles on 152 SMs: 728
-// against 752 us with the stride; 952 items of 33 to 87 tiles 745 against 804.)
+// tokens), blocks are counted by rows and their requests searched.  (1,760 items
+// of 34 tiles on 152 SMs: 728 us against 752 with the stride; 952 items of 33 to
+// 87 tiles 745 against 804.)
 //
 // Split (CL = true), for calls with few items and long key ranges: the key tiles
 // of one item are cut into runs, one per CTA of a cluster (item =
@@ -98,6 +99,11 @@
 // O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c.  No workspace, no second
 // launch.  (Writing to the owner, not reading from the others: a remote load is
 // waited for, a remote store is not.)
+//
+// All of these are launched while the launch before them in the stream still
+// runs: barriers and TMEM are set up, then they wait for its end before their
+// first load (plain loads; calls one after another, a short prompt 12.3 -> 10.3
+// us, 8 chat turns 45.1 -> 42.8).
 //
 // Half tiles (HALF = true, with CL): where every request's rows fit one row tile,
 // tile B would be empty.  Both tiles then hold the same rows and share the keys

@@ -21,10 +21,15 @@
 // Append: one warp per (block, kv head, K or V).  The page's new rows stay in
 // registers between the pass for the maximum and the store of the codes, so
 // every input is read once; there is no shared memory and no barrier.  Prompts
-// are bound by memory: 63,600 rows of 8 heads x 128 dims (391 MB) in 60.6 us,
-// 95 % of the measured copy; a step of one token per request by the launch and
-// four dependent loads (lengths, block id, row, old scale): 2.6 us for 4
-// requests, 4.1 for 256.
+// are bound by memory: 63,600 rows of 8 heads x 128 dims (391 MB) in 59.8 us,
+// 96 % of the measured copy; a step of one token per request by the launch and
+// four dependent loads (lengths, block id, row, old scale): 2.4 us for 4
+// requests (2.6 a call, which is the host's time for it).
+//
+// Both kernels are launched while the launch before them in the stream still
+// runs and wait for its end before their first load: calls one after another
+// 4.1 -> 2.6 us.  (All their loads are plain ones: read-only loads need not stay
+// behind that wait.)
 #include <algorithm>
 
 #include "internal.h"

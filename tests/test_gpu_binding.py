@@ -249,3 +249,52 @@ def test_calls_one_after_another_without_a_pause():
             assert all(torch.equal(x, y) for x, y in zip(chain.results(), want))
     # some of the drawn starts of the second request lie below 0: reported, its rows left alone
     assert bool((Chain().extra[:, 1] > PREFIX[1]).any()) and pkv.get_device_error() == 3
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "graph"])
+def test_calls_wait_for_other_streams(name, captured):
+    # an event of another stream between a call and the one before it in its stream: the inputs
+    # arrive there late (a pause of about a millisecond, then the copies)
+    pkv.load()
+    calls, other, mine = Calls(), torch.cuda.Stream(), torch.cuda.Stream()
+    _, a = calls.args(name)
+    inputs = [a[k] for k in ("v_new" if "v_new" in a else "v_cache", "q", "k_new") if k in a]
+    right = [t.clone() for t in inputs]
+    kept = [t.clone() for t in (calls.c.k, calls.c.v, calls.c.ks, calls.c.vs)]
+    want = [bits(t) for t in calls.run(name)]
+
+    def restore():
+        for t, f in zip((calls.c.k, calls.c.v, calls.c.ks, calls.c.vs), kept):
+            t.copy_(f)
+        for t in inputs:
+            t.zero_()
+        torch.cuda.synchronize()
+
+    got = [t for t in (a.get(x) for x in ("k_cache", "v_cache", "k_scales", "v_scales", "k_out", "v_out", "out",
+                                          "lse_out")) if t is not None]
+
+    def work():  # on `mine`
+        other.wait_stream(mine)
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(2_000_000)
+            for t, r in zip(inputs, right):
+                t.copy_(r)
+        before, b = calls.args("gather")
+        before(**b)  # the call just before: its result is not looked at
+        mine.wait_stream(other)
+        calls.args(name)[0](**a)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=mine):
+            work()
+    for _ in range(3):
+        restore()
+        if captured:
+            graph.replay()
+        else:
+            with torch.cuda.stream(mine):
+                work()
+        torch.cuda.synchronize()
+        assert all(torch.equal(bits(t), w) for t, w in zip(got, want))
+    assert pkv.get_device_error() == 0
