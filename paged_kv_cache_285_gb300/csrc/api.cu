@@ -224,7 +224,16 @@ struct DecodePlan {
   size_t ws_lse_offset = 0;
   size_t ws_span_offset = 0;  // cascade: int2 (first own token, length) per request
   bool cluster = false;       // window / block-scaled: the splits form clusters, no workspace
+  int num_cuts = 0;           // window / block-scaled: splits of different lengths
+  int cut[kMaxCuts + 1] = {};
 };
+
+// The workspace of a plan's partials: O and LSE per (request, head, split).
+void size_partials(DecodePlan& pl, const pkv_cache_desc* d, int batch, int hq) {
+  const size_t o_bytes = (size_t)batch * hq * pl.splits * d->head_dim * sizeof(float);
+  pl.ws_lse_offset = (o_bytes + 255) & ~(size_t)255;
+  pl.ws_bytes = pl.ws_lse_offset + (size_t)batch * hq * pl.splits * sizeof(float);
+}
 
 // Split plan: the sequence is cut into runs of `chunk` tokens (a multiple of
 // 16).  Automatic: aim for about six waves of two CTAs per SM over the worst
@@ -247,11 +256,7 @@ DecodePlan plan_decode(const pkv_cache_desc* d, int batch, int hq, int max_seq_l
   pl.chunk = chunk_sub * kSubTokens;
   pl.splits = ceil_div(max_sub, chunk_sub);
   if (pl.splits < 1) pl.splits = 1;
-  if (pl.splits > 1) {
-    const size_t o_bytes = (size_t)batch * hq * pl.splits * d->head_dim * sizeof(float);
-    pl.ws_lse_offset = (o_bytes + 255) & ~(size_t)255;
-    pl.ws_bytes = pl.ws_lse_offset + (size_t)batch * hq * pl.splits * sizeof(float);
-  }
+  if (pl.splits > 1) size_partials(pl, d, batch, hq);
   return pl;
 }
 
@@ -600,8 +605,22 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
 // 16 x 4,096 tokens 39 -> 31 us, 8 x 5,000-20,000 50 -> 47, 1 x 100,000 69 -> 45,
 // 128 x 100-300 27.5 -> 21; windows: 32 x 1,024 (bf16) 37.6 -> 26.7, 128 x 4,096
 // (fp8) 179 -> 168.  (Since launches are set up while the one before runs: 29.5,
-// 45.5, 42.9, 19.8; 26.3, 168.  The best split of a sweep is 0 to 7 % faster, 11 %
-// where all lengths are equal and one split would just fill the GPU.)
+// 45.5, 42.9, 19.8; 26.3, 168.)
+//
+// With a quarter of a round of items or more, a launch ends unevenly: the CTAs of
+// its last round are few, and a CTA alone reads at r1.  Splits of falling length
+// (each 0.45 to 0.78 of the one before; a split's CTAs start after all of the one
+// before) end it with short ones.  Block-scaled, lengths spread up to n, equal
+// splits -> falling ones: 64 x 4,096 62.5 -> 56.2 us, 32 x 4,096 38.8 -> 34.4, 128 x
+// 4,096 109 -> 103, 32 x 1,500 22.5 -> 17.5, 20 x 8,192 46.6 -> 42.5, 100 x 8,192
+// 165 -> 164, d64 128 x 4,096 86.6 -> 71.9, 64 heads 64 x 4,096 66.0 -> 59.6; all of
+// one length: 76 x 4,096 115 -> 106, 100 x 8,192 268 -> 251, but 24 x 2,048 23.9 ->
+// 27.4.  Where many short sequences make several rounds of their own the short
+// splits only cost (256 x 1,024 59 -> 64, 400 x 2,048 155 -> 162: excluded).  In a
+// window the lengths are the same: taken from 0.9 MB of K and V an item on, up to
+// 1.5 rounds (fp8 40 x 4,096 62.7 -> 54.9, 100 x 4,096 130 -> 122, bf16 64 x 4,096
+// 154 -> 146; excluded: fp8 64 x 2,048 50.1 -> 52.5, 128 x 4,096 of 64 heads 165 ->
+// 170).
 static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_seq_len, int window,
                             int sink_tokens, int forced, int sm_count) {
   const int len = visible_bound(max_seq_len, window, sink_tokens);
@@ -643,6 +662,30 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   if (best_cluster && pl.splits >= 2) {
     pl.cluster = true;
     pl.ws_bytes = 0;
+  }
+  // splits of falling length: see above
+  const double fill = items / slots;
+  const bool falling = window > 0 ? fill <= 1.5 && 2.0 * len * d->head_dim * elem_bytes(d->cache_dtype) >= 0.9e6
+                                  : len >= 1000 && fill <= len / 800.0;
+  if (fill >= 0.25 && falling) {
+    const double ratio = std::min(0.78, std::max(0.45, 0.45 + 0.75 * (0.75 - fill)));
+    int k = kMaxCuts;
+    double first = 0;
+    for (; k > 1; --k) {  // the last one of 192 tokens at least
+      first = len * (1 - ratio) / (1 - std::pow(ratio, k));
+      if (first * std::pow(ratio, k - 1) >= 192) break;
+    }
+    if (k > 1) {
+      pl = DecodePlan{};
+      pl.splits = pl.num_cuts = k;
+      double at = 0;
+      for (int i = 0; i <= kMaxCuts; ++i, at += first, first *= ratio)
+        pl.cut[i] = i < k    ? (int)(at / kSubTokens + 0.5) * kSubTokens
+                    : i == k ? tiles * kSubTokens
+                             : INT32_MAX;
+      pl.chunk = pl.cut[1];
+      size_partials(pl, d, batch, hq);
+    }
   }
   return pl;
 }
@@ -723,6 +766,8 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
     ap.k_scales = view->k_scales;
     ap.v_scales = view->v_scales;
     ap.join_cluster = pl.cluster ? 1 : 0;
+    ap.num_cuts = pl.num_cuts;
+    std::copy(pl.cut, pl.cut + kMaxCuts + 1, ap.cut);
     e = launch_decode_window(kmap, vmap, p, ap, desc->head_dim, (int)desc->cache_dtype,
                              (int)act_dtype, stream);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

@@ -43,9 +43,12 @@
 //     (O = al O + s_v (V^T P^T)): scales of any size keep P in f16's range.
 //     The lane that holds a tile's block id holds its scales too, issues the
 //     tile's copies and leaves the scales in the stage's slot.  64 requests of
-//     512-4,096 tokens: 62 us = 5.0 TB/s, 74 %: of each doubling of the tokens the
-//     kernel takes 101 % of the copy's time; the other 10 to 15 us are the launches,
-//     the first tiles' latency and the CTAs' uneven ends.
+//     512-4,096 tokens: 56 us = 5.5 TB/s, 81 %; more tokens add the copy's time for
+//     them (64 -> 128 requests of 4,096: +78 us, 79 for the copy), the other 10 us
+//     are the launches, the first tiles' latency and the CTAs' uneven ends.
+//   * WIN and BSC splits may fall in length, each a part of the one before (cut[]):
+//     the CTAs that start last are short, so that they end together (62 -> 56 us
+//     above; the plan says where).
 //   * WIN and BSC kernels are launched while the launch before them in the stream
 //     still runs and wait for its end before their first load (3 requests of up
 //     to 700 tokens, calls one after another: 8.2 -> 5.0 us).  Letting the next
@@ -173,6 +176,24 @@ __device__ __forceinline__ WinSpan win_span(int n, int window, int sinks) {
   return s;
 }
 
+// Where split s begins, and the splits that n tokens take (CUT: a launch whose
+// splits may differ in length).
+template <bool CUT>
+__device__ __forceinline__ int split_begin(const DecodeParams& p, const DecodeExtraParams& ap, int s) {
+  if (CUT && ap.num_cuts > 0) return ap.cut[s];
+  return s * p.chunk;
+}
+template <bool CUT>
+__device__ __forceinline__ int splits_of(const DecodeParams& p, const DecodeExtraParams& ap, int n) {
+  if (CUT && ap.num_cuts > 0) {
+    int k = 0;
+#pragma unroll
+    for (int s = 0; s < kMaxCuts; ++s) k += ap.cut[s] < n;
+    return k;
+  }
+  return (n + p.chunk - 1) / p.chunk;
+}
+
 // CASC: a cascade launch (tokens from the group's shared prefix on; partials
 // in the workspace slots after the prefix's chunks, always merged).  WIN: a
 // window with sink tokens.  BSC: fp8 codes with scales per block and kv head.
@@ -182,6 +203,7 @@ __global__ void __launch_bounds__(NW * 32)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const DecodeParams p, const DecodeExtraParams ap) {
   constexpr bool LEAN = WIN || BSC;  // a leaner inner loop than the plain and cascade forms
+  constexpr bool CUT = LEAN && !CLM;
   static_assert(!(CASC && CLM), "unsupported combination");
   static_assert(!(CASC && (WIN || BSC)) && (!BSC || CT == DT_E4M3), "unsupported combination");
   using C = DecodeCfg<HD, CT, NW, NS>;
@@ -207,7 +229,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   int tb = 0;  // first token of this launch (cascade: the end of the shared prefix)
   if constexpr (CASC) tb = group_prefix_len(ap, b);
   const int cap = WIN ? p.max_blocks * bs
-                      : min(p.max_blocks * bs, (tb > 0 ? tb : 0) + p.num_splits * p.chunk);
+                      : min(p.max_blocks * bs, (tb > 0 ? tb : 0) + split_begin<CUT>(p, ap, p.num_splits));
   if (n < 0 || n > cap) {
     if (threadIdx.x == 0 && split == 0) set_err(p.err, 3);
     n = n < 0 ? 0 : cap;
@@ -225,13 +247,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   WinSpan ws{};
   if constexpr (WIN) {
     ws = win_span(n, ap.window, ap.sink_tokens);
-    if (ws.nv > p.num_splits * p.chunk) {  // longer than the call's hint
+    const int most = split_begin<CUT>(p, ap, p.num_splits);
+    if (ws.nv > most) {  // longer than the call's hint
       if (threadIdx.x == 0 && split == 0) set_err(p.err, 3);
-      ws = win_span(p.num_splits * p.chunk, ap.window, ap.sink_tokens);
+      ws = win_span(most, ap.window, ap.sink_tokens);
     }
     n = ws.nv;
   }
-  const int t0 = tb + split * p.chunk;
+  const int t0 = tb + split_begin<CUT>(p, ap, split);
   // CLM: this CTA's share of the outputs from the parts of the cluster's active
   // CTAs, [8][HD] O and [2][8] (max, sum) at the start of their shared memory
   auto join_cluster = [&]() {
@@ -288,9 +311,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     return;
   }
-  const int t1 = min(n, t0 + p.chunk);
+  const int t1 = min(n, tb + split_begin<CUT>(p, ap, split + 1));
   const int nsub = (t1 - t0 + kSubTokens - 1) / kSubTokens;
-  const int nsplit_b = (n - tb + p.chunk - 1) / p.chunk;
+  const int nsplit_b = splits_of<CUT>(p, ap, n - tb);
   const int cnt = warp < nsub ? (nsub - warp + NW - 1) / NW : 0;
 
   if (ap.k_new != nullptr && split == nsplit_b - 1) {
@@ -829,15 +852,15 @@ __global__ void __launch_bounds__(128) merge_kernel(const DecodeParams p, const 
   } else {
     const int bs = 1 << p.bs_shift;
     n = p.seq_lens[b];
-    const int cap = WIN ? p.max_blocks * bs : min(p.max_blocks * bs, p.num_splits * p.chunk);
+    const int most = split_begin<PDL>(p, ap, p.num_splits);
+    const int cap = WIN ? p.max_blocks * bs : min(p.max_blocks * bs, most);
     n = n < 0 ? 0 : (n > cap ? cap : n);
     if constexpr (WIN) {  // the compact length, clamped as the split kernel does
       n = win_span(n, ap.window, ap.sink_tokens).nv;
-      if (n > p.num_splits * p.chunk)
-        n = win_span(p.num_splits * p.chunk, ap.window, ap.sink_tokens).nv;
+      if (n > most) n = win_span(most, ap.window, ap.sink_tokens).nv;
     }
   }
-  const int ns = (n - tb + p.chunk - 1) / p.chunk;
+  const int ns = splits_of<PDL>(p, ap, n - tb);
   if (!CASC && ns <= 1) return;  // written directly by the split kernel
   const int kSlot0 = CASC ? ap.prefix_slots : 0;
   const int nslots = p.num_splits + kSlot0;

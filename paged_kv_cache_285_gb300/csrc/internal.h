@@ -53,6 +53,7 @@ struct DecodeParams {
 //    group_prefix_lens[g] tokens, which a prefix pass attends once for the
 //    group; the decode then covers each request's tokens from there on and
 //    its partials start at workspace slot 1 (slot 0 is the prefix's).
+constexpr int kMaxCuts = 8;
 struct DecodeExtraParams {
   const void* k_new;
   const void* v_new;
@@ -80,6 +81,11 @@ struct DecodeExtraParams {
   const float* k_scales;
   const float* v_scales;
   int join_cluster;  // window / block-scaled launches: the splits (2 .. 8) form clusters
+  // window / block-scaled launches with splits of different lengths (at most
+  // kMaxCuts; num_cuts 0: of p.chunk tokens each): split s takes tokens cut[s] ..
+  // cut[s + 1] - 1; entries past the last are INT32_MAX
+  int num_cuts;
+  int cut[kMaxCuts + 1];
 };
 
 // Division of unsigned n < 2^31 by a divisor fixed for a launch, as a

@@ -204,6 +204,38 @@ def test_decode(cfg, splits, window, sinks):
     assert pkv.get_device_error() == 0
 
 
+MANY = [
+    # batch, hq, hkv, d, bs, act, most: enough CTAs for splits of falling length
+    (28, 8, 8, 64, 16, BF16, 1100),
+    (80, 16, 8, 128, 32, F16, 1000),
+    (40, 18, 2, 64, 16, F16, 1500),
+    (160, 1, 1, 128, 16, BF16, 2100),
+]
+
+
+@pytest.mark.parametrize("cfg", MANY, ids=lambda c: f"b{c[0]}h{c[1]}x{c[2]}d{c[3]}n{c[6]}")
+def test_decode_of_many_requests(cfg):
+    batch, hq, hkv, d, bs, act, most = cfg
+    rng = np.random.default_rng(batch)
+    lens = [most, 0, 1, 16, most - 1] + list(rng.integers(0, most // 32, batch - 25) + 16 * rng.integers(0, 2, batch - 25))
+    lens += list(16 * rng.integers(4, most // 16, 20) + rng.integers(-1, 2, 20))  # at and beside splits' ends
+    lens = [int(n) for n in rng.permutation(lens)]
+    c = Case(SCALED, act, hkv, d, bs, lens, seed=batch).cuda()
+    q = c.rows(batch, hq).cuda()
+    assert pkv.decode_window_workspace_bytes(c.k, batch, hq, most) > 0
+    out, lse = run_decode(c, q, hq, lens, most=most)
+    ref = R.attention(*c.values(), to_f64(q), range(batch + 1), [n - 1 for n in lens], c.tables, hq, 1 / d ** 0.5)
+    check_attention(out, lse, ref, act, d, f"{cfg}")
+    assert pkv.get_device_error() == 0
+    # a request past the hint is reported, the others are what they were
+    short = sorted(lens)[-2] - 40
+    again, _ = run_decode(c, q, hq, lens, most=short)
+    kept = [i for i, n in enumerate(lens) if n <= short]
+    ref = [r[kept] if isinstance(r, np.ndarray) else {k: v[kept] for k, v in r.items()} for r in ref]
+    check_attention(again[kept], _[kept], ref, act, d, f"{cfg} hint")
+    assert pkv.get_device_error() == 3 and bool(torch.isfinite(again).all())
+
+
 def test_decode_scales_of_any_size():
     # V scales 60 binary orders apart, and scales that are no powers of two
     c = Case(SCALED, BF16, 2, 128, 16, [300, 64], seed=3)

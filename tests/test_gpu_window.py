@@ -69,6 +69,26 @@ def test_decode(cfg, window, sinks):
         check_attention(out, lse, ref, act, d, f"{cfg} {window} {sinks} {splits}")
 
 
+@pytest.mark.parametrize("cache,act,hq,hkv,d,window,sinks", [(BF16, BF16, 4, 2, 128, 1800, 20), (F16, F16, 2, 2, 64, 3600, 0),
+                                                               (E4M3, F16, 2, 2, 128, 3590, 33)])
+def test_decode_of_many_requests(cache, act, hq, hkv, d, window, sinks):
+    # splits of falling length in the numbering without the hidden tokens: most requests short,
+    # some as long as the window, some longer
+    batch, rng = 80, np.random.default_rng(window)
+    long = [window, window + 1, window + 17, window + sinks + 700, window - 16, 16 * (window // 32), 16 * (window // 64) + 1]
+    lens = [int(n) for n in rng.permutation(long + list(rng.integers(0, 90, batch - len(long))))]
+    c = Case(cache, act, hkv, d, 16, lens, seed=window)
+    q = c.rows(batch, hq).cuda()
+    give_back(c, [n - 1 for n in lens], window, sinks)
+    c.cuda()
+    assert pkv.decode_window_workspace_bytes(c.k, batch, hq, max(lens), window, sinks) > 0
+    out, lse = run_decode(c, q, hq, lens, window, sinks)
+    assert pkv.get_device_error() == 0
+    ref = R.attention(*c.values(), to_f64(q), range(batch + 1), [n - 1 for n in lens], c.tables, hq, 1 / d ** 0.5, window,
+                      sinks)
+    check_attention(out, lse, ref, act, d)
+
+
 def test_decode_of_a_whole_window_is_the_plain_decode():
     lens = [700, 33, 1]
     c = Case(BF16, BF16, 2, 128, 16, lens, seed=3).cuda()
