@@ -83,12 +83,16 @@
 // walking a fixed stride: items differ by their key tiles, and the pairs past a
 // short request's rows are empty.  The K producer asks for the next block when
 // it is three tiles from its item's end, looks the item up and passes both on to
-// the other roles through a two-slot ring.  Later pairs of a (request, head),
-// which see more keys, come first.  Where the requests' lengths differ so much
-// that most pairs up to the length hint would be empty (a prompt among single
-// tokens), blocks are counted by rows and their requests searched.  (1,760 items
-// of 34 tiles on 152 SMs: 728 us against 752 with the stride; 952 items of 33 to
-// 87 tiles 745 against 804.)
+// the other roles through a two-slot ring.  (1,760 items of 34 tiles on 152 SMs:
+// 728 us against 752 with the stride; 952 items of 33 to 87 tiles 745 against
+// 804.)  A request's later pairs, which see more keys, come first, for all its
+// heads; head by head, where the pairs of a head would share its keys in L2, 16
+// requests of 100-1,000 rows over up to 9,000 tokens took 796 us against 760, 64
+// of 100-300 over up to 4,000 581 against 540, 4 of 2,000 over up to 9,000 742
+// against 745; the longest requests first, 700, 546 and 763.  Where the requests'
+// lengths differ so much that most pairs up to the length hint would be empty (a
+// prompt among single tokens), blocks are counted by rows and their requests
+// searched.
 //
 // Split (CL = true), for calls with few items and long key ranges: the key tiles
 // of one item are cut into runs, one per CTA of a cluster (item =
@@ -841,15 +845,17 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     item0 = (j % heads) * pairs + j / heads;
     stride = p.num_items;
   }
-  // DYN: block j's item (the whole warp; a head's later pairs first), or
-  // num_items where it has none
+  // DYN: block j's item (the whole warp; a request's later pairs first, all its
+  // heads of a pair one after another), or num_items where it has none
   auto item_of = [&](int j) -> int {
     const int pairs = (int)p.div_pairs.d;
     if constexpr (TAKE == 2)
       return item_by_rows(p.q_indptr, p.batch, p.num_kv_heads, p.num_units, (int)p.div_rows.d, pairs,
                           p.num_items, j);
-    const int q = (int)p.div_pairs.div((uint32_t)j);
-    return q * pairs + (pairs - 1 - (j - q * pairs));
+    const int t = (int)p.div_hkv.div((uint32_t)j), g = j - t * p.num_kv_heads;
+    const int b = (int)p.div_pairs.div((uint32_t)t);
+    const int pair = pairs - 1 - (t - b * pairs);
+    return (b * p.num_kv_heads + g) * pairs + pair;
   };
   int4* sched = reinterpret_cast<int4*>(smem + C::OFF_SCHED);
   auto sbar = [&](int i) -> uint32_t { return s_base + C::OFF_SCHED + 48 + 8 * i; };
