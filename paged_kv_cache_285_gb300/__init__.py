@@ -1,4 +1,5 @@
-"""Paged-KV attention for GB300 (sm_103a): a thin ctypes binding of libpkv.so.
+"""Paged-KV attention for GB300 (sm_103a): a thin binding of libpkv.so (ctypes;
+the block-scaled, gather and window calls through a compiled one, _calls.so).
 
 Every call here only marshals arguments (PyTorch tensors -> device pointers,
 the current CUDA stream) and forwards them to the C ABI declared in
