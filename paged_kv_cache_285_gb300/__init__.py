@@ -182,9 +182,11 @@ def load():
         # go through ctypes, 5 to 7 us more host time each.
         try:
             from . import _calls
+            if _calls.torch_version != torch.__version__:
+                raise ImportError(f"it is built for torch {_calls.torch_version}")
             _direct = _calls
         except ImportError as e:
-            warnings.warn(f"_calls.so does not load ({e}): rebuild with build.build()")
+            warnings.warn(f"_calls.so is not used ({e}): rebuild with build.build()")
         _lib = lib
         return lib
 

@@ -62,6 +62,7 @@ def _calls_cmd():
                  f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include",
                  f"-I{toolkit}/include", f"-I{sysconfig.get_paths()['include']}",
                  f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                 f'-DPKV_TORCH_VERSION="{torch.__version__}"',
                  "-c", CALLS_SRC, "-o", obj], os.path.join(root, "lib")
 
 
@@ -95,12 +96,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if force or jobs or _stale(CALLS, [calls_obj, LIB]):
+    stamp = os.path.join(BUILD, "calls.linked")  # the object that _calls.so was linked from
+    linked = open(stamp).read() if os.path.exists(stamp) else ""
+    if force or jobs or linked != calls_obj or _stale(CALLS, [calls_obj, LIB]):
         tmp = CALLS + f".tmp{os.getpid()}"
         run([shutil.which("g++") or "g++", "-shared", calls_obj, "-o", tmp, f"-L{HERE}",
              "-l:libpkv.so", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
              "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
         os.replace(tmp, CALLS)
+        with open(stamp, "w") as f:
+            f.write(calls_obj)
     return LIB
 
 

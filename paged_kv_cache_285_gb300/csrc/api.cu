@@ -623,7 +623,8 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
 // 170).
 static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_seq_len, int window,
                             int sink_tokens, int forced, int sm_count) {
-  const int len = visible_bound(max_seq_len, window, sink_tokens);
+  // (so far below 2^31 that whole splits stay below it too)
+  const int len = std::min(visible_bound(max_seq_len, window, sink_tokens), INT32_MAX - (1 << 21));
   const int tiles = std::max(1, ceil_div(len, kSubTokens));
   if (forced > 0 || tiles <= 4) return plan_decode(d, batch, hq, len, forced > 0 ? forced : 1, sm_count);
   const int sms = sm_count > 0 ? sm_count : 152;

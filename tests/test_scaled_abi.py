@@ -101,6 +101,9 @@ def test_decode_window_workspace_plan(lib):
     assert f(d, 2, 8, 1 << 30, 300, 4, 4) == lib.pkv_decode_workspace_bytes(d, 2, 8, 21 * 16, 4)
     # never more than the sequence itself
     assert f(d, 2, 8, 100, 1 << 30, 1 << 30, 4) == lib.pkv_decode_workspace_bytes(d, 2, 8, 100, 4)
+    # a bound near 2^31 is planned as one a little below it
+    for b in (1, 2, 64):
+        assert 0 < f(d, b, 8, 2 ** 31 - 1, 0, 0, 0) == f(d, b, 8, 2 ** 31 - 2 ** 21 - 1, 0, 0, 0)
     assert f(d, 2, 8, -1, 3, 0, 0) == 0 and f(d, 2, 8, 10, -1, 0, 0) == 0 and f(d, 2, 8, 10, 1, -1, 0) == 0
 
 
@@ -136,8 +139,8 @@ def test_binding_refusals(lib):
 
 
 def test_compiled_binding(lib):
-    # built and loaded; what is not on a device is left to the Python functions, which refuse it
-    assert pkv._direct is not None
+    # built for this torch and loaded; what is not on a device is left to the Python functions, which refuse it
+    assert pkv._direct is not None and pkv._direct.torch_version == torch.__version__
     t = torch.zeros(3)
     for name, n in [("append_block_scaled", 11), ("gather", 12), ("decode_window", 16), ("decode_block_scaled", 16),
                     ("extend_window", 17), ("extend_block_scaled", 17)]:
