@@ -767,6 +767,15 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
     ap.k_scales = view->k_scales;
     ap.v_scales = view->v_scales;
     ap.join_cluster = pl.cluster ? 1 : 0;
+    // Short sequences, one CTA each and more of them than fit at once in CTAs of
+    // four warps: twice as many of half the size overlap their fixed costs (setup,
+    // first copy, epilogue).  Block-scaled, 8 kv heads, four warps -> two: 128 x 64
+    // tokens 11.1 -> 8.4 us, 512 x 64 39.8 -> 28.0, 256 x 128 24.5 -> 19.3, 128 x 300
+    // 19.0 -> 17.3, 512 x 300 55.4 -> 46.3; 64 x 300 (fewer than a round) 10.0 -> 11.6,
+    // 256 x 600 43.0 -> 43.5, 256 x 1,024 58.5 -> 65.5.  Windows: fp8 512 x 128 65.3 ->
+    // 51.3, 128 x 256 26.6 -> 22.3, bf16 256 x 128 46.1 -> 42.8, 128 x 256 37.0 -> 38.2.
+    const int64_t ctas = (int64_t)batch * desc->num_kv_heads * ((group + 7) / 8);
+    ap.two_warps = !pl.cluster && pl.splits == 1 && pl.chunk <= 400 && ctas > 4 * ds->sm_count ? 1 : 0;
     ap.num_cuts = pl.num_cuts;
     std::copy(pl.cut, pl.cut + kMaxCuts + 1, ap.cut);
     e = launch_decode_window(kmap, vmap, p, ap, desc->head_dim, (int)desc->cache_dtype,

@@ -6,12 +6,14 @@ namespace pkv {
 
 namespace {
 
-template <int HD, int AT, bool WIN>
-cudaError_t launch_scaled(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
-                          const DecodeExtraParams& ap, cudaStream_t stream) {
-  return ap.join_cluster
-             ? launch_decode_t<HD, DT_E4M3, AT, false, 0, kNW, WIN, true, true>(kmap, vmap, p, ap, stream)
-             : launch_decode_t<HD, DT_E4M3, AT, false, 0, kNW, WIN, true>(kmap, vmap, p, ap, stream);
+template <int HD, int CT, int AT, bool WIN, bool BSC>
+cudaError_t launch_view(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
+                        const DecodeExtraParams& ap, cudaStream_t stream) {
+  if (ap.join_cluster)
+    return launch_decode_t<HD, CT, AT, false, 0, kNW, WIN, BSC, true>(kmap, vmap, p, ap, stream);
+  if (ap.two_warps)
+    return launch_decode_t<HD, CT, AT, false, 0, 2, WIN, BSC>(kmap, vmap, p, ap, stream);
+  return launch_decode_t<HD, CT, AT, false, 0, kNW, WIN, BSC>(kmap, vmap, p, ap, stream);
 }
 
 }  // namespace
@@ -25,13 +27,12 @@ cudaError_t launch_decode_window(const CUtensorMap& kmap, const CUtensorMap& vma
   if (ap.join_cluster && (p.num_splits < 2 || p.num_splits > 8)) return cudaErrorInvalidValue;
 #define PKV_WIN(HD, CT, AT)                                                              \
   if (head_dim == HD && cache_dt == CT && act_dt == AT && !scaled)                       \
-    return ap.join_cluster                                                               \
-               ? launch_decode_t<HD, CT, AT, false, 0, kNW, true, false, true>(kmap, vmap, p, ap, stream) \
-               : launch_decode_t<HD, CT, AT, false, 0, kNW, true, false>(kmap, vmap, p, ap, stream);
+    return launch_view<HD, CT, AT, true, false>(kmap, vmap, p, ap, stream);
 #define PKV_BSC(HD, AT)                                                                  \
   if (head_dim == HD && act_dt == AT && scaled)                                          \
-    return ap.window > 0 ? launch_scaled<HD, AT, true>(kmap, vmap, p, ap, stream)        \
-                         : launch_scaled<HD, AT, false>(kmap, vmap, p, ap, stream);
+    return ap.window > 0                                                                 \
+               ? launch_view<HD, DT_E4M3, AT, true, true>(kmap, vmap, p, ap, stream)     \
+               : launch_view<HD, DT_E4M3, AT, false, true>(kmap, vmap, p, ap, stream);
   PKV_WIN(64, DT_F16, DT_F16)
   PKV_WIN(64, DT_BF16, DT_BF16)
   PKV_WIN(64, DT_E4M3, DT_F16)

@@ -81,6 +81,7 @@ struct DecodeExtraParams {
   const float* k_scales;
   const float* v_scales;
   int join_cluster;  // window / block-scaled launches: the splits (2 .. 8) form clusters
+  int two_warps;     // window / block-scaled launches: CTAs of two warps, not four (no cluster)
   // window / block-scaled launches with splits of different lengths (at most
   // kMaxCuts; num_cuts 0: of p.chunk tokens each): split s takes tokens cut[s] ..
   // cut[s + 1] - 1; entries past the last are INT32_MAX

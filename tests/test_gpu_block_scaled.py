@@ -236,6 +236,22 @@ def test_decode_of_many_requests(cfg):
     assert pkv.get_device_error() == 3 and bool(torch.isfinite(again).all())
 
 
+@pytest.mark.parametrize("batch,hq,hkv,d,bs,act,most", [(90, 16, 8, 128, 16, BF16, 130), (80, 8, 8, 64, 32, F16, 400),
+                                                         (330, 36, 2, 64, 16, BF16, 70), (700, 2, 1, 128, 32, F16, 33)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (25, 2)])
+def test_decode_of_many_short_requests(batch, hq, hkv, d, bs, act, most, window, sinks):
+    # more CTAs than fit at once (CTAs of two warps)
+    lens = [int(n) for n in np.random.default_rng(batch).integers(0, most + 1, batch)]
+    lens[3], lens[batch - 1] = most, 0
+    c = Case(SCALED, act, hkv, d, bs, lens, seed=batch).cuda()
+    q = c.rows(batch, hq).cuda()
+    out, lse = run_decode(c, q, hq, lens, window, sinks)
+    ref = R.attention(*c.values(), to_f64(q), range(batch + 1), [n - 1 for n in lens], c.tables, hq, 1 / d ** 0.5, window,
+                      sinks)
+    check_attention(out, lse, ref, act, d)
+    assert pkv.get_device_error() == 0
+
+
 def test_decode_scales_of_any_size():
     # V scales 60 binary orders apart, and scales that are no powers of two
     c = Case(SCALED, BF16, 2, 128, 16, [300, 64], seed=3)

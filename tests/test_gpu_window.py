@@ -89,6 +89,23 @@ def test_decode_of_many_requests(cache, act, hq, hkv, d, window, sinks):
     check_attention(out, lse, ref, act, d)
 
 
+@pytest.mark.parametrize("cache,act,hq,hkv,d,window,sinks", [(BF16, BF16, 16, 4, 128, 128, 4), (F16, F16, 4, 4, 64, 300, 0),
+                                                               (E4M3, F16, 8, 4, 128, 64, 33), (E4M3, BF16, 4, 4, 64, 17, 1)])
+def test_decode_of_many_requests_in_a_short_window(cache, act, hq, hkv, d, window, sinks):
+    # more CTAs than fit at once (CTAs of two warps)
+    batch = 170
+    lens = [int(n) for n in np.random.default_rng(window).integers(0, 500, batch)]
+    c = Case(cache, act, hkv, d, 32, lens, seed=window)
+    q = c.rows(batch, hq).cuda()
+    give_back(c, [n - 1 for n in lens], window, sinks)
+    c.cuda()
+    out, lse = run_decode(c, q, hq, lens, window, sinks)
+    assert pkv.get_device_error() == 0
+    ref = R.attention(*c.values(), to_f64(q), range(batch + 1), [n - 1 for n in lens], c.tables, hq, 1 / d ** 0.5, window,
+                      sinks)
+    check_attention(out, lse, ref, act, d)
+
+
 def test_decode_of_a_whole_window_is_the_plain_decode():
     lens = [700, 33, 1]
     c = Case(BF16, BF16, 2, 128, 16, lens, seed=3).cuda()
