@@ -604,8 +604,8 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
 // Against the plain plan's runs (128 to 4,096 tokens, six rounds): block-scaled,
 // 16 x 4,096 tokens 39 -> 31 us, 8 x 5,000-20,000 50 -> 47, 1 x 100,000 69 -> 45,
 // 128 x 100-300 27.5 -> 21; windows: 32 x 1,024 (bf16) 37.6 -> 26.7, 128 x 4,096
-// (fp8) 179 -> 168.  (Since launches are set up while the one before runs: 29.5,
-// 45.5, 42.9, 19.8; 26.3, 168.)
+// (fp8) 179 -> 168.  (Since launches are set up while the one before runs: 29.3,
+// 46.2, 42.1, 17.1 with CTAs of two warps; 26.2, 167.)
 //
 // With a quarter of a round of items or more, a launch ends unevenly: the CTAs of
 // its last round are few, and a CTA alone reads at r1.  Splits of falling length
