@@ -1,5 +1,7 @@
 """GPU checks of the compiled binding of the block-scaled, gather and window calls: the same results
 and refusals as through the Python checks, and which arguments it leaves to them."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -297,4 +299,37 @@ def test_calls_wait_for_other_streams(name, captured):
                 work()
         torch.cuda.synchronize()
         assert all(torch.equal(bits(t), w) for t, w in zip(got, want))
+    assert pkv.get_device_error() == 0
+
+
+def test_calls_from_several_threads_at_once():
+    pkv.load()
+    # (the append first: appending the same rows again changes nothing)
+    one = Calls()
+    want = [[bits(t) for t in one.run(name)] for name in NAMES]
+    failures = []
+
+    def serve():
+        try:
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(stream):
+                calls = Calls()
+                for _ in range(30):
+                    for name, w in zip(NAMES, want):
+                        fn, a = calls.args(name)
+                        fn(**a)
+                        stream.synchronize()
+                        got = [a[x] for x in ("k_cache", "v_cache", "k_scales", "v_scales", "k_out", "v_out", "out",
+                                              "lse_out") if x in a]
+                        assert all(torch.equal(bits(t), x) for t, x in zip(got, w)), name
+        except BaseException as e:  # noqa: BLE001
+            failures.append(e)
+
+    threads = [threading.Thread(target=serve) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures[0]
     assert pkv.get_device_error() == 0
