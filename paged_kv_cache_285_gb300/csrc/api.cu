@@ -660,7 +660,7 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
     }
   }
   DecodePlan pl = plan_decode(d, batch, hq, len, best_s, sm_count);
-  if (best_cluster && pl.splits >= 2) {
+  if (best_cluster && pl.splits == best_s) {
     pl.cluster = true;
     pl.ws_bytes = 0;
   }

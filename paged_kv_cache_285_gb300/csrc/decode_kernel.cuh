@@ -55,10 +55,12 @@
 //     launch's CTAs in before this one's have ended gave nothing more (62.5
 //     against 62.1, 7.8 against 7.4).
 //   * splits joined in a cluster (CLM, few requests): the splits of one (request,
-//     head chunk) are the CTAs of a cluster.  Each leaves its heads' (max, sum,
-//     unnormalised O) in shared memory, and after a cluster barrier each adds up
-//     its share of the outputs, reading the others' over the cluster: no
-//     workspace and no second launch.
+//     head chunk) are the CTAs of a cluster.  Each writes its heads' (max, sum,
+//     unnormalised O) into the shared memory of the CTAs that own the outputs, and
+//     after a cluster barrier each adds up its share: no workspace and no second
+//     launch.  3 requests of up to 700 tokens 4.7 us, 4 in a window of 1,024 6.8
+//     (parts read from the CTAs that hold them, between two barriers: 5.0, 7.4; one
+//     split 8.3, 14.3; splits merged by a second launch 5.4, 7.7 at best).
 //   * warps are combined through shared memory with their (max, sum); a split
 //     either writes the final output (single-split requests) or a normalised
 //     partial plus its log-sum-exp, merged by merge_kernel.
@@ -89,6 +91,8 @@ struct DecodeCfg {
   static constexpr int AREA = STAGE_AREA > COMB_BYTES ? STAGE_AREA : COMB_BYTES;
   static constexpr int SMEM = 1024 /*align slack*/ + AREA + NW * NS * 8;
   static constexpr int SMEM_BSC = SMEM + NW * NS * 8;  // and a tile's two scales per stage
+  // CLM: and the parts of 2, 4 or 8 splits
+  static constexpr int PARTS = (8 * HD > 8 * 128 ? 8 * HD : 8 * 128) * 4 + 8 * 16 * 4;
 };
 
 // Byte offset of (token t, row byte x) inside a staged tile, matching the TMA
@@ -208,6 +212,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   static_assert(!(CASC && (WIN || BSC)) && (!BSC || CT == DT_E4M3), "unsupported combination");
   using C = DecodeCfg<HD, CT, NW, NS>;
   extern __shared__ uint8_t smem_raw[];
+  if constexpr (CLM) cluster_arrive_relaxed();
   if constexpr (LEAN) grid_dependency_wait();
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -255,13 +260,17 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     n = ws.nv;
   }
   const int t0 = tb + split_begin<CUT>(p, ap, split);
-  // CLM: this CTA's share of the outputs from the parts of the cluster's active
-  // CTAs, [8][HD] O and [2][8] (max, sum) at the start of their shared memory
+  // CLM: the CTAs of the cluster write their parts into shared memory of the CTA
+  // that sums them up: element idx of the heads' [GC][HD] outputs belongs to rank
+  // (idx / 128) % splits.  parts: [rank][8 HD / splits], then [rank][2][8] (max, sum).
+  float* parts = reinterpret_cast<float*>(smem + C::AREA + NW * NS * 8 * (BSC ? 2 : 1));
   auto join_cluster = [&]() {
-    cluster_sync();
+    static_assert(!CLM || NW * 32 == 128, "one thread per element of a run");
+    cluster_sync();  // every part is here; no shared memory of another CTA is touched from now on
     const int active = (n + p.chunk - 1) / p.chunk, S = p.num_splits;
-    const uint32_t o_at = smem_u32(smem), ml_at = o_at + 8 * HD * 4;
-    for (int idx = split * (NW * 32) + (int)threadIdx.x; idx < GC * HD; idx += S * NW * 32) {
+    const int stride = (8 * HD / 128 + S - 1) / S * 128;
+    const float* ml = parts + S * stride;
+    for (int at = threadIdx.x, idx = split * 128 + at; idx < GC * HD; at += 128, idx += S * 128) {
       const int jh = idx / HD, d = idx % HD;
       constexpr int MAXC = 8;
       float m[MAXC], l[MAXC], o[MAXC], mstar = -INFINITY;
@@ -270,9 +279,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         m[c] = -INFINITY;
         l[c] = o[c] = 0.f;
         if (c < active) {
-          m[c] = cluster_ld(cluster_map(ml_at + jh * 4, c));
-          l[c] = cluster_ld(cluster_map(ml_at + 32 + jh * 4, c));
-          o[c] = cluster_ld(cluster_map(o_at + idx * 4, c));
+          m[c] = ml[c * 16 + jh];
+          l[c] = ml[c * 16 + 8 + jh];
+          o[c] = parts[c * stride + at];
         }
       }
 #pragma unroll
@@ -290,8 +299,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       store_act<AT>(p.out, bh * HD + d, (O / L) * p.out_scale);
       if (p.lse_out && d == 0) p.lse_out[bh] = (mstar + log2f(L)) * kLn2;
     }
-    cluster_sync();  // no CTA leaves while another reads its shared memory
   };
+  if constexpr (CLM) cluster_wait();  // (of the arrival above) every CTA of the cluster runs
   if constexpr (CLM) {
     if (t0 >= n && n > p.chunk) {  // nothing here, but the cluster has more than one part
       join_cluster();
@@ -747,30 +756,28 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
   if constexpr (CLM) {
     if (nsplit_b > 1) {
-      // (an element's sums over the warps are read by the thread that replaces them)
-      float* sm_ml = sm_o + 8 * HD;  // over warp 1's rows: read before it is written
-      for (int idx = threadIdx.x; idx < 8 * HD; idx += NW * 32) {
-        const int jh = idx / HD;
+      const int S = p.num_splits, stride = (8 * HD / 128 + S - 1) / S * 128;
+      for (int idx = threadIdx.x; idx < GC * HD; idx += 128) {
+        const int jh = idx / HD, run = idx / 128;
         float mstar = -INFINITY, O = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) mstar = fmaxf(mstar, sm_m[w * 8 + jh]);
 #pragma unroll
         for (int w = 0; w < NW; ++w)
           O += fast_exp2(sm_m[w * 8 + jh] - mstar) * sm_o[w * 8 * HD + idx];
-        sm_o[idx] = O;
+        cluster_st(cluster_map(smem_u32(parts + split * stride + run / S * 128 + idx % 128), run % S), O);
       }
-      float mstar = -INFINITY, L = 0.f;
-      if (threadIdx.x < 8) {
+      if ((int)threadIdx.x < S * 16) {  // thread 16 c + 8 q + jh: (max, sum)[q] of head jh to rank c
+        const int jh = threadIdx.x & 7;
+        float mstar = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) mstar = fmaxf(mstar, sm_m[w * 8 + threadIdx.x]);
+        for (int w = 0; w < NW; ++w) mstar = fmaxf(mstar, sm_m[w * 8 + jh]);
 #pragma unroll
         for (int w = 0; w < NW; ++w)
-          L += fast_exp2(sm_m[w * 8 + threadIdx.x] - mstar) * sm_l[w * 8 + threadIdx.x];
-      }
-      __syncthreads();
-      if (threadIdx.x < 8) {
-        sm_ml[threadIdx.x] = mstar;
-        sm_ml[8 + threadIdx.x] = L;
+          L += fast_exp2(sm_m[w * 8 + jh] - mstar) * sm_l[w * 8 + jh];
+        cluster_st(cluster_map(smem_u32(parts + S * stride + split * 16 + (threadIdx.x & 15)),
+                               threadIdx.x >> 4),
+                   threadIdx.x & 8 ? L : mstar);
       }
       join_cluster();
       return;
@@ -953,7 +960,7 @@ cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
   constexpr int NS = NSO > 0 ? NSO : stages_for<HD, CT>();
   using C = DecodeCfg<HD, CT, NW, NS>;
   auto kern = decode_kernel<HD, CT, AT, NW, NS, CASC, WIN, BSC, CLM>;
-  constexpr int smem = BSC ? C::SMEM_BSC : C::SMEM;
+  constexpr int smem = (BSC ? C::SMEM_BSC : C::SMEM) + (CLM ? C::PARTS : 0);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.num_kv_heads * ((p.group + 7) / 8), p.batch, p.num_splits);

@@ -24,7 +24,8 @@ cudaError_t launch_decode_window(const CUtensorMap& kmap, const CUtensorMap& vma
   const bool scaled = ap.k_scales != nullptr;
   if (scaled && (!ap.v_scales || cache_dt != DT_E4M3)) return cudaErrorInvalidValue;
   if (!scaled && ap.window <= 0) return cudaErrorInvalidValue;
-  if (ap.join_cluster && (p.num_splits < 2 || p.num_splits > 8)) return cudaErrorInvalidValue;
+  if (ap.join_cluster && p.num_splits != 2 && p.num_splits != 4 && p.num_splits != 8)
+    return cudaErrorInvalidValue;
 #define PKV_WIN(HD, CT, AT)                                                              \
   if (head_dim == HD && cache_dt == CT && act_dt == AT && !scaled)                       \
     return launch_view<HD, CT, AT, true, false>(kmap, vmap, p, ap, stream);

@@ -80,7 +80,7 @@ struct DecodeExtraParams {
   int sink_tokens;
   const float* k_scales;
   const float* v_scales;
-  int join_cluster;  // window / block-scaled launches: the splits (2 .. 8) form clusters
+  int join_cluster;  // window / block-scaled launches: the splits (2, 4 or 8) form clusters
   int two_warps;     // window / block-scaled launches: CTAs of two warps, not four (no cluster)
   // window / block-scaled launches with splits of different lengths (at most
   // kMaxCuts; num_cuts 0: of p.chunk tokens each): split s takes tokens cut[s] ..
