@@ -479,6 +479,13 @@ pkv_status pkv_paged_extend_attn_append(const pkv_cache_desc* desc, void* k_cach
  * desc->cache_dtype must be PKV_FP8_E4M3 (else PKV_ERR_UNSUPPORTED);
  * desc->k_scale / v_scale are not used (finite and > 0 all the same).
  *
+ * Stream order: the kernels of these calls, of pkv_kv_gather and of the window
+ * calls are set up while the kernel before them in the stream still runs and
+ * wait for its end before their first access to memory; for the caller that is
+ * stream order as everywhere.  (A kernel of the caller's that was itself
+ * launched so has to wait for its predecessor likewise, or the order of three
+ * is not kept.)
+ *
  * pkv_kv_append_block_scaled -- quantise the K/V rows of new tokens into their
  * blocks.
  *
