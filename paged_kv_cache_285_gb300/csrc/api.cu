@@ -596,16 +596,19 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
 // Split plan of a decode call through a view, from what a CTA and an SM do (us;
 // four CTAs fit an SM): a CTA alone goes through r1 tokens per us (100 at 128
 // dims, 160 at 64: the latency of its four warps' tiles), an SM through its
-// share of the bandwidth, whatever its CTAs.  A launch costs its full rounds of
-// CTAs, then the last round (5.5 more each), and a fixed part: 5, 7 for splits
-// joined in a cluster, 8 with a merge launch (and more for long rows of
-// partials).  Under a window the sequences are taken as all of the bound's
+// share of the bandwidth, whatever its CTAs (in a window, 1.25 times its share
+// while others have fewer).  A launch costs its full rounds of CTAs, then the last
+// round (5.5 more each), and a fixed part: 5, 6 for splits joined in a cluster, 8
+// with a merge launch (and more for long rows of partials).  Under a window the sequences are taken as all of the bound's
 // length, else for a third as that, for the rest as spread evenly up to it.
 // Against the plain plan's runs (128 to 4,096 tokens, six rounds): block-scaled,
 // 16 x 4,096 tokens 39 -> 31 us, 8 x 5,000-20,000 50 -> 47, 1 x 100,000 69 -> 45,
 // 128 x 100-300 27.5 -> 21; windows: 32 x 1,024 (bf16) 37.6 -> 26.7, 128 x 4,096
 // (fp8) 179 -> 168.  (Since launches are set up while the one before runs: 29.3,
-// 46.2, 42.1, 17.1 with CTAs of two warps; 26.2, 167.)
+// 46.2, 42.1, 17.1 with CTAs of two warps; 26.2, 167.  With no more
+// than its share for an SM of a window's last round, and 7 for a cluster: bf16 8 x
+// 1,024 11.3 us where it is 9.7 now, 24 x 1,024 27.1 and 21.8, 4 x 4,096 17.3 and
+// 15.1, 1 x 4,096 9.1 and 9.5.)
 //
 // With a quarter of a round of items or more, a launch ends unevenly: the CTAs of
 // its last round are few, and a CTA alone reads at r1.  Splits of falling length
@@ -629,7 +632,8 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   if (forced > 0 || tiles <= 4) return plan_decode(d, batch, hq, len, forced > 0 ? forced : 1, sm_count);
   const int sms = sm_count > 0 ? sm_count : 152;
   const double items = (double)batch * d->num_kv_heads * ((hq / d->num_kv_heads + 7) / 8);
-  const double r1 = d->head_dim == 128 ? 100.0 : 160.0;
+  const double r1 = d->head_dim != 128 ? 160.0 : window > 0 ? 90.0 : 100.0;
+  const double over = window > 0 ? 1.25 : 1.0;
   const double sm_rate = 44600.0 / (2.0 * d->head_dim * elem_bytes(d->cache_dtype));
   const double slots = 4.0 * sms;
   double best = 1e30;
@@ -643,7 +647,9 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
     const double tokens = 16.0 * chunk;
     const double ctas = items * s, full = std::floor(ctas / slots), rest = ctas - full * slots;
     double cost = full * (tokens * 4 / sm_rate + 5.5);
-    if (rest > 0) cost += tokens / std::min(r1, sm_rate / std::ceil(rest / sms)) + 5.5;
+    if (rest > 0)
+      cost += std::max(tokens / std::min(r1, over * sm_rate / std::ceil(rest / sms)),
+                       rest * tokens / (sm_rate * sms)) + 5.5;
     if (window <= 0) {
       const double some = items * (s + 1) * 0.5, k = std::min(4.0, std::ceil(some / sms));
       const double one = tokens / std::min(r1, sm_rate / k);
@@ -652,7 +658,7 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
       cost = 0.35 * cost + 0.65 * spread;
     }
     const bool cl = s >= 2 && s <= 8 && (s & (s - 1)) == 0 && items * s <= 0.75 * slots;
-    cost += s == 1 ? 5.0 : cl ? 7.0 : 8.0 + 0.2 * std::max(0, s - 8);
+    cost += s == 1 ? 5.0 : cl ? 6.0 : 8.0 + 0.2 * std::max(0, s - 8);
     if (cost < best) {
       best = cost;
       best_s = s;

@@ -58,7 +58,7 @@
 //     head chunk) are the CTAs of a cluster.  Each writes its heads' (max, sum,
 //     unnormalised O) into the shared memory of the CTAs that own the outputs, and
 //     after a cluster barrier each adds up its share: no workspace and no second
-//     launch.  3 requests of up to 700 tokens 4.7 us, 4 in a window of 1,024 6.8
+//     launch.  3 requests of up to 700 tokens 4.7 us, 4 in a window of 1,024 6.3
 //     (parts read from the CTAs that hold them, between two barriers: 5.0, 7.4; one
 //     split 8.3, 14.3; splits merged by a second launch 5.4, 7.7 at best).
 //   * warps are combined through shared memory with their (max, sum); a split
