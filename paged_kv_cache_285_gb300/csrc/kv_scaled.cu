@@ -127,16 +127,26 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const AppendScaledPa
     b = (int)p.div_units.div((uint32_t)unit);
     j = unit - b * p.units_per_request;
   } else {
+    if (unit < p.batch && h == 0 && !isv && lane == 0) {
+      // where q_indptr falls, the search need not come to the request that does:
+      // the first units (there are more than requests) look at its entries in order
+      const int at = *(p.q_indptr + unit), next = *(p.q_indptr + unit + 1);
+      if (at < 0 || next < at) set_err(p.err, 3);
+    }
     b = find_unit(p, unit);
     j = unit - ((*(p.q_indptr + b) >> p.bs_shift) + 2 * b);
   }
   const int r0 = *(p.q_indptr + b), r1 = *(p.q_indptr + b + 1);
   const int P = *(p.prefix_lens + b);
-  int S = r1 - r0;
-  if (S == 0 || j < 0 || j > (S >> p.bs_shift) + 2) return;
+  if (r1 == r0) return;
   const bool report = j == 0 && h == 0 && !isv && lane == 0;
-  if (r0 < 0 || r1 < r0 || r1 > p.total_rows || P < 0 ||
-      (int64_t)P + S > min((int64_t)p.max_blocks * BS, (int64_t)INT32_MAX - 128)) {
+  if (r0 < 0 || r1 < r0 || r1 > p.total_rows) {
+    if (report) set_err(p.err, 3);
+    return;
+  }
+  int S = r1 - r0;
+  if (j < 0 || j > (S >> p.bs_shift) + 2) return;
+  if (P < 0 || (int64_t)P + S > min((int64_t)p.max_blocks * BS, (int64_t)INT32_MAX - 128)) {
     if (report) set_err(p.err, 3);
     return;
   }
