@@ -742,6 +742,10 @@ __device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, cons
   }
 }
 
+// CL: whether a row has seen a key in a part of (max, sum) ml.  Maxima pass NaN over, so a
+// part all of whose scores are NaN keeps -inf as its max; its sum is NaN.
+__device__ __forceinline__ bool has_keys(const float2& ml) { return ml.x != -INFINITY || ml.y != 0.f; }
+
 // CL: this CTA's share of the item's 2 x 128 rows (row R belongs to CTA R mod
 // splits, as its row R / splits) out of the parts that the cluster's CTAs left at
 // co [parts][share][HD] (fp32) and ml [parts][share] (max, sum): one part per CTA,
@@ -770,12 +774,12 @@ __device__ __forceinline__ void combine_parts(const ExtendParams& p, const Split
     for (int k = 0; k < C; ++k) m = fmaxf(m, ml[k * share + lr].x);
     for (int k = 0; k < C; ++k) {
       const float2 s = ml[k * share + lr];
-      if (s.x != -INFINITY) l += fast_exp2(s.x - m) * s.y;
+      if (has_keys(s)) l += fast_exp2(s.x - m) * s.y;
     }
-    const float mine = ml[tid].x;
+    const float2 mine = ml[tid];
     asm volatile("bar.sync 1, 256;" ::: "memory");
     // (a part without a key has weight 0 and was not written)
-    ml[tid].x = mine != -INFINITY ? fast_exp2(mine - m) * (p.out_scale / l) : 0.f;
+    ml[tid].x = has_keys(mine) ? fast_exp2(mine.x - m) * (p.out_scale / l) : 0.f;
     const int64_t q = p.lse_out && c == 0 ? out_row(lr) : -1;
     if (q >= 0) p.lse_out[q] = (m + log2f(l)) * kLn2f;
     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1241,7 +1245,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const uint32_t part = HALF ? cluster_rank() * 2 + x : cluster_rank();
       cluster_st2(cluster_map(s_base + C::OFF_Q + (part * share + (row >> sh)) * 8, row & cmask),
                   make_float2(m_fin, l_fin));
-      const uint32_t send = __ballot_sync(0xFFFFFFFFu, m_fin != -INFINITY && rtok < fin.ntok[x]);
+      const uint32_t send = __ballot_sync(0xFFFFFFFFu, has_keys(make_float2(m_fin, l_fin)) && rtok < fin.ntok[x]);
       if (send != 0u) {
         uint8_t* stg = smem + C::OFF_Q + 4096 + (x * 4 + qw) * 4096;
 #pragma unroll 1
