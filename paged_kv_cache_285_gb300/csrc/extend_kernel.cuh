@@ -265,7 +265,14 @@ __device__ __forceinline__ void conv_tile16(uint8_t* tile, int ct, int key0, int
                                             int h1 = 0) {
   constexpr int PER = BN * HD * 2 / 16 / NCONV;  // 16-byte units per thread
   uint4* v4 = reinterpret_cast<uint4*>(tile);
-  if constexpr (TAIL) {
+  if constexpr (WIN && !CVT) {  // (nothing to convert: only the zeros are written)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int uu = ct + i * NCONV;
+      const int key = key0 + ((uu * 16) % CHUNK) / 128;
+      if (key >= kv_end || (key >= h0 && key < h1)) v4[uu] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  } else if constexpr (TAIL) {
 #pragma unroll 4
     for (int i = 0; i < PER; ++i) {
       const int uu = ct + i * NCONV;
@@ -1662,9 +1669,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           if (!mbar_wait(bar(C::B_VFULL + s), ph)) { ok = false; break; }
           // keys at or past the segment's end are zeroed (a shared prefix's
           // last tile reaches into one member's own keys, which no row of the
-          // segment sees)
+          // segment sees; WIN: the item's end, later tokens being other items')
           const int kbase = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, CL>(it, kt);
-          const int kv_end = SX ? si.sg.kv_total : it.kv_total;
+          const int kv_end = SX ? si.sg.kv_total : WIN ? it.k_hi : it.kv_total;
           // WIN: keys between the sinks and the first row's window too
           bool zero = kbase + t >= kv_end, hole = false;
           if constexpr (WIN) {

@@ -65,3 +65,24 @@ def test_a_key_that_is_nan_alone_in_its_part(cache, act, d, bs, window):
     ref = P.attention(*c.values(), to_f64(q), ip, [896, 896], c.tables, 8, 1 / d ** 0.5, window)
     ref = (ref[0][1:], ref[1][1:], {k: v[1:] for k, v in ref[2].items()})
     check_attention(out[1:], lse[1:], ref, act, d)
+
+
+@pytest.mark.parametrize("cache,act,d,bs", [(BF16, BF16, 128, 16), (BF16, BF16, 64, 32), (F16, F16, 128, 32),
+                                            (E4M3, BF16, 64, 16), (E4M3, F16, 128, 16), (SCALED, BF16, 128, 16),
+                                            (SCALED, F16, 64, 32)])
+@pytest.mark.parametrize("prefix,window,sinks", [(37, 4096, 0), (46, 50, 3), (1005, 4096, 0), (990, 300, 7)])
+def test_values_of_later_tokens_that_no_row_of_an_item_sees(cache, act, d, bs, prefix, window, sinks):
+    # 4 heads a kv head: items of 64 rows.  The token after the first item's last one lies in that
+    # one's 16 tokens: its V (NaN) is the second item's alone, whose rows all see it
+    c = Case(cache, act, 2, d, bs, [prefix + 90], seed=prefix).cuda()
+    assert (prefix + 64) % 16
+    q = c.rows(90, 8).cuda()
+    put_nan(c, c.v, 0, prefix + 64)
+    out, lse, ip = extend(c, q, [90], [prefix], window, sinks)
+    assert pkv.get_device_error() == 0
+    vals = c.values()
+    vals[1] = np.nan_to_num(vals[1])
+    ref = P.attention(*vals, to_f64(q), ip, [prefix], c.tables, 8, 1 / d ** 0.5, window, sinks)
+    ref = (ref[0][:64], ref[1][:64], {k: v[:64] for k, v in ref[2].items()})
+    check_attention(out[:64], lse[:64], ref, act, d)
+    assert bool(torch.isnan(out[64:]).all())
