@@ -2,7 +2,8 @@
 
 Each .cu (and host-only .cpp) under csrc/ is compiled in parallel to an object under _build/, then
 linked (static CUDA runtime) into paged_kv_cache_285_gb300/libpkv.so.  bind/calls.cpp, the binding
-of the small calls, becomes _calls.so against libpkv.so and the installed torch.
+of the small calls, becomes _calls.so against libpkv.so and the installed torch; where that cannot
+be built, a warning says so and the library stands without it.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -66,6 +68,28 @@ def _calls_cmd():
                  "-c", CALLS_SRC, "-o", obj], os.path.join(root, "lib")
 
 
+def _link_calls(run, force, calls_obj, torch_lib, made):
+    """Links _calls.so where it is not that object's; None, or what went wrong."""
+    stamp = os.path.join(BUILD, "calls.linked")  # the object that _calls.so was linked from
+    linked = ""
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            linked = f.read()
+    if not (force or made or linked != calls_obj or _stale(CALLS, [calls_obj, LIB])):
+        return None
+    tmp = CALLS + f".tmp{os.getpid()}"
+    try:
+        run([shutil.which("g++") or "g++", "-shared", calls_obj, "-o", tmp, f"-L{HERE}",
+             "-l:libpkv.so", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+             "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+    except (OSError, RuntimeError) as e:
+        return e
+    os.replace(tmp, CALLS)
+    with open(stamp, "w") as f:
+        f.write(calls_obj)
+    return None
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -78,10 +102,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(obj, [src] + headers):
             jobs.append([cc, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj])
 
-    calls_obj, calls_cmd, torch_lib = _calls_cmd()
-    if force or _stale(calls_obj, [CALLS_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
-        jobs.append(calls_cmd)
-
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:
@@ -89,23 +109,33 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"{os.path.basename(cmd[0])} failed on {cmd[-3]}")
 
-    if jobs:
-        with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            list(ex.map(run, jobs))
+    # The binding is optional (the package has the same calls through ctypes): what stands in its
+    # way, a missing g++, Python.h or torch's headers, does not keep the library from being built.
+    def compile_calls():
+        try:
+            calls_obj, calls_cmd, torch_lib = _calls_cmd()
+            made = force or _stale(calls_obj, [CALLS_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+            if made:
+                run(calls_cmd)
+            return calls_obj, torch_lib, made
+        except (ImportError, OSError, RuntimeError) as e:
+            return e
+
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(compile_calls)
+        list(ex.map(run, jobs))
+        calls = calls.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    stamp = os.path.join(BUILD, "calls.linked")  # the object that _calls.so was linked from
-    linked = open(stamp).read() if os.path.exists(stamp) else ""
-    if force or jobs or linked != calls_obj or _stale(CALLS, [calls_obj, LIB]):
-        tmp = CALLS + f".tmp{os.getpid()}"
-        run([shutil.which("g++") or "g++", "-shared", calls_obj, "-o", tmp, f"-L{HERE}",
-             "-l:libpkv.so", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
-             "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
-        os.replace(tmp, CALLS)
-        with open(stamp, "w") as f:
-            f.write(calls_obj)
+    if not isinstance(calls, Exception):
+        calls = _link_calls(run, force or bool(jobs), *calls)
+    if isinstance(calls, Exception):
+        for left in (CALLS, os.path.join(BUILD, "calls.linked")):  # made for another library
+            if os.path.exists(left):
+                os.remove(left)
+        warnings.warn(f"_calls.so was not built ({calls}): the small calls go through ctypes")
     return LIB
 
 
