@@ -562,9 +562,11 @@ pkv_status pkv_kv_gather(const pkv_cache_desc* desc, const void* k_cache, const 
  * pkv_paged_decode_attn_window -- pkv_paged_decode_attn under a window: the
  * query is at position seq_lens[b] - 1.  A long sequence costs what its visible
  * tokens cost.  max_seq_len bounds seq_lens as there, and the workspace is
- * pkv_decode_window_workspace_bytes() (window 0: no window): 0 where the call's
- * plan has one split or joins its splits in clusters, and not monotonic in the
- * batch or the lengths -- size it for the arguments of the call.
+ * pkv_decode_window_workspace_bytes() (window 0: no window).  With num_splits 0
+ * that serves every smaller batch and bound too (of the same heads, window and
+ * sinks), so that a server sizes it once; a call whose plan has one split or
+ * joins its splits in clusters leaves it alone.  With num_splits given it is
+ * that call's own.
  * ------------------------------------------------------------------------- */
 size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
                                          int32_t num_q_heads, int32_t max_seq_len, int32_t window,

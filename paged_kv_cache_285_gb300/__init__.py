@@ -687,7 +687,8 @@ def kv_gather(k_cache, v_cache, k_out, v_out, row_indptr, start_positions, block
 def decode_window_workspace_bytes(k_cache, batch, num_q_heads, max_seq_len, window=0,
                                   sink_tokens=0, num_splits=0) -> int:
     """pkv_decode_window_workspace_bytes: the workspace of paged_decode_attn_window and
-    paged_decode_attn_block_scaled."""
+    paged_decode_attn_block_scaled; with num_splits 0 it serves every smaller batch and max_seq_len
+    too."""
     desc = _desc(k_cache, 1.0, 1.0)
     return int(load().pkv_decode_window_workspace_bytes(ctypes.byref(desc), batch, num_q_heads,
                                                         max_seq_len, window, sink_tokens,

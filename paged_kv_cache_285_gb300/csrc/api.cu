@@ -697,6 +697,24 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   return pl;
 }
 
+// Bytes that serve the automatic plan of every batch up to `batch` with every bound
+// up to max_seq_len (plans come and go with both: 512 requests of 4,096 tokens take
+// one split each and no workspace, 400 take partials).  plan_view's splits: at most
+// 2 slots / items + 8, and of 64 tokens at least; those of falling length at most
+// kMaxCuts, of 192.  Both bounds, times the batch, grow with it.
+static size_t view_workspace_bound(const pkv_cache_desc* d, int batch, int hq, int max_seq_len,
+                                   int window, int sink_tokens, int sm_count) {
+  static_assert(kMaxCuts <= 8, "the bound below");
+  const int len = std::min(visible_bound(max_seq_len, window, sink_tokens), INT32_MAX - (1 << 21));
+  const int tiles = ceil_div(len, kSubTokens);
+  if (tiles / 4 < 2) return 0;
+  const double ctas = (double)d->num_kv_heads * ((hq / d->num_kv_heads + 7) / 8);  // of a request's split
+  const double slots = 4.0 * (sm_count > 0 ? sm_count : 152);
+  const double splits = std::min((double)batch * (tiles / 4), 2.0 * slots / ctas + 8.0 * batch);
+  const size_t rows = (size_t)splits * (size_t)hq;  // partials: splits of all requests x heads
+  return align256(rows * d->head_dim * sizeof(float)) + rows * sizeof(float);
+}
+
 // Decode, optionally with the current token's K/V (k_new/v_new, [B][Hkv][D]
 // act dtype) appended to position seq_len-1 inside the decode kernel, or
 // through a view (a window and / or scales per block).
@@ -827,9 +845,11 @@ size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* desc, int32_t bat
     return 0;
   cudaError_t e;
   DeviceState* ds = device_state(&e);
-  return plan_view(desc, batch, num_q_heads, max_seq_len, window, sink_tokens, num_splits,
-                   ds ? ds->sm_count : 0)
-      .ws_bytes;
+  const int sm_count = ds ? ds->sm_count : 0;
+  if (num_splits > 0)
+    return plan_view(desc, batch, num_q_heads, max_seq_len, window, sink_tokens, num_splits, sm_count)
+        .ws_bytes;
+  return view_workspace_bound(desc, batch, num_q_heads, max_seq_len, window, sink_tokens, sm_count);
 }
 
 pkv_status pkv_paged_decode_attn_window(const pkv_cache_desc* desc, const void* k_cache,
