@@ -62,11 +62,15 @@ def launches(names):
 
 
 def profiled(call):
-    """call()'s result, and launches() of the kernels that it ran: None where no tracer is to be had."""
+    """call()'s result, and launches() of the kernels that it ran (None where no tracer is to be had).
+    call() may be made twice."""
     import torch
     from torch.profiler import ProfilerActivity, profile
-    with profile(activities=[ProfilerActivity.CUDA]) as prof:
-        result = call()
-        torch.cuda.synchronize()
-    names = [e.name for e in prof.events() if "pkv::" in e.name]
-    return result, launches(names) if names else None
+    for _ in range(2):  # (a tracer's first use may come too late for its kernels)
+        with profile(activities=[ProfilerActivity.CUDA]) as prof:
+            result = call()
+            torch.cuda.synchronize()
+        names = [e.name for e in prof.events() if "pkv::" in e.name]
+        if names:
+            return result, launches(names)
+    return result, None
