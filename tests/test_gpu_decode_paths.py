@@ -135,3 +135,37 @@ def test_a_step_in_a_graph_and_on_two_streams_with_its_lse():
             s.lse.fill_(float("nan"))
         torch.cuda.synchronize()
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("cache,act,d,bs", KINDS)
+@pytest.mark.parametrize("lens", [[700, 33, 1], [20, 40, 64], [700, 300, 9] + [50] * 77])
+def test_nan_comes_out_as_nan(cache, act, d, bs, lens):
+    # a query that is NaN, and a key and a value of a visible token that are: their rows' outputs
+    # alone are NaN, in clusters, with partials and in one split
+    c = Case(cache, act, 2, d, bs, lens, seed=len(lens))
+    bad = 0x7F if c.k.dtype == torch.uint8 else float("nan")
+    at = lens[1] // 2
+    c.k[int(c.tables[1, at // bs]), 0, at % bs] = bad        # request 1, kv head 0
+    c.v[int(c.tables[1, at // bs]), 1, at % bs] = bad        # request 1, kv head 1
+    q = c.rows(len(lens), 8)
+    q[2, 5, 7] = float("nan")
+    c.cuda()
+    q = q.cuda()
+    nan = np.zeros((len(lens), 8), bool)
+    nan[1], nan[2, 5] = True, True
+    for splits in (0, 1, 5):
+        out, lse = (torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"))
+        ws = torch.full((max(pkv.decode_window_workspace_bytes(c.k, len(lens), 8, max(lens), 4096, 0, splits), 1),), 0xFF,
+                        dtype=torch.uint8, device="cuda")
+        args = (q, out, c.bt, ints(lens), 1 / d ** 0.5, max(lens))
+        if cache == SCALED:
+            pkv.paged_decode_attn_block_scaled(c.k, c.v, c.ks, c.vs, *args, num_splits=splits, lse_out=lse, workspace=ws)
+        else:
+            pkv.paged_decode_attn_window(c.k, c.v, *args, 4096, k_scale=c.k_scale, v_scale=c.v_scale, num_splits=splits,
+                                         lse_out=lse, workspace=ws)
+        assert pkv.get_device_error() == 0
+        got = torch.isnan(out).all(-1).cpu().numpy()
+        assert np.array_equal(got, nan) and np.array_equal(torch.isnan(out).any(-1).cpu().numpy(), nan)
+        nan_lse = nan.copy()
+        nan_lse[1, 4:] = False                               # (V does not enter it)
+        assert np.array_equal(torch.isnan(lse).cpu().numpy(), nan_lse)

@@ -229,3 +229,47 @@ def test_values_under_small_scales(act, rows, prefix):
                                        max(p + n for p, n in zip(prefix, rows)), lse_out=lse)
     check_attention(out, lse, ref, act, 64)
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", [WIDE[0], WIDE[3], WIDE[4], WIDE[7]], ids=[WIDE_IDS[i] for i in (0, 3, 4, 7)])
+def test_widened_pages_in_two_graphs_of_one_workspace(kind):
+    # two captured calls, replayed in turn over one workspace, with the pools' contents changed between
+    cache, act, d, bs, window, sinks = kind
+    rows, prefix = [125, 128, 1, 0, 120], [40, 7, 300, 5, 0]
+    calls = [Call(cache, act, 256, 8, d, bs, rows, [p + 16 * i for p in prefix], window, sinks, seed=i + d) for i in range(2)]
+    ws = torch.empty(max(c.need for c in calls), dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for call in calls:
+        c, out = call.c, torch.empty_like(call.q)
+        args = (call.q, out, *call.layout, c.bt, 1 / d ** 0.5, max(rows), max(p + n for p, n in zip(call.prefix, rows)))
+
+        def step():
+            if cache == SCALED:
+                pkv.paged_extend_attn_block_scaled(c.k, c.v, c.ks, c.vs, *args, window=window, sink_tokens=sinks, workspace=ws)
+            else:
+                pkv.paged_extend_attn_window(c.k, c.v, *args, window, sinks, k_scale=c.k_scale, v_scale=c.v_scale,
+                                             workspace=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                step()
+        graphs.append(graph)
+        outs.append(out)
+    for turn in range(3):
+        for out in outs:
+            out.fill_(7.0)
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for call, out in zip(calls, outs):
+            want, _, used = call.run(0xFF)
+            assert len(call.claimed(used)) >= len(call.seen) > 0      # (these calls do widen)
+            assert torch.equal(out, want)
+            pools = (call.c.k, call.c.v) if cache in (F16, BF16) else (call.c.ks, call.c.vs) if cache == SCALED else (call.c.k,)
+            for t in pools:
+                t.mul_(0.5) if t.dtype != torch.uint8 else t.bitwise_xor_(0x80)
+        torch.cuda.synchronize()
+    assert pkv.get_device_error() == 0
