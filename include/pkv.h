@@ -623,7 +623,8 @@ pkv_status pkv_paged_extend_attn_window(const pkv_cache_desc* desc, const void* 
  * pkv_paged_extend_attn_block_scaled -- pkv_paged_extend_attn over a cache with
  * a scale per block and kv head, optionally under a window (0: none).
  * The kernel reads the codes: K's scales multiply the scores in fp32 (bf16
- * queries are taken as f16, as over the fp8 cache above), V takes part as
+ * queries are taken as f16, as over the fp8 cache above; a call that widens its
+ * pages, below, takes them as they are), V takes part as
  * f16(code * scale) (finite values beyond f16's range become its largest, values
  * below 2^-14 lose bits).
  * workspace:    optional, as for pkv_paged_extend_attn: given
@@ -762,7 +763,9 @@ pkv_status pkv_get_device_error(int32_t* word, int32_t clear, cudaStream_t strea
 /* Library version, major*10000 + minor*100 + patch.  2.0.0: the shared-prefix
  * extend takes a workspace (two arguments before the stream).  2.1.0:
  * pkv_extend_widen_workspace_bytes; the plain extend uses a workspace of that
- * size (its signature unchanged). */
+ * size (its signature unchanged).  The block-scaled, read-back and window calls
+ * came without a number of their own: a caller that has to know looks their
+ * symbols up. */
 int32_t pkv_version(void);
 
 #ifdef __cplusplus

@@ -183,7 +183,7 @@ bool plan_extend(ExtendParams& p, int batch, int num_kv_heads, int group, int ma
 // 254 tiles 458 / 259 / 278 / 365, 128 of up to 21 tiles 43 / 53 / 62 / 107, 8 of
 // 63 tiles 115 / 66 / 39 / 25; the last in half tiles 100 / 55 / 33 / 22.5, and
 // 512 of 1 to 4 tiles 44 whole, 56 in half tiles.  (Two of these at each end
-// again with launches set up early: 257, 42.8; the order is the same.)
+// again with launches set up early: 257, 44; the order is the same.)
 void plan_view_items(ExtendParams& p, int max_total_len, int sm_count) {
   int64_t tiles = ((int64_t)max_total_len + 127) / 128;
   if (p.window > 0)

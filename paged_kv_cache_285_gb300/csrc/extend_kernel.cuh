@@ -85,7 +85,7 @@
 // it is three tiles from its item's end, looks the item up and passes both on to
 // the other roles through a two-slot ring.  (1,760 items of 34 tiles on 152 SMs:
 // 728 us against 752 with the stride; 952 items of 33 to 87 tiles 745 against
-// 804.)  A request's later pairs, which see more keys, come first, for all its
+// 804; both are 740 to 765 now, by the clocks that the power limit leaves.)  A request's later pairs, which see more keys, come first, for all its
 // heads; head by head, where the pairs of a head would share its keys in L2, 16
 // requests of 100-1,000 rows over up to 9,000 tokens took 796 us against 760, 64
 // of 100-300 over up to 4,000 581 against 540, 4 of 2,000 over up to 9,000 742
@@ -107,7 +107,7 @@
 // All of these are launched while the launch before them in the stream still
 // runs: barriers and TMEM are set up, then they wait for its end before their
 // first load (plain loads; calls one after another, a short prompt 12.3 -> 10.3
-// us, 8 chat turns 45.1 -> 42.8).
+// us, 8 chat turns 45.1 -> 44).
 //
 // Half tiles (HALF = true, with CL): where every request's rows fit one row tile,
 // tile B would be empty.  Both tiles then hold the same rows and share the keys
