@@ -59,7 +59,13 @@ typedef enum {
                                 unlocked leaf */
 } pkv_status;
 
-typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
+typedef enum {
+  PKV_F16 = 0,
+  PKV_BF16 = 1,
+  PKV_FP8_E4M3 = 2,
+  PKV_MX4 = 3              /* e2m1 codes with a power-of-two scale per 32 values: a cache dtype of
+                              the pkv_..._mx4 calls alone */
+} pkv_dtype;
 
 /* Device error word values (pkv_get_device_error). */
 #define PKV_DEVERR_NONE 0
@@ -647,6 +653,155 @@ pkv_status pkv_paged_extend_attn_block_scaled(
     float* lse_out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * A cache held in 4 bits with a scale for every 32 values of a row.
+ *
+ * desc->cache_dtype is PKV_MX4 (another valid one: PKV_ERR_UNSUPPORTED);
+ * desc->k_scale / v_scale are not used.  Pools:
+ *   k_cache, v_cache    uint8 [num_blocks][num_kv_heads][block_size][head_dim / 2]:
+ *                       e2m1 codes (sign, two exponent bits, one of mantissa:
+ *                       0, 0.5, 1, 1.5, 2, 3, 4, 6), value 2 i of a row in the low
+ *                       bits of byte i, value 2 i + 1 in its high bits
+ *   k_scales, v_scales  uint8 [num_blocks][num_kv_heads][block_size][head_dim / 32]:
+ *                       byte b of values 32 j .. 32 j + 31 of a row is the scale
+ *                       2^(b - 127); 255 makes its 32 values NaN
+ * (elements, scales and groups of the OCP Microscaling format MXFP4), all 16-byte
+ * aligned.  A token takes 17/32 of its bytes in fp8.  Rows share no scale, so
+ * that a token can be written, moved (pkv_kv_compact) and dropped by itself.
+ * The stream order is that of the block-scaled calls.
+ *
+ * pkv_kv_append_mx4 -- quantise the K/V rows of new tokens into their slots.
+ * Rows, layout, hint and reports are those of pkv_kv_append_block_scaled; two
+ * rows for one slot: one of them wins, or a mixture of both (unspecified).
+ * For every 32 values x of a row:
+ *   s = the smallest power of two >= 2^-126 with |x| <= 7 s for the finite x
+ *       (2^-126 if all are 0);
+ *   codes are e2m1(x / s), to nearest even, so that no finite value is off by more
+ *       than s (one of 6 s to 7 s becomes 6 s); infinities become +-6 s;
+ *   with a NaN among them the scale byte is 255, else log2(s) + 127.
+ * Only the new rows' codes and scales are written.
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_kv_append_mx4(const pkv_cache_desc* desc, void* k_cache, void* v_cache,
+                             uint8_t* k_scales, uint8_t* v_scales, const void* k_new,
+                             const void* v_new, pkv_dtype act_dtype, const int32_t* q_indptr,
+                             const int32_t* prefix_lens, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, int32_t batch, int32_t total_rows,
+                             int32_t max_suffix_len, cudaStream_t stream);
+
+/* pkv_kv_gather_mx4 -- pkv_kv_gather over such a cache: act(code * scale), rounded
+ * once (bf16: exact but for subnormals); for f16 outputs finite values beyond the
+ * type's range become its largest. */
+pkv_status pkv_kv_gather_mx4(const pkv_cache_desc* desc, const void* k_cache, const void* v_cache,
+                             const uint8_t* k_scales, const uint8_t* v_scales, void* k_out,
+                             void* v_out, pkv_dtype act_dtype, const int32_t* row_indptr,
+                             const int32_t* start_positions, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, int32_t batch, int32_t total_rows,
+                             cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_paged_decode_attn_mx4 -- pkv_paged_decode_attn over such a cache, optionally
+ * under a window (0: none; as pkv_paged_decode_attn_window).  K's scales multiply
+ * the scores' parts in fp32; V's are taken into the weights relative to the
+ * largest of the tokens that a warp has gone through (a token whose scale for 32
+ * dims is 2^20 below that adds nothing to them); bf16 queries are taken as f16, as
+ * over the fp8 caches.  A block id outside the pool reads zeros
+ * (PKV_DEVERR_BAD_BLOCK).  The workspace is pkv_decode_mx4_workspace_bytes(), with
+ * num_splits 0 for every smaller batch and bound too.
+ * ------------------------------------------------------------------------- */
+size_t pkv_decode_mx4_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                      int32_t num_q_heads, int32_t max_seq_len, int32_t window,
+                                      int32_t sink_tokens, int32_t num_splits);
+
+pkv_status pkv_paged_decode_attn_mx4(const pkv_cache_desc* desc, const void* k_cache,
+                                     const void* v_cache, const uint8_t* k_scales,
+                                     const uint8_t* v_scales, const void* q, void* out,
+                                     pkv_dtype act_dtype, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                     int32_t batch, int32_t num_q_heads, float sm_scale,
+                                     int32_t max_seq_len, int32_t window, int32_t sink_tokens,
+                                     int32_t num_splits, float* lse_out, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_paged_extend_attn_mx4 -- pkv_paged_extend_attn over such a cache, optionally
+ * under a window (0: none; as pkv_paged_extend_attn_window).  The call first
+ * widens each block that its rows see, once, into 16-bit copies in the workspace:
+ * K as code * scale in the act dtype, V in f16 (finite values beyond f16's range
+ * become its largest, values below 2^-14 lose bits).
+ * workspace: pkv_extend_mx4_workspace_bytes() bytes or more, 256-byte aligned, any
+ * contents (else PKV_ERR_WORKSPACE).  Calls that run at the same time need
+ * workspaces of their own.  batch <= 65,535.
+ * ------------------------------------------------------------------------- */
+size_t pkv_extend_mx4_workspace_bytes(const pkv_cache_desc* desc);
+
+pkv_status pkv_paged_extend_attn_mx4(const pkv_cache_desc* desc, const void* k_cache,
+                                     const void* v_cache, const uint8_t* k_scales,
+                                     const uint8_t* v_scales, const void* q, void* out,
+                                     pkv_dtype act_dtype, const int32_t* q_indptr,
+                                     const int32_t* prefix_lens, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, int32_t batch, int32_t num_q_heads,
+                                     float sm_scale, int32_t total_q_rows, int32_t max_suffix_len,
+                                     int32_t max_total_len, int32_t window, int32_t sink_tokens,
+                                     float* lse_out, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Moving what a cache holds: pages, and tokens within a request.
+ *
+ * Both calls take any number of pools of the same blocks -- K, V and scales of
+ * every layer -- and move the same blocks or tokens in each, in one launch (128
+ * pools a launch).  A pool is [num_blocks][num_kv_heads][block_size][row_bytes]
+ * bytes of any type; a scale per block and kv head is a pool with block_size 1.
+ * `pools` is host memory, read during the call.  The stream order is that of the
+ * block-scaled calls.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* base;               /* device */
+  int32_t num_blocks;       /* the same for all pools of a call */
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t row_bytes;        /* of one token and kv head */
+} pkv_pool;
+
+/* pkv_kv_copy_blocks -- block dst_blocks[i] becomes what block src_blocks[i] holds,
+ * in every pool: a request is forked by giving its full blocks to each of its
+ * branches and copying the last, partial one for all but one of them; a request
+ * moves to other blocks by copying them.
+ * src_blocks, dst_blocks: int32 [num_pairs], device.  A pair with a negative id is
+ * skipped (so that a list may have a fixed length), one with an id >= num_blocks
+ * too (PKV_DEVERR_BAD_BLOCK).  A block may be the source of several pairs; one
+ * that is the destination of a pair must be in no other pair (what it, and what
+ * is copied from it, holds then is unspecified).
+ * Pools: 4-byte aligned, blocks a multiple of 4 bytes and below 2^31 (of 32 for
+ * the fastest copies). */
+pkv_status pkv_kv_copy_blocks(const pkv_pool* pools, int32_t num_pools, const int32_t* src_blocks,
+                              const int32_t* dst_blocks, int32_t num_pairs, cudaStream_t stream);
+
+/* pkv_kv_compact -- tokens of a request moved together, in place: the token at
+ * position src_positions[row_indptr[b] + i] of request b goes to position
+ * dst_starts[b] + i, in every pool, as if all were read before any is written.
+ * (Tokens kept by an eviction, or the accepted ones of a tree of drafts; the
+ * blocks behind the last one can then be given back.)  What other positions
+ * hold is left alone; pools whose tokens share a scale (one per block and kv head)
+ * cannot be compacted.
+ * src_positions:  int32 [total_rows], device; a request's rise, the first not
+ *                 before dst_starts[b].  A row that does not, or whose positions do
+ *                 not fit the table, is not moved (PKV_DEVERR_BAD_LENGTH; what the
+ *                 request's positions from dst_starts[b] on hold is then
+ *                 unspecified), nor one with a block outside the pool
+ *                 (PKV_DEVERR_BAD_BLOCK).
+ * row_indptr:     int32 [batch+1], device, non-decreasing; dst_starts: int32 [batch].
+ * block_tables:   int32 [batch][max_blocks_per_seq].  No block that a request
+ *                 writes may be in the table of another request of the call.
+ * max_rows:       host bound of the rows per request; rows beyond it are not moved
+ *                 (PKV_DEVERR_BAD_LENGTH).
+ * Pools: the same num_kv_heads and block_size (16 or 32), row_bytes a power of two
+ * from 2 to 1,024, base aligned to it or to 16 bytes, whichever is less. */
+pkv_status pkv_kv_compact(const pkv_pool* pools, int32_t num_pools, const int32_t* src_positions,
+                          const int32_t* row_indptr, const int32_t* dst_starts,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                          int32_t total_rows, int32_t max_rows, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Prefix index (host): radix tree over token ids with leaf-first LRU eviction.
  *
  * "PagedAttention과 RadixAttention으로 LLM KV 캐시 최적화", section 03: the KV
@@ -763,9 +918,9 @@ pkv_status pkv_get_device_error(int32_t* word, int32_t clear, cudaStream_t strea
 /* Library version, major*10000 + minor*100 + patch.  2.0.0: the shared-prefix
  * extend takes a workspace (two arguments before the stream).  2.1.0:
  * pkv_extend_widen_workspace_bytes; the plain extend uses a workspace of that
- * size (its signature unchanged).  The block-scaled, read-back and window calls
- * came without a number of their own: a caller that has to know looks their
- * symbols up. */
+ * size (its signature unchanged).  The block-scaled, read-back, window, microscaled
+ * and moving calls came without a number of their own: a caller that has to know
+ * looks their symbols up. */
 int32_t pkv_version(void);
 
 #ifdef __cplusplus

@@ -1,5 +1,5 @@
 """Paged-KV attention for GB300 (sm_103a): a thin binding of libpkv.so (ctypes;
-the block-scaled, gather and window calls through a compiled one, _calls.so).
+the calls that check their tensors in one pass through a compiled one, _calls.so).
 
 Every call here only marshals arguments (PyTorch tensors -> device pointers,
 the current CUDA stream) and forwards them to the C ABI declared in
@@ -26,6 +26,11 @@ paged_extend_attn_block_scaled; kv_gather reads rows back out of any cache.
 paged_decode_attn_window and paged_extend_attn_window: attention with a
 sliding window and a few first tokens that stay visible (the block-scaled calls
 take a window too).
+
+A cache of 4-bit floating-point codes with a scale per 32 values of a row:
+kv_append_mx4, kv_gather_mx4, paged_decode_attn_mx4 and paged_extend_attn_mx4.
+kv_copy_blocks and kv_compact move pages, and tokens within a request, in all
+the pools of a KvPools.
 """
 from __future__ import annotations
 
@@ -47,9 +52,11 @@ __all__ = ["F16", "BF16", "FP8_E4M3", "PkvError", "CacheDesc", "lib_path", "load
            "kv_append_block_scaled", "kv_gather", "decode_window_workspace_bytes",
            "paged_decode_attn_window", "paged_decode_attn_block_scaled",
            "paged_extend_attn_window", "extend_block_scaled_workspace_bytes",
-           "paged_extend_attn_block_scaled"]
+           "paged_extend_attn_block_scaled", "MX4", "kv_append_mx4", "kv_gather_mx4",
+           "decode_mx4_workspace_bytes", "paged_decode_attn_mx4", "extend_mx4_workspace_bytes",
+           "paged_extend_attn_mx4", "KvPools", "kv_copy_blocks", "kv_compact"]
 
-F16, BF16, FP8_E4M3 = 0, 1, 2
+F16, BF16, FP8_E4M3, MX4 = 0, 1, 2, 3
 NO_SPACE = 5  # PKV_ERR_NO_SPACE
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libpkv.so")
@@ -76,6 +83,13 @@ class CacheDesc(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("cache_dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float)]
+
+
+class Pool(ctypes.Structure):
+    """Mirror of pkv_pool."""
+    _fields_ = [("base", ctypes.c_void_p), ("num_blocks", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int32)]
 
 
 def lib_path() -> str:
@@ -159,6 +173,22 @@ def load():
                                                            I32, F, I32, I32, I32, I32, I32, P, P,
                                                            SZ, P]
         lib.pkv_paged_extend_attn_block_scaled.restype = I
+        lib.pkv_kv_append_mx4.argtypes = [D, P, P, P, P, P, P, I, P, P, P, I32, I32, I32, I32, P]
+        lib.pkv_kv_append_mx4.restype = I
+        lib.pkv_kv_gather_mx4.argtypes = [D, P, P, P, P, P, P, I, P, P, P, I32, I32, I32, P]
+        lib.pkv_kv_gather_mx4.restype = I
+        lib.pkv_decode_mx4_workspace_bytes.argtypes = [D, I32, I32, I32, I32, I32, I32]
+        lib.pkv_decode_mx4_workspace_bytes.restype = SZ
+        lib.pkv_paged_decode_attn_mx4.argtypes = lib.pkv_paged_decode_attn_block_scaled.argtypes
+        lib.pkv_paged_decode_attn_mx4.restype = I
+        lib.pkv_extend_mx4_workspace_bytes.argtypes = [D]
+        lib.pkv_extend_mx4_workspace_bytes.restype = SZ
+        lib.pkv_paged_extend_attn_mx4.argtypes = lib.pkv_paged_extend_attn_block_scaled.argtypes
+        lib.pkv_paged_extend_attn_mx4.restype = I
+        lib.pkv_kv_copy_blocks.argtypes = [P, I32, P, P, I32, P]
+        lib.pkv_kv_copy_blocks.restype = I
+        lib.pkv_kv_compact.argtypes = [P, I32, P, P, P, P, I32, I32, I32, I32, P]
+        lib.pkv_kv_compact.restype = I
         VP = ctypes.c_void_p
         lib.pkv_radix_create.argtypes = [I32, I32, ctypes.POINTER(VP)]
         lib.pkv_radix_create.restype = ctypes.c_int
@@ -812,6 +842,188 @@ def paged_extend_attn_block_scaled(k_cache, v_cache, k_scales, v_scales, q, out,
     _run("pkv_paged_extend_attn_block_scaled", dev, stream, desc, kc, vc, ks, vs, qp, op,
          _code(q), qi, pl, bt, width, batch, hq, float(sm_scale), rows,
          int(max_suffix_len), int(max_total_len), int(window), int(sink_tokens), lse, ws, ws_bytes)
+
+
+def _pools_mx4(k_cache, v_cache, k_scales, v_scales):
+    """The desc of pools of e2m1 codes, the pointers of pools and scales, Hkv, head dim, device."""
+    shape = _dim("cache", k_cache, 4, "[num_blocks, num_kv_heads, block_size, head_dim / 2]")
+    nb, hkv, bs, half = shape
+    index = k_cache.get_device()
+    scales = (nb, hkv, bs, half // 16)
+    return (_desc_ref(nb, hkv, bs, 2 * half, MX4, 1.0, 1.0),
+            _arg("k_cache", k_cache, shape, torch.uint8, index),
+            _arg("v_cache", v_cache, shape, torch.uint8, index),
+            _arg("k_scales", k_scales, scales, torch.uint8, index),
+            _arg("v_scales", v_scales, scales, torch.uint8, index), hkv, 2 * half, index)
+
+
+def _desc_mx4(k_cache):
+    nb, hkv, bs, half = _dim("cache", k_cache, 4, "[num_blocks, num_kv_heads, block_size, head_dim / 2]")
+    return _desc_ref(nb, hkv, bs, 2 * half, MX4, 1.0, 1.0)
+
+
+def kv_append_mx4(k_cache, v_cache, k_scales, v_scales, k_new, v_new, q_indptr, prefix_lens,
+                  block_tables, max_suffix_len, stream=None):
+    """pkv_kv_append_mx4: k_new/v_new [rows, Hkv, D] act dtype; row q_indptr[b] + i goes to position
+    prefix_lens[b] + i of request b, quantised to e2m1 codes (k_cache/v_cache uint8
+    [num_blocks, Hkv, block_size, D / 2]) with a power-of-two scale per 32 values
+    (k_scales/v_scales uint8 [num_blocks, Hkv, block_size, D / 32]).  q_indptr int32 [B+1];
+    prefix_lens int32 [B]; max_suffix_len bounds the rows per request."""
+    if _direct is not None:
+        st = _direct.append_mx4(k_cache, v_cache, k_scales, v_scales, k_new, v_new, q_indptr,
+                                prefix_lens, block_tables, max_suffix_len, stream)
+        if st is not None:
+            return _check(st, "pkv_kv_append_mx4")
+    desc, kc, vc, ks, vs, hkv, d, dev = _pools_mx4(k_cache, v_cache, k_scales, v_scales)
+    rows = _dim("k_new", k_new, 3, "[rows, num_kv_heads, head_dim]")[0]
+    shape, dtype = (rows, hkv, d), k_new.dtype
+    kn = _arg("k_new", k_new, shape, dtype, dev)
+    vn = _arg("v_new", v_new, shape, dtype, dev)
+    qi, pl, bt, batch, width = _layout("q_indptr", q_indptr, "prefix_lens", prefix_lens,
+                                       block_tables, dev)
+    _run("pkv_kv_append_mx4", dev, stream, desc, kc, vc, ks, vs, kn, vn, _code(k_new), qi, pl, bt,
+         width, batch, rows, int(max_suffix_len))
+
+
+def kv_gather_mx4(k_cache, v_cache, k_scales, v_scales, k_out, v_out, row_indptr, start_positions,
+                  block_tables, stream=None):
+    """pkv_kv_gather_mx4: rows row_indptr[b] .. row_indptr[b+1]-1 of k_out/v_out [rows, Hkv, D] (f16
+    or bf16) are positions start_positions[b] ... of request b of a cache that kv_append_mx4
+    wrote."""
+    if _direct is not None:
+        st = _direct.gather_mx4(k_cache, v_cache, k_scales, v_scales, k_out, v_out, row_indptr,
+                                start_positions, block_tables, stream)
+        if st is not None:
+            return _check(st, "pkv_kv_gather_mx4")
+    desc, kc, vc, ks, vs, hkv, d, dev = _pools_mx4(k_cache, v_cache, k_scales, v_scales)
+    rows = _dim("k_out", k_out, 3, "[rows, num_kv_heads, head_dim]")[0]
+    shape, dtype = (rows, hkv, d), k_out.dtype
+    ko = _arg("k_out", k_out, shape, dtype, dev)
+    vo = _arg("v_out", v_out, shape, dtype, dev)
+    ri, sp, bt, batch, width = _layout("row_indptr", row_indptr, "start_positions", start_positions,
+                                       block_tables, dev)
+    _run("pkv_kv_gather_mx4", dev, stream, desc, kc, vc, ks, vs, ko, vo, _code(k_out), ri, sp, bt,
+         width, batch, rows)
+
+
+def decode_mx4_workspace_bytes(k_cache, batch, num_q_heads, max_seq_len, window=0, sink_tokens=0,
+                               num_splits=0) -> int:
+    """pkv_decode_mx4_workspace_bytes: the workspace of paged_decode_attn_mx4; with num_splits 0 it
+    serves every smaller batch and max_seq_len too."""
+    return int(load().pkv_decode_mx4_workspace_bytes(_desc_mx4(k_cache), batch, num_q_heads,
+                                                     max_seq_len, window, sink_tokens, num_splits))
+
+
+def paged_decode_attn_mx4(k_cache, v_cache, k_scales, v_scales, q, out, block_tables, seq_lens,
+                          sm_scale, max_seq_len, window=0, sink_tokens=0, num_splits=0, lse_out=None,
+                          workspace=None, stream=None):
+    """pkv_paged_decode_attn_mx4: paged_decode_attn over e2m1 codes with microscales (the pools of
+    kv_append_mx4); window 0: every token, else as paged_decode_attn_window.  ``workspace`` is a
+    uint8 device tensor of at least decode_mx4_workspace_bytes() bytes."""
+    if _direct is not None:
+        st = _direct.decode_mx4(k_cache, v_cache, k_scales, v_scales, q, out, block_tables, seq_lens,
+                                sm_scale, max_seq_len, window, sink_tokens, num_splits, lse_out,
+                                workspace, stream)
+        if st is not None:
+            return _check(st, "pkv_paged_decode_attn_mx4")
+    desc, kc, vc, ks, vs, _, d, dev = _pools_mx4(k_cache, v_cache, k_scales, v_scales)
+    qp, op, bt, sl, lse, b, hq, width = _decode_args(q, out, block_tables, seq_lens, lse_out, d, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run("pkv_paged_decode_attn_mx4", dev, stream, desc, kc, vc, ks, vs, qp, op, _code(q), bt, width,
+         sl, b, hq, float(sm_scale), int(max_seq_len), int(window), int(sink_tokens),
+         int(num_splits), lse, ws, ws_bytes)
+
+
+def extend_mx4_workspace_bytes(k_cache) -> int:
+    """pkv_extend_mx4_workspace_bytes: the workspace that paged_extend_attn_mx4 needs (16-bit copies
+    of the K and V pools, and the per-block claims)."""
+    return int(load().pkv_extend_mx4_workspace_bytes(_desc_mx4(k_cache)))
+
+
+def paged_extend_attn_mx4(k_cache, v_cache, k_scales, v_scales, q, out, q_indptr, prefix_lens,
+                          block_tables, sm_scale, max_suffix_len, max_total_len, window=0,
+                          sink_tokens=0, lse_out=None, workspace=None, stream=None):
+    """pkv_paged_extend_attn_mx4: paged_extend_attn over e2m1 codes with microscales; window 0: every
+    key, else as paged_extend_attn_window.  ``workspace`` is a uint8 device tensor of at least
+    extend_mx4_workspace_bytes() bytes (the pages read are widened there once per block)."""
+    if _direct is not None:
+        st = _direct.extend_mx4(k_cache, v_cache, k_scales, v_scales, q, out, q_indptr, prefix_lens,
+                                block_tables, sm_scale, max_suffix_len, max_total_len, window,
+                                sink_tokens, lse_out, workspace, stream)
+        if st is not None:
+            return _check(st, "pkv_paged_extend_attn_mx4")
+    desc, kc, vc, ks, vs, _, d, dev = _pools_mx4(k_cache, v_cache, k_scales, v_scales)
+    qp, op, qi, pl, bt, lse, rows, hq, batch, width = _extend_args(
+        q, out, q_indptr, prefix_lens, block_tables, lse_out, d, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run("pkv_paged_extend_attn_mx4", dev, stream, desc, kc, vc, ks, vs, qp, op, _code(q), qi, pl, bt,
+         width, batch, hq, float(sm_scale), rows, int(max_suffix_len), int(max_total_len),
+         int(window), int(sink_tokens), lse, ws, ws_bytes)
+
+
+class KvPools:
+    """The pools that kv_copy_blocks and kv_compact move pages and tokens in: K, V and scales of any
+    layers, contiguous device tensors [num_blocks, num_kv_heads, block_size, ...] of any dtypes, or
+    [num_blocks, num_kv_heads] (a scale per block and kv head: copied, not compacted).  They are
+    checked once, here, and held for as long as this object."""
+
+    def __init__(self, pools):
+        self.tensors = tuple(pools)
+        self._array = (Pool * len(self.tensors))()
+        self._at, self._count, self._index = ctypes.addressof(self._array), len(self.tensors), -1
+        for i, t in enumerate(self.tensors):
+            if not isinstance(t, torch.Tensor) or t.dim() < 2:
+                raise ValueError(f"pool {i} must be a tensor [num_blocks, num_kv_heads, ...]")
+            if not t.is_cuda or t.device != self.tensors[0].device:
+                raise ValueError(f"libpkv takes device tensors of one device: pool {i} is on {t.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"libpkv takes contiguous tensors: pool {i} is not")
+            if t.numel() == 0 or t.shape[0] != self.tensors[0].shape[0]:
+                raise ValueError(f"pool {i} must have {self.tensors[0].shape[0]} blocks, got {tuple(t.shape)}")
+            nb, hkv = t.shape[0], t.shape[1]
+            bs = t.shape[2] if t.dim() > 2 else 1
+            row = t.numel() * t.element_size() // (nb * hkv * bs)
+            if max(nb, hkv, bs, row) > 2 ** 31 - 1:
+                raise ValueError(f"pool {i} is too large")
+            self._array[i] = Pool(t.data_ptr(), nb, hkv, bs, row)
+            self._index = t.get_device()
+
+
+def kv_copy_blocks(pools, src_blocks, dst_blocks, stream=None):
+    """pkv_kv_copy_blocks: block dst_blocks[i] becomes what src_blocks[i] holds in every pool of a
+    KvPools; int32 [pairs] each, a pair with a negative id is skipped."""
+    if _direct is not None and type(pools) is KvPools:
+        st = _direct.copy_blocks(pools._at, pools._count, pools._index, src_blocks, dst_blocks, stream)
+        if st is not None:
+            return _check(st, "pkv_kv_copy_blocks")
+    if not isinstance(pools, KvPools):
+        raise ValueError("pools must be a KvPools")
+    pairs, = _dim("src_blocks", src_blocks, 1, "[pairs]")
+    dev = src_blocks.get_device() if pools._count == 0 else pools._index
+    src = _arg("src_blocks", src_blocks, (pairs,), torch.int32, dev)
+    dst = _arg("dst_blocks", dst_blocks, (pairs,), torch.int32, dev)
+    _run("pkv_kv_copy_blocks", dev, stream, pools._at, pools._count, src, dst, pairs)
+
+
+def kv_compact(pools, src_positions, row_indptr, dst_starts, block_tables, max_rows, stream=None):
+    """pkv_kv_compact: in every pool of a KvPools the token at position
+    src_positions[row_indptr[b] + i] of request b goes to position dst_starts[b] + i, in place, as
+    if all were read first.  src_positions int32 [rows], rising within a request; row_indptr int32
+    [B+1]; dst_starts int32 [B]; max_rows bounds the rows per request."""
+    if _direct is not None and type(pools) is KvPools:
+        st = _direct.compact(pools._at, pools._count, pools._index, src_positions, row_indptr,
+                             dst_starts, block_tables, max_rows, stream)
+        if st is not None:
+            return _check(st, "pkv_kv_compact")
+    if not isinstance(pools, KvPools):
+        raise ValueError("pools must be a KvPools")
+    rows, = _dim("src_positions", src_positions, 1, "[rows]")
+    dev = src_positions.get_device() if pools._count == 0 else pools._index
+    src = _arg("src_positions", src_positions, (rows,), torch.int32, dev)
+    ri, ds, bt, batch, width = _layout("row_indptr", row_indptr, "dst_starts", dst_starts, block_tables,
+                                       dev)
+    _run("pkv_kv_compact", dev, stream, pools._at, pools._count, src, ri, ds, bt, width, batch, rows,
+         int(max_rows))
 
 
 def chain_hash(tokens, token_indptr, block_size, hashes, salts=None, stream=None):

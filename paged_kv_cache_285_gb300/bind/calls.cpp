@@ -1,5 +1,5 @@
-// The block-scaled, gather and window calls from Python tensors straight to the
-// C ABI: the argument checks of the package's Python functions on the tensors
+// The block-scaled, microscaled, gather, window and moving calls from Python
+// tensors straight to the C ABI: the argument checks of the package's Python functions on the tensors
 // themselves.
 //
 // What bounds a small call is the host: its kernel takes 2 to 8 us, the ABI call
@@ -72,24 +72,29 @@ T* array(PyObject* o, at::IntArrayRef shape, int device) {
   return static_cast<T*>(data(o, shape, c10::CppTypeToScalarType<T>::value, device));
 }
 
+// What a call's pools hold: values with a scale per tensor (or none), codes with
+// fp32 scales per block and head, or e2m1 codes with microscales.
+enum Kind { PLAIN, SCALED, MX4 };
+
 struct Pools {
   pkv_cache_desc desc;
   void *k, *v;
   int64_t blocks, heads, dim;
   int device;
 
-  Pools(PyObject* ko, PyObject* vo, float k_scale, float v_scale) {
+  Pools(PyObject* ko, PyObject* vo, float k_scale, float v_scale, bool mx4 = false) {
     const at::Tensor& t = tensor(ko);
     if (t.dim() != 4 || !t.is_cuda()) throw Unplain();
     device = t.get_device();
     blocks = t.size(0);
     heads = t.size(1);
-    dim = t.size(3);
+    dim = mx4 ? 2 * t.size(3) : t.size(3);
+    if (mx4 && t.scalar_type() != at::kByte) throw Unplain();
     desc.num_blocks = i32(blocks);
     desc.block_size = i32(t.size(2));
     desc.num_kv_heads = i32(heads);
     desc.head_dim = i32(dim);
-    desc.cache_dtype = code(t);
+    desc.cache_dtype = mx4 ? PKV_MX4 : code(t);
     desc.k_scale = k_scale;
     desc.v_scale = v_scale;
     k = data(ko, t.sizes(), t.scalar_type(), device);
@@ -97,6 +102,9 @@ struct Pools {
     if (c10::cuda::current_device() != device) throw Unplain();
   }
   float* scales(PyObject* o) const { return array<float>(o, {blocks, heads}, device); }
+  uint8_t* microscales(PyObject* o) const {
+    return array<uint8_t>(o, {blocks, heads, desc.block_size, dim / 32}, device);
+  }
 };
 
 // A pair of activation tensors [rows][heads][dim] of one 16-bit dtype.
@@ -212,6 +220,93 @@ PyObject* append_block_scaled(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The same arguments, over microscaled codes.
+PyObject* append_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 11, [&] {
+    const Pools c(a[0], a[1], 1.f, 1.f, true);
+    uint8_t *ks = c.microscales(a[2]), *vs = c.microscales(a[3]);
+    const Rows r(a[4], a[5], c, true);
+    const Layout l(a[6], a[7], a[8], c.device);
+    const int32_t longest = integer(a[9]);
+    const cudaStream_t s = stream(a[10], c.device);
+    return unlocked([&] {
+      return pkv_kv_append_mx4(&c.desc, c.k, c.v, ks, vs, r.a, r.b, r.dtype, l.indptr, l.starts,
+                               l.blocks, (int32_t)l.width, (int32_t)l.batch, (int32_t)r.rows, longest, s);
+    });
+  });
+}
+
+// k, v, k_scales, v_scales, k_out, v_out, row_indptr, start_positions,
+// block_tables, stream
+PyObject* gather_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, [&] {
+    const Pools c(a[0], a[1], 1.f, 1.f, true);
+    const uint8_t *ks = c.microscales(a[2]), *vs = c.microscales(a[3]);
+    const Rows r(a[4], a[5], c, true);
+    const Layout l(a[6], a[7], a[8], c.device);
+    const cudaStream_t s = stream(a[9], c.device);
+    return unlocked([&] {
+      return pkv_kv_gather_mx4(&c.desc, c.k, c.v, ks, vs, r.a, r.b, r.dtype, l.indptr, l.starts,
+                               l.blocks, (int32_t)l.width, (int32_t)l.batch, (int32_t)r.rows, s);
+    });
+  });
+}
+
+// The pools of a KvPools: the address and number of its pkv_pool structs.
+struct PoolSet {
+  const pkv_pool* at;
+  int32_t count;
+
+  PoolSet(PyObject* address, PyObject* count_o) {
+    if (!PyLong_CheckExact(address)) throw Unplain();
+    at = static_cast<const pkv_pool*>(PyLong_AsVoidPtr(address));
+    if (PyErr_Occurred()) throw Unplain();
+    count = integer(count_o);
+  }
+};
+
+int device_of(PyObject* o) {
+  const int d = integer(o);
+  if (d < 0 || c10::cuda::current_device() != d) throw Unplain();
+  return d;
+}
+
+int64_t length(PyObject* o) {
+  const at::Tensor& t = tensor(o);
+  if (t.dim() != 1) throw Unplain();
+  return i32(t.size(0));
+}
+
+// pools, count, device, src_blocks, dst_blocks, stream
+PyObject* copy_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 6, [&] {
+    const PoolSet p(a[0], a[1]);
+    const int device = device_of(a[2]);
+    const int64_t pairs = length(a[3]);
+    const int32_t *src = array<int32_t>(a[3], {pairs}, device), *dst = array<int32_t>(a[4], {pairs}, device);
+    const cudaStream_t s = stream(a[5], device);
+    return unlocked([&] { return pkv_kv_copy_blocks(p.at, p.count, src, dst, (int32_t)pairs, s); });
+  });
+}
+
+// pools, count, device, src_positions, row_indptr, dst_starts, block_tables,
+// max_rows, stream
+PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 9, [&] {
+    const PoolSet p(a[0], a[1]);
+    const int device = device_of(a[2]);
+    const int64_t rows = length(a[3]);
+    const int32_t* src = array<int32_t>(a[3], {rows}, device);
+    const Layout l(a[4], a[5], a[6], device);
+    const int32_t most = integer(a[7]);
+    const cudaStream_t s = stream(a[8], device);
+    return unlocked([&] {
+      return pkv_kv_compact(p.at, p.count, src, l.indptr, l.starts, l.blocks, (int32_t)l.width,
+                            (int32_t)l.batch, (int32_t)rows, most, s);
+    });
+  });
+}
+
 // k, v, k_out, v_out, row_indptr, start_positions, block_tables, k_scale, v_scale,
 // k_scales, v_scales, stream
 PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -231,15 +326,17 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// k, v, then k_scales, v_scales (SCALED) or k_scale, v_scale; q, out, block_tables,
+// k, v, then k_scales, v_scales (SCALED, MX4) or k_scale, v_scale; q, out, block_tables,
 // seq_lens, sm_scale, max_seq_len, window, sink_tokens, num_splits, lse_out,
 // workspace, stream
-template <bool SCALED>
+template <Kind K>
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 16, [&] {
-    const Pools c(a[0], a[1], SCALED ? 1.f : number(a[2]), SCALED ? 1.f : number(a[3]));
-    const float* ks = SCALED ? c.scales(a[2]) : nullptr;
-    const float* vs = SCALED ? c.scales(a[3]) : nullptr;
+    const Pools c(a[0], a[1], K != PLAIN ? 1.f : number(a[2]), K != PLAIN ? 1.f : number(a[3]), K == MX4);
+    const float* ks = K == SCALED ? c.scales(a[2]) : nullptr;
+    const float* vs = K == SCALED ? c.scales(a[3]) : nullptr;
+    const uint8_t* km = K == MX4 ? c.microscales(a[2]) : nullptr;
+    const uint8_t* vm = K == MX4 ? c.microscales(a[3]) : nullptr;
     const Rows r(a[4], a[5], c, false);
     const Table t(a[6], c.device);
     if (t.batch != r.rows) throw Unplain();
@@ -252,7 +349,11 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const cudaStream_t s = stream(a[15], c.device);
     const int32_t width = (int32_t)t.width, batch = (int32_t)r.rows, heads = (int32_t)r.heads;
     return unlocked([&] {
-      if constexpr (SCALED)
+      if constexpr (K == MX4)
+        return pkv_paged_decode_attn_mx4(&c.desc, c.k, c.v, km, vm, r.a, r.b, r.dtype, t.blocks, width,
+                                         lens, batch, heads, sm_scale, longest, window, sinks, splits,
+                                         l, w.at, w.bytes, s);
+      else if constexpr (K == SCALED)
         return pkv_paged_decode_attn_block_scaled(&c.desc, c.k, c.v, ks, vs, r.a, r.b, r.dtype,
                                                   t.blocks, width, lens, batch, heads, sm_scale,
                                                   longest, window, sinks, splits, l, w.at, w.bytes,
@@ -265,15 +366,17 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// k, v, then k_scales, v_scales (SCALED) or k_scale, v_scale; q, out, q_indptr,
+// k, v, then k_scales, v_scales (SCALED, MX4) or k_scale, v_scale; q, out, q_indptr,
 // prefix_lens, block_tables, sm_scale, max_suffix_len, max_total_len, window,
 // sink_tokens, lse_out, workspace, stream
-template <bool SCALED>
+template <Kind K>
 PyObject* extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 17, [&] {
-    const Pools c(a[0], a[1], SCALED ? 1.f : number(a[2]), SCALED ? 1.f : number(a[3]));
-    const float* ks = SCALED ? c.scales(a[2]) : nullptr;
-    const float* vs = SCALED ? c.scales(a[3]) : nullptr;
+    const Pools c(a[0], a[1], K != PLAIN ? 1.f : number(a[2]), K != PLAIN ? 1.f : number(a[3]), K == MX4);
+    const float* ks = K == SCALED ? c.scales(a[2]) : nullptr;
+    const float* vs = K == SCALED ? c.scales(a[3]) : nullptr;
+    const uint8_t* km = K == MX4 ? c.microscales(a[2]) : nullptr;
+    const uint8_t* vm = K == MX4 ? c.microscales(a[3]) : nullptr;
     const Rows r(a[4], a[5], c, false);
     const Layout y(a[6], a[7], a[8], c.device);
     const float sm_scale = number(a[9]);
@@ -285,7 +388,11 @@ PyObject* extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t width = (int32_t)y.width, batch = (int32_t)y.batch, rows = (int32_t)r.rows;
     const int32_t heads = (int32_t)r.heads;
     return unlocked([&] {
-      if constexpr (SCALED)
+      if constexpr (K == MX4)
+        return pkv_paged_extend_attn_mx4(&c.desc, c.k, c.v, km, vm, r.a, r.b, r.dtype, y.indptr,
+                                         y.starts, y.blocks, width, batch, heads, sm_scale, rows,
+                                         suffix, total, window, sinks, l, w.at, w.bytes, s);
+      else if constexpr (K == SCALED)
         return pkv_paged_extend_attn_block_scaled(&c.desc, c.k, c.v, ks, vs, r.a, r.b, r.dtype,
                                                   y.indptr, y.starts, y.blocks, width, batch, heads,
                                                   sm_scale, rows, suffix, total, window, sinks, l,
@@ -302,10 +409,16 @@ PyObject* extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   { name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {FN("append_block_scaled", append_block_scaled),
                          FN("gather", gather),
-                         FN("decode_window", decode<false>),
-                         FN("decode_block_scaled", decode<true>),
-                         FN("extend_window", extend<false>),
-                         FN("extend_block_scaled", extend<true>),
+                         FN("decode_window", decode<PLAIN>),
+                         FN("decode_block_scaled", decode<SCALED>),
+                         FN("extend_window", extend<PLAIN>),
+                         FN("extend_block_scaled", extend<SCALED>),
+                         FN("append_mx4", append_mx4),
+                         FN("gather_mx4", gather_mx4),
+                         FN("decode_mx4", decode<MX4>),
+                         FN("extend_mx4", extend<MX4>),
+                         FN("copy_blocks", copy_blocks),
+                         FN("compact", compact),
                          {nullptr, nullptr, 0, nullptr}};
 #undef FN
 

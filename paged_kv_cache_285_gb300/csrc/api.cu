@@ -82,6 +82,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 int elem_bytes(pkv_dtype d) { return d == PKV_FP8_E4M3 ? 1 : 2; }
 
+// Bytes that a value takes in a cache, its share of the scales included.
+double value_bytes(pkv_dtype d) { return d == PKV_MX4 ? 0.5 + 1.0 / kMxGroup : (double)elem_bytes(d); }
+
+// Bytes of a row (a token and kv head) of a cache.
+int row_bytes(const pkv_cache_desc* d) {
+  return d->cache_dtype == PKV_MX4 ? d->head_dim / 2 : d->head_dim * elem_bytes(d->cache_dtype);
+}
+
 bool valid_dtype(pkv_dtype d) { return d == PKV_F16 || d == PKV_BF16 || d == PKV_FP8_E4M3; }
 
 pkv_status check_desc(const pkv_cache_desc* d) {
@@ -100,9 +108,22 @@ pkv_status check_desc(const pkv_cache_desc* d) {
   return PKV_OK;
 }
 
+// The desc of a call over microscaled codes (the calls over other caches refuse
+// their dtype).
+pkv_status check_desc_mx4(const pkv_cache_desc* d) {
+  if (!d) return PKV_ERR_INVALID_ARG;
+  pkv_cache_desc as_fp8 = *d;  // the same checks of its sizes
+  as_fp8.cache_dtype = PKV_FP8_E4M3;
+  as_fp8.k_scale = as_fp8.v_scale = 1.f;
+  const pkv_status st = check_desc(&as_fp8);
+  if (st != PKV_OK) return st;
+  return d->cache_dtype == PKV_MX4 ? PKV_OK : valid_dtype(d->cache_dtype) ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID_ARG;
+}
+
 pkv_status check_act(const pkv_cache_desc* d, pkv_dtype act) {
   if (act != PKV_F16 && act != PKV_BF16) return PKV_ERR_INVALID_ARG;
-  if (d->cache_dtype != PKV_FP8_E4M3 && d->cache_dtype != act) return PKV_ERR_UNSUPPORTED;
+  if (d->cache_dtype != PKV_FP8_E4M3 && d->cache_dtype != PKV_MX4 && d->cache_dtype != act)
+    return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
 }
 
@@ -113,21 +134,38 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 pkv_status make_page_map(CUtensorMap* m, const void* base, const pkv_cache_desc* d) {
   auto enc = encode_fn();
   if (!enc) return PKV_ERR_CUDA;
-  const int elem = elem_bytes(d->cache_dtype);
-  const int rowb = d->head_dim * elem;
+  const int elem = d->cache_dtype == PKV_MX4 ? 1 : elem_bytes(d->cache_dtype);
+  const int rowb = row_bytes(d);
   const int chunkb = rowb < 128 ? rowb : 128;
-  cuuint64_t dims[3] = {(cuuint64_t)d->head_dim, (cuuint64_t)d->block_size,
+  cuuint64_t dims[3] = {(cuuint64_t)(rowb / elem), (cuuint64_t)d->block_size,
                         (cuuint64_t)d->num_blocks * (cuuint64_t)d->num_kv_heads};
   cuuint64_t strides[2] = {(cuuint64_t)rowb, (cuuint64_t)rowb * (cuuint64_t)d->block_size};
   cuuint32_t box[3] = {(cuuint32_t)(chunkb / elem), (cuuint32_t)kSubTokens, 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUtensorMapDataType dt =
       elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-  const CUtensorMapSwizzle sw =
-      chunkb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapSwizzle sw = chunkb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : chunkb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                               : CU_TENSOR_MAP_SWIZZLE_32B;
   CUresult r = enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// The microscales of a pool's pages: dims {block_size * head_dim / 32 bytes,
+// num_blocks*Hkv}, a box the bytes of 16 tokens (32 or 64).
+pkv_status make_microscale_map(CUtensorMap* m, const void* base, const pkv_cache_desc* d) {
+  auto enc = encode_fn();
+  if (!enc) return PKV_ERR_CUDA;
+  const cuuint64_t page = (cuuint64_t)d->block_size * d->head_dim / kMxGroup;
+  cuuint64_t dims[2] = {page, (cuuint64_t)d->num_blocks * (cuuint64_t)d->num_kv_heads};
+  cuuint64_t strides[1] = {page};
+  cuuint32_t box[2] = {(cuuint32_t)(kSubTokens * d->head_dim / kMxGroup), 1u};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -562,6 +600,10 @@ struct AttnView {
   const float* v_scales;
   int32_t window;
   int32_t sink_tokens;
+  // a cache of dtype PKV_MX4 and its microscales
+  bool mx4 = false;
+  const uint8_t* k_mx = nullptr;
+  const uint8_t* v_mx = nullptr;
 };
 
 static pkv_status check_view(const pkv_cache_desc* desc, const AttnView& w, bool scaled) {
@@ -572,6 +614,12 @@ static pkv_status check_view(const pkv_cache_desc* desc, const AttnView& w, bool
 }
 static pkv_status check_scales(const float* k_scales, const float* v_scales) {
   if (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4))
+    return PKV_ERR_INVALID_ARG;
+  return PKV_OK;
+}
+
+static pkv_status check_microscales(const uint8_t* k_scales, const uint8_t* v_scales) {
+  if (!k_scales || !v_scales || !aligned(k_scales, 16) || !aligned(v_scales, 16))
     return PKV_ERR_INVALID_ARG;
   return PKV_OK;
 }
@@ -634,7 +682,7 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   const double items = (double)batch * d->num_kv_heads * ((hq / d->num_kv_heads + 7) / 8);
   const double r1 = d->head_dim != 128 ? 160.0 : window > 0 ? 90.0 : 100.0;
   const double over = window > 0 ? 1.25 : 1.0;
-  const double sm_rate = 44600.0 / (2.0 * d->head_dim * elem_bytes(d->cache_dtype));
+  const double sm_rate = 44600.0 / (2.0 * d->head_dim * value_bytes(d->cache_dtype));
   const double slots = 4.0 * sms;
   double best = 1e30;
   int best_s = 1;
@@ -672,7 +720,7 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   }
   // splits of falling length: see above
   const double fill = items / slots;
-  const bool falling = window > 0 ? fill <= 1.5 && 2.0 * len * d->head_dim * elem_bytes(d->cache_dtype) >= 0.9e6
+  const bool falling = window > 0 ? fill <= 1.5 && 2.0 * len * d->head_dim * value_bytes(d->cache_dtype) >= 0.9e6
                                   : len >= 1000 && fill <= len / 800.0;
   if (fill >= 0.25 && falling) {
     const double ratio = std::min(0.78, std::max(0.45, 0.45 + 0.75 * (0.75 - fill)));
@@ -726,7 +774,8 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
                                 float sm_scale, int32_t max_seq_len, int32_t num_splits,
                                 float* lse_out, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream, const AttnView* view = nullptr) {
-  pkv_status st = check_desc(desc);
+  const bool mx4 = view && view->mx4;
+  pkv_status st = mx4 ? check_desc_mx4(desc) : check_desc(desc);
   if (st != PKV_OK) return st;
   if ((st = check_act(desc, act_dtype)) != PKV_OK) return st;
   if (batch < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || max_seq_len < 0 ||
@@ -802,6 +851,13 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
     ap.two_warps = !pl.cluster && pl.splits == 1 && pl.chunk <= 400 && ctas > 4 * ds->sm_count ? 1 : 0;
     ap.num_cuts = pl.num_cuts;
     std::copy(pl.cut, pl.cut + kMaxCuts + 1, ap.cut);
+    if (mx4) {
+      CUtensorMap k_mx_map, v_mx_map;
+      if ((st = make_microscale_map(&k_mx_map, view->k_mx, desc)) != PKV_OK) return st;
+      if ((st = make_microscale_map(&v_mx_map, view->v_mx, desc)) != PKV_OK) return st;
+      e = launch_decode_mx4(kmap, vmap, k_mx_map, v_mx_map, p, ap, desc->head_dim, (int)act_dtype, stream);
+      return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    }
     e = launch_decode_window(kmap, vmap, p, ap, desc->head_dim, (int)desc->cache_dtype,
                              (int)act_dtype, stream);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
@@ -837,11 +893,11 @@ pkv_status pkv_paged_decode_attn_append(const pkv_cache_desc* desc, void* k_cach
                        num_splits, lse_out, workspace, workspace_bytes, stream);
 }
 
-size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
-                                         int32_t num_q_heads, int32_t max_seq_len, int32_t window,
-                                         int32_t sink_tokens, int32_t num_splits) {
-  if (check_desc(desc) != PKV_OK || batch <= 0 || num_q_heads <= 0 || max_seq_len < 0 ||
-      window < 0 || sink_tokens < 0 || num_splits < 0)
+// Workspace of a decode through a view (its desc checked by the caller).
+static size_t view_workspace_bytes(const pkv_cache_desc* desc, int32_t batch, int32_t num_q_heads,
+                                   int32_t max_seq_len, int32_t window, int32_t sink_tokens,
+                                   int32_t num_splits) {
+  if (batch <= 0 || num_q_heads <= 0 || max_seq_len < 0 || window < 0 || sink_tokens < 0 || num_splits < 0)
     return 0;
   cudaError_t e;
   DeviceState* ds = device_state(&e);
@@ -850,6 +906,39 @@ size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* desc, int32_t bat
     return plan_view(desc, batch, num_q_heads, max_seq_len, window, sink_tokens, num_splits, sm_count)
         .ws_bytes;
   return view_workspace_bound(desc, batch, num_q_heads, max_seq_len, window, sink_tokens, sm_count);
+}
+
+size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* desc, int32_t batch,
+                                         int32_t num_q_heads, int32_t max_seq_len, int32_t window,
+                                         int32_t sink_tokens, int32_t num_splits) {
+  if (check_desc(desc) != PKV_OK) return 0;
+  return view_workspace_bytes(desc, batch, num_q_heads, max_seq_len, window, sink_tokens, num_splits);
+}
+
+size_t pkv_decode_mx4_workspace_bytes(const pkv_cache_desc* desc, int32_t batch, int32_t num_q_heads,
+                                      int32_t max_seq_len, int32_t window, int32_t sink_tokens,
+                                      int32_t num_splits) {
+  if (check_desc_mx4(desc) != PKV_OK) return 0;
+  return view_workspace_bytes(desc, batch, num_q_heads, max_seq_len, window, sink_tokens, num_splits);
+}
+
+pkv_status pkv_paged_decode_attn_mx4(const pkv_cache_desc* desc, const void* k_cache,
+                                     const void* v_cache, const uint8_t* k_scales,
+                                     const uint8_t* v_scales, const void* q, void* out,
+                                     pkv_dtype act_dtype, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                     int32_t batch, int32_t num_q_heads, float sm_scale,
+                                     int32_t max_seq_len, int32_t window, int32_t sink_tokens,
+                                     int32_t num_splits, float* lse_out, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream) {
+  const AttnView view{nullptr, nullptr, window, sink_tokens, true, k_scales, v_scales};
+  pkv_status st = check_desc_mx4(desc);
+  if (st == PKV_OK) st = check_view(desc, view, false);
+  if (st == PKV_OK && batch > 0) st = check_microscales(k_scales, v_scales);
+  if (st != PKV_OK) return st;
+  return decode_common(desc, k_cache, v_cache, nullptr, nullptr, q, out, act_dtype, block_tables,
+                       max_blocks_per_seq, seq_lens, batch, num_q_heads, sm_scale, max_seq_len,
+                       num_splits, lse_out, workspace, workspace_bytes, stream, &view);
 }
 
 pkv_status pkv_paged_decode_attn_window(const pkv_cache_desc* desc, const void* k_cache,
@@ -977,6 +1066,185 @@ pkv_status pkv_kv_gather(const pkv_cache_desc* desc, const void* k_cache, const 
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+pkv_status pkv_kv_append_mx4(const pkv_cache_desc* desc, void* k_cache, void* v_cache,
+                             uint8_t* k_scales, uint8_t* v_scales, const void* k_new,
+                             const void* v_new, pkv_dtype act_dtype, const int32_t* q_indptr,
+                             const int32_t* prefix_lens, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, int32_t batch, int32_t total_rows,
+                             int32_t max_suffix_len, cudaStream_t stream) {
+  pkv_status st = check_desc_mx4(desc);
+  if (st != PKV_OK) return st;
+  if ((st = check_act(desc, act_dtype)) != PKV_OK) return st;
+  if (batch < 0 || max_blocks_per_seq <= 0 || total_rows < 0 || max_suffix_len < 0)
+    return PKV_ERR_INVALID_ARG;
+  if (batch == 0 || total_rows == 0 || max_suffix_len == 0) return PKV_OK;
+  if ((st = check_microscales(k_scales, v_scales)) != PKV_OK) return st;
+  if (!k_cache || !v_cache || !k_new || !v_new || !q_indptr || !prefix_lens || !block_tables)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return PKV_ERR_INVALID_ARG;
+  cudaError_t e;
+  DeviceState* ds = device_state(&e);
+  if (!ds) return PKV_ERR_CUDA;
+  AppendMx4Params p{};
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_mx = k_scales;
+  p.v_mx = v_scales;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.q_indptr = q_indptr;
+  p.prefix_lens = prefix_lens;
+  p.block_tables = block_tables;
+  p.err = ds->err;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = desc->num_blocks;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.batch = batch;
+  p.total_rows = total_rows;
+  p.max_suffix_len = max_suffix_len;
+  e = launch_append_mx4(p, (int)act_dtype, desc->head_dim, desc->block_size, stream);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_gather_mx4(const pkv_cache_desc* desc, const void* k_cache, const void* v_cache,
+                             const uint8_t* k_scales, const uint8_t* v_scales, void* k_out,
+                             void* v_out, pkv_dtype act_dtype, const int32_t* row_indptr,
+                             const int32_t* start_positions, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, int32_t batch, int32_t total_rows,
+                             cudaStream_t stream) {
+  pkv_status st = check_desc_mx4(desc);
+  if (st != PKV_OK) return st;
+  if ((st = check_act(desc, act_dtype)) != PKV_OK) return st;
+  if (batch < 0 || max_blocks_per_seq <= 0 || total_rows < 0) return PKV_ERR_INVALID_ARG;
+  if (batch == 0 || total_rows == 0) return PKV_OK;
+  if ((st = check_microscales(k_scales, v_scales)) != PKV_OK) return st;
+  if (!k_cache || !v_cache || !k_out || !v_out || !row_indptr || !start_positions || !block_tables)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return PKV_ERR_INVALID_ARG;
+  cudaError_t e;
+  DeviceState* ds = device_state(&e);
+  if (!ds) return PKV_ERR_CUDA;
+  GatherMx4Params p{};
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_mx = k_scales;
+  p.v_mx = v_scales;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.row_indptr = row_indptr;
+  p.start_positions = start_positions;
+  p.block_tables = block_tables;
+  p.err = ds->err;
+  p.total_rows = total_rows;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = desc->num_blocks;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.batch = batch;
+  p.bs_shift = desc->block_size == 16 ? 4 : 5;
+  e = launch_gather_mx4(p, (int)act_dtype, desc->head_dim, stream);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// The pools of a move: the same number of blocks in each.
+static pkv_status check_pools(const pkv_pool* pools, int32_t num_pools) {
+  if (num_pools < 0) return PKV_ERR_INVALID_ARG;
+  if (num_pools == 0) return PKV_OK;
+  if (!pools) return PKV_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < num_pools; ++i) {
+    const pkv_pool& q = pools[i];
+    if (!q.base || q.num_blocks <= 0 || q.num_kv_heads <= 0 || q.block_size <= 0 || q.row_bytes <= 0 ||
+        q.num_blocks != pools[0].num_blocks)
+      return PKV_ERR_INVALID_ARG;
+  }
+  return PKV_OK;
+}
+
+extern "C" {
+
+pkv_status pkv_kv_copy_blocks(const pkv_pool* pools, int32_t num_pools, const int32_t* src_blocks,
+                              const int32_t* dst_blocks, int32_t num_pairs, cudaStream_t stream) {
+  pkv_status st = check_pools(pools, num_pools);
+  if (st != PKV_OK) return st;
+  if (num_pairs < 0) return PKV_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < num_pools; ++i) {
+    const int64_t rows = (int64_t)pools[i].num_kv_heads * pools[i].block_size;
+    if (rows > INT32_MAX || rows * pools[i].row_bytes > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (!aligned(pools[i].base, 4) || (rows * pools[i].row_bytes) % 4 != 0) return PKV_ERR_INVALID_ARG;
+  }
+  if (num_pools == 0 || num_pairs == 0) return PKV_OK;
+  if (!src_blocks || !dst_blocks) return PKV_ERR_INVALID_ARG;
+  cudaError_t e;
+  DeviceState* ds = device_state(&e);
+  if (!ds) return PKV_ERR_CUDA;
+  for (int32_t at = 0; at < num_pools; at += kMaxPools) {
+    CopyBlocksParams p;
+    p.src = src_blocks;
+    p.dst = dst_blocks;
+    p.err = ds->err;
+    p.num_blocks = pools[0].num_blocks;
+    p.num_pools = std::min(kMaxPools, num_pools - at);
+    for (int k = 0; k < p.num_pools; ++k) {
+      const pkv_pool& q = pools[at + k];
+      p.pool[k] = Pool{static_cast<uint8_t*>(q.base), (uint32_t)q.row_bytes,
+                       (int64_t)q.num_kv_heads * q.block_size * q.row_bytes};
+    }
+    e = launch_copy_blocks(p, num_pairs, stream);
+    if (e != cudaSuccess) return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
+}
+
+pkv_status pkv_kv_compact(const pkv_pool* pools, int32_t num_pools, const int32_t* src_positions,
+                          const int32_t* row_indptr, const int32_t* dst_starts,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                          int32_t total_rows, int32_t max_rows, cudaStream_t stream) {
+  pkv_status st = check_pools(pools, num_pools);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || total_rows < 0 || max_rows < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < num_pools; ++i) {
+    const pkv_pool& q = pools[i];
+    if (q.num_kv_heads != pools[0].num_kv_heads || q.block_size != pools[0].block_size)
+      return PKV_ERR_INVALID_ARG;
+    if (q.block_size != 16 && q.block_size != 32) return PKV_ERR_UNSUPPORTED;
+    if (q.row_bytes < 2 || q.row_bytes > 1024 || (q.row_bytes & (q.row_bytes - 1)) != 0)
+      return PKV_ERR_UNSUPPORTED;
+    if (!aligned(q.base, std::min(q.row_bytes, 16))) return PKV_ERR_INVALID_ARG;
+  }
+  if (num_pools == 0 || batch == 0 || total_rows == 0 || max_rows == 0) return PKV_OK;
+  if (!src_positions || !row_indptr || !dst_starts || !block_tables) return PKV_ERR_INVALID_ARG;
+  cudaError_t e;
+  DeviceState* ds = device_state(&e);
+  if (!ds) return PKV_ERR_CUDA;
+  for (int32_t at = 0; at < num_pools; at += kMaxPools) {
+    CompactParams p;
+    p.src_positions = src_positions;
+    p.row_indptr = row_indptr;
+    p.dst_starts = dst_starts;
+    p.block_tables = block_tables;
+    p.err = ds->err;
+    p.total_rows = total_rows;
+    p.max_rows = std::min(max_rows, total_rows);
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = pools[0].num_blocks;
+    p.num_kv_heads = pools[0].num_kv_heads;
+    p.bs_shift = pools[0].block_size == 16 ? 4 : 5;
+    p.batch = batch;
+    p.num_pools = std::min(kMaxPools, num_pools - at);
+    for (int k = 0; k < p.num_pools; ++k) {
+      const pkv_pool& q = pools[at + k];
+      p.pool[k] = Pool{static_cast<uint8_t*>(q.base), (uint32_t)q.row_bytes,
+                       (int64_t)q.num_kv_heads * q.block_size * q.row_bytes};
+    }
+    e = launch_compact(p, ds->sm_count, stream);
+    if (e != cudaSuccess) return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
+}
+
 size_t pkv_extend_workspace_bytes(const pkv_cache_desc* desc, int32_t batch, int32_t num_q_heads,
                                   int32_t total_q_rows, int32_t max_total_len) {
   // every dtype, fp8 included, is read straight from the cache: no scratch
@@ -1006,7 +1274,7 @@ static size_t shared_prefix_pool16_bytes(const pkv_cache_desc* d) {
 }
 static size_t shared_prefix_widen_bytes(const pkv_cache_desc* d) {
   if (d->cache_dtype == PKV_BF16) return shared_prefix_pool16_bytes(d);
-  if (d->cache_dtype == PKV_FP8_E4M3) return 2 * shared_prefix_pool16_bytes(d);
+  if (d->cache_dtype == PKV_FP8_E4M3 || d->cache_dtype == PKV_MX4) return 2 * shared_prefix_pool16_bytes(d);
   return 0;
 }
 // The plain extend's optional workspace: the same pools, then a counter, a
@@ -1028,7 +1296,8 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
                                 size_t workspace_bytes, cudaStream_t stream,
                                 const ExtendGroups* groups = nullptr,
                                 const AttnView* view = nullptr) {
-  pkv_status st = check_desc(desc);
+  const bool mx4 = view && view->mx4;
+  pkv_status st = mx4 ? check_desc_mx4(desc) : check_desc(desc);
   if (st != PKV_OK) return st;
   if ((st = check_act(desc, act_dtype)) != PKV_OK) return st;
   if (batch < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || total_q_rows < 0 ||
@@ -1036,9 +1305,10 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     return PKV_ERR_INVALID_ARG;
   if (num_q_heads % desc->num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
   const int group = num_q_heads / desc->num_kv_heads;
-  if (!extend_supported(desc->head_dim, (int)desc->cache_dtype, (int)act_dtype, group))
+  if (!extend_supported(desc->head_dim, mx4 ? (int)act_dtype : (int)desc->cache_dtype, (int)act_dtype, group))
     return PKV_ERR_UNSUPPORTED;
-  // no call needs scratch; either may take one to widen the pages it reads
+  // no call needs scratch (but one over microscaled codes, which are only read
+  // widened); either may take one to widen the pages it reads
   // once instead of per tile (a plain call whose workspace is smaller than
   // that, such as the 0 bytes of pkv_extend_workspace_bytes, does without)
   const size_t plain_bytes = groups ? 0 : plain_widen_bytes(desc);
@@ -1060,6 +1330,8 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   if (batch == 0 || total_q_rows == 0 || rows_hint == 0) return PKV_OK;
   if (!k_cache || !v_cache || !q || !out || !block_tables || !q_indptr || !prefix_lens)
     return PKV_ERR_INVALID_ARG;
+  if (mx4 && batch > 65535) return PKV_ERR_UNSUPPORTED;
+  if (mx4 && !widen_plain) return PKV_ERR_WORKSPACE;
   if (groups && (!groups->group_indptr || !groups->group_shared)) return PKV_ERR_INVALID_ARG;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) || !aligned(out, 16))
     return PKV_ERR_INVALID_ARG;
@@ -1067,8 +1339,8 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   DeviceState* ds = device_state(&e);
   if (!ds) return PKV_ERR_CUDA;
   CUtensorMap kmap, vmap, qmap, omap;
-  if ((st = make_page_map(&kmap, k_cache, desc)) != PKV_OK) return st;
-  if ((st = make_page_map(&vmap, v_cache, desc)) != PKV_OK) return st;
+  if (!mx4 && (st = make_page_map(&kmap, k_cache, desc)) != PKV_OK) return st;
+  if (!mx4 && (st = make_page_map(&vmap, v_cache, desc)) != PKV_OK) return st;
   if ((st = make_q_map(&qmap, q, desc->head_dim, num_q_heads, total_q_rows, group)) != PKV_OK)
     return st;
   // the output has q's shape and layout: the same map over out
@@ -1154,7 +1426,7 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   int cache_dt = (int)desc->cache_dtype;
   bool widen_pages = widen_plain;
   if (view) {
-    plan_view_items(p, max_total_len, ds->sm_count);
+    if (!mx4) plan_view_items(p, max_total_len, ds->sm_count);
     if (p.splits > 1 || p.half) p.out_tma = 0;  // (every row leaves with its parts' sum)
     const int64_t units = total_q_rows / (2 * p.tok) + (int64_t)batch;
     p.num_blocks_dyn = p.num_items;
@@ -1169,7 +1441,7 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     // pairs: 804 against 957 us), the pass itself three launches and three
     // times the pages' bytes (300 rows, 10 pairs: 140 against 132; 16 rows: 123
     // against 68).
-    if (p.splits > 1 || p.half || (p.tiles_per_head + 1) / 2 < 16) widen_pages = false;
+    if (!mx4 && (p.splits > 1 || p.half || (p.tiles_per_head + 1) / 2 < 16)) widen_pages = false;
     if (scaled && !widen_pages) {
       p.k_scales = view->k_scales;
       p.v_scales = view->v_scales;
@@ -1180,14 +1452,17 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     // workspace) into 16-bit pools read through maps over them
     pkv_cache_desc d16 = *desc;
     d16.cache_dtype = PKV_F16;
-    const bool fp8 = desc->cache_dtype == PKV_FP8_E4M3;
+    const bool fp8 = desc->cache_dtype == PKV_FP8_E4M3 || mx4;  // K is widened too
     uint8_t* base = static_cast<uint8_t*>(workspace);
     void* k16 = fp8 ? base : nullptr;
     void* v16 = base + (fp8 ? shared_prefix_pool16_bytes(desc) : 0);
     int32_t* claims = reinterpret_cast<int32_t*>(base + shared_prefix_widen_bytes(desc));
     if (fp8 && (st = make_page_map(&kmap, k16, &d16)) != PKV_OK) return st;
     if ((st = make_page_map(&vmap, v16, &d16)) != PKV_OK) return st;
-    if (scaled)
+    if (mx4)
+      e = launch_widen_mx4((int)act_dtype, k_cache, v_cache, view->k_mx, view->v_mx, k16, v16, claims,
+                           p, desc->head_dim, desc->block_size, max_total_len, ds->sm_count, stream);
+    else if (scaled)
       e = launch_widen_scaled((int)act_dtype, k_cache, v_cache, view->k_scales, view->v_scales, k16,
                               v16, claims, p, desc->head_dim, desc->block_size, max_total_len,
                               ds->sm_count, stream);
@@ -1262,6 +1537,32 @@ pkv_status pkv_paged_extend_attn_block_scaled(
   if (st != PKV_OK) return st;
   const pkv_cache_desc d = scaled_desc(desc);
   return extend_common(&d, k_cache, v_cache, nullptr, nullptr, q, out, act_dtype, q_indptr,
+                       prefix_lens, block_tables, max_blocks_per_seq, batch, num_q_heads,
+                       sm_scale, total_q_rows, max_suffix_len, max_total_len, lse_out, workspace,
+                       workspace_bytes, stream, nullptr, &view);
+}
+
+size_t pkv_extend_mx4_workspace_bytes(const pkv_cache_desc* desc) {
+  if (check_desc_mx4(desc) != PKV_OK) return 0;
+  return plain_widen_bytes(desc);
+}
+
+pkv_status pkv_paged_extend_attn_mx4(const pkv_cache_desc* desc, const void* k_cache,
+                                     const void* v_cache, const uint8_t* k_scales,
+                                     const uint8_t* v_scales, const void* q, void* out,
+                                     pkv_dtype act_dtype, const int32_t* q_indptr,
+                                     const int32_t* prefix_lens, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, int32_t batch, int32_t num_q_heads,
+                                     float sm_scale, int32_t total_q_rows, int32_t max_suffix_len,
+                                     int32_t max_total_len, int32_t window, int32_t sink_tokens,
+                                     float* lse_out, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+  const AttnView view{nullptr, nullptr, window, sink_tokens, true, k_scales, v_scales};
+  pkv_status st = check_desc_mx4(desc);
+  if (st == PKV_OK) st = check_view(desc, view, false);
+  if (st == PKV_OK && batch > 0) st = check_microscales(k_scales, v_scales);
+  if (st != PKV_OK) return st;
+  return extend_common(desc, k_cache, v_cache, nullptr, nullptr, q, out, act_dtype, q_indptr,
                        prefix_lens, block_tables, max_blocks_per_seq, batch, num_q_heads,
                        sm_scale, total_q_rows, max_suffix_len, max_total_len, lse_out, workspace,
                        workspace_bytes, stream, nullptr, &view);

@@ -78,13 +78,20 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <int HD, int CT, int NW, int NS>
 struct DecodeCfg {
-  static constexpr int ELEM = (CT == DT_E4M3) ? 1 : 2;
-  static constexpr int ROWB = HD * ELEM;                // bytes of one token row
-  static constexpr int CHUNKB = ROWB < 128 ? ROWB : 128;  // swizzle span (64 or 128)
+  static constexpr bool MX = (CT == DT_E2M1);
+  static constexpr int ELEM = (CT == DT_E4M3 || MX) ? 1 : 2;  // (e2m1: two codes)
+  static constexpr int ROWB = MX ? HD / 2 : HD * ELEM;  // bytes of one token row
+  static constexpr int CHUNKB = ROWB < 128 ? ROWB : 128;  // swizzle span (32, 64 or 128)
   static constexpr int NCH = ROWB / CHUNKB;             // TMA boxes per tile
   static constexpr int TILEB = kSubTokens * ROWB;       // one 16-token K (or V) tile
   static constexpr int STAGEB = 2 * TILEB;              // K tile + V tile
-  static constexpr int STAGE_AREA = NW * NS * STAGEB;
+  // MX: a stage's microscales of K and V (16 tokens x HD / 32 bytes each, copied
+  // to 128-byte boundaries), and per warp a tile's scales as the products take them
+  static constexpr int MXB = kSubTokens * HD / kMxGroup;
+  static constexpr int MXSTAGEB = MX ? 256 : 0;
+  static constexpr int MXFLOATS = MX ? 96 : 0;
+  static constexpr int MX_AREA = NW * NS * MXSTAGEB + NW * MXFLOATS * 4;
+  static constexpr int STAGE_AREA = NW * NS * STAGEB + MX_AREA;
   static constexpr int MT = HD / 16;                    // output m-tiles (dims)
   static constexpr bool MMA_BF16 = (CT == DT_BF16);
   static constexpr int COMB_BYTES = NW * 8 * HD * 4 + NW * 8 * 2 * 4;
@@ -103,6 +110,7 @@ __device__ __forceinline__ uint32_t tile_off(int t, int x) {
   const uint32_t o = (uint32_t)((x / CHUNKB) * (kSubTokens * CHUNKB) + t * CHUNKB + (x % CHUNKB));
   if constexpr (CHUNKB == 128) return o ^ ((o >> 3) & 0x70u);
   else if constexpr (CHUNKB == 64) return o ^ ((o >> 3) & 0x30u);
+  else if constexpr (CHUNKB == 32) return o ^ ((o >> 3) & 0x10u);
   else return o;
 }
 
@@ -113,6 +121,8 @@ __device__ __forceinline__ int out_dim(int u, int row) {
   if constexpr (CT == DT_E4M3) {
     const int pp = u >> 1, e = u & 1;
     return 32 * pp + (row >= 8 ? 16 : 0) + 2 * (row & 7) + e;
+  } else if constexpr (CT == DT_E2M1) {
+    return 32 * (u >> 1) + 4 * (row & 7) + 2 * (u & 1) + (row >> 3);
   } else {
     return 16 * u + row;
   }
@@ -198,6 +208,15 @@ __device__ __forceinline__ int splits_of(const DecodeParams& p, const DecodeExtr
   return (n + p.chunk - 1) / p.chunk;
 }
 
+// The maps of the microscale pools, a kernel argument of the launches that have
+// them.
+template <bool MX>
+struct ScaleMaps {};
+template <>
+struct ScaleMaps<true> {
+  CUtensorMap k, v;
+};
+
 // CASC: a cascade launch (tokens from the group's shared prefix on; partials
 // in the workspace slots after the prefix's chunks, always merged).  WIN: a
 // window with sink tokens.  BSC: fp8 codes with scales per block and kv head.
@@ -205,11 +224,13 @@ __device__ __forceinline__ int splits_of(const DecodeParams& p, const DecodeExtr
 template <int HD, int CT, int AT, int NW, int NS, bool CASC, bool WIN, bool BSC, bool CLM>
 __global__ void __launch_bounds__(NW * 32)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-              const DecodeParams p, const DecodeExtraParams ap) {
-  constexpr bool LEAN = WIN || BSC;  // a leaner inner loop than the plain and cascade forms
+              const DecodeParams p, const DecodeExtraParams ap,
+              const __grid_constant__ ScaleMaps<CT == DT_E2M1> mx) {
+  constexpr bool MX = CT == DT_E2M1;
+  constexpr bool LEAN = WIN || BSC || MX;  // a leaner inner loop than the plain and cascade forms
   constexpr bool CUT = LEAN && !CLM;
   static_assert(!(CASC && CLM), "unsupported combination");
-  static_assert(!(CASC && (WIN || BSC)) && (!BSC || CT == DT_E4M3), "unsupported combination");
+  static_assert(!(CASC && LEAN) && (!BSC || CT == DT_E4M3), "unsupported combination");
   using C = DecodeCfg<HD, CT, NW, NS>;
   extern __shared__ uint8_t smem_raw[];
   if constexpr (CLM) cluster_arrive_relaxed();
@@ -325,7 +346,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const int nsplit_b = splits_of<CUT>(p, ap, n - tb);
   const int cnt = warp < nsub ? (nsub - warp + NW - 1) / NW : 0;
 
-  if (ap.k_new != nullptr && split == nsplit_b - 1) {
+  if (!MX && ap.k_new != nullptr && split == nsplit_b - 1) {
     // Fused append: this CTA covers position n-1, the current token; its K/V
     // rows of kv head g go to their slot before any tile of this CTA is
     // loaded (TMA reads the slot after the proxy fence and the barrier
@@ -392,11 +413,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       int d0, d1, d2, d3;
       if constexpr (CT == DT_E4M3) {  // permuted k order, see the fp8 score product
         d0 = 16 * s + 4 * tig; d1 = d0 + 1; d2 = d0 + 2; d3 = d0 + 3;
+      } else if constexpr (MX) {  // likewise, 32 dims to two steps
+        d0 = 32 * (s >> 1) + 8 * tig + 4 * (s & 1); d1 = d0 + 1; d2 = d0 + 2; d3 = d0 + 3;
       } else {
         d0 = 16 * s + 2 * tig; d1 = d0 + 1; d2 = d0 + 8; d3 = d0 + 9;
       }
       if (gid < GC) {
-        if constexpr (CT != DT_E4M3) {
+        if constexpr (CT != DT_E4M3 && !MX) {
           qf[s][0] = *reinterpret_cast<const uint32_t*>(
               reinterpret_cast<const uint16_t*>(p.q) + qbase + d0);
           qf[s][1] = *reinterpret_cast<const uint32_t*>(
@@ -457,6 +480,11 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const uint32_t wstage_s = smem_u32(wstage);
   const uint32_t wbar_s = smem_u32(&bars[warp * NS]);
   float2* wscale = reinterpret_cast<float2*>(bars + NW * NS) + warp * NS;  // BSC
+  // MX: this warp's stages of microscales, and a tile's scales for the products
+  const uint8_t* mxstage = smem + NW * NS * C::STAGEB + warp * NS * C::MXSTAGEB;
+  const uint32_t mxstage_s = smem_u32(mxstage);
+  float* mxk = reinterpret_cast<float*>(smem + NW * NS * (C::STAGEB + C::MXSTAGEB)) + warp * C::MXFLOATS;
+  uint32_t* mxv = reinterpret_cast<uint32_t*>(mxk + 64);
   auto issue = [&](int i, int blk) {  // one lane only
     const int s = i % NS;
     const uint32_t bar = wbar_s + 8 * s;
@@ -466,13 +494,18 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     if constexpr (WIN) tok += tok >= ws.sv ? ws.skip : 0;
     const int row = tok & (bs - 1);
     const int page = blk < 0 ? -1 : blk * p.num_kv_heads + g;
-    mbar_arrive_expect_tx(bar, C::STAGEB);
+    mbar_arrive_expect_tx(bar, C::STAGEB + (MX ? 2 * C::MXB : 0));
 #pragma unroll
     for (int ch = 0; ch < C::NCH; ++ch)
       tma_load_3d(kdst + ch * kSubTokens * C::CHUNKB, &kmap, bar, ch * (C::CHUNKB / C::ELEM), row, page);
 #pragma unroll
     for (int ch = 0; ch < C::NCH; ++ch)
       tma_load_3d(vdst + ch * kSubTokens * C::CHUNKB, &vmap, bar, ch * (C::CHUNKB / C::ELEM), row, page);
+    if constexpr (MX) {  // (x: a multiple of 16 bytes, as row is one of 16)
+      const uint32_t at = mxstage_s + s * C::MXSTAGEB;
+      tma_load_2d(at, &mx.k, bar, row * (HD / kMxGroup), page);
+      tma_load_2d(at + 128, &mx.v, bar, row * (HD / kMxGroup), page);
+    }
   };
 
   auto give_scales = [&](int i) {  // BSC: in place before the stage's barrier completes
@@ -503,6 +536,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
   for (int u = 0; u < C::MT; ++u) acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
   float m_e = -INFINITY, m_o = -INFINITY, l_e = 0.f, l_o = 0.f;
+  // MX: the lane's group of dims is held relative to 2^(ref - 127): V's scales
+  // enter as f16 factors 2^(byte - ref) of the weights, of at most 2^7 (with
+  // weights of at most 2^8 their products stay inside f16).  When a byte above
+  // ref + 7 comes, ref moves to 5 below the largest one and the sums follow; a
+  // token whose scale is 2^-15 of that reference or less (2^-20 of the largest or
+  // less, when that set it) adds nothing.
+  [[maybe_unused]] int ref = -8;
   int done = 0;  // tiles consumed (all issued tiles are waited on before exit)
   bool timed_out = false;
 
@@ -530,7 +570,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // LEAN: a tile with hidden tokens gets their V rows zeroed in shared memory,
     // so that the other tiles carry no masks
     const bool edge = nvalid < kSubTokens || (WIN && w_lo > 0 && w_sk < kSubTokens);
-    if constexpr (LEAN) {
+    if constexpr (LEAN && !MX) {  // (an e2m1 code is finite, whatever it is)
       if (edge) {
         constexpr int UPR = C::ROWB / 16;
         for (int e = lane; e < kSubTokens * UPR; e += 32) {
@@ -545,12 +585,83 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     float2 bsc = make_float2(1.f, 1.f);
     if constexpr (BSC) bsc = wscale[s];
+    if constexpr (MX) {
+      // The tile's scales, each unpacked by one lane for the warp: lane 4 i + c
+      // takes tokens 2 i and 2 i + 1 of group c (64 dims: two groups only).
+      constexpr int GR = HD / kMxGroup;
+      const int i2 = (lane >> 2) * 2, c = lane & (GR - 1);
+      const uint8_t* at = mxstage + s * C::MXSTAGEB + i2 * GR + c;
+      const uint32_t k0 = at[0], k1 = at[GR];
+      uint32_t v0 = at[128], v1 = at[128 + GR];
+      if (edge) {  // what a hidden token holds does not count (K: its score is masked)
+        v0 = hidden(i2) ? 0u : v0;
+        v1 = hidden(i2 + 1) ? 0u : v1;
+      }
+      const int e0 = v0 == 255u ? 0 : (int)v0, e1 = v1 == 255u ? 0 : (int)v1;
+      int top = max(e0, e1);
+      if (__any_sync(kFull, top > ref + 7)) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
+        const int next = top > ref + 7 ? top - 5 : ref;
+        const float f = next - ref > 126 ? 0.f : __uint_as_float((uint32_t)(127 - (next - ref)) << 23);
+        ref = next;
+#pragma unroll
+        for (int c2 = 0; c2 < GR; ++c2) {
+          const float fc = __shfl_sync(kFull, f, c2);
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            acc[2 * c2][q4] *= fc;
+            acc[2 * c2 + 1][q4] *= fc;
+          }
+        }
+      }
+      const uint32_t h0 = v0 == 255u ? 0x7E00u : (uint32_t)max(e0 - ref + 15, 0) << 10;
+      const uint32_t h1 = v1 == 255u ? 0x7E00u : (uint32_t)max(e1 - ref + 15, 0) << 10;
+      __syncwarp();  // the scales of the tile before have been read
+      if (GR == 4 || (lane & 2) == 0) {
+        mxk[i2 * GR + c] = e8m0_to_f32(k0);
+        mxk[(i2 + 1) * GR + c] = e8m0_to_f32(k1);
+        mxv[(lane >> 2) * GR + c] = h0 | (h1 << 16);
+      }
+      __syncwarp();
+    }
 
     // ---- S^T (16 tokens x 8 heads) = K_tile . q^T --------------------------
     float sc[4] = {0.f, 0.f, 0.f, 0.f};
     {
       const int t = (lane & 7) + ((lane >> 3) & 1) * 8;
-      if constexpr (CT != DT_E4M3) {
+      if constexpr (MX) {
+        // one ldmatrix row is 32 codes of one token (a group with one scale):
+        // thread (gid, tig) receives codes 8 tig .. 8 tig + 7, four for each of
+        // two steps; the group's sum is scaled per token as it is added up
+        constexpr int GR = HD / kMxGroup;
+        float ka[GR], kb2[GR];
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {
+          ka[c] = mxk[gid * GR + c];
+          kb2[c] = mxk[(gid + 8) * GR + c];
+        }
+#pragma unroll
+        for (int kp = 0; kp < HD / 64; ++kp) {
+          uint32_t r[4];
+          ldsm_x4(kb + tile_off<C::CHUNKB>(t, (2 * kp + (lane >> 4)) * 16), r);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t lo[4], hi[4];
+            e2m1x8_to_f16x8(r[2 * e], lo);
+            e2m1x8_to_f16x8(r[2 * e + 1], hi);
+            const int c = 2 * kp + e;
+            float part[4];
+            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+            mma16816_f16_zero(part, a0, qf[2 * c][0], qf[2 * c][1]);
+            mma16816<false>(part, a1, qf[2 * c + 1][0], qf[2 * c + 1][1]);
+            sc[0] = fmaf(part[0], ka[c], sc[0]);
+            sc[1] = fmaf(part[1], ka[c], sc[1]);
+            sc[2] = fmaf(part[2], kb2[c], sc[2]);
+            sc[3] = fmaf(part[3], kb2[c], sc[3]);
+          }
+        }
+      } else if constexpr (CT != DT_E4M3) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           uint32_t a[4];
@@ -659,7 +770,37 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     {
       const int j = lane >> 3;
       const int t = (lane & 7) + (j >> 1) * 8;
-      if constexpr (CT != DT_E4M3) {
+      if constexpr (MX) {
+        // an 8x8 b16 transpose of codes gives thread (gid, tig) dims 4 gid ..
+        // 4 gid + 3 of tokens 2 tig and 2 tig + 1; widened, a byte permute pairs
+        // equal dims of the two tokens.  The weights carry the tokens' scales of
+        // the group, so that its product adds up as it is.
+        constexpr int GR = HD / kMxGroup;
+        uint32_t w0[GR], w1[GR];
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {
+          w0[c] = mul_f16x2(bh0, mxv[tig * GR + c]);
+          w1[c] = mul_f16x2(bh1, mxv[(tig + 4) * GR + c]);
+        }
+#pragma unroll
+        for (int pp = 0; pp < HD / 64; ++pp) {
+          uint32_t r[4];
+          ldsm_x4_t(vb + tile_off<C::CHUNKB>(t, (2 * pp + (j & 1)) * 16), r);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t lo[4], hi[4];  // tokens 0-7, 8-15
+            e2m1x8_to_f16x8(r[e], lo);
+            e2m1x8_to_f16x8(r[2 + e], hi);
+            const int c = 2 * pp + e;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t a[4] = {__byte_perm(lo[y], lo[y + 2], 0x5410), __byte_perm(lo[y], lo[y + 2], 0x7632),
+                                     __byte_perm(hi[y], hi[y + 2], 0x5410), __byte_perm(hi[y], hi[y + 2], 0x7632)};
+              mma16816<false>(acc[2 * c + y], a, w0[c], w1[c]);
+            }
+          }
+        }
+      } else if constexpr (CT != DT_E4M3) {
 #pragma unroll
         for (int u = 0; u < C::MT; ++u) {
           uint32_t a[4];
@@ -733,6 +874,15 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   for (int off = 4; off < 32; off <<= 1) {
     l_e += __shfl_xor_sync(kFull, l_e, off);
     l_o += __shfl_xor_sync(kFull, l_o, off);
+  }
+  if constexpr (MX) {  // the sums in their own scale
+    const float f = __uint_as_float((uint32_t)max(ref, 0) << 23);
+#pragma unroll
+    for (int u = 0; u < C::MT; ++u) {
+      const float fc = __shfl_sync(kFull, f, u >> 1);
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) acc[u][q4] *= fc;
+    }
   }
   __syncthreads();  // every warp is done with its stages: reuse them
   float* sm_o = reinterpret_cast<float*>(smem);        // [NW][8][HD]
@@ -946,6 +1096,7 @@ constexpr int stages_for() {
   // registers).  More CTAs in flight beat deeper pipelines: on GB300, fp8 d128
   // at 3 stages took 180 us where 6 took 206 us (70B-shaped layer), bf16 d128
   // at 2 stages 98.6 us where 3 took 99.2 us (8B-shaped layer).
+  if (CT == DT_E2M1) return 5;
   constexpr int st = DecodeCfg<HD, CT, kNW, 1>::STAGEB;
   constexpr int ns = (12 * 1024) / st;
   return ns < 2 ? 2 : (ns > 8 ? 8 : ns);
@@ -956,7 +1107,8 @@ template <int HD, int CT, int AT, bool CASC, int NSO = 0, int NW = kNW, bool WIN
           bool BSC = false, bool CLM = false>
 cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const DecodeParams& p, const DecodeExtraParams& ap,
-                            cudaStream_t stream, cudaEvent_t merge_after = nullptr) {
+                            cudaStream_t stream, cudaEvent_t merge_after = nullptr,
+                            const ScaleMaps<CT == DT_E2M1>& mx = {}) {
   constexpr int NS = NSO > 0 ? NSO : stages_for<HD, CT>();
   using C = DecodeCfg<HD, CT, NW, NS>;
   auto kern = decode_kernel<HD, CT, AT, NW, NS, CASC, WIN, BSC, CLM>;
@@ -964,7 +1116,8 @@ cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.num_kv_heads * ((p.group + 7) / 8), p.batch, p.num_splits);
-  if constexpr (WIN || BSC) {
+  constexpr bool LEAN = WIN || BSC || CT == DT_E2M1;
+  if constexpr (LEAN) {
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -979,17 +1132,17 @@ cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = CLM ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, ap);
+    e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, ap, mx);
     if (CLM) return e;
   } else {
-    kern<<<grid, NW * 32, smem, stream>>>(kmap, vmap, p, ap);
+    kern<<<grid, NW * 32, smem, stream>>>(kmap, vmap, p, ap, mx);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || (!CASC && p.num_splits <= 1)) return e;
   if (merge_after != nullptr && (e = cudaStreamWaitEvent(stream, merge_after, 0)) != cudaSuccess)
     return e;
   const int64_t pairs = (int64_t)p.batch * p.num_q_heads;
-  if constexpr (WIN || BSC) {
+  if constexpr (LEAN) {
     // Its launch overlaps the splits' last CTAs (it waits for all of them before
     // its first read).  Calls one after another, block-scaled: 64 requests of
     // 512-4,096 tokens 67.7 -> 66.3 us, 16 x 4,096 33.5 -> 32.4, 1 x 100,000

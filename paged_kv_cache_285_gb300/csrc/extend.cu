@@ -218,6 +218,63 @@ __global__ void __launch_bounds__(256) widen_scaled_list_kernel(
   }
 }
 
+// Eight e2m1 codes times s as OUT values, as above.
+template <int OUT>
+__device__ __forceinline__ void widen8_mx4(uint32_t codes, float s, uint32_t* o) {
+  uint32_t h[4];
+  e2m1x8_to_f16x8(codes, h);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float a = lo_f32<false>(h[e]) * s, b = hi_f32<false>(h[e]) * s;
+    if constexpr (OUT != DT_BF16) {
+      if (fabsf(a) > 65504.f) a = copysignf(65504.f, a);
+      if (fabsf(b) > 65504.f) b = copysignf(65504.f, b);
+    }
+    o[e] = pack2<OUT == DT_BF16>(a, b);
+  }
+}
+
+// One block's page of e2m1 codes (vectors of 16, two to a microscale) widened.
+template <int OUT>
+__device__ __forceinline__ void widen_block_mx4(const uint2* __restrict__ src, uint4* __restrict__ dst,
+                                                const uint8_t* __restrict__ scales, int in_vec) {
+  for (int u0 = threadIdx.x; u0 < in_vec; u0 += 4 * 256) {
+    uint2 x[4];
+    uint32_t b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (u0 + e * 256 < in_vec) {
+        x[e] = __ldg(src + u0 + e * 256);
+        b[e] = __ldg(scales + ((u0 + e * 256) >> 1));
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int u = u0 + e * 256;
+      if (u < in_vec) {
+        const float s = e8m0_to_f32(b[e]);
+        uint32_t o[8];
+        widen8_mx4<OUT>(x[e].x, s, o);
+        widen8_mx4<OUT>(x[e].y, s, o + 4);
+        st_global_v8(dst + 2 * u, o);  // (the workspace is 256-byte aligned)
+      }
+    }
+  }
+}
+
+template <int KOUT>
+__global__ void __launch_bounds__(256) widen_mx4_list_kernel(
+    const uint2* __restrict__ k, const uint2* __restrict__ v, const uint8_t* __restrict__ k_scales,
+    const uint8_t* __restrict__ v_scales, uint4* __restrict__ k16, uint4* __restrict__ v16,
+    const int* __restrict__ claims, int num_blocks, int in_vec) {
+  const int n = min(claims[0], num_blocks);
+  const int* list = claims + 1 + num_blocks;
+  for (int j = blockIdx.x; j < n; j += gridDim.x) {
+    const int64_t at = (int64_t)list[j] * in_vec;
+    widen_block_mx4<KOUT>(k + at, k16 + 2 * at, k_scales + at / 2, in_vec);
+    widen_block_mx4<DT_F16>(v + at, v16 + 2 * at, v_scales + at / 2, in_vec);
+  }
+}
+
 template <int SRC, int KOUT>
 __global__ void __launch_bounds__(256) widen_list_kernel(const uint4* __restrict__ k,
                                                          const uint4* __restrict__ v,
@@ -297,6 +354,32 @@ cudaError_t launch_widen_scaled(int act_dt, const void* k_cache, const void* v_c
   else
     widen_scaled_list_kernel<DT_F16><<<ctas, 256, 0, stream>>>(
         k, v, k_scales, v_scales, k16v, v16v, claims, p.num_blocks, p.num_kv_heads, in_vec, head_shift);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_widen_mx4(int act_dt, const void* k_cache, const void* v_cache,
+                             const uint8_t* k_scales, const uint8_t* v_scales, void* k16, void* v16,
+                             int* claims, const ExtendParams& p, int head_dim, int block_size,
+                             int max_total_len, int sm_count, cudaStream_t stream) {
+  if (!k_cache || !v_cache || !k_scales || !v_scales || !k16 || !v16 || !claims || p.batch <= 0 ||
+      p.num_blocks <= 0 || sm_count <= 0 || p.batch > 65535)
+    return cudaErrorInvalidValue;
+  const int in_vec = p.num_kv_heads * block_size * head_dim / 16;
+  const int max_nb = std::min(p.max_blocks, (std::max(max_total_len, 1) + block_size - 1) / block_size);
+  cudaError_t e = cudaMemsetAsync(claims, 0, (size_t)(1 + p.num_blocks) * sizeof(int), stream);
+  if (e != cudaSuccess) return e;
+  claim_kernel<<<dim3((unsigned)((max_nb + 255) / 256), (unsigned)p.batch), 256, 0, stream>>>(claims, p);
+  const int ctas = std::min(8 * sm_count, p.num_blocks);
+  const uint2* k = static_cast<const uint2*>(k_cache);
+  const uint2* v = static_cast<const uint2*>(v_cache);
+  uint4* k16v = static_cast<uint4*>(k16);
+  uint4* v16v = static_cast<uint4*>(v16);
+  if (act_dt == DT_BF16)
+    widen_mx4_list_kernel<DT_BF16><<<ctas, 256, 0, stream>>>(k, v, k_scales, v_scales, k16v, v16v,
+                                                              claims, p.num_blocks, in_vec);
+  else
+    widen_mx4_list_kernel<DT_F16><<<ctas, 256, 0, stream>>>(k, v, k_scales, v_scales, k16v, v16v,
+                                                             claims, p.num_blocks, in_vec);
   return cudaGetLastError();
 }
 

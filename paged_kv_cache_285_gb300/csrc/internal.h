@@ -16,10 +16,13 @@ enum : int {
   // extend with K read as bf16 and V pages widened to f16 beforehand (a
   // widening pass): a bf16 cache's K with its V shadow pool, or an fp8 cache's
   // K and V shadow pools (bf16 queries)
-  DT_BF16_V16 = 3
+  DT_BF16_V16 = 3,
+  // e2m1 codes, two to a byte, with a power-of-two scale per 32 of a row
+  DT_E2M1 = 4
 };
 
 constexpr int kSubTokens = 16;  // tokens per staged K/V tile (one MMA row block)
+constexpr int kMxGroup = 32;    // values of a row that share a microscale
 
 struct DecodeParams {
   const int32_t* block_tables;
@@ -172,6 +175,13 @@ struct AppendScaledParams {
   FastDiv div_hkv;
 };
 
+// Append into a cache of e2m1 codes with microscales [num_blocks][num_kv_heads]
+// [block_size][head_dim / 32] (the fp32 scales above are not used).
+struct AppendMx4Params : AppendScaledParams {
+  uint8_t* k_mx;
+  uint8_t* v_mx;
+};
+
 // Rows out of a cache: request b's rows row_indptr[b] .. row_indptr[b+1]-1 are
 // its positions start_positions[b] ...
 struct GatherParams {
@@ -197,6 +207,51 @@ struct GatherParams {
   int rows_per_cta;
   int out_32b;                 // both outputs are 32-byte aligned
   FastDiv div_hkv;
+};
+struct GatherMx4Params : GatherParams {
+  const uint8_t* k_mx;
+  const uint8_t* v_mx;
+};
+
+// Pools whose pages (or tokens) are moved within each of them by one launch.
+constexpr int kMaxPools = 128;
+struct Pool {
+  uint8_t* base;
+  uint32_t row_bytes;    // of a token and kv head (compaction)
+  int64_t block_bytes;
+};
+struct CopyBlocksParams {
+  const int32_t* src;    // [num_pairs]
+  const int32_t* dst;
+  int32_t* err;
+  int num_blocks;
+  int num_pools;
+  int pieces;            // CTAs per pair and pool
+  FastDiv div_pieces;
+  FastDiv div_pools;
+  Pool pool[kMaxPools];
+};
+struct CompactParams {
+  const int32_t* src_positions;  // [total_rows]
+  const int32_t* row_indptr;     // [batch + 1]
+  const int32_t* dst_starts;     // [batch]
+  const int32_t* block_tables;
+  int32_t* err;
+  int total_rows;
+  int max_rows;
+  int max_blocks;
+  int num_blocks;
+  int num_kv_heads;
+  int bs_shift;
+  int batch;
+  int num_pools;
+  int heads;             // kv heads that a CTA takes
+  int head_groups;       // ceil(num_kv_heads / heads)
+  int cluster_shift;     // log2(CTAs per item)
+  FastDiv div_heads;
+  FastDiv div_groups;
+  FastDiv div_pools;
+  Pool pool[kMaxPools];
 };
 
 struct ExtendParams {
@@ -277,10 +332,21 @@ cudaError_t launch_decode_cascade(const CUtensorMap& kmap, const CUtensorMap& vm
 cudaError_t launch_decode_window(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
                                  int cache_dt, int act_dt, cudaStream_t stream);
+// Decode of e2m1 codes with microscales (their pools' maps k_mx_map, v_mx_map),
+// optionally under a window (ap.window > 0).
+cudaError_t launch_decode_mx4(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              const CUtensorMap& k_mx_map, const CUtensorMap& v_mx_map,
+                              const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
+                              int act_dt, cudaStream_t stream);
 size_t decode_smem_bytes(int head_dim, int cache_dt);
 cudaError_t launch_append(const AppendParams& p, int cache_dt, int act_dt, cudaStream_t stream);
 cudaError_t launch_append_scaled(const AppendScaledParams& p, int act_dt, int head_dim,
                                  int block_size, cudaStream_t stream);
+cudaError_t launch_append_mx4(const AppendMx4Params& p, int act_dt, int head_dim, int block_size,
+                              cudaStream_t stream);
+cudaError_t launch_gather_mx4(const GatherMx4Params& p, int act_dt, int head_dim, cudaStream_t stream);
+cudaError_t launch_copy_blocks(CopyBlocksParams& p, int num_pairs, cudaStream_t stream);
+cudaError_t launch_compact(CompactParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_gather(const GatherParams& p, int cache_dt, int act_dt, int head_dim,
                           cudaStream_t stream);
 // Chain hashes of the full blocks of each request's token ids.
@@ -364,5 +430,10 @@ cudaError_t launch_widen_scaled(int act_dt, const void* k_cache, const void* v_c
                                 const float* k_scales, const float* v_scales, void* k16, void* v16,
                                 int* claims, const ExtendParams& p, int head_dim, int block_size,
                                 int max_total_len, int sm_count, cudaStream_t stream);
+// The same for e2m1 codes with microscales.
+cudaError_t launch_widen_mx4(int act_dt, const void* k_cache, const void* v_cache,
+                             const uint8_t* k_scales, const uint8_t* v_scales, void* k16, void* v16,
+                             int* claims, const ExtendParams& p, int head_dim, int block_size,
+                             int max_total_len, int sm_count, cudaStream_t stream);
 
 }  // namespace pkv

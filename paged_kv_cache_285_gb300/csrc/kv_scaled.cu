@@ -32,31 +32,13 @@
 // behind that wait.)
 #include <algorithm>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "pages.cuh"
 
 namespace pkv {
 
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-
-__device__ __forceinline__ void set_err(int32_t* err, int code) {
-  if (err) atomicCAS(err, 0, code);
-}
-
-// max of the two 16-bit halves, unsigned
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-template <int AT>
-__device__ __forceinline__ float bits_to_f32(uint32_t b) {
-  if constexpr (AT == DT_BF16) return __uint_as_float(b << 16);
-  else return __half2float(__ushort_as_half((unsigned short)b));
-}
 
 // Bits of the smallest power of two s >= 2^-126 with a <= 448 s = 1.75 2^8 s
 // (a finite, >= 0): a = 1.m 2^e takes 2^(e-8), or 2^(e-7) if 1.m > 1.75.
@@ -66,47 +48,11 @@ __device__ __forceinline__ uint32_t pow2_scale_bits(float a) {
   return (uint32_t)max(e, 1) << 23;
 }
 
-// The launch of a kernel that begins with grid_dependency_wait(): it is set up
-// while the launch before it in the stream still runs.
-template <typename P>
-cudaError_t launch_dependent(void (*kern)(P), unsigned ctas, unsigned threads, cudaStream_t stream,
-                             const P& p) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 // Four e4m3 codes times f (in fp32), as codes again (one rounding each).
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
   const uint32_t h0 = e4m3x2_to_f16x2(c & 0xFFFFu), h1 = e4m3x2_to_f16x2(c >> 16);
   return f32x2_to_e4m3x2(lo_f32<false>(h0) * f, hi_f32<false>(h0) * f) |
          (f32x2_to_e4m3x2(lo_f32<false>(h1) * f, hi_f32<false>(h1) * f) << 16);
-}
-
-// The request whose units contain unit u: request b's start at
-// q_indptr[b] / block_size + 2 b (it touches at most S / block_size + 2
-// blocks).  The whole warp, 32 entries per round.
-__device__ __forceinline__ int find_unit(const AppendScaledParams& p, int u) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) >> 5;
-    const int idx = lo + lane * step;
-    const int64_t v = idx < hi ? (int64_t)(*(p.q_indptr + idx) >> p.bs_shift) + 2 * (int64_t)idx
-                               : INT64_MAX;
-    const unsigned m = __ballot_sync(kFull, v <= u);
-    const int k = m ? 31 - __clz(m) : 0;
-    lo += k * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
 }
 
 template <int AT, int HD, int BS>
@@ -115,57 +61,13 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const AppendScaledPa
   constexpr int NV = BS * VPR / 32;     // per lane
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  const uint32_t task = blockIdx.x * 4u + (threadIdx.x >> 5);
-  if (task >= p.num_tasks) return;
-  const bool isv = task & 1u;
-  const uint32_t uh = task >> 1;
-  const int unit = (int)p.div_hkv.div(uh);
-  const int h = (int)(uh - (uint32_t)unit * p.div_hkv.d);
-  // the unit's request and which of its touched blocks
-  int b, j;
-  if (p.units_per_request > 0) {
-    b = (int)p.div_units.div((uint32_t)unit);
-    j = unit - b * p.units_per_request;
-  } else {
-    if (unit < p.batch && h == 0 && !isv && lane == 0) {
-      // where q_indptr falls, the search need not come to the request that does:
-      // the first units (there are more than requests) look at its entries in order
-      const int at = *(p.q_indptr + unit), next = *(p.q_indptr + unit + 1);
-      if (at < 0 || next < at) set_err(p.err, 3);
-    }
-    b = find_unit(p, unit);
-    j = unit - ((*(p.q_indptr + b) >> p.bs_shift) + 2 * b);
-  }
-  const int r0 = *(p.q_indptr + b), r1 = *(p.q_indptr + b + 1);
-  const int P = *(p.prefix_lens + b);
-  if (r1 == r0) return;
-  const bool report = j == 0 && h == 0 && !isv && lane == 0;
-  if (r0 < 0 || r1 < r0 || r1 > p.total_rows) {
-    if (report) set_err(p.err, 3);
-    return;
-  }
-  int S = r1 - r0;
-  if (j < 0 || j > (S >> p.bs_shift) + 2) return;
-  if (P < 0 || (int64_t)P + S > min((int64_t)p.max_blocks * BS, (int64_t)INT32_MAX - 128)) {
-    if (report) set_err(p.err, 3);
-    return;
-  }
-  if (S > p.max_suffix_len) {
-    if (report) set_err(p.err, 3);
-    S = p.max_suffix_len;
-  }
-  const int lb = (P >> p.bs_shift) + j;                 // logical block
-  const int start = max(P - lb * BS, 0);                // rows [start, end) of the page are new
-  const int end = min(P + S - lb * BS, BS);
-  if (end <= start) return;  // (the last unit or two of a request may be empty)
-  const int blk = *(p.block_tables + (int64_t)b * p.max_blocks + lb);
-  if (blk < 0 || blk >= p.num_blocks) {
-    if (h == 0 && !isv && lane == 0) set_err(p.err, 2);
-    return;
-  }
+  PageTask t;
+  if (!find_page_task<BS>(p, blockIdx.x * 4u + (threadIdx.x >> 5), t)) return;
+  const bool isv = t.isv;
+  const int h = t.h, blk = t.blk, start = t.start, end = t.end;
   const uint16_t* src = reinterpret_cast<const uint16_t*>(isv ? p.v_new : p.k_new) + h * HD;
   const int64_t row_elems = (int64_t)p.num_kv_heads * HD;
-  const int64_t first_row = (int64_t)r0 + ((int64_t)lb * BS - P);  // new row of page row 0
+  const int64_t first_row = t.first_row;
   uint4 x[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -273,17 +175,6 @@ __device__ __forceinline__ void read16(const uint4& x, float s, uint32_t (&o)[8]
   }
 }
 
-// 16 values of a row, in one 32-byte store where the output is aligned to that.
-__device__ __forceinline__ void store16(void* out, int64_t u, const uint32_t (&o)[8], bool aligned32) {
-  uint4* at = static_cast<uint4*>(out) + 2 * u;
-  if (aligned32) {
-    st_global_v8(at, o);
-  } else {
-    at[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    at[1] = make_uint4(o[4], o[5], o[6], o[7]);
-  }
-}
-
 template <int CT, int AT, int HD, bool BSC>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
   constexpr int EPV = CT == DT_E4M3 ? 16 : 8;  // elements per vector
@@ -294,29 +185,10 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
   const int64_t row0 = (int64_t)blockIdx.x * p.rows_per_cta;
   const int rows = (int)min((int64_t)p.rows_per_cta, p.total_rows - row0);
   if (threadIdx.x < rows) {
-    const int64_t t = row0 + threadIdx.x;
-    int lo = 0, hi = p.batch;  // the request of row t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (*(p.row_indptr + mid) <= t) lo = mid;
-      else hi = mid;
-    }
-    const int64_t pos = (int64_t)*(p.start_positions + lo) + (t - *(p.row_indptr + lo));
-    int blk = -1;
-    // rows that no request owns (before the first or after the last one's) are left alone
-    if (t < *(p.row_indptr + lo) || t >= *(p.row_indptr + lo + 1)) {
-      blk = -2;
-    } else if (pos < 0 || (pos >> p.bs_shift) >= p.max_blocks) {
-      set_err(p.err, 3);
-    } else {
-      blk = *(p.block_tables + (int64_t)lo * p.max_blocks + (pos >> p.bs_shift));
-      if (blk < 0 || blk >= p.num_blocks) {
-        set_err(p.err, 1);
-        blk = -1;
-      }
-    }
+    int blk, off;
+    find_row(p, row0 + threadIdx.x, blk, off);
     s_blk[threadIdx.x] = blk;
-    s_off[threadIdx.x] = (int)(pos & ((1 << p.bs_shift) - 1));
+    s_off[threadIdx.x] = off;
   }
   __syncthreads();
   const int vecs = rows * p.num_kv_heads * VPR;
@@ -378,20 +250,7 @@ cudaError_t launch_gather_t(const GatherParams& p, int head_dim, unsigned ctas, 
 cudaError_t launch_append_scaled(const AppendScaledParams& in, int act_dt, int head_dim,
                                  int block_size, cudaStream_t stream) {
   AppendScaledParams p = in;
-  p.bs_shift = block_size == 16 ? 4 : 5;
-  // Units: candidates for touched blocks.  Bounded by the length hint for
-  // every request (no search), or, when the requests' lengths differ so much
-  // that this would give more, by the rows (a search over q_indptr).
-  const int64_t per_request = ((int64_t)p.max_suffix_len + 2 * block_size - 2) / block_size;
-  const int64_t by_hint = per_request * p.batch;
-  const int64_t by_rows = p.total_rows / block_size + 2 * (int64_t)p.batch;
-  const bool direct = by_hint <= by_rows;
-  const int64_t tasks = std::min(by_hint, by_rows) * p.num_kv_heads * 2;
-  if (tasks > INT32_MAX) return cudaErrorInvalidValue;
-  p.units_per_request = direct ? (int)per_request : 0;
-  p.div_units = make_fastdiv((uint32_t)std::max(p.units_per_request, 1));
-  p.div_hkv = make_fastdiv((uint32_t)p.num_kv_heads);
-  p.num_tasks = (uint32_t)tasks;
+  if (!plan_pages(p, block_size)) return cudaErrorInvalidValue;
 #define PKV_APP(AT, HD, BS)                                   \
   if (act_dt == AT && head_dim == HD && block_size == BS)     \
     return launch_append_scaled_t<AT, HD, BS>(p, stream);
