@@ -85,11 +85,6 @@ int elem_bytes(pkv_dtype d) { return d == PKV_FP8_E4M3 ? 1 : 2; }
 // Bytes that a value takes in a cache, its share of the scales included.
 double value_bytes(pkv_dtype d) { return d == PKV_MX4 ? 0.5 + 1.0 / kMxGroup : (double)elem_bytes(d); }
 
-// Bytes of a row (a token and kv head) of a cache.
-int row_bytes(const pkv_cache_desc* d) {
-  return d->cache_dtype == PKV_MX4 ? d->head_dim / 2 : d->head_dim * elem_bytes(d->cache_dtype);
-}
-
 bool valid_dtype(pkv_dtype d) { return d == PKV_F16 || d == PKV_BF16 || d == PKV_FP8_E4M3; }
 
 pkv_status check_desc(const pkv_cache_desc* d) {
@@ -134,38 +129,21 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 pkv_status make_page_map(CUtensorMap* m, const void* base, const pkv_cache_desc* d) {
   auto enc = encode_fn();
   if (!enc) return PKV_ERR_CUDA;
-  const int elem = d->cache_dtype == PKV_MX4 ? 1 : elem_bytes(d->cache_dtype);
-  const int rowb = row_bytes(d);
+  const int elem = elem_bytes(d->cache_dtype);
+  const int rowb = d->head_dim * elem;
   const int chunkb = rowb < 128 ? rowb : 128;
-  cuuint64_t dims[3] = {(cuuint64_t)(rowb / elem), (cuuint64_t)d->block_size,
+  cuuint64_t dims[3] = {(cuuint64_t)d->head_dim, (cuuint64_t)d->block_size,
                         (cuuint64_t)d->num_blocks * (cuuint64_t)d->num_kv_heads};
   cuuint64_t strides[2] = {(cuuint64_t)rowb, (cuuint64_t)rowb * (cuuint64_t)d->block_size};
   cuuint32_t box[3] = {(cuuint32_t)(chunkb / elem), (cuuint32_t)kSubTokens, 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUtensorMapDataType dt =
       elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-  const CUtensorMapSwizzle sw = chunkb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : chunkb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                               : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUtensorMapSwizzle sw =
+      chunkb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   CUresult r = enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
-}
-
-// The microscales of a pool's pages: dims {block_size * head_dim / 32 bytes,
-// num_blocks*Hkv}, a box the bytes of 16 tokens (32 or 64).
-pkv_status make_microscale_map(CUtensorMap* m, const void* base, const pkv_cache_desc* d) {
-  auto enc = encode_fn();
-  if (!enc) return PKV_ERR_CUDA;
-  const cuuint64_t page = (cuuint64_t)d->block_size * d->head_dim / kMxGroup;
-  cuuint64_t dims[2] = {page, (cuuint64_t)d->num_blocks * (cuuint64_t)d->num_kv_heads};
-  cuuint64_t strides[1] = {page};
-  cuuint32_t box[2] = {(cuuint32_t)(kSubTokens * d->head_dim / kMxGroup), 1u};
-  cuuint32_t estr[2] = {1u, 1u};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -802,8 +780,8 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
     return PKV_ERR_WORKSPACE;
   if (pl.splits > 65535) return PKV_ERR_UNSUPPORTED;
   CUtensorMap kmap, vmap;
-  if ((st = make_page_map(&kmap, k_cache, desc)) != PKV_OK) return st;
-  if ((st = make_page_map(&vmap, v_cache, desc)) != PKV_OK) return st;
+  if (!mx4 && (st = make_page_map(&kmap, k_cache, desc)) != PKV_OK) return st;
+  if (!mx4 && (st = make_page_map(&vmap, v_cache, desc)) != PKV_OK) return st;
   DecodeParams p;
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
@@ -852,10 +830,9 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
     ap.num_cuts = pl.num_cuts;
     std::copy(pl.cut, pl.cut + kMaxCuts + 1, ap.cut);
     if (mx4) {
-      CUtensorMap k_mx_map, v_mx_map;
-      if ((st = make_microscale_map(&k_mx_map, view->k_mx, desc)) != PKV_OK) return st;
-      if ((st = make_microscale_map(&v_mx_map, view->v_mx, desc)) != PKV_OK) return st;
-      e = launch_decode_mx4(kmap, vmap, k_mx_map, v_mx_map, p, ap, desc->head_dim, (int)act_dtype, stream);
+      ap.k_scales = view->k_mx;
+      ap.v_scales = view->v_mx;
+      e = launch_decode_mx4(p, ap, desc->head_dim, (int)act_dtype, stream);
       return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
     }
     e = launch_decode_window(kmap, vmap, p, ap, desc->head_dim, (int)desc->cache_dtype,

@@ -84,13 +84,15 @@ struct DecodeCfg {
   static constexpr int CHUNKB = ROWB < 128 ? ROWB : 128;  // swizzle span (32, 64 or 128)
   static constexpr int NCH = ROWB / CHUNKB;             // TMA boxes per tile
   static constexpr int TILEB = kSubTokens * ROWB;       // one 16-token K (or V) tile
-  static constexpr int STAGEB = 2 * TILEB;              // K tile + V tile
+  static constexpr int TPS = MX ? 2 : 1;                // tiles per stage
+  static constexpr int STAGEB = TPS * 2 * TILEB;        // K tile + V tile, of each
   // MX: a stage's microscales of K and V (16 tokens x HD / 32 bytes each, copied
-  // to 128-byte boundaries), and per warp a tile's scales as the products take them
+  // to 128-byte boundaries), and per warp its tiles' scales as the products take
+  // them: K's as fp32, V's as pairs of f16
   static constexpr int MXB = kSubTokens * HD / kMxGroup;
-  static constexpr int MXSTAGEB = MX ? 256 : 0;
-  static constexpr int MXFLOATS = MX ? 96 : 0;
-  static constexpr int MX_AREA = NW * NS * MXSTAGEB + NW * MXFLOATS * 4;
+  static constexpr int MXSTAGEB = MX ? TPS * 256 : 0;
+  static constexpr int MXBUF = MX ? TPS * kSubTokens * (HD / kMxGroup) * 6 : 0;
+  static constexpr int MX_AREA = NW * NS * MXSTAGEB + NW * MXBUF;
   static constexpr int STAGE_AREA = NW * NS * STAGEB + MX_AREA;
   static constexpr int MT = HD / 16;                    // output m-tiles (dims)
   static constexpr bool MMA_BF16 = (CT == DT_BF16);
@@ -208,24 +210,14 @@ __device__ __forceinline__ int splits_of(const DecodeParams& p, const DecodeExtr
   return (n + p.chunk - 1) / p.chunk;
 }
 
-// The maps of the microscale pools, a kernel argument of the launches that have
-// them.
-template <bool MX>
-struct ScaleMaps {};
-template <>
-struct ScaleMaps<true> {
-  CUtensorMap k, v;
-};
-
 // CASC: a cascade launch (tokens from the group's shared prefix on; partials
 // in the workspace slots after the prefix's chunks, always merged).  WIN: a
 // window with sink tokens.  BSC: fp8 codes with scales per block and kv head.
 // CLM: the splits of a (request, head chunk) form a cluster that joins them.
 template <int HD, int CT, int AT, int NW, int NS, bool CASC, bool WIN, bool BSC, bool CLM>
-__global__ void __launch_bounds__(NW * 32)
+__global__ void __launch_bounds__(NW * 32, CT == DT_E2M1 ? 16 / NW : 0)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-              const DecodeParams p, const DecodeExtraParams ap,
-              const __grid_constant__ ScaleMaps<CT == DT_E2M1> mx) {
+              const DecodeParams p, const DecodeExtraParams ap) {
   constexpr bool MX = CT == DT_E2M1;
   constexpr bool LEAN = WIN || BSC || MX;  // a leaner inner loop than the plain and cascade forms
   constexpr bool CUT = LEAN && !CLM;
@@ -394,13 +386,15 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 
   if (threadIdx.x == 0) {
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
-    // BSC: two arrivals, the copies and the tile's scales
-    for (int i = 0; i < NW * NS; ++i) mbar_init(smem_u32(&bars[i]), BSC ? 2 : 1);
-    fence_mbar_init();
+    if constexpr (!MX) {
+      prefetch_tensormap(&kmap);
+      prefetch_tensormap(&vmap);
+      // BSC: two arrivals, the copies and the tile's scales
+      for (int i = 0; i < NW * NS; ++i) mbar_init(smem_u32(&bars[i]), BSC ? 2 : 1);
+      fence_mbar_init();
+    }
   }
-  __syncthreads();
+  if constexpr (!MX) __syncthreads();
 
   // ---- query fragments (B operand: k = head dim, n = head in group) --------
   constexpr bool MMA_BF16 = C::MMA_BF16;
@@ -454,7 +448,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       sc_next = make_float2(1.f, 1.f);
       if (blk >= 0) {
         const int64_t at = (int64_t)blk * p.num_kv_heads + g;
-        sc_next = make_float2(ap.k_scales[at], ap.v_scales[at]);
+        sc_next = make_float2(static_cast<const float*>(ap.k_scales)[at],
+                              static_cast<const float*>(ap.v_scales)[at]);
       }
     }
     return blk;
@@ -480,11 +475,6 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const uint32_t wstage_s = smem_u32(wstage);
   const uint32_t wbar_s = smem_u32(&bars[warp * NS]);
   float2* wscale = reinterpret_cast<float2*>(bars + NW * NS) + warp * NS;  // BSC
-  // MX: this warp's stages of microscales, and a tile's scales for the products
-  const uint8_t* mxstage = smem + NW * NS * C::STAGEB + warp * NS * C::MXSTAGEB;
-  const uint32_t mxstage_s = smem_u32(mxstage);
-  float* mxk = reinterpret_cast<float*>(smem + NW * NS * (C::STAGEB + C::MXSTAGEB)) + warp * C::MXFLOATS;
-  uint32_t* mxv = reinterpret_cast<uint32_t*>(mxk + 64);
   auto issue = [&](int i, int blk) {  // one lane only
     const int s = i % NS;
     const uint32_t bar = wbar_s + 8 * s;
@@ -494,18 +484,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     if constexpr (WIN) tok += tok >= ws.sv ? ws.skip : 0;
     const int row = tok & (bs - 1);
     const int page = blk < 0 ? -1 : blk * p.num_kv_heads + g;
-    mbar_arrive_expect_tx(bar, C::STAGEB + (MX ? 2 * C::MXB : 0));
+    mbar_arrive_expect_tx(bar, C::STAGEB);
 #pragma unroll
     for (int ch = 0; ch < C::NCH; ++ch)
       tma_load_3d(kdst + ch * kSubTokens * C::CHUNKB, &kmap, bar, ch * (C::CHUNKB / C::ELEM), row, page);
 #pragma unroll
     for (int ch = 0; ch < C::NCH; ++ch)
       tma_load_3d(vdst + ch * kSubTokens * C::CHUNKB, &vmap, bar, ch * (C::CHUNKB / C::ELEM), row, page);
-    if constexpr (MX) {  // (x: a multiple of 16 bytes, as row is one of 16)
-      const uint32_t at = mxstage_s + s * C::MXSTAGEB;
-      tma_load_2d(at, &mx.k, bar, row * (HD / kMxGroup), page);
-      tma_load_2d(at + 128, &mx.v, bar, row * (HD / kMxGroup), page);
-    }
   };
 
   auto give_scales = [&](int i) {  // BSC: in place before the stage's barrier completes
@@ -524,7 +509,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
   };
 
-  {
+  if constexpr (!MX) {
     const int pre = cnt < NS ? cnt : NS;
     for (int i = 0; i < pre; ++i) load_tile(i);
     // (the first copies do not wait for the scales, one more dependent load)
@@ -536,17 +521,275 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
   for (int u = 0; u < C::MT; ++u) acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
   float m_e = -INFINITY, m_o = -INFINITY, l_e = 0.f, l_o = 0.f;
-  // MX: the lane's group of dims is held relative to 2^(ref - 127): V's scales
-  // enter as f16 factors 2^(byte - ref) of the weights, of at most 2^7 (with
-  // weights of at most 2^8 their products stay inside f16).  When a byte above
-  // ref + 7 comes, ref moves to 5 below the largest one and the sums follow; a
-  // token whose scale is 2^-15 of that reference or less (2^-20 of the largest or
-  // less, when that set it) adds nothing.
-  [[maybe_unused]] int ref = -8;
   int done = 0;  // tiles consumed (all issued tiles are waited on before exit)
   bool timed_out = false;
 
-  for (int i = 0; i < cnt; ++i) {
+  if constexpr (MX) {
+    // Two tiles of the warp at a time (a stage): they share the wait, the scales'
+    // unpacking (a lane a token) and the check of the running maximum.  A tile's
+    // codes and scales are contiguous in their pages: the lanes copy them in 16-byte
+    // units (cp.async, to swizzled places for ldmatrix), which takes a quarter of the
+    // instructions that four TMA copies by one lane take.
+    constexpr int GR = HD / kMxGroup;  // groups of a row that have a scale
+    const uint32_t mxstage_s = smem_u32(smem) + NW * NS * C::STAGEB + warp * NS * C::MXSTAGEB;
+    // a stage's scales as the products take them: K's [32 tokens][GR] fp32, V's [16
+    // pairs of tokens][GR] f16x2
+    const uint32_t mxk = smem_u32(smem) + NW * NS * (C::STAGEB + C::MXSTAGEB) + warp * C::MXBUF;
+    const uint32_t mxv = mxk + C::TPS * kSubTokens * GR * 4;
+    constexpr int UNITS = C::TILEB / 16;            // 16-byte units of a tile's codes ...
+    constexpr int SUNITS = C::MXB / 16;             // ... and scales
+    const uint32_t unit0 = tile_off<C::CHUNKB>(lane * 16 / C::ROWB, lane * 16 % C::ROWB);
+    const uint8_t* kcodes = static_cast<const uint8_t*>(ap.k_cache) + lane * 16;
+    const uint8_t* vcodes = static_cast<const uint8_t*>(ap.v_cache) + lane * 16;
+    const uint8_t* scales = static_cast<const uint8_t*>(lane < SUNITS ? ap.k_scales : ap.v_scales) +
+                            lane % SUNITS * 16;
+    const uint32_t scale_dst = mxstage_s + lane / SUNITS * 128 + lane % SUNITS * 16;
+    auto load_pair = [&](int i, int st) {
+      window_of(i);  // (i even: both tiles are in one window of block ids)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (i + x < cnt) {
+          const int blk = __shfl_sync(kFull, bw_cur, (i + x) & 31);
+          int tok = t0 + kSubTokens * (warp + (i + x) * NW);
+          if constexpr (WIN) tok += tok >= ws.sv ? ws.skip : 0;
+          const uint32_t n = blk < 0 ? 0u : 16u;  // a block outside the pool gives zeros
+          const int64_t row = ((int64_t)(max(blk, 0) * p.num_kv_heads + g) << p.bs_shift) + (tok & (bs - 1));
+          const int64_t at = row * C::ROWB;
+          const uint32_t dst = wstage_s + st * C::STAGEB + x * 2 * C::TILEB + unit0;
+#pragma unroll
+          for (int u = 0; u < UNITS / 32; ++u) {
+            cp_async16(dst + u * 512, kcodes + at + u * 512, n);
+            cp_async16(dst + C::TILEB + u * 512, vcodes + at + u * 512, n);
+          }
+          if (lane < 2 * SUNITS) cp_async16(scale_dst + st * C::MXSTAGEB + x * 256, scales + row * GR, n);
+        }
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      if (2 * k < cnt) load_pair(2 * k, k);
+      cp_async_commit();
+    }
+    // The sums of group c's dims are held relative to 2^(ref[c] - 127): V's scales
+    // enter as f16 factors 2^(byte - ref) of the weights, of at most 2^7 (with
+    // weights of at most 2^8 their products stay inside f16).  When a byte above
+    // ref + 7 comes, ref moves to 5 below the largest one and the sums follow.  A
+    // factor below 2^-14 is 0: a token whose scale is 2^20 below the largest so far
+    // adds nothing.
+    int ref[GR];
+#pragma unroll
+    for (int c = 0; c < GR; ++c) ref[c] = -8;
+    int st = 0;
+    for (int i = 0; i < cnt; i += 2) {
+      cp_async_wait<NS - 1>();
+      __syncwarp();
+      // of the two tiles: valid rows; rows below lo are hidden unless below sk
+      int nvalid[2], lo[2] = {0, 0}, sk[2] = {0, 0};
+      bool edge = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int tok = t0 + kSubTokens * (warp + (i + x) * NW);
+        nvalid[x] = t1 - tok;
+        edge |= nvalid[x] < kSubTokens;
+        if constexpr (WIN) {
+          const int at = tok + (tok >= ws.sv ? ws.skip : 0);
+          lo[x] = ws.w0 - at;
+          sk[x] = ws.sinks - at;
+          edge |= lo[x] > 0 && sk[x] < kSubTokens;
+        }
+      }
+      auto hidden = [&](int x, int row) -> bool {
+        return row >= nvalid[x] || (WIN && row < lo[x] && row >= sk[x]);
+      };
+
+      // ---- the tokens' scales, unpacked for the warp: lane = token ---------------
+      {
+        const uint32_t at = mxstage_s + st * C::MXSTAGEB + (lane >> 4) * 256 + (lane & 15) * GR;
+        const uint32_t wk = lds_u<GR>(at);
+        uint32_t wv = lds_u<GR>(at + 128);
+        // what a hidden token holds does not count (K: its score is masked)
+        if (edge && (lane < 16 ? hidden(0, lane) : hidden(1, lane - 16))) wv = 0u;
+        // bytes of 255 (NaN), at their highest bits
+        const uint32_t nan_k = ((wk & 0x7F7F7F7Fu) + 0x01010101u) & wk & 0x80808080u;
+        const uint32_t nan_v = ((wv & 0x7F7F7F7Fu) + 0x01010101u) & wv & 0x80808080u;
+        float fk[GR];
+        int ev[GR];
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {
+          fk[c] = __uint_as_float((c == 3 ? wk >> 1 : wk << (23 - 8 * c)) & 0x7F800000u) * p.scale_log2;
+          ev[c] = (int)((wv >> (8 * c)) & 0xFFu);
+        }
+        if (__any_sync(kFull, (nan_k | nan_v) != 0u)) {
+#pragma unroll
+          for (int c = 0; c < GR; ++c) {
+            if ((nan_k >> (8 * c)) & 0x80u) fk[c] = __uint_as_float(0x7FC00000u);
+            if ((nan_v >> (8 * c)) & 0x80u) ev[c] = 0;
+          }
+        }
+        bool above = false;
+#pragma unroll
+        for (int c = 0; c < GR; ++c) above |= ev[c] > ref[c] + 7;
+        if (__any_sync(kFull, above)) {
+#pragma unroll
+          for (int c = 0; c < GR; ++c) {
+            const int top = __reduce_max_sync(kFull, ev[c]);
+            if (top > ref[c] + 7) {
+              const int up = top - 5 - ref[c];
+              ref[c] += up;
+              const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+                acc[2 * c][q4] *= f;
+                acc[2 * c + 1][q4] *= f;
+              }
+            }
+          }
+        }
+        __syncwarp();  // the scales of the tiles before have been read
+        sts_f<GR>(mxk + lane * GR * 4, fk);
+#pragma unroll
+        for (int c = 0; c < GR; ++c)
+          sts_u16(mxv + (lane >> 1) * GR * 4 + c * 4 + (lane & 1) * 2,
+                  (nan_v >> (8 * c)) & 0x80u ? 0x7E00u : (uint32_t)max(ev[c] - ref[c] + 15, 0) << 10);
+        __syncwarp();
+      }
+
+      // ---- S^T = K_tile . q^T ---------------------------------------------------
+      // One ldmatrix row is 32 codes of one token (a group): thread (gid, tig)
+      // receives codes 8 tig .. 8 tig + 7, four for each of two steps; the group's
+      // sum is scaled per token as it is added up.
+      float sc[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t kb = wstage_s + st * C::STAGEB + x * 2 * C::TILEB;
+        const int t = (lane & 7) + ((lane >> 3) & 1) * 8;
+        uint32_t ka[GR], kc[GR];
+        lds_v<GR>(mxk + (16 * x + gid) * GR * 4, ka);
+        lds_v<GR>(mxk + (16 * x + gid + 8) * GR * 4, kc);
+        sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
+#pragma unroll
+        for (int kp = 0; kp < HD / 64; ++kp) {
+          uint32_t r[4];
+          ldsm_x4(kb + tile_off<C::CHUNKB>(t, (2 * kp + (lane >> 4)) * 16), r);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t a[4], b2[4];
+            e2m1x8_to_f16x8(r[2 * e], a);
+            e2m1x8_to_f16x8(r[2 * e + 1], b2);
+            const int c = 2 * kp + e;
+            float part[4];
+            const uint32_t a0[4] = {a[0], b2[0], a[1], b2[1]}, a1[4] = {a[2], b2[2], a[3], b2[3]};
+            mma16816_f16_zero(part, a0, qf[2 * c][0], qf[2 * c][1]);
+            mma16816<false>(part, a1, qf[2 * c + 1][0], qf[2 * c + 1][1]);
+            sc[x][0] = fmaf(part[0], __uint_as_float(ka[c]), sc[x][0]);
+            sc[x][1] = fmaf(part[1], __uint_as_float(ka[c]), sc[x][1]);
+            sc[x][2] = fmaf(part[2], __uint_as_float(kc[c]), sc[x][2]);
+            sc[x][3] = fmaf(part[3], __uint_as_float(kc[c]), sc[x][3]);
+          }
+        }
+      }
+
+      // ---- online softmax (base 2), per head column -------------------------------
+      if (edge) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4)
+            if (hidden(x, gid + (q4 >> 1) * 8)) sc[x][q4] = -INFINITY;
+      }
+      // The base of the exponents moves only when a score passes it by more than
+      // 2^8: as long as no lane has one, the columns' maxima are not needed.
+      float mx_e = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
+      float mx_o = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
+      if (__any_sync(kFull, mx_e > m_e + 8.f || mx_o > m_o + 8.f)) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          mx_e = fmaxf(mx_e, __shfl_xor_sync(kFull, mx_e, off));
+          mx_o = fmaxf(mx_o, __shfl_xor_sync(kFull, mx_o, off));
+        }
+        const float mn_e = mx_e > m_e + 8.f ? mx_e : m_e, mn_o = mx_o > m_o + 8.f ? mx_o : m_o;
+        const float al_e = mn_e == m_e ? 1.f : fast_exp2(m_e - mn_e);
+        const float al_o = mn_o == m_o ? 1.f : fast_exp2(m_o - mn_o);
+        m_e = mn_e;
+        m_o = mn_o;
+        l_e *= al_e;
+        l_o *= al_o;
+#pragma unroll
+        for (int u = 0; u < C::MT; ++u) {
+          acc[u][0] *= al_e;
+          acc[u][1] *= al_o;
+          acc[u][2] *= al_e;
+          acc[u][3] *= al_o;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        sc[x][0] = fast_exp2(sc[x][0] - m_e);
+        sc[x][1] = fast_exp2(sc[x][1] - m_o);
+        sc[x][2] = fast_exp2(sc[x][2] - m_e);
+        sc[x][3] = fast_exp2(sc[x][3] - m_o);
+        l_e += sc[x][0] + sc[x][2];
+        l_o += sc[x][1] + sc[x][3];
+      }
+
+      // ---- O^T[dim][head] += V^T . P^T ----------------------------------------------
+      // An 8x8 b16 transpose of codes gives thread (gid, tig) dims 4 gid .. 4 gid + 3
+      // of tokens 2 tig and 2 tig + 1; widened, a byte permute pairs equal dims of
+      // the two tokens.  The weights carry the tokens' scales of the group, so that
+      // its product adds up as it is.
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t vb = wstage_s + st * C::STAGEB + x * 2 * C::TILEB + C::TILEB;
+        const uint32_t bh0 = movmatrix_t(pack2<false>(sc[x][0], sc[x][1]));
+        const uint32_t bh1 = movmatrix_t(pack2<false>(sc[x][2], sc[x][3]));
+        uint32_t w0[GR], w1[GR];
+        lds_v<GR>(mxv + (8 * x + tig) * GR * 4, w0);
+        lds_v<GR>(mxv + (8 * x + tig + 4) * GR * 4, w1);
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {
+          w0[c] = mul_f16x2(bh0, w0[c]);
+          w1[c] = mul_f16x2(bh1, w1[c]);
+        }
+        const int j = lane >> 3, t = (lane & 7) + (j >> 1) * 8;
+#pragma unroll
+        for (int pp = 0; pp < HD / 64; ++pp) {
+          uint32_t r[4];
+          ldsm_x4_t(vb + tile_off<C::CHUNKB>(t, (2 * pp + (j & 1)) * 16), r);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t v0[4], v1[4];  // tokens 0-7, 8-15
+            e2m1x8_to_f16x8(r[e], v0);
+            e2m1x8_to_f16x8(r[2 + e], v1);
+            const int c = 2 * pp + e;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t a[4] = {__byte_perm(v0[y], v0[y + 2], 0x5410), __byte_perm(v0[y], v0[y + 2], 0x7632),
+                                     __byte_perm(v1[y], v1[y + 2], 0x5410), __byte_perm(v1[y], v1[y + 2], 0x7632)};
+              mma16816<false>(acc[2 * c + y], a, w0[c], w1[c]);
+            }
+          }
+        }
+      }
+
+      __syncwarp();
+      if (i + 2 * NS < cnt) load_pair(i + 2 * NS, st);
+      cp_async_commit();
+      if (++st == NS) st = 0;
+    }
+    cp_async_wait<0>();
+    // the sums in their own scale
+#pragma unroll
+    for (int c = 0; c < GR; ++c) {
+      const float f = __uint_as_float((uint32_t)max(ref[c], 0) << 23);
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        acc[2 * c][q4] *= f;
+        acc[2 * c + 1][q4] *= f;
+      }
+    }
+  }
+
+  for (int i = 0; !MX && i < cnt; ++i) {
     const int s = i % NS;
     if (!mbar_wait(wbar_s + 8 * s, (uint32_t)((i / NS) & 1))) {
       timed_out = true;
@@ -570,7 +813,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // LEAN: a tile with hidden tokens gets their V rows zeroed in shared memory,
     // so that the other tiles carry no masks
     const bool edge = nvalid < kSubTokens || (WIN && w_lo > 0 && w_sk < kSubTokens);
-    if constexpr (LEAN && !MX) {  // (an e2m1 code is finite, whatever it is)
+    if constexpr (LEAN) {
       if (edge) {
         constexpr int UPR = C::ROWB / 16;
         for (int e = lane; e < kSubTokens * UPR; e += 32) {
@@ -585,83 +828,11 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     float2 bsc = make_float2(1.f, 1.f);
     if constexpr (BSC) bsc = wscale[s];
-    if constexpr (MX) {
-      // The tile's scales, each unpacked by one lane for the warp: lane 4 i + c
-      // takes tokens 2 i and 2 i + 1 of group c (64 dims: two groups only).
-      constexpr int GR = HD / kMxGroup;
-      const int i2 = (lane >> 2) * 2, c = lane & (GR - 1);
-      const uint8_t* at = mxstage + s * C::MXSTAGEB + i2 * GR + c;
-      const uint32_t k0 = at[0], k1 = at[GR];
-      uint32_t v0 = at[128], v1 = at[128 + GR];
-      if (edge) {  // what a hidden token holds does not count (K: its score is masked)
-        v0 = hidden(i2) ? 0u : v0;
-        v1 = hidden(i2 + 1) ? 0u : v1;
-      }
-      const int e0 = v0 == 255u ? 0 : (int)v0, e1 = v1 == 255u ? 0 : (int)v1;
-      int top = max(e0, e1);
-      if (__any_sync(kFull, top > ref + 7)) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
-        const int next = top > ref + 7 ? top - 5 : ref;
-        const float f = next - ref > 126 ? 0.f : __uint_as_float((uint32_t)(127 - (next - ref)) << 23);
-        ref = next;
-#pragma unroll
-        for (int c2 = 0; c2 < GR; ++c2) {
-          const float fc = __shfl_sync(kFull, f, c2);
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            acc[2 * c2][q4] *= fc;
-            acc[2 * c2 + 1][q4] *= fc;
-          }
-        }
-      }
-      const uint32_t h0 = v0 == 255u ? 0x7E00u : (uint32_t)max(e0 - ref + 15, 0) << 10;
-      const uint32_t h1 = v1 == 255u ? 0x7E00u : (uint32_t)max(e1 - ref + 15, 0) << 10;
-      __syncwarp();  // the scales of the tile before have been read
-      if (GR == 4 || (lane & 2) == 0) {
-        mxk[i2 * GR + c] = e8m0_to_f32(k0);
-        mxk[(i2 + 1) * GR + c] = e8m0_to_f32(k1);
-        mxv[(lane >> 2) * GR + c] = h0 | (h1 << 16);
-      }
-      __syncwarp();
-    }
-
     // ---- S^T (16 tokens x 8 heads) = K_tile . q^T --------------------------
     float sc[4] = {0.f, 0.f, 0.f, 0.f};
     {
       const int t = (lane & 7) + ((lane >> 3) & 1) * 8;
-      if constexpr (MX) {
-        // one ldmatrix row is 32 codes of one token (a group with one scale):
-        // thread (gid, tig) receives codes 8 tig .. 8 tig + 7, four for each of
-        // two steps; the group's sum is scaled per token as it is added up
-        constexpr int GR = HD / kMxGroup;
-        float ka[GR], kb2[GR];
-#pragma unroll
-        for (int c = 0; c < GR; ++c) {
-          ka[c] = mxk[gid * GR + c];
-          kb2[c] = mxk[(gid + 8) * GR + c];
-        }
-#pragma unroll
-        for (int kp = 0; kp < HD / 64; ++kp) {
-          uint32_t r[4];
-          ldsm_x4(kb + tile_off<C::CHUNKB>(t, (2 * kp + (lane >> 4)) * 16), r);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t lo[4], hi[4];
-            e2m1x8_to_f16x8(r[2 * e], lo);
-            e2m1x8_to_f16x8(r[2 * e + 1], hi);
-            const int c = 2 * kp + e;
-            float part[4];
-            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-            mma16816_f16_zero(part, a0, qf[2 * c][0], qf[2 * c][1]);
-            mma16816<false>(part, a1, qf[2 * c + 1][0], qf[2 * c + 1][1]);
-            sc[0] = fmaf(part[0], ka[c], sc[0]);
-            sc[1] = fmaf(part[1], ka[c], sc[1]);
-            sc[2] = fmaf(part[2], kb2[c], sc[2]);
-            sc[3] = fmaf(part[3], kb2[c], sc[3]);
-          }
-        }
-      } else if constexpr (CT != DT_E4M3) {
+      if constexpr (CT != DT_E4M3) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           uint32_t a[4];
@@ -770,37 +941,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     {
       const int j = lane >> 3;
       const int t = (lane & 7) + (j >> 1) * 8;
-      if constexpr (MX) {
-        // an 8x8 b16 transpose of codes gives thread (gid, tig) dims 4 gid ..
-        // 4 gid + 3 of tokens 2 tig and 2 tig + 1; widened, a byte permute pairs
-        // equal dims of the two tokens.  The weights carry the tokens' scales of
-        // the group, so that its product adds up as it is.
-        constexpr int GR = HD / kMxGroup;
-        uint32_t w0[GR], w1[GR];
-#pragma unroll
-        for (int c = 0; c < GR; ++c) {
-          w0[c] = mul_f16x2(bh0, mxv[tig * GR + c]);
-          w1[c] = mul_f16x2(bh1, mxv[(tig + 4) * GR + c]);
-        }
-#pragma unroll
-        for (int pp = 0; pp < HD / 64; ++pp) {
-          uint32_t r[4];
-          ldsm_x4_t(vb + tile_off<C::CHUNKB>(t, (2 * pp + (j & 1)) * 16), r);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t lo[4], hi[4];  // tokens 0-7, 8-15
-            e2m1x8_to_f16x8(r[e], lo);
-            e2m1x8_to_f16x8(r[2 + e], hi);
-            const int c = 2 * pp + e;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t a[4] = {__byte_perm(lo[y], lo[y + 2], 0x5410), __byte_perm(lo[y], lo[y + 2], 0x7632),
-                                     __byte_perm(hi[y], hi[y + 2], 0x5410), __byte_perm(hi[y], hi[y + 2], 0x7632)};
-              mma16816<false>(acc[2 * c + y], a, w0[c], w1[c]);
-            }
-          }
-        }
-      } else if constexpr (CT != DT_E4M3) {
+      if constexpr (CT != DT_E4M3) {
 #pragma unroll
         for (int u = 0; u < C::MT; ++u) {
           uint32_t a[4];
@@ -874,15 +1015,6 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   for (int off = 4; off < 32; off <<= 1) {
     l_e += __shfl_xor_sync(kFull, l_e, off);
     l_o += __shfl_xor_sync(kFull, l_o, off);
-  }
-  if constexpr (MX) {  // the sums in their own scale
-    const float f = __uint_as_float((uint32_t)max(ref, 0) << 23);
-#pragma unroll
-    for (int u = 0; u < C::MT; ++u) {
-      const float fc = __shfl_sync(kFull, f, u >> 1);
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) acc[u][q4] *= fc;
-    }
   }
   __syncthreads();  // every warp is done with its stages: reuse them
   float* sm_o = reinterpret_cast<float*>(smem);        // [NW][8][HD]
@@ -1096,7 +1228,7 @@ constexpr int stages_for() {
   // registers).  More CTAs in flight beat deeper pipelines: on GB300, fp8 d128
   // at 3 stages took 180 us where 6 took 206 us (70B-shaped layer), bf16 d128
   // at 2 stages 98.6 us where 3 took 99.2 us (8B-shaped layer).
-  if (CT == DT_E2M1) return 5;
+  if (CT == DT_E2M1) return 2;
   constexpr int st = DecodeCfg<HD, CT, kNW, 1>::STAGEB;
   constexpr int ns = (12 * 1024) / st;
   return ns < 2 ? 2 : (ns > 8 ? 8 : ns);
@@ -1107,8 +1239,7 @@ template <int HD, int CT, int AT, bool CASC, int NSO = 0, int NW = kNW, bool WIN
           bool BSC = false, bool CLM = false>
 cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const DecodeParams& p, const DecodeExtraParams& ap,
-                            cudaStream_t stream, cudaEvent_t merge_after = nullptr,
-                            const ScaleMaps<CT == DT_E2M1>& mx = {}) {
+                            cudaStream_t stream, cudaEvent_t merge_after = nullptr) {
   constexpr int NS = NSO > 0 ? NSO : stages_for<HD, CT>();
   using C = DecodeCfg<HD, CT, NW, NS>;
   auto kern = decode_kernel<HD, CT, AT, NW, NS, CASC, WIN, BSC, CLM>;
@@ -1132,10 +1263,10 @@ cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = CLM ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, ap, mx);
+    e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, ap);
     if (CLM) return e;
   } else {
-    kern<<<grid, NW * 32, smem, stream>>>(kmap, vmap, p, ap, mx);
+    kern<<<grid, NW * 32, smem, stream>>>(kmap, vmap, p, ap);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || (!CASC && p.num_splits <= 1)) return e;

@@ -7,28 +7,25 @@ namespace pkv {
 namespace {
 
 template <int HD, int AT, bool WIN>
-cudaError_t launch_mx4_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const ScaleMaps<true>& mx,
-                         const DecodeParams& p, const DecodeExtraParams& ap, cudaStream_t stream) {
+cudaError_t launch_mx4_t(const DecodeParams& p, const DecodeExtraParams& ap, cudaStream_t stream) {
+  const CUtensorMap none{};  // (copied by each thread, without TMA)
   if (ap.join_cluster)
-    return launch_decode_t<HD, DT_E2M1, AT, false, 0, kNW, WIN, false, true>(kmap, vmap, p, ap, stream, nullptr, mx);
+    return launch_decode_t<HD, DT_E2M1, AT, false, 0, kNW, WIN, false, true>(none, none, p, ap, stream);
   if (ap.two_warps)
-    return launch_decode_t<HD, DT_E2M1, AT, false, 0, 2, WIN, false>(kmap, vmap, p, ap, stream, nullptr, mx);
-  return launch_decode_t<HD, DT_E2M1, AT, false, 0, kNW, WIN, false>(kmap, vmap, p, ap, stream, nullptr, mx);
+    return launch_decode_t<HD, DT_E2M1, AT, false, 0, 2, WIN, false>(none, none, p, ap, stream);
+  return launch_decode_t<HD, DT_E2M1, AT, false, 0, kNW, WIN, false>(none, none, p, ap, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_mx4(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                              const CUtensorMap& k_mx_map, const CUtensorMap& v_mx_map,
-                              const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
+cudaError_t launch_decode_mx4(const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
                               int act_dt, cudaStream_t stream) {
   if (ap.join_cluster && p.num_splits != 2 && p.num_splits != 4 && p.num_splits != 8)
     return cudaErrorInvalidValue;
-  const ScaleMaps<true> mx{k_mx_map, v_mx_map};
-#define PKV_MX4(HD, AT)                                                        \
-  if (head_dim == HD && act_dt == AT)                                          \
-    return ap.window > 0 ? launch_mx4_t<HD, AT, true>(kmap, vmap, mx, p, ap, stream)   \
-                         : launch_mx4_t<HD, AT, false>(kmap, vmap, mx, p, ap, stream);
+#define PKV_MX4(HD, AT)                                                \
+  if (head_dim == HD && act_dt == AT)                                  \
+    return ap.window > 0 ? launch_mx4_t<HD, AT, true>(p, ap, stream)   \
+                         : launch_mx4_t<HD, AT, false>(p, ap, stream);
   PKV_MX4(64, DT_F16)
   PKV_MX4(64, DT_BF16)
   PKV_MX4(128, DT_F16)

@@ -78,11 +78,12 @@ struct DecodeExtraParams {
   int prefix_chunks;  // chunks the prefix pass computes (<= prefix_slots)
   //  - window launches: the query of length n sees tokens [0, sink_tokens) and
   //    [n - window, n) (window > 0);
-  //  - block-scaled launches: fp32 scales [num_blocks][num_kv_heads] of the codes.
+  //  - block-scaled launches: fp32 scales [num_blocks][num_kv_heads] of the codes;
+  //    launches over e2m1 codes: the bytes of their microscales.
   int window;
   int sink_tokens;
-  const float* k_scales;
-  const float* v_scales;
+  const void* k_scales;
+  const void* v_scales;
   int join_cluster;  // window / block-scaled launches: the splits (2, 4 or 8) form clusters
   int two_warps;     // window / block-scaled launches: CTAs of two warps, not four (no cluster)
   // window / block-scaled launches with splits of different lengths (at most
@@ -332,11 +333,9 @@ cudaError_t launch_decode_cascade(const CUtensorMap& kmap, const CUtensorMap& vm
 cudaError_t launch_decode_window(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
                                  int cache_dt, int act_dt, cudaStream_t stream);
-// Decode of e2m1 codes with microscales (their pools' maps k_mx_map, v_mx_map),
-// optionally under a window (ap.window > 0).
-cudaError_t launch_decode_mx4(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                              const CUtensorMap& k_mx_map, const CUtensorMap& v_mx_map,
-                              const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
+// Decode of e2m1 codes with microscales (ap.k_cache, ap.v_cache and the scales'
+// pools as ap.k_scales, ap.v_scales), optionally under a window (ap.window > 0).
+cudaError_t launch_decode_mx4(const DecodeParams& p, const DecodeExtraParams& ap, int head_dim,
                               int act_dt, cudaStream_t stream);
 size_t decode_smem_bytes(int head_dim, int cache_dt);
 cudaError_t launch_append(const AppendParams& p, int cache_dt, int act_dt, cudaStream_t stream);
