@@ -544,25 +544,33 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint8_t* scales = static_cast<const uint8_t*>(lane < SUNITS ? ap.k_scales : ap.v_scales) +
                             lane % SUNITS * 16;
     const uint32_t scale_dst = mxstage_s + lane / SUNITS * 128 + lane % SUNITS * 16;
+    // a tile's number in the pools from its block (-1 stays: outside the pool)
+    auto number = [&](int win, int blk) -> int {
+      if (blk < 0) return -1;
+      int tok = t0 + kSubTokens * (warp + (win * 32 + lane) * NW);
+      if constexpr (WIN) tok += tok >= ws.sv ? ws.skip : 0;
+      return (int)((((uint32_t)blk * p.num_kv_heads + g) << (p.bs_shift - 4)) + ((tok & (bs - 1)) >> 4));
+    };
+    int at_cur = number(0, bw_cur), at_next = number(1, bw_next);
     auto load_pair = [&](int i, int st) {
-      window_of(i);  // (i even: both tiles are in one window of block ids)
+      if ((i & 31) == 0 && i > 0) {  // (i even: both tiles are in one window of numbers)
+        at_cur = at_next;
+        ++win_cur;
+        at_next = number(win_cur + 1, fetch(win_cur + 1));
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (i + x < cnt) {
-          const int blk = __shfl_sync(kFull, bw_cur, (i + x) & 31);
-          int tok = t0 + kSubTokens * (warp + (i + x) * NW);
-          if constexpr (WIN) tok += tok >= ws.sv ? ws.skip : 0;
-          const uint32_t n = blk < 0 ? 0u : 16u;  // a block outside the pool gives zeros
-          const int64_t row = ((int64_t)(max(blk, 0) * p.num_kv_heads + g) << p.bs_shift) + (tok & (bs - 1));
-          const int64_t at = row * C::ROWB;
-          const uint32_t dst = wstage_s + st * C::STAGEB + x * 2 * C::TILEB + unit0;
+        const int tile = __shfl_sync(kFull, at_cur, (i + x) & 31);
+        const uint32_t n = tile == -1 ? 0u : 16u;  // a block outside the pool gives zeros
+        const uint64_t at = tile == -1 ? 0u : (uint32_t)tile;
+        const bool has = i + x < cnt;
+        const uint32_t dst = wstage_s + st * C::STAGEB + x * 2 * C::TILEB + unit0;
 #pragma unroll
-          for (int u = 0; u < UNITS / 32; ++u) {
-            cp_async16(dst + u * 512, kcodes + at + u * 512, n);
-            cp_async16(dst + C::TILEB + u * 512, vcodes + at + u * 512, n);
-          }
-          if (lane < 2 * SUNITS) cp_async16(scale_dst + st * C::MXSTAGEB + x * 256, scales + row * GR, n);
+        for (int u = 0; u < UNITS / 32; ++u) {
+          cp_async16_if(has, dst + u * 512, kcodes + at * C::TILEB + u * 512, n);
+          cp_async16_if(has, dst + C::TILEB + u * 512, vcodes + at * C::TILEB + u * 512, n);
         }
+        cp_async16_if(has && lane < 2 * SUNITS, scale_dst + st * C::MXSTAGEB + x * 256, scales + at * C::MXB, n);
       }
     };
 #pragma unroll
@@ -570,15 +578,17 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (2 * k < cnt) load_pair(2 * k, k);
       cp_async_commit();
     }
-    // The sums of group c's dims are held relative to 2^(ref[c] - 127): V's scales
-    // enter as f16 factors 2^(byte - ref) of the weights, of at most 2^7 (with
-    // weights of at most 2^8 their products stay inside f16).  When a byte above
-    // ref + 7 comes, ref moves to 5 below the largest one and the sums follow.  A
-    // factor below 2^-14 is 0: a token whose scale is 2^20 below the largest so far
+    // The sums of group c's dims are held relative to 2^(ref - 127), ref byte c of
+    // refs: V's scales enter as f16 factors 2^(byte - ref) of the weights, of at most
+    // 2^7 (with weights of at most 2^8 their products stay inside f16).  When a byte
+    // above ref + 7 comes, ref moves to 5 below the largest one and the sums follow.
+    // A factor below 2^-14 is 0: a token whose scale is 2^20 below the largest so far
     // adds nothing.
-    int ref[GR];
-#pragma unroll
-    for (int c = 0; c < GR; ++c) ref[c] = -8;
+    uint32_t refs = 0u;
+    // where the lane finds its groups' bytes of a pair of tokens (the even token's in
+    // the low half): groups 0 and 1, an odd lane 2 and 3 (two groups: 0, and 1)
+    const uint32_t pick0 = lane & 1 ? (GR == 4 ? 0x2266u : 0x1155u) : 0x4400u;
+    const uint32_t pick1 = lane & 1 ? 0x3377u : 0x5511u;
     int st = 0;
     for (int i = 0; i < cnt; i += 2) {
       cp_async_wait<NS - 1>();
@@ -607,35 +617,34 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const uint32_t at = mxstage_s + st * C::MXSTAGEB + (lane >> 4) * 256 + (lane & 15) * GR;
         const uint32_t wk = lds_u<GR>(at);
         uint32_t wv = lds_u<GR>(at + 128);
-        // what a hidden token holds does not count (K: its score is masked)
-        if (edge && (lane < 16 ? hidden(0, lane) : hidden(1, lane - 16))) wv = 0u;
-        // bytes of 255 (NaN), at their highest bits
-        const uint32_t nan_k = ((wk & 0x7F7F7F7Fu) + 0x01010101u) & wk & 0x80808080u;
-        const uint32_t nan_v = ((wv & 0x7F7F7F7Fu) + 0x01010101u) & wv & 0x80808080u;
+        // what a hidden token holds does not count (K: its score is masked; V: its
+        // weight is 0)
+        if (edge && (lane < 16 ? hidden(0, lane) : hidden(1, lane - 16))) wv = refs;
         float fk[GR];
-        int ev[GR];
 #pragma unroll
-        for (int c = 0; c < GR; ++c) {
+        for (int c = 0; c < GR; ++c)
           fk[c] = __uint_as_float((c == 3 ? wk >> 1 : wk << (23 - 8 * c)) & 0x7F800000u) * p.scale_log2;
-          ev[c] = (int)((wv >> (8 * c)) & 0xFFu);
-        }
-        if (__any_sync(kFull, (nan_k | nan_v) != 0u)) {
+        // V's factors 2^(byte - ref): their f16 exponents, 15 more, are 0 .. 22 in the
+        // usual case and need no borrow; else, and for a NaN, byte by byte
+        uint32_t x4 = wv + (0x0F0F0F0Fu - refs);
+        const uint32_t nan_k = ((wk & 0x7F7F7F7Fu) + 0x01010101u) & wk & 0x80808080u;
+        if (__any_sync(kFull, (nan_k | ((x4 | (x4 + 0x09090909u)) & 0xE0E0E0E0u)) != 0u)) {
+          x4 = 0u;
 #pragma unroll
           for (int c = 0; c < GR; ++c) {
             if ((nan_k >> (8 * c)) & 0x80u) fk[c] = __uint_as_float(0x7FC00000u);
-            if ((nan_v >> (8 * c)) & 0x80u) ev[c] = 0;
-          }
-        }
-        bool above = false;
+            int e = (int)((wv >> (8 * c)) & 0xFFu), ref = (int)((refs >> (8 * c)) & 0xFFu);
+            if (__any_sync(kFull, e == 255)) {  // a NaN: every head's sums of these dims
 #pragma unroll
-        for (int c = 0; c < GR; ++c) above |= ev[c] > ref[c] + 7;
-        if (__any_sync(kFull, above)) {
-#pragma unroll
-          for (int c = 0; c < GR; ++c) {
-            const int top = __reduce_max_sync(kFull, ev[c]);
-            if (top > ref[c] + 7) {
-              const int up = top - 5 - ref[c];
-              ref[c] += up;
+              for (int q4 = 0; q4 < 4; ++q4)
+                acc[2 * c][q4] = acc[2 * c + 1][q4] = __uint_as_float(0x7FC00000u);
+              if (e == 255) e = 0;
+            }
+            const int top = __reduce_max_sync(kFull, e);
+            if (top > ref + 7) {
+              const int up = top - 5 - ref;
+              ref += up;
+              refs += (uint32_t)up << (8 * c);
               const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
               for (int q4 = 0; q4 < 4; ++q4) {
@@ -643,14 +652,18 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 acc[2 * c + 1][q4] *= f;
               }
             }
+            x4 |= (uint32_t)max(e - ref + 15, 0) << (8 * c);
           }
         }
+        const uint32_t y4 = __shfl_xor_sync(kFull, x4, 1);  // the other token of the pair
         __syncwarp();  // the scales of the tiles before have been read
-        sts_f<GR>(mxk + lane * GR * 4, fk);
+        uint32_t kw[GR], vw[GR / 2];
 #pragma unroll
-        for (int c = 0; c < GR; ++c)
-          sts_u16(mxv + (lane >> 1) * GR * 4 + c * 4 + (lane & 1) * 2,
-                  (nan_v >> (8 * c)) & 0x80u ? 0x7E00u : (uint32_t)max(ev[c] - ref[c] + 15, 0) << 10);
+        for (int c = 0; c < GR; ++c) kw[c] = __float_as_uint(fk[c]);
+        vw[0] = (__byte_perm(x4, y4, pick0) & 0x001F001Fu) << 10;
+        if constexpr (GR == 4) vw[1] = (__byte_perm(x4, y4, pick1) & 0x001F001Fu) << 10;
+        sts_v<GR>(mxk + lane * GR * 4, kw);
+        sts_v<GR / 2>(mxv + lane * GR * 2, vw);
         __syncwarp();
       }
 
@@ -780,7 +793,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // the sums in their own scale
 #pragma unroll
     for (int c = 0; c < GR; ++c) {
-      const float f = __uint_as_float((uint32_t)max(ref[c], 0) << 23);
+      const float f = e8m0_to_f32((refs >> (8 * c)) & 0xFFu);
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) {
         acc[2 * c][q4] *= f;

@@ -194,8 +194,12 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
 
 // ---- copies by each thread --------------------------------------------------------
 // 16 bytes to shared memory, of which the first n come from `src` (the others are 0).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// If `on`.
+__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst, const void* src, uint32_t n) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+      "@q cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst), "l"(src), "r"(n), "r"((uint32_t)on)
+      : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the N youngest groups of this thread's copies have arrived
@@ -213,9 +217,6 @@ __device__ __forceinline__ uint32_t lds_u(uint32_t a) {
   else asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ void sts_u16(uint32_t a, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.u16 [%0], h;\n\t}" ::"r"(a), "r"(v) : "memory");
-}
 // 2 or 4 words
 template <int N>
 __device__ __forceinline__ void lds_v(uint32_t a, uint32_t (&v)[N]) {
@@ -225,12 +226,15 @@ __device__ __forceinline__ void lds_v(uint32_t a, uint32_t (&v)[N]) {
   else
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
 }
+// 1, 2 or 4 words
 template <int N>
-__device__ __forceinline__ void sts_f(uint32_t a, const float (&v)[N]) {
+__device__ __forceinline__ void sts_v(uint32_t a, const uint32_t (&v)[N]) {
   if constexpr (N == 4)
-    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(v[0]), "r"(v[1]) : "memory");
   else
-    asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(v[0]), "f"(v[1]) : "memory");
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v[0]) : "memory");
 }
 
 // ---- warp-level MMA -----------------------------------------------------------
