@@ -92,7 +92,8 @@ struct DecodeCfg {
   static constexpr int MXB = kSubTokens * HD / kMxGroup;
   static constexpr int MXSTAGEB = MX ? TPS * 256 : 0;
   static constexpr int MXBUF = MX ? TPS * kSubTokens * (HD / kMxGroup) * 6 : 0;
-  static constexpr int MX_AREA = NW * NS * MXSTAGEB + NW * MXBUF;
+  static constexpr int MXQB = MX ? HD / 16 * 32 * 8 : 0;  // and the CTA's query fragments
+  static constexpr int MX_AREA = NW * NS * MXSTAGEB + NW * MXBUF + MXQB;
   static constexpr int STAGE_AREA = NW * NS * STAGEB + MX_AREA;
   static constexpr int MT = HD / 16;                    // output m-tiles (dims)
   static constexpr bool MMA_BF16 = (CT == DT_BF16);
@@ -536,6 +537,17 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // pairs of tokens][GR] f16x2
     const uint32_t mxk = smem_u32(smem) + NW * NS * (C::STAGEB + C::MXSTAGEB) + warp * C::MXBUF;
     const uint32_t mxv = mxk + C::TPS * kSubTokens * GR * 4;
+    // the query fragments, the same for all warps: [group][lane] 16 bytes (read again
+    // for every tile: 16 registers less of the 128 that let four CTAs fit an SM)
+    const uint32_t mxq = smem_u32(smem) + NW * NS * (C::STAGEB + C::MXSTAGEB) + NW * C::MXBUF + lane * 16;
+    if (warp == 0) {
+#pragma unroll
+      for (int c = 0; c < GR; ++c) {
+        const uint32_t f[4] = {qf[2 * c][0], qf[2 * c][1], qf[2 * c + 1][0], qf[2 * c + 1][1]};
+        sts_v<4>(mxq + c * 512, f);
+      }
+    }
+    __syncthreads();
     constexpr int UNITS = C::TILEB / 16;            // 16-byte units of a tile's codes ...
     constexpr int SUNITS = C::MXB / 16;             // ... and scales
     const uint32_t unit0 = tile_off<C::CHUNKB>(lane * 16 / C::ROWB, lane * 16 % C::ROWB);
@@ -560,17 +572,17 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
+        // a block outside the pool (or none, behind the warp's last tile) gives zeros
         const int tile = __shfl_sync(kFull, at_cur, (i + x) & 31);
-        const uint32_t n = tile == -1 ? 0u : 16u;  // a block outside the pool gives zeros
+        const uint32_t n = tile == -1 ? 0u : 16u;
         const uint64_t at = tile == -1 ? 0u : (uint32_t)tile;
-        const bool has = i + x < cnt;
         const uint32_t dst = wstage_s + st * C::STAGEB + x * 2 * C::TILEB + unit0;
 #pragma unroll
         for (int u = 0; u < UNITS / 32; ++u) {
-          cp_async16_if(has, dst + u * 512, kcodes + at * C::TILEB + u * 512, n);
-          cp_async16_if(has, dst + C::TILEB + u * 512, vcodes + at * C::TILEB + u * 512, n);
+          cp_async16_if(true, dst + u * 512, kcodes + at * C::TILEB + u * 512, n);
+          cp_async16_if(true, dst + C::TILEB + u * 512, vcodes + at * C::TILEB + u * 512, n);
         }
-        cp_async16_if(has && lane < 2 * SUNITS, scale_dst + st * C::MXSTAGEB + x * 256, scales + at * C::MXB, n);
+        cp_async16_if(lane < 2 * SUNITS, scale_dst + st * C::MXSTAGEB + x * 256, scales + at * C::MXB, n);
       }
     };
 #pragma unroll
@@ -585,6 +597,10 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // A factor below 2^-14 is 0: a token whose scale is 2^20 below the largest so far
     // adds nothing.
     uint32_t refs = 0u;
+    // the lane's rows for ldmatrix: groups 0 and 1 of K's tokens, of V's (groups 2 and
+    // 3 are 32 bytes on, with the swizzle: bit 5 flipped)
+    const uint32_t kunit = tile_off<C::CHUNKB>(lane & 15, (lane >> 4) * 16);
+    const uint32_t vunit = tile_off<C::CHUNKB>((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 16);
     // where the lane finds its groups' bytes of a pair of tokens (the even token's in
     // the low half): groups 0 and 1, an odd lane 2 and 3 (two groups: 0, and 1)
     const uint32_t pick0 = lane & 1 ? (GR == 4 ? 0x2266u : 0x1155u) : 0x4400u;
@@ -600,12 +616,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int x = 0; x < 2; ++x) {
         const int tok = t0 + kSubTokens * (warp + (i + x) * NW);
         nvalid[x] = t1 - tok;
-        edge |= nvalid[x] < kSubTokens;
+        if (x == 1) edge |= nvalid[1] < kSubTokens;  // (the first tile is never the shorter)
         if constexpr (WIN) {
           const int at = tok + (tok >= ws.sv ? ws.skip : 0);
           lo[x] = ws.w0 - at;
           sk[x] = ws.sinks - at;
-          edge |= lo[x] > 0 && sk[x] < kSubTokens;
+          // tokens are hidden beside the gap only: in the tiles before and behind it
+          edge |= (unsigned)(tok - ws.sv + kSubTokens) <= (unsigned)kSubTokens;
         }
       }
       auto hidden = [&](int x, int row) -> bool {
@@ -672,10 +689,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // receives codes 8 tig .. 8 tig + 7, four for each of two steps; the group's
       // sum is scaled per token as it is added up.
       float sc[2][4];
+      const uint32_t kat = wstage_s + st * C::STAGEB + kunit;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint32_t kb = wstage_s + st * C::STAGEB + x * 2 * C::TILEB;
-        const int t = (lane & 7) + ((lane >> 3) & 1) * 8;
         uint32_t ka[GR], kc[GR];
         lds_v<GR>(mxk + (16 * x + gid) * GR * 4, ka);
         lds_v<GR>(mxk + (16 * x + gid + 8) * GR * 4, kc);
@@ -683,7 +699,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
         for (int kp = 0; kp < HD / 64; ++kp) {
           uint32_t r[4];
-          ldsm_x4(kb + tile_off<C::CHUNKB>(t, (2 * kp + (lane >> 4)) * 16), r);
+          ldsm_x4((kat ^ (32 * kp)) + x * 2 * C::TILEB, r);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t a[4], b2[4];
@@ -691,9 +707,11 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             e2m1x8_to_f16x8(r[2 * e + 1], b2);
             const int c = 2 * kp + e;
             float part[4];
+            uint32_t f[4];
+            lds_v<4>(mxq + c * 512, f);
             const uint32_t a0[4] = {a[0], b2[0], a[1], b2[1]}, a1[4] = {a[2], b2[2], a[3], b2[3]};
-            mma16816_f16_zero(part, a0, qf[2 * c][0], qf[2 * c][1]);
-            mma16816<false>(part, a1, qf[2 * c + 1][0], qf[2 * c + 1][1]);
+            mma16816_f16_zero(part, a0, f[0], f[1]);
+            mma16816<false>(part, a1, f[2], f[3]);
             sc[x][0] = fmaf(part[0], __uint_as_float(ka[c]), sc[x][0]);
             sc[x][1] = fmaf(part[1], __uint_as_float(ka[c]), sc[x][1]);
             sc[x][2] = fmaf(part[2], __uint_as_float(kc[c]), sc[x][2]);
@@ -746,13 +764,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
 
       // ---- O^T[dim][head] += V^T . P^T ----------------------------------------------
+      const uint32_t vat = wstage_s + st * C::STAGEB + C::TILEB + vunit;
       // An 8x8 b16 transpose of codes gives thread (gid, tig) dims 4 gid .. 4 gid + 3
       // of tokens 2 tig and 2 tig + 1; widened, a byte permute pairs equal dims of
       // the two tokens.  The weights carry the tokens' scales of the group, so that
       // its product adds up as it is.
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint32_t vb = wstage_s + st * C::STAGEB + x * 2 * C::TILEB + C::TILEB;
         const uint32_t bh0 = movmatrix_t(pack2<false>(sc[x][0], sc[x][1]));
         const uint32_t bh1 = movmatrix_t(pack2<false>(sc[x][2], sc[x][3]));
         uint32_t w0[GR], w1[GR];
@@ -763,11 +781,10 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           w0[c] = mul_f16x2(bh0, w0[c]);
           w1[c] = mul_f16x2(bh1, w1[c]);
         }
-        const int j = lane >> 3, t = (lane & 7) + (j >> 1) * 8;
 #pragma unroll
         for (int pp = 0; pp < HD / 64; ++pp) {
           uint32_t r[4];
-          ldsm_x4_t(vb + tile_off<C::CHUNKB>(t, (2 * pp + (j & 1)) * 16), r);
+          ldsm_x4_t((vat ^ (32 * pp)) + x * 2 * C::TILEB, r);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t v0[4], v1[4];  // tokens 0-7, 8-15
