@@ -969,24 +969,29 @@ class KvPools:
 
     def __init__(self, pools):
         self.tensors = tuple(pools)
-        self._array = (Pool * len(self.tensors))()
-        self._at, self._count, self._index = ctypes.addressof(self._array), len(self.tensors), -1
+        self._count, self._index = len(self.tensors), -1
+        rows = []
         for i, t in enumerate(self.tensors):
             if not isinstance(t, torch.Tensor) or t.dim() < 2:
                 raise ValueError(f"pool {i} must be a tensor [num_blocks, num_kv_heads, ...]")
-            if not t.is_cuda or t.device != self.tensors[0].device:
+            index = t.get_device()
+            if not t.is_cuda or (i > 0 and index != self._index):
                 raise ValueError(f"libpkv takes device tensors of one device: pool {i} is on {t.device}")
             if not t.is_contiguous():
                 raise ValueError(f"libpkv takes contiguous tensors: pool {i} is not")
-            if t.numel() == 0 or t.shape[0] != self.tensors[0].shape[0]:
-                raise ValueError(f"pool {i} must have {self.tensors[0].shape[0]} blocks, got {tuple(t.shape)}")
-            nb, hkv = t.shape[0], t.shape[1]
-            bs = t.shape[2] if t.dim() > 2 else 1
-            row = t.numel() * t.element_size() // (nb * hkv * bs)
-            if max(nb, hkv, bs, row) > 2 ** 31 - 1:
-                raise ValueError(f"pool {i} is too large")
-            self._array[i] = Pool(t.data_ptr(), nb, hkv, bs, row)
-            self._index = t.get_device()
+            shape, size = t.shape, t.element_size()
+            nb, hkv = shape[0], shape[1]
+            bs = shape[2] if len(shape) > 2 else 1
+            for n in shape[3:]:
+                size *= n
+            if i > 0 and nb != rows[0][1]:
+                raise ValueError(f"pool {i} must have {rows[0][1]} blocks, got {tuple(shape)}")
+            if not 0 < min(nb, hkv, bs, size) <= max(nb, hkv, bs, size) <= 2 ** 31 - 1:
+                raise ValueError(f"pool {i} is empty or too large: {tuple(shape)}")
+            rows.append((t.data_ptr(), nb, hkv, bs, size))
+            self._index = index
+        self._array = (Pool * self._count)(*rows)
+        self._at = ctypes.addressof(self._array)
 
 
 def kv_copy_blocks(pools, src_blocks, dst_blocks, stream=None):

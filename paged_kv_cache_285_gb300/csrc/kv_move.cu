@@ -3,7 +3,9 @@
 // (kept after an eviction, or accepted out of a tree of drafts), in any number
 // of pools of any type (K, V and scales of every layer) by one launch.
 //
-// Both are bound by memory: each byte is read once and written once.
+// Both are bound by memory: each byte is read once and written once.  Copies: 9,000
+// pairs of 64 KB (K and V) 172 us, the measured copy's rate; 7 pages in each of 64
+// pools, which L2 holds, 3.8 us.
 #include <algorithm>
 
 #include "pages.cuh"
@@ -82,11 +84,17 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_
 // behind (or at) the sources of later passes only if those were read already.
 // Within a pass every load precedes a barrier and every store follows it.
 //
-// A cluster of CTAs takes one (request, pool, run of kv heads), a pass
-// `rows` rows of it per CTA (each with up to eight 16-byte vectors in flight
-// per thread).  While a pass's loads are under way its threads look up the
-// next pass's rows, so that there is one barrier a pass.
-constexpr int kMoveThreads = 256, kMoveUnroll = 8, kMoveRows = 256;
+// A CTA (or a cluster of them) takes one (request, pool, run of kv heads), a pass
+// `rows` rows of it per CTA (each thread up to four 16-byte vectors, few enough
+// registers for two CTAs of 512 threads or four of 256 an SM).  While a pass's
+// loads are under way its threads look up the next pass's rows, so that there is
+// one barrier a pass.  32 layers x 8 requests of 4,000 of 8,000 tokens (8 heads x
+// 128 dims, bf16, 8.4 GB): 1.27 ms, 97 % of the measured copy; 8 layers x 6 of 4,000
+// to 16,000 (fp8, 1.8 GB) 306 us, 87 %, since the longest requests' CTAs end last;
+// one layer of one request, 16,000 tokens, 52 us (clusters of 8; 235 without).
+// Loads of the next pass ahead of a pass's stores took registers from CTAs (306 ->
+// 444 us), eight vectors a thread too (332), pointers kept from load to store 317.
+constexpr int kMoveUnroll = 4;
 
 struct RowMove {
   int src_blk, dst_blk;  // src_blk < 0: not moved
@@ -126,61 +134,65 @@ template <> struct MoveVec<8> { using T = uint2; };
 template <> struct MoveVec<4> { using T = uint32_t; };
 template <> struct MoveVec<2> { using T = uint16_t; };
 
-template <int VEC, bool CL>
+template <int VEC, bool CL, int NT>
 __device__ __forceinline__ void compact_rows(const CompactParams& p, const Pool& pool, int b, int r0,
                                              int n, int dst0, int h0, int heads, bool report,
-                                             RowMove (*s_row)[kMoveRows]) {
+                                             RowMove (*s_row)[NT]) {
   using T = typename MoveVec<VEC>::T;
   const int vpr = (int)pool.row_bytes / VEC;       // vectors per row and head, a power of two
   const int vpr_shift = 31 - __clz(vpr);
   const int vph = vpr * p.heads;                   // per row
-  const int rows = max(1, min(kMoveRows, kMoveThreads * kMoveUnroll / vph));  // per CTA and pass
+  const int rows = max(1, min(NT, NT * kMoveUnroll / vph));  // per CTA and pass
   const int rank = CL ? (int)(blockIdx.x & ((1u << p.cluster_shift) - 1u)) : 0;
   const int step = CL ? rows << p.cluster_shift : rows, passes = (n + step - 1) / step;
+  const int vecs = rows * vph;  // at most what the threads hold (the launcher picks p.heads so)
   auto look_up = [&](int pass) {
-    const int i = pass * step + rank * rows + threadIdx.x;
     if ((int)threadIdx.x < rows) {
+      const int i = pass * step + rank * rows + threadIdx.x;
       RowMove m;
       m.src_blk = -1;
       if (i < n) m = find_move(p, b, r0, i, dst0, report);
-      s_row[pass & 1][threadIdx.x] = m;
+      s_row[pass % 3][threadIdx.x] = m;
     }
+  };
+  // the vector `at` of a pass: its row's move, and its place in a block's page of
+  // the pool (beside the row's offset there)
+  auto place = [&](int at, int pass, RowMove& m, int& h, int& c) -> bool {
+    if (at >= vecs) return false;
+    const int rh = at >> vpr_shift;
+    const int r = (int)p.div_heads.div((uint32_t)rh);
+    c = at & (vpr - 1);
+    h = rh - r * p.heads;
+    m = s_row[pass % 3][r];
+    return m.src_blk >= 0 && h < heads;
+  };
+  auto address = [&](int blk, int off, int h, int c) -> T* {
+    return reinterpret_cast<T*>(pool.base) +
+           ((((int64_t)blk * p.num_kv_heads + (h0 + h)) << p.bs_shift) + off) * vpr + c;
   };
   look_up(0);
   __syncthreads();
-  const int vecs = rows * vph;  // at most what the threads hold (the launcher picks p.heads so)
   for (int pass = 0; pass < passes; ++pass) {
-    const RowMove* row = s_row[pass & 1];
     T x[kMoveUnroll];
-    T* to[kMoveUnroll];
+    RowMove m;
+    int h, c;
 #pragma unroll
-    for (int e = 0; e < kMoveUnroll; ++e) {
-      const int v = e * kMoveThreads + (int)threadIdx.x;
-      to[e] = nullptr;
-      if (v < vecs) {
-        const int rh = v >> vpr_shift, c = v & (vpr - 1);
-        const int r = (int)p.div_heads.div((uint32_t)rh), h = rh - r * p.heads;
-        const RowMove m = row[r];
-        if (m.src_blk >= 0 && h < heads) {
-          const int64_t hh = h0 + h;
-          T* base = reinterpret_cast<T*>(pool.base);
-          x[e] = base[((((int64_t)m.src_blk * p.num_kv_heads + hh) << p.bs_shift) + (m.off & 255)) * vpr + c];
-          to[e] = base + ((((int64_t)m.dst_blk * p.num_kv_heads + hh) << p.bs_shift) + (m.off >> 8)) * vpr + c;
-        }
-      }
-    }
+    for (int e = 0; e < kMoveUnroll; ++e)
+      if (place(e * NT + (int)threadIdx.x, pass, m, h, c)) x[e] = *address(m.src_blk, m.off & 255, h, c);
     if (pass + 1 < passes) look_up(pass + 1);
     if constexpr (CL) cluster_sync();
     else __syncthreads();
+    // (the rows are looked at once more: s_row[pass % 3] stands until every thread
+    // has been through two more barriers)
 #pragma unroll
     for (int e = 0; e < kMoveUnroll; ++e)
-      if (to[e]) *to[e] = x[e];
+      if (place(e * NT + (int)threadIdx.x, pass, m, h, c)) *address(m.dst_blk, m.off >> 8, h, c) = x[e];
   }
 }
 
-template <bool CL>
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ RowMove s_row[2][kMoveRows];
+template <bool CL, int NT>
+__global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ RowMove s_row[3][NT];
   grid_dependency_wait();
   const uint32_t item = CL ? blockIdx.x >> p.cluster_shift : blockIdx.x;
   const uint32_t rest = p.div_groups.div(item);
@@ -202,10 +214,34 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_cons
   const int h0 = hg * p.heads, heads = min(p.heads, p.num_kv_heads - h0);
   const Pool& pool = p.pool[k];
   const uint64_t a = reinterpret_cast<uint64_t>(pool.base) | pool.row_bytes;
-  if ((a & 15) == 0) compact_rows<16, CL>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
-  else if ((a & 7) == 0) compact_rows<8, CL>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
-  else if ((a & 3) == 0) compact_rows<4, CL>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
-  else compact_rows<2, CL>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+  if ((a & 15) == 0) compact_rows<16, CL, NT>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+  else if ((a & 7) == 0) compact_rows<8, CL, NT>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+  else if ((a & 3) == 0) compact_rows<4, CL, NT>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+  else compact_rows<2, CL, NT>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+}
+
+template <int NT>
+cudaError_t launch_compact_t(CompactParams& p, int vpr, int sm_count, cudaStream_t stream) {
+  // Heads per CTA: as many as let the longest request pass at once (a request of
+  // few rows then takes one CTA a pool), one where no number does.
+  constexpr int kHold = NT * kMoveUnroll;
+  const int64_t width = (int64_t)p.max_rows * vpr;
+  p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(p.num_kv_heads, kHold / width));
+  p.head_groups = (p.num_kv_heads + p.heads - 1) / p.heads;
+  p.div_heads = make_fastdiv((uint32_t)p.heads);
+  p.div_groups = make_fastdiv((uint32_t)p.head_groups);
+  p.div_pools = make_fastdiv((uint32_t)p.num_pools);
+  const int64_t items = (int64_t)p.batch * p.num_pools * p.head_groups;
+  // Clusters of up to 8 CTAs an item where the items alone leave SMs idle and
+  // their rows take several passes.
+  const int64_t passes = (width * p.heads + kHold - 1) / kHold;
+  int shift = 0;
+  while (shift < 3 && (items << shift) < sm_count && passes > (1 << shift)) ++shift;
+  p.cluster_shift = shift;
+  const int64_t ctas = items << shift;
+  if (ctas <= 0 || ctas > INT32_MAX) return cudaErrorInvalidValue;
+  return shift > 0 ? launch_dependent(compact_kernel<true, NT>, (unsigned)ctas, NT, stream, p, 1u << shift)
+                   : launch_dependent(compact_kernel<false, NT>, (unsigned)ctas, NT, stream, p);
 }
 
 }  // namespace
@@ -223,27 +259,13 @@ cudaError_t launch_copy_blocks(CopyBlocksParams& p, int num_pairs, cudaStream_t 
 }
 
 cudaError_t launch_compact(CompactParams& p, int sm_count, cudaStream_t stream) {
-  // Heads per CTA: as many as let the longest request pass at once (a request of
-  // few rows then takes one CTA a pool), one where no number does.
   int vpr = 1;
   for (int k = 0; k < p.num_pools; ++k) vpr = std::max(vpr, (int)p.pool[k].row_bytes / 16);
-  const int64_t width = (int64_t)p.max_rows * vpr;
-  p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(p.num_kv_heads, kMoveThreads * kMoveUnroll / width));
-  p.head_groups = (p.num_kv_heads + p.heads - 1) / p.heads;
-  p.div_heads = make_fastdiv((uint32_t)p.heads);
-  p.div_groups = make_fastdiv((uint32_t)p.head_groups);
-  p.div_pools = make_fastdiv((uint32_t)p.num_pools);
-  const int64_t items = (int64_t)p.batch * p.num_pools * p.head_groups;
-  // Clusters of up to 8 CTAs an item where the items alone leave SMs idle and
-  // their rows take several passes.
-  const int64_t passes = (width * p.heads + kMoveThreads * kMoveUnroll - 1) / (kMoveThreads * kMoveUnroll);
-  int shift = 0;
-  while (shift < 3 && (items << shift) < 2 * (int64_t)sm_count && passes > (1 << shift)) ++shift;
-  p.cluster_shift = shift;
-  const int64_t ctas = items << shift;
-  if (ctas <= 0 || ctas > INT32_MAX) return cudaErrorInvalidValue;
-  return shift > 0 ? launch_dependent(compact_kernel<true>, (unsigned)ctas, kMoveThreads, stream, p, 1u << shift)
-                   : launch_dependent(compact_kernel<false>, (unsigned)ctas, kMoveThreads, stream, p);
+  // CTAs of 512 threads from more than two passes of 256 on (64 requests of 100 rows
+  // of 256 bytes, 4 layers, 56 -> 48 us with 256; 16 of 1,000, one layer, 39 -> 31
+  // with 512)
+  return (int64_t)p.max_rows * vpr > 2 * 256 * kMoveUnroll ? launch_compact_t<512>(p, vpr, sm_count, stream)
+                                                        : launch_compact_t<256>(p, vpr, sm_count, stream);
 }
 
 }  // namespace pkv
