@@ -723,13 +723,15 @@ pkv_status pkv_paged_decode_attn_mx4(const pkv_cache_desc* desc, const void* k_c
 
 /* ---------------------------------------------------------------------------
  * pkv_paged_extend_attn_mx4 -- pkv_paged_extend_attn over such a cache, optionally
- * under a window (0: none; as pkv_paged_extend_attn_window).  The call first
- * widens each block that its rows see, once, into 16-bit copies in the workspace:
- * K as code * scale in the act dtype, V in f16 (finite values beyond f16's range
- * become its largest, values below 2^-14 lose bits).
- * workspace: pkv_extend_mx4_workspace_bytes() bytes or more, 256-byte aligned, any
- * contents (else PKV_ERR_WORKSPACE).  Calls that run at the same time need
- * workspaces of their own.  batch <= 65,535.
+ * under a window (0: none; as pkv_paged_extend_attn_window).  The kernel reads the
+ * codes; K and V take part as f16(code * scale) (finite values beyond f16's range
+ * become its largest, values below 2^-14 lose bits), bf16 queries as f16.
+ * workspace: optional, as for pkv_paged_extend_attn: given
+ *            pkv_extend_mx4_workspace_bytes() bytes or more, 256-byte aligned, any
+ *            contents, a call with many rows per request first widens each block
+ *            that its rows see, once, into 16-bit copies there, K as code * scale
+ *            in the act dtype (bf16 queries are then taken as they are), V as above.
+ *            Calls that run at the same time need workspaces of their own.
  * ------------------------------------------------------------------------- */
 size_t pkv_extend_mx4_workspace_bytes(const pkv_cache_desc* desc);
 

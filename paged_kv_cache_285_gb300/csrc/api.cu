@@ -129,18 +129,20 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 pkv_status make_page_map(CUtensorMap* m, const void* base, const pkv_cache_desc* d) {
   auto enc = encode_fn();
   if (!enc) return PKV_ERR_CUDA;
-  const int elem = elem_bytes(d->cache_dtype);
-  const int rowb = d->head_dim * elem;
+  const bool mx4 = d->cache_dtype == PKV_MX4;  // (as bytes of two codes)
+  const int elem = mx4 ? 1 : elem_bytes(d->cache_dtype);
+  const int rowb = mx4 ? d->head_dim / 2 : d->head_dim * elem;
   const int chunkb = rowb < 128 ? rowb : 128;
-  cuuint64_t dims[3] = {(cuuint64_t)d->head_dim, (cuuint64_t)d->block_size,
+  cuuint64_t dims[3] = {(cuuint64_t)(rowb / elem), (cuuint64_t)d->block_size,
                         (cuuint64_t)d->num_blocks * (cuuint64_t)d->num_kv_heads};
   cuuint64_t strides[2] = {(cuuint64_t)rowb, (cuuint64_t)rowb * (cuuint64_t)d->block_size};
   cuuint32_t box[3] = {(cuuint32_t)(chunkb / elem), (cuuint32_t)kSubTokens, 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUtensorMapDataType dt =
       elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-  const CUtensorMapSwizzle sw =
-      chunkb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapSwizzle sw = chunkb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : chunkb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                               : CU_TENSOR_MAP_SWIZZLE_32B;
   CUresult r = enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1284,8 +1286,7 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   const int group = num_q_heads / desc->num_kv_heads;
   if (!extend_supported(desc->head_dim, mx4 ? (int)act_dtype : (int)desc->cache_dtype, (int)act_dtype, group))
     return PKV_ERR_UNSUPPORTED;
-  // no call needs scratch (but one over microscaled codes, which are only read
-  // widened); either may take one to widen the pages it reads
+  // no call needs scratch; either may take one to widen the pages it reads
   // once instead of per tile (a plain call whose workspace is smaller than
   // that, such as the 0 bytes of pkv_extend_workspace_bytes, does without)
   const size_t plain_bytes = groups ? 0 : plain_widen_bytes(desc);
@@ -1307,8 +1308,6 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   if (batch == 0 || total_q_rows == 0 || rows_hint == 0) return PKV_OK;
   if (!k_cache || !v_cache || !q || !out || !block_tables || !q_indptr || !prefix_lens)
     return PKV_ERR_INVALID_ARG;
-  if (mx4 && batch > 65535) return PKV_ERR_UNSUPPORTED;
-  if (mx4 && !widen_plain) return PKV_ERR_WORKSPACE;
   if (groups && (!groups->group_indptr || !groups->group_shared)) return PKV_ERR_INVALID_ARG;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) || !aligned(out, 16))
     return PKV_ERR_INVALID_ARG;
@@ -1403,7 +1402,7 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   int cache_dt = (int)desc->cache_dtype;
   bool widen_pages = widen_plain;
   if (view) {
-    if (!mx4) plan_view_items(p, max_total_len, ds->sm_count);
+    plan_view_items(p, max_total_len, ds->sm_count);
     if (p.splits > 1 || p.half) p.out_tma = 0;  // (every row leaves with its parts' sum)
     const int64_t units = total_q_rows / (2 * p.tok) + (int64_t)batch;
     p.num_blocks_dyn = p.num_items;
@@ -1418,7 +1417,15 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     // pairs: 804 against 957 us), the pass itself three launches and three
     // times the pages' bytes (300 rows, 10 pairs: 140 against 132; 16 rows: 123
     // against 68).
-    if (!mx4 && (p.splits > 1 || p.half || (p.tiles_per_head + 1) / 2 < 16)) widen_pages = false;
+    if (p.splits > 1 || p.half || (p.tiles_per_head + 1) / 2 < 16) widen_pages = false;
+    if (mx4 && !widen_pages) {
+      if ((st = make_page_map(&kmap, k_cache, desc)) != PKV_OK) return st;
+      if ((st = make_page_map(&vmap, v_cache, desc)) != PKV_OK) return st;
+      p.k_mx = view->k_mx;
+      p.v_mx = view->v_mx;
+      e = launch_extend_mx4(kmap, vmap, qmap, omap, p, desc->head_dim, (int)act_dtype, stream);
+      return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    }
     if (scaled && !widen_pages) {
       p.k_scales = view->k_scales;
       p.v_scales = view->v_scales;

@@ -218,22 +218,6 @@ __global__ void __launch_bounds__(256) widen_scaled_list_kernel(
   }
 }
 
-// Eight e2m1 codes times s as OUT values, as above.
-template <int OUT>
-__device__ __forceinline__ void widen8_mx4(uint32_t codes, float s, uint32_t* o) {
-  uint32_t h[4];
-  e2m1x8_to_f16x8(codes, h);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float a = lo_f32<false>(h[e]) * s, b = hi_f32<false>(h[e]) * s;
-    if constexpr (OUT != DT_BF16) {
-      if (fabsf(a) > 65504.f) a = copysignf(65504.f, a);
-      if (fabsf(b) > 65504.f) b = copysignf(65504.f, b);
-    }
-    o[e] = pack2<OUT == DT_BF16>(a, b);
-  }
-}
-
 // One block's page of e2m1 codes (vectors of 16, two to a microscale) widened.
 template <int OUT>
 __device__ __forceinline__ void widen_block_mx4(const uint2* __restrict__ src, uint4* __restrict__ dst,
@@ -251,10 +235,9 @@ __device__ __forceinline__ void widen_block_mx4(const uint2* __restrict__ src, u
     for (int e = 0; e < 4; ++e) {
       const int u = u0 + e * 256;
       if (u < in_vec) {
-        const float s = e8m0_to_f32(b[e]);
         uint32_t o[8];
-        widen8_mx4<OUT>(x[e].x, s, o);
-        widen8_mx4<OUT>(x[e].y, s, o + 4);
+        mx4_widen8<OUT == DT_BF16>(x[e].x, b[e], o);
+        mx4_widen8<OUT == DT_BF16>(x[e].y, b[e], o + 4);
         st_global_v8(dst + 2 * u, o);  // (the workspace is 256-byte aligned)
       }
     }

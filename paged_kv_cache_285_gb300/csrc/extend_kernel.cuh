@@ -77,6 +77,11 @@
 // ring.  The converters set its pace where few rows use a key tile: 1.9 us a
 // tile, both row tiles, against 1.75 for 16-bit pages.
 //
+// Microscaled codes (CT = e2m1; MX): codes (TMA) and scales (the producer's lanes)
+// are copied into the 16-bit slot, both counted on the tile's barrier; a converter thread
+// takes its key row's into registers and, once its warp has, writes the row as
+// f16(code * scale), K and V alike.
+//
 // Items taken as they come (DYN = true; the kernels of calls with a window or
 // block scales): the grid has a CTA per item, one fits an SM, and a running CTA
 // takes over blocks that have not started (cluster launch control) instead of
@@ -140,7 +145,8 @@ constexpr int CHUNK = 16384;  // one 64-element column block of a 16-bit tile: [
 
 template <int HD, int CT, int AT>
 struct ExtCfg {
-  static constexpr bool FP8 = (CT == DT_E4M3);
+  static constexpr bool MX = (CT == DT_E2M1);
+  static constexpr bool FP8 = (CT == DT_E4M3) || MX;  // codes: widened by the converters
   // S = Q K^T runs in f16 for fp8 caches: K codes widen to f16 with one
   // convert per pair, and bf16 queries (QCVT) are converted to f16 once per
   // item instead of K to bf16 at every key tile
@@ -154,7 +160,15 @@ struct ExtCfg {
   // in place at d128 (each converter thread owns one key row, and the 16-bit
   // bytes of that row's dims 0-63 are exactly its fp8 row); at d64 a 16-bit
   // row covers two fp8 rows, so the fp8 tiles get a staging ring of their own
-  static constexpr bool STAGE8 = FP8 && HD == 64;
+  static constexpr bool STAGE8 = CT == DT_E4M3 && HD == 64;
+  // e2m1 codes (a row of HD / 2 bytes) and their microscales are loaded into their
+  // 16-bit slot, those of 32 rows where a converter warp's 32 rows of dims 0-63 go:
+  // the warp takes them into registers before it writes there
+  static constexpr int MXROW = HD / 2;
+  static constexpr int MXWARP = 32 * 128;
+  static constexpr int MXSCALES = MXWARP - 128;   // in a warp's part
+  static constexpr int MXUNITS = HD / kMxGroup;   // 16-byte units of 16 rows' scales
+  static_assert(32 * MXROW <= MXSCALES && 32 * HD / kMxGroup <= 128, "codes and scales in a warp's part");
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + NQB * T16;
   static constexpr int OFF_V = OFF_K + NST * T16;
@@ -356,6 +370,46 @@ __device__ __forceinline__ void widen_row(const uint8_t* src, uint8_t* dst, int 
       if (!zero) widen16<OUT>(a[j], lo, hi);
       *reinterpret_cast<uint4*>(blk + (dbase ^ (uint32_t)((2 * (u & 3)) << 4))) = lo;
       *reinterpret_cast<uint4*>(blk + (dbase ^ (uint32_t)((2 * (u & 3) + 1) << 4))) = hi;
+    }
+  }
+}
+
+// A key row of e2m1 codes (a[c]: group c of 32) under its microscales (byte c of
+// sw) as f16 row t of the tile at dst, or zeros: rounded once, finite values kept
+// inside f16's range.
+template <int HD>
+__device__ __forceinline__ void widen_row_mx4(const uint4 (&a)[HD / kMxGroup], uint32_t sw, uint8_t* dst,
+                                              int t, bool zero) {
+  const uint32_t dbase = ((uint32_t)t * 128u) | (((uint32_t)t & 7u) << 4);
+  constexpr int GR = HD / kMxGroup;
+  auto put = [&](int u, const uint4& o) {  // dims 8 u ..: one 16-byte unit
+    *reinterpret_cast<uint4*>(dst + (u >> 3) * CHUNK + (dbase ^ (uint32_t)((u & 7) << 4))) = o;
+  };
+  bool plain = true;  // scales of 2^-14 to 2^13 multiply in f16 (the same bits)
+#pragma unroll
+  for (int c = 0; c < GR; ++c) plain &= ((sw >> (8 * c)) & 0xFFu) - 113u <= 27u;
+  if (plain || zero) {
+#pragma unroll
+    for (int c = 0; c < GR; ++c) {
+      const uint32_t w[4] = {a[c].x, a[c].y, a[c].z, a[c].w};
+      const uint32_t s2 = zero ? 0u : ((((sw >> (8 * c)) & 0xFFu) - 112u) << 10) * 0x10001u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[4];
+        e2m1x8_to_f16x8(w[i], o);
+        put(4 * c + i, make_uint4(mul_f16x2(o[0], s2), mul_f16x2(o[1], s2), mul_f16x2(o[2], s2), mul_f16x2(o[3], s2)));
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int u = 0; u < 4 * GR; ++u) {  // (the codes of a unit picked by compares, not by address)
+      uint32_t w = 0u, o[4];
+#pragma unroll
+      for (int c = 0; c < GR; ++c) {
+        if (u >> 2 == c) w = u & 2 ? (u & 1 ? a[c].w : a[c].z) : (u & 1 ? a[c].y : a[c].x);
+      }
+      mx4_widen8<false>(w, (sw >> (8 * (u >> 2))) & 0xFFu, o);
+      put(u, make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
 }
@@ -882,8 +936,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     prefetch_tensormap(&vmap);
     prefetch_tensormap(&qmap);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(bar(C::B_KFULL + i), BSC ? 2 : 1);  // BSC: the copy, and the tile's scales
-      mbar_init(bar(C::B_VFULL + i), BSC ? 2 : 1);
+      // BSC: the copy, and the tile's scales; MX: the copy, and each lane's of scales
+      mbar_init(bar(C::B_KFULL + i), C::MX ? 33 : BSC ? 2 : 1);
+      mbar_init(bar(C::B_VFULL + i), C::MX ? 33 : BSC ? 2 : 1);
       mbar_init(bar(C::B_KCONV + i), NCONV / 32);
       mbar_init(bar(C::B_VCONV + i), NCONV / 32);
       mbar_init(bar(C::B_KFREE + i), 1);
@@ -945,8 +1000,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // MMA warpgroup (0-3) lowers its to 96 and the converters (12-15) to 48
   // (fp8 caches, whose converters widen K and V: 88 and 56); the shares add up
   // to the launch budget, 4 x 128.
-  // (BSC: 80 and 64; the converters hold a scale)
-  constexpr int kRegsProd = BSC ? 80 : C::FP8 ? 88 : 96, kRegsConv = BSC ? 64 : C::FP8 ? 56 : 48;
+  // (BSC, MX: 80 and 64; the converters hold a scale, or a row of codes)
+  constexpr int kRegsProd = BSC || C::MX ? 80 : C::FP8 ? 88 : 96;
+  constexpr int kRegsConv = BSC || C::MX ? 64 : C::FP8 ? 56 : 48;
   static_assert(2 * 184 + kRegsProd + kRegsConv == 4 * 128,
                 "register split must equal the launch budget");
   if (warp >= 4 && warp < 12) {
@@ -1424,8 +1480,35 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           int pg[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) pg[q] = __shfl_sync(0xFFFFFFFFu, cur, (st & 3) * 8 + q);
+          // MX: the lane's 16 bytes of the tile's scales (sub-tile lane / MXUNITS)
+          [[maybe_unused]] const uint8_t* mx_src = nullptr;
+          [[maybe_unused]] uint32_t mx_dst = 0;
+          [[maybe_unused]] int mx_page = -1;
+          if constexpr (C::MX) {
+            const int q = lane / C::MXUNITS & 7;
+            mx_page = __shfl_sync(0xFFFFFFFFu, cur, (st & 3) * 8 + q);
+            const int rip = ((WIN || CL ? tile_key<WIN, CL>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
+            mx_src = (is_k ? p.k_mx : p.v_mx) +
+                     (((int64_t)max(mx_page, 0) << p.bs_shift) + rip) * (HD / kMxGroup) + lane % C::MXUNITS * 16;
+            mx_dst = (q >> 1) * C::MXWARP + C::MXSCALES + lane % (2 * C::MXUNITS) * 16;
+          }
           if (n >= NST && !mbar_wait(bar(free0 + s), (uint32_t)((n / NST - 1) & 1))) { ok = false; break; }
-          if (lane == 0) {
+          if constexpr (C::MX) {
+            // the codes by TMA (a box of 16 keys per sub-tile), the scales, which are
+            // contiguous in their pages, by the lanes in 16-byte units (zeros for a page
+            // of -1), counted on the same barrier
+            const uint32_t slot = s_base + (is_k ? C::OFF_K : C::OFF_V) + s * C::T16, fb = bar(full0 + s);
+            cp_async16_if(lane < 8 * C::MXUNITS, slot + mx_dst, mx_src, mx_page < 0 ? 0u : 16u);
+            cp_async_arrive(fb);
+            if (lane == 0) {
+              mbar_arrive_expect_tx(fb, BN * C::MXROW);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const int rip = ((WIN || CL ? tile_key<WIN, CL>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
+                tma_load_3d(slot + (q >> 1) * C::MXWARP + (q & 1) * 16 * C::MXROW, map, fb, 0, rip, pg[q]);
+              }
+            }
+          } else if (lane == 0) {
             const uint32_t fb = bar(full0 + s);
             if constexpr (C::FP8) {
               // one box of 16 keys x head_dim codes per sub-tile
@@ -1463,6 +1546,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         ++j;
       }
+      if constexpr (C::MX) cp_async_wait_all();
       // a failed wait ended the loop: the request under way still writes its answer
       if constexpr (DYN) {
         if (asked) (void)mbar_wait(sbar(C::B_ASK), asks & 1);
@@ -1640,6 +1724,22 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (lane == 0) mbar_arrive(bar(C::B_QCONV + 2 * xq + (j & 1)));
         return true;
       };
+      // MX: key row t of a slot, from its codes and scales in the warp's part of it,
+      // once the warp has them all in registers
+      auto widen_mx4 = [&](uint8_t* slot, bool zero) {
+        constexpr int GR = HD / kMxGroup;
+        const uint8_t* part = slot + (t >> 5) * C::MXWARP;
+        uint4 a[GR];
+        uint32_t sw;
+#pragma unroll
+        for (int c = 0; c < GR; ++c)
+          a[c] = *reinterpret_cast<const uint4*>(part + lane * C::MXROW +
+                                                 ((c ^ (HD == 128 ? (t >> 1) & 3 : (t >> 2) & 1)) << 4));
+        if constexpr (GR == 4) sw = *reinterpret_cast<const uint32_t*>(part + C::MXSCALES + lane * 4);
+        else sw = *reinterpret_cast<const uint16_t*>(part + C::MXSCALES + lane * 2);
+        __syncwarp();
+        widen_row_mx4<HD>(a, sw, slot, t, zero);
+      };
       ItemRaw nxt_raw = load_raw<SX, DEP>(p, DYN ? p.num_items : item0);
       for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
@@ -1658,7 +1758,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
           if constexpr (C::FP8) {
             if (!mbar_wait(bar(C::B_KFULL + s), ph)) { ok = false; break; }
-            widen_row<HD, DT_F16>(smem + C::src8(false, s), smem + C::OFF_K + s * C::T16, t, false);
+            if constexpr (C::MX)
+              widen_mx4(smem + C::OFF_K + s * C::T16, false);
+            else
+              widen_row<HD, DT_F16>(smem + C::src8(false, s), smem + C::OFF_K + s * C::T16, t, false);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_KCONV + s));
@@ -1680,7 +1783,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
           uint8_t* vt = smem + C::OFF_V + s * C::T16;
           if constexpr (C::FP8) {
-            if constexpr (BSC)
+            if constexpr (C::MX)
+              widen_mx4(vt, zero);
+            else if constexpr (BSC)
               widen_row_scaled<HD>(smem + C::src8(true, s), vt, t, zero, vscale[(n % C::NSC) * 8 + (t >> 4)]);
             else
               widen_row<HD, DT_F16>(smem + C::src8(true, s), vt, t, zero);

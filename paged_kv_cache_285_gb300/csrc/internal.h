@@ -181,6 +181,7 @@ struct AppendScaledParams {
 struct AppendMx4Params : AppendScaledParams {
   uint8_t* k_mx;
   uint8_t* v_mx;
+  int in_32b;                  // k_new and v_new are 32-byte aligned (set by the launcher)
 };
 
 // Rows out of a cache: request b's rows row_indptr[b] .. row_indptr[b+1]-1 are
@@ -302,6 +303,8 @@ struct ExtendParams {
   int by_rows;
   int num_units;
   FastDiv div_rows;     // by 2 tok
+  const uint8_t* k_mx;  // launches over e2m1 codes: their microscales
+  const uint8_t* v_mx;
 };
 
 // Partial output of the extend kernel's prefix pass: row q (request b, head h:
@@ -387,6 +390,19 @@ cudaError_t launch_extend_view(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const CUtensorMap& qmap, const CUtensorMap& omap,
                                const ExtendParams& p, int head_dim, int cache_dt, int act_dt,
                                cudaStream_t stream);
+// The same over e2m1 codes (microscales p.k_mx, p.v_mx); which of its kernels p says.
+cudaError_t launch_extend_mx4(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              const CUtensorMap& qmap, const CUtensorMap& omap, const ExtendParams& p,
+                              int head_dim, int act_dt, cudaStream_t stream);
+cudaError_t launch_extend_mx4_split(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              const CUtensorMap& qmap, const CUtensorMap& omap,
+                                    const ExtendParams& p, int head_dim, int act_dt, cudaStream_t stream);
+cudaError_t launch_extend_mx4_half(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              const CUtensorMap& qmap, const CUtensorMap& omap,
+                                   const ExtendParams& p, int head_dim, int act_dt, cudaStream_t stream);
+cudaError_t launch_extend_mx4_by_rows(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              const CUtensorMap& qmap, const CUtensorMap& omap,
+                                      const ExtendParams& p, int head_dim, int act_dt, cudaStream_t stream);
 cudaError_t launch_extend_half(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const CUtensorMap& qmap, const CUtensorMap& omap,
                                const ExtendParams& p, int head_dim, int cache_dt, int act_dt,

@@ -12,9 +12,9 @@
 // +-6 s; a NaN takes its 32 values with it (scale byte 255), since e2m1 has none.
 // Rows do not share scales: a token is written, moved and dropped by itself.
 //
-// Append: one warp per page (block, kv head, K or V); a lane takes 8 values, four
-// lanes a scale (two shuffles find the largest magnitude), so that a warp reads
-// 512 consecutive bytes of two rows and writes 128 consecutive bytes of codes.
+// Append: one warp per page (block, kv head, K or V); a lane takes 16 values, two
+// lanes a scale (one shuffle joins their largest magnitudes), so that a warp reads
+// 1,024 consecutive bytes of rows at once and writes 256 of codes.
 #include <algorithm>
 
 #include "pages.cuh"
@@ -33,9 +33,32 @@ __device__ __forceinline__ uint32_t microscale_byte(float a) {
   return (uint32_t)max(e, 1);
 }
 
+// Eight values (four 16-bit pairs) times inv as e2m1 codes.  bf16: multiplied as
+// they are (inv is a power of two: exact, and what underflows is 0 in e2m1 anyway).
+template <int AT>
+__device__ __forceinline__ uint32_t quantise8(const uint32_t* w, float inv) {
+  float y[8];
+  if constexpr (AT == DT_BF16) {
+    const uint32_t i2 = __float_as_uint(inv) >> 16 | (__float_as_uint(inv) & 0xFFFF0000u);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t z = mul_bf16x2(w[q], i2);
+      y[2 * q] = lo_f32<true>(z);
+      y[2 * q + 1] = hi_f32<true>(z);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      y[2 * q] = bits_to_f32<AT>(w[q] & 0xFFFFu) * inv;
+      y[2 * q + 1] = bits_to_f32<AT>(w[q] >> 16) * inv;
+    }
+  }
+  return f32x8_to_e2m1x8(y);
+}
+
 template <int AT, int HD, int BS>
 __global__ void __launch_bounds__(128) append_mx4_kernel(const AppendMx4Params p) {
-  constexpr int VPR = HD / 8;           // 16-byte input vectors per row
+  constexpr int VPR = HD / 16;          // vectors of 16 values per row
   constexpr int NV = BS * VPR / 32;     // per lane
   constexpr uint32_t kInf = AT == DT_BF16 ? 0x7F80u : 0x7C00u;
   grid_dependency_wait();
@@ -44,51 +67,53 @@ __global__ void __launch_bounds__(128) append_mx4_kernel(const AppendMx4Params p
   if (!find_page_task<BS>(p, blockIdx.x * 4u + (threadIdx.x >> 5), t)) return;
   const uint16_t* src = reinterpret_cast<const uint16_t*>(t.isv ? p.v_new : p.k_new) + t.h * HD;
   const int64_t row_elems = (int64_t)p.num_kv_heads * HD;
-  uint4 x[NV];
+  uint32_t x[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = lane + 32 * i, row = v / VPR, col = (v % VPR) * 8;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= t.start && row < t.end)
-      x[i] = *(reinterpret_cast<const uint4*>(src + (t.first_row + row) * row_elems + col));
+    const int v = lane + 32 * i, row = v / VPR, col = (v % VPR) * 16;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[i][q] = 0u;
+    if (row >= t.start && row < t.end) {
+      const uint16_t* at = src + (t.first_row + row) * row_elems + col;
+      if (p.in_32b) {
+        ld_global_v8(at, x[i]);
+      } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(at), b = *(reinterpret_cast<const uint4*>(at) + 1);
+        x[i][0] = a.x; x[i][1] = a.y; x[i][2] = a.z; x[i][3] = a.w;
+        x[i][4] = b.x; x[i][5] = b.y; x[i][6] = b.z; x[i][7] = b.w;
+      }
+    }
   }
   const int64_t page = (int64_t)t.blk * p.num_kv_heads + t.h;
-  uint32_t* codes = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.isv ? p.v_cache : p.k_cache) +
-                                                page * (BS * HD / 2));
+  uint2* codes = reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.isv ? p.v_cache : p.k_cache) +
+                                          page * (BS * HD / 2));
   uint8_t* scales = (t.isv ? p.v_mx : p.k_mx) + page * (BS * HD / kMxGroup);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = lane + 32 * i, row = v / VPR;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    // the largest finite magnitude of the 32: 16-bit magnitudes order as integers
+    // the largest finite magnitude of the 32 (two lanes'): 16-bit magnitudes order
+    // as integers
     uint32_t m2 = 0u;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) m2 = max_u16x2(m2, w[q] & 0x7FFF7FFFu);
+    for (int q = 0; q < 8; ++q) m2 = max_u16x2(m2, x[i][q] & 0x7FFF7FFFu);
     uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
     m = max(m, __shfl_xor_sync(kFull, m, 1));
-    m = max(m, __shfl_xor_sync(kFull, m, 2));
     const bool nan = m > kInf;
     if (__any_sync(kFull, m >= kInf)) {  // infinities or NaN: once more without those
       m = 0u;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t lo = w[q] & 0x7FFFu, hi = (w[q] >> 16) & 0x7FFFu;
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t lo = x[i][q] & 0x7FFFu, hi = (x[i][q] >> 16) & 0x7FFFu;
         m = max(m, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
       }
       m = max(m, __shfl_xor_sync(kFull, m, 1));
-      m = max(m, __shfl_xor_sync(kFull, m, 2));
     }
     const uint32_t sb = microscale_byte(bits_to_f32<AT>(m));
     const float inv = __uint_as_float((254u - sb) << 23);  // 1 / s (sb is 1 .. 253)
-    float y[8];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      y[2 * q] = bits_to_f32<AT>(w[q] & 0xFFFFu) * inv;
-      y[2 * q + 1] = bits_to_f32<AT>(w[q] >> 16) * inv;
-    }
+    const uint2 c = make_uint2(quantise8<AT>(x[i], inv), quantise8<AT>(x[i] + 4, inv));
     if (row >= t.start && row < t.end) {
-      codes[v] = f32x8_to_e2m1x8(y);
-      if ((lane & 3) == 0) scales[v >> 2] = (uint8_t)(nan ? 255u : sb);
+      codes[v] = c;
+      if ((lane & 1) == 0) scales[v >> 1] = (uint8_t)(nan ? 255u : sb);
     }
   }
 }
@@ -97,25 +122,6 @@ __global__ void __launch_bounds__(128) append_mx4_kernel(const AppendMx4Params p
 // As the read-back of the other caches: a CTA takes p.rows_per_cta rows, finds
 // their slots, and streams vectors of 16 codes (8 bytes in, 32 out).
 constexpr int kGatherRows = 256;
-
-template <int AT>
-__device__ __forceinline__ void widen_codes16(const uint2& x, float s, uint32_t (&o)[8]) {
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t h[4];
-    e2m1x8_to_f16x8(q ? x.y : x.x, h);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float a = lo_f32<false>(h[e]) * s, b = hi_f32<false>(h[e]) * s;
-      if constexpr (AT == DT_F16) {
-        // the code of a value near 65504 may stand for one above it (NaN stays)
-        if (fabsf(a) > 65504.f) a = copysignf(65504.f, a);
-        if (fabsf(b) > 65504.f) b = copysignf(65504.f, b);
-      }
-      o[4 * q + e] = pack2<AT == DT_BF16>(a, b);
-    }
-  }
-}
 
 template <int AT, int HD>
 __global__ void __launch_bounds__(256) gather_mx4_kernel(const GatherMx4Params p) {
@@ -163,9 +169,11 @@ __global__ void __launch_bounds__(256) gather_mx4_kernel(const GatherMx4Params p
       if (blk[e] == -2) continue;
       const int64_t u = row0 * p.num_kv_heads * VPR + base + e * 256;
       uint32_t o[8];
-      widen_codes16<AT>(kx[e], e8m0_to_f32(kb[e]), o);
+      mx4_widen8<AT == DT_BF16>(kx[e].x, kb[e], o);
+      mx4_widen8<AT == DT_BF16>(kx[e].y, kb[e], o + 4);
       store16(p.k_out, u, o, p.out_32b);
-      widen_codes16<AT>(vx[e], e8m0_to_f32(vb[e]), o);
+      mx4_widen8<AT == DT_BF16>(vx[e].x, vb[e], o);
+      mx4_widen8<AT == DT_BF16>(vx[e].y, vb[e], o + 4);
       store16(p.v_out, u, o, p.out_32b);
     }
   }
@@ -177,6 +185,8 @@ cudaError_t launch_append_mx4(const AppendMx4Params& in, int act_dt, int head_di
                               cudaStream_t stream) {
   AppendMx4Params p = in;
   if (!plan_pages(p, block_size)) return cudaErrorInvalidValue;
+  p.in_32b = (reinterpret_cast<uintptr_t>(p.k_new) % 32 == 0 &&
+              reinterpret_cast<uintptr_t>(p.v_new) % 32 == 0) ? 1 : 0;
 #define PKV_APP(AT, HD, BS)                                                                       \
   if (act_dt == AT && head_dim == HD && block_size == BS)                                         \
     return launch_dependent(append_mx4_kernel<AT, HD, BS>, (p.num_tasks + 3) / 4, 128, stream, p);

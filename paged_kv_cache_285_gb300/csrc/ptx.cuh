@@ -208,6 +208,12 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// an arrival on `bar`, one of its expected count, when this thread's copies so far have arrived
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // ---- shared memory by address ------------------------------------------------------
 // N = 2 or 4 bytes
 template <int N>
@@ -370,9 +376,41 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // The value of a microscale's byte: 2^(b - 127), NaN for 255.
 __device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
   return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
+}
+
+// Eight e2m1 codes times the microscale of byte b as f16 or bf16 pairs, rounded
+// once (exact but for subnormals); in f16 finite values beyond its range become
+// its largest.  f16 scales from 2^-14 to 2^13 (6 of which f16 holds) multiply in
+// f16, the same bits.
+template <bool TO_BF16>
+__device__ __forceinline__ void mx4_widen8(uint32_t codes, uint32_t b, uint32_t* o) {
+  uint32_t h[4];
+  e2m1x8_to_f16x8(codes, h);
+  if (!TO_BF16 && b - 113u <= 27u) {
+    const uint32_t s2 = ((b - 112u) << 10) * 0x10001u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = mul_f16x2(h[e], s2);
+    return;
+  }
+  const float s = e8m0_to_f32(b);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x = lo_f32<false>(h[e]) * s, y = hi_f32<false>(h[e]) * s;
+    if constexpr (!TO_BF16) {  // (a NaN stays)
+      if (fabsf(x) > 65504.f) x = copysignf(65504.f, x);
+      if (fabsf(y) > 65504.f) y = copysignf(65504.f, y);
+    }
+    o[e] = pack2<TO_BF16>(x, y);
+  }
 }
 
 // f16/bf16 pair (as stored, low half first) -> f16 pair.  bf16 values beyond

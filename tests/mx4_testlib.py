@@ -70,10 +70,10 @@ def decode_ref(c, q, hq, lens, window=0, sinks=0):
                        window, sinks)
 
 
-def run_extend(c, q, hq, rows, prefix, window=0, sinks=0):
+def run_extend(c, q, hq, rows, prefix, window=0, sinks=0, work=True):
     out = torch.full((q.shape[0], hq, c.d), float("nan"), dtype=TDT[c.act], device="cuda")
     lse = torch.full((q.shape[0], hq), float("nan"), device="cuda")
-    ws = torch.full((pkv.extend_mx4_workspace_bytes(c.k),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((pkv.extend_mx4_workspace_bytes(c.k),), 0xFF, dtype=torch.uint8, device="cuda") if work else None
     pkv.paged_extend_attn_mx4(c.k, c.v, c.ks, c.vs, q, out, ints(indptr(rows)), ints(prefix), c.bt, 1 / c.d ** 0.5,
                               max(rows), max(p + n for p, n in zip(prefix, rows)), window=window, sink_tokens=sinks,
                               lse_out=lse, workspace=ws)

@@ -279,8 +279,10 @@ def test_extend(cfg, window, sinks):
     hq, hkv, d, bs, act, prefix, rows = cfg
     c = Mx4Case(act, hkv, d, bs, [p + n for p, n in zip(prefix, rows)], seed=sum(rows)).cuda()
     q = c.rows(sum(rows), hq).cuda()
-    out, lse = run_extend(c, q, hq, rows, prefix, window, sinks)
-    check_attention(out, lse, extend_ref(c, q, hq, rows, prefix, window, sinks), act, d, f"{cfg} {window}")
+    ref = extend_ref(c, q, hq, rows, prefix, window, sinks)
+    for work in (False, True):
+        out, lse = run_extend(c, q, hq, rows, prefix, window, sinks, work)
+        check_attention(out, lse, ref, act, d, f"{cfg} {window} {work}")
     assert pkv.get_device_error() == 0
 
 
@@ -295,8 +297,10 @@ def test_extend_regimes(cfg, d, bs, act):
     rows, prefix, hq, window, sinks = cfg
     c = Mx4Case(act, 1, d, bs, [p + n for p, n in zip(prefix, rows)], seed=sum(rows)).cuda()
     q = c.rows(sum(rows), hq).cuda()
-    out, lse = run_extend(c, q, hq, rows, prefix, window, sinks)
-    check_attention(out, lse, extend_ref(c, q, hq, rows, prefix, window, sinks), act, d, f"{cfg}")
+    ref = extend_ref(c, q, hq, rows, prefix, window, sinks)
+    for work in (False, True):
+        out, lse = run_extend(c, q, hq, rows, prefix, window, sinks, work)
+        check_attention(out, lse, ref, act, d, f"{cfg} {work}")
     assert pkv.get_device_error() == 0
 
 
