@@ -660,9 +660,12 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   if (forced > 0 || tiles <= 4) return plan_decode(d, batch, hq, len, forced > 0 ? forced : 1, sm_count);
   const int sms = sm_count > 0 ? sm_count : 152;
   const double items = (double)batch * d->num_kv_heads * ((hq / d->num_kv_heads + 7) / 8);
-  const double r1 = d->head_dim != 128 ? 160.0 : window > 0 ? 90.0 : 100.0;
-  const double over = window > 0 ? 1.25 : 1.0;
-  const double sm_rate = 44600.0 / (2.0 * d->head_dim * value_bytes(d->cache_dtype));
+  const bool mx4 = d->cache_dtype == PKV_MX4;
+  const double r1 = mx4 ? (d->head_dim != 128 ? 205.0 : 140.0)
+                        : d->head_dim != 128 ? 160.0 : window > 0 ? 90.0 : 100.0;
+  const double over = window > 0 && !mx4 ? 1.25 : 1.0;
+  const double sm_rate = mx4 ? (d->head_dim != 128 ? 416.0 : 236.0)
+                             : 44600.0 / (2.0 * d->head_dim * value_bytes(d->cache_dtype));
   const double slots = 4.0 * sms;
   double best = 1e30;
   int best_s = 1;
@@ -701,7 +704,7 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   // splits of falling length: see above
   const double fill = items / slots;
   const bool falling = window > 0 ? fill <= 1.5 && 2.0 * len * d->head_dim * value_bytes(d->cache_dtype) >= 0.9e6
-                                  : len >= 1000 && fill <= len / 800.0;
+                                  : len >= (mx4 ? 2500 : 1000) && fill <= len / 800.0;
   if (fill >= 0.25 && falling) {
     const double ratio = std::min(0.78, std::max(0.45, 0.45 + 0.75 * (0.75 - fill)));
     int k = kMaxCuts;
