@@ -86,11 +86,10 @@ struct DecodeCfg {
   static constexpr int TILEB = kSubTokens * ROWB;       // one 16-token K (or V) tile
   static constexpr int TPS = MX ? 2 : 1;                // tiles per stage
   static constexpr int STAGEB = TPS * 2 * TILEB;        // K tile + V tile, of each
-  // MX: a stage's microscales of K and V (16 tokens x HD / 32 bytes each, copied
-  // to 128-byte boundaries), and per warp its tiles' scales as the products take
-  // them: K's as fp32, V's as pairs of f16
+  // MX: a stage's microscales of K and V (16 tokens x HD / 32 bytes each), and per
+  // warp its tiles' scales as the products take them: K's as fp32, V's as pairs of f16
   static constexpr int MXB = kSubTokens * HD / kMxGroup;
-  static constexpr int MXSTAGEB = MX ? TPS * 256 : 0;
+  static constexpr int MXSTAGEB = MX ? TPS * 2 * MXB : 0;
   static constexpr int MXBUF = MX ? TPS * kSubTokens * (HD / kMxGroup) * 6 : 0;
   static constexpr int MXQB = MX ? HD / 16 * 32 * 8 : 0;  // and the CTA's query fragments
   static constexpr int MX_AREA = NW * NS * MXSTAGEB + NW * MXBUF + MXQB;
@@ -99,7 +98,10 @@ struct DecodeCfg {
   static constexpr bool MMA_BF16 = (CT == DT_BF16);
   static constexpr int COMB_BYTES = NW * 8 * HD * 4 + NW * 8 * 2 * 4;
   static constexpr int AREA = STAGE_AREA > COMB_BYTES ? STAGE_AREA : COMB_BYTES;
-  static constexpr int SMEM = 1024 /*align slack*/ + AREA + NW * NS * 8;
+  // (MX: no TMA, so neither the slack to align a tile to its swizzle nor barriers;
+  // at 128 dims and three stages a CTA takes a quarter of an SM's shared memory)
+  static constexpr int SLACK = MX ? 0 : 1024;
+  static constexpr int SMEM = SLACK + AREA + (MX ? 0 : NW * NS * 8);
   static constexpr int SMEM_BSC = SMEM + NW * NS * 8;  // and a tile's two scales per stage
   // CLM: and the parts of 2, 4 or 8 splits
   static constexpr int PARTS = (8 * HD > 8 * 128 ? 8 * HD : 8 * 128) * 4 + 8 * 16 * 4;
@@ -225,11 +227,12 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   static_assert(!(CASC && CLM), "unsupported combination");
   static_assert(!(CASC && LEAN) && (!BSC || CT == DT_E4M3), "unsupported combination");
   using C = DecodeCfg<HD, CT, NW, NS>;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   if constexpr (CLM) cluster_arrive_relaxed();
   if constexpr (LEAN) grid_dependency_wait();
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = MX ? smem_raw
+                     : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                  ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::AREA);
 
   // split is the slowest grid dimension: every request's first chunk runs
@@ -277,7 +280,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // CLM: the CTAs of the cluster write their parts into shared memory of the CTA
   // that sums them up: element idx of the heads' [GC][HD] outputs belongs to rank
   // (idx / 128) % splits.  parts: [rank][8 HD / splits], then [rank][2][8] (max, sum).
-  float* parts = reinterpret_cast<float*>(smem + C::AREA + NW * NS * 8 * (BSC ? 2 : 1));
+  float* parts = reinterpret_cast<float*>(smem + C::AREA + (MX ? 0 : NW * NS * 8 * (BSC ? 2 : 1)));
   auto join_cluster = [&]() {
     static_assert(!CLM || NW * 32 == 128, "one thread per element of a run");
     cluster_sync();  // every part is here; no shared memory of another CTA is touched from now on
@@ -555,7 +558,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint8_t* vcodes = static_cast<const uint8_t*>(ap.v_cache) + lane * 16;
     const uint8_t* scales = static_cast<const uint8_t*>(lane < SUNITS ? ap.k_scales : ap.v_scales) +
                             lane % SUNITS * 16;
-    const uint32_t scale_dst = mxstage_s + lane / SUNITS * 128 + lane % SUNITS * 16;
+    const uint32_t scale_dst = mxstage_s + lane * 16;
     // a tile's number in the pools from its block (-1 stays: outside the pool)
     auto number = [&](int win, int blk) -> int {
       if (blk < 0) return -1;
@@ -582,7 +585,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           cp_async16_if(true, dst + u * 512, kcodes + at * C::TILEB + u * 512, n);
           cp_async16_if(true, dst + C::TILEB + u * 512, vcodes + at * C::TILEB + u * 512, n);
         }
-        cp_async16_if(lane < 2 * SUNITS, scale_dst + st * C::MXSTAGEB + x * 256, scales + at * C::MXB, n);
+        cp_async16_if(lane < 2 * SUNITS, scale_dst + st * C::MXSTAGEB + x * 2 * C::MXB, scales + at * C::MXB, n);
       }
     };
 #pragma unroll
@@ -631,9 +634,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
       // ---- the tokens' scales, unpacked for the warp: lane = token ---------------
       {
-        const uint32_t at = mxstage_s + st * C::MXSTAGEB + (lane >> 4) * 256 + (lane & 15) * GR;
+        const uint32_t at = mxstage_s + st * C::MXSTAGEB + (lane >> 4) * 2 * C::MXB + (lane & 15) * GR;
         const uint32_t wk = lds_u<GR>(at);
-        uint32_t wv = lds_u<GR>(at + 128);
+        uint32_t wv = lds_u<GR>(at + C::MXB);
         // what a hidden token holds does not count (K: its score is masked; V: its
         // weight is 0)
         if (edge && (lane < 16 ? hidden(0, lane) : hidden(1, lane - 16))) wv = refs;
