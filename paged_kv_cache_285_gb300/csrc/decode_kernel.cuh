@@ -127,7 +127,7 @@ __device__ __forceinline__ int out_dim(int u, int row) {
     const int pp = u >> 1, e = u & 1;
     return 32 * pp + (row >= 8 ? 16 : 0) + 2 * (row & 7) + e;
   } else if constexpr (CT == DT_E2M1) {
-    return 32 * (u >> 1) + 4 * (row & 7) + 2 * (u & 1) + (row >> 3);
+    return 32 * (u >> 1) + 4 * (row & 7) + (u & 1) + 2 * (row >> 3);
   } else {
     return 16 * u + row;
   }
@@ -543,17 +543,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // the query fragments, the same for all warps: [group][lane] 16 bytes (read again
     // for every tile: 16 registers less of the 128 that let four CTAs fit an SM)
     const uint32_t mxq = smem_u32(smem) + NW * NS * (C::STAGEB + C::MXSTAGEB) + NW * C::MXBUF + lane * 16;
-    if (warp == 0) {
-#pragma unroll
-      for (int c = 0; c < GR; ++c) {
-        const uint32_t f[4] = {qf[2 * c][0], qf[2 * c][1], qf[2 * c + 1][0], qf[2 * c + 1][1]};
-        sts_v<4>(mxq + c * 512, f);
-      }
-    }
-    __syncthreads();
     constexpr int UNITS = C::TILEB / 16;            // 16-byte units of a tile's codes ...
     constexpr int SUNITS = C::MXB / 16;             // ... and scales
-    const uint32_t unit0 = tile_off<C::CHUNKB>(lane * 16 / C::ROWB, lane * 16 % C::ROWB);
+    // Where the lane's unit (and the one 512 bytes on) goes: K's tokens in order, of
+    // V's the even ones before the odd ones (see the PV product).
+    const uint32_t kdst = tile_off<C::CHUNKB>(lane * 16 / C::ROWB, lane * 16 % C::ROWB);
+    auto vplace = [](int token) { return (token >> 1) + 8 * (token & 1); };
+    const uint32_t vdst[2] = {tile_off<C::CHUNKB>(vplace(lane * 16 / C::ROWB), lane * 16 % C::ROWB),
+                              tile_off<C::CHUNKB>(vplace((lane * 16 / C::ROWB + 512 / C::ROWB) & 15), lane * 16 % C::ROWB)};
     const uint8_t* kcodes = static_cast<const uint8_t*>(ap.k_cache) + lane * 16;
     const uint8_t* vcodes = static_cast<const uint8_t*>(ap.v_cache) + lane * 16;
     const uint8_t* scales = static_cast<const uint8_t*>(lane < SUNITS ? ap.k_scales : ap.v_scales) +
@@ -579,11 +576,11 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const int tile = __shfl_sync(kFull, at_cur, (i + x) & 31);
         const uint32_t n = tile == -1 ? 0u : 16u;
         const uint64_t at = tile == -1 ? 0u : (uint32_t)tile;
-        const uint32_t dst = wstage_s + st * C::STAGEB + x * 2 * C::TILEB + unit0;
+        const uint32_t dst = wstage_s + st * C::STAGEB + x * 2 * C::TILEB;
 #pragma unroll
         for (int u = 0; u < UNITS / 32; ++u) {
-          cp_async16_if(true, dst + u * 512, kcodes + at * C::TILEB + u * 512, n);
-          cp_async16_if(true, dst + C::TILEB + u * 512, vcodes + at * C::TILEB + u * 512, n);
+          cp_async16_if(true, dst + kdst + u * 512, kcodes + at * C::TILEB + u * 512, n);
+          cp_async16_if(true, dst + C::TILEB + vdst[u], vcodes + at * C::TILEB + u * 512, n);
         }
         cp_async16_if(lane < 2 * SUNITS, scale_dst + st * C::MXSTAGEB + x * 2 * C::MXB, scales + at * C::MXB, n);
       }
@@ -593,6 +590,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (2 * k < cnt) load_pair(2 * k, k);
       cp_async_commit();
     }
+    if (warp == 0) {
+#pragma unroll
+      for (int c = 0; c < GR; ++c) {
+        const uint32_t f[4] = {qf[2 * c][0], qf[2 * c][1], qf[2 * c + 1][0], qf[2 * c + 1][1]};
+        sts_v<4>(mxq + c * 512, f);
+      }
+    }
+    __syncthreads();
     // The sums of group c's dims are held relative to 2^(ref - 127), ref byte c of
     // refs: V's scales enter as f16 factors 2^(byte - ref) of the weights, of at most
     // 2^7 (with weights of at most 2^8 their products stay inside f16).  When a byte
@@ -603,7 +608,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // the lane's rows for ldmatrix: groups 0 and 1 of K's tokens, of V's (groups 2 and
     // 3 are 32 bytes on, with the swizzle: bit 5 flipped)
     const uint32_t kunit = tile_off<C::CHUNKB>(lane & 15, (lane >> 4) * 16);
-    const uint32_t vunit = tile_off<C::CHUNKB>((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 16);
+    const uint32_t vunit =
+        tile_off<C::CHUNKB>(((lane & 7) >> 1) + (lane & 1) * 4 + (lane >> 4) * 8, ((lane >> 3) & 1) * 16);
     // where the lane finds its groups' bytes of a pair of tokens (the even token's in
     // the low half): groups 0 and 1, an odd lane 2 and 3 (two groups: 0, and 1)
     const uint32_t pick0 = lane & 1 ? (GR == 4 ? 0x2266u : 0x1155u) : 0x4400u;
@@ -767,11 +773,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
 
       // ---- O^T[dim][head] += V^T . P^T ----------------------------------------------
+      // A transposed 8x8 b16 matrix gives thread (gid, tig) the codes of dims 4 gid ..
+      // 4 gid + 3 of two tokens.  The rows of one matrix are tokens 0, 8, 2, 10, .., 14
+      // (the thread's: 2 tig and 2 tig + 8), of another 1, 9, 3, 11, .., 15: merging
+      // them by nibbles puts equal dims of tokens 2 tig and 2 tig + 1 into a byte, and
+      // of 2 tig + 8 and 2 tig + 9, so that widening the four bytes gives an operand as
+      // it is (even dims; odd ones likewise).  The weights carry the tokens' scales of
+      // the group, so that its product adds up as it is.
       const uint32_t vat = wstage_s + st * C::STAGEB + C::TILEB + vunit;
-      // An 8x8 b16 transpose of codes gives thread (gid, tig) dims 4 gid .. 4 gid + 3
-      // of tokens 2 tig and 2 tig + 1; widened, a byte permute pairs equal dims of
-      // the two tokens.  The weights carry the tokens' scales of the group, so that
-      // its product adds up as it is.
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const uint32_t bh0 = movmatrix_t(pack2<false>(sc[x][0], sc[x][1]));
@@ -790,16 +799,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           ldsm_x4_t((vat ^ (32 * pp)) + x * 2 * C::TILEB, r);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            uint32_t v0[4], v1[4];  // tokens 0-7, 8-15
-            e2m1x8_to_f16x8(r[e], v0);
-            e2m1x8_to_f16x8(r[2 + e], v1);
             const int c = 2 * pp + e;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t a[4] = {__byte_perm(v0[y], v0[y + 2], 0x5410), __byte_perm(v0[y], v0[y + 2], 0x7632),
-                                     __byte_perm(v1[y], v1[y + 2], 0x5410), __byte_perm(v1[y], v1[y + 2], 0x7632)};
-              mma16816<false>(acc[2 * c + y], a, w0[c], w1[c]);
-            }
+            const uint32_t even = (r[e] & 0x0F0F0F0Fu) | ((r[2 + e] << 4) & 0xF0F0F0F0u);
+            const uint32_t odd = ((r[e] >> 4) & 0x0F0F0F0Fu) | (r[2 + e] & 0xF0F0F0F0u);
+            uint32_t a[4];
+            e2m1x8_to_f16x8(even, a);
+            mma16816<false>(acc[2 * c], a, w0[c], w1[c]);
+            e2m1x8_to_f16x8(odd, a);
+            mma16816<false>(acc[2 * c + 1], a, w0[c], w1[c]);
           }
         }
       }
