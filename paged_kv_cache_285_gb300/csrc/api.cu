@@ -652,6 +652,12 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
 // 1.5 rounds (fp8 40 x 4,096 62.7 -> 54.9, 100 x 4,096 130 -> 122, bf16 64 x 4,096
 // 154 -> 146; excluded: fp8 64 x 2,048 50.1 -> 52.5, 128 x 4,096 of 64 heads 165 ->
 // 170).
+//
+// Microscaled codes: the widening takes as much of a CTA's time as their copies,
+// so that an SM reads at less than its share of the bandwidth (236 tokens per us at
+// 128 dims, 416 at 64, a CTA alone 140 and 205); falling splits pay from 2,500
+// tokens on (24 x 2,048 23.4 -> 29.0 us with them, 32 of 100-1,500 21.0 -> 25.1; 20 of
+// 500-8,192 43.0 -> 34.8, 64 of 512-4,096 44.3 -> 40.9).
 static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_seq_len, int window,
                             int sink_tokens, int forced, int sm_count) {
   // (so far below 2^31 that whole splits stay below it too)
@@ -831,7 +837,9 @@ static pkv_status decode_common(const pkv_cache_desc* desc, const void* k_cache,
     // 256 x 600 43.0 -> 43.5, 256 x 1,024 58.5 -> 65.5.  Windows: fp8 512 x 128 65.3 ->
     // 51.3, 128 x 256 26.6 -> 22.3, bf16 256 x 128 46.1 -> 42.8, 128 x 256 37.0 -> 38.2.
     const int64_t ctas = (int64_t)batch * desc->num_kv_heads * ((group + 7) / 8);
-    ap.two_warps = !pl.cluster && pl.splits == 1 && pl.chunk <= 400 && ctas > 4 * ds->sm_count ? 1 : 0;
+    // Microscaled codes (a tile of theirs is 3/10 of a bf16 one): 128 x 1,024 45.1 ->
+    // 41.0, 256 x 512 49.2 -> 46.0; 128 in a window of 4,096 113.4 -> 118.9.
+    ap.two_warps = !pl.cluster && pl.splits == 1 && pl.chunk <= (mx4 ? 1200 : 400) && ctas > 4 * ds->sm_count ? 1 : 0;
     ap.num_cuts = pl.num_cuts;
     std::copy(pl.cut, pl.cut + kMaxCuts + 1, ap.cut);
     if (mx4) {
