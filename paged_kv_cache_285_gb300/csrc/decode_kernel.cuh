@@ -61,6 +61,27 @@
 //     launch.  3 requests of up to 700 tokens 4.7 us, 4 in a window of 1,024 6.3
 //     (parts read from the CTAs that hold them, between two barriers: 5.0, 7.4; one
 //     split 8.3, 14.3; splits merged by a second launch 5.4, 7.7 at best).
+//   * microscaled codes (CT = e2m1, MX): two codes a byte and a scale for 32 values of
+//     a row, so K's scale multiplies the partial product of its 32 dims
+//     (s[t] = sum_g 2^(kb[t][g]) (K_g q_g)[t], fp32) and V's, which sits on the
+//     contracted side (tokens), goes into P: O_g += V_g^T (P 2^(vb[t][g] - ref)), with
+//     2^ref, near the tile's largest V scale, multiplied back in fp32 at the end.
+//     A tile is a quarter of a 16-bit one and the arithmetic the same, so the kernel is
+//     bound by instructions (57 % of the ALU pipe's cycles and 58 % of the issue slots
+//     with two tiles a turn, memory 67 % of the copy's rate) and everything in it saves
+//     those: V's codes are merged by nibbles into the operands of two products (a token
+//     of each in one byte, where a convert per nibble needed a permute each); scales are
+//     unpacked by one lane per token and passed through shared memory; the running
+//     maximum is looked at by a vote and reduced only when a score exceeds it by 8; NaN
+//     scales, a growing ref and scales below f16's range share one rare path.  Lanes
+//     copy 16 bytes each (cp.async): one lane issuing TMA copies of 1 KB was the longest
+//     chain of a turn (128 requests in a window of 4,096: 164 us; 113 now, 5.0 TB/s;
+//     copies alone 90, arithmetic alone 101).  64 requests of 512-4,096 tokens 40.6 us,
+//     3 of up to 700 3.8.
+//     Not kept, on the window: masks by a multiply of f16 pairs instead of a permute
+//     (123 against 114), five CTAs an SM by spilling (131), three stages or L2 prefetches
+//     (no change), K and V in copy groups of their own (117 against 114), rolled loops
+//     over the two tiles (125).
 //   * warps are combined through shared memory with their (max, sum); a split
 //     either writes the final output (single-split requests) or a normalised
 //     partial plus its log-sum-exp, merged by merge_kernel.
