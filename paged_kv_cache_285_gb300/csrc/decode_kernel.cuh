@@ -672,10 +672,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int c = 0; c < GR; ++c)
           fk[c] = __uint_as_float((c == 3 ? wk >> 1 : wk << (23 - 8 * c)) & 0x7F800000u) * p.scale_log2;
         // V's factors 2^(byte - ref): their f16 exponents, 15 more, are 0 .. 22 in the
-        // usual case and need no borrow; else, and for a NaN, byte by byte
+        // usual case and need no borrow; else, and for a NaN, byte by byte.  (What passes
+        // 0 .. 22 shows in the sum's upper bits, unless it comes round to 0 .. 22 again:
+        // a byte of 241 or more over a ref of 13 or less, whose upper bits show it; ref
+        // is 248 at most, so that none comes round from below.)
         uint32_t x4 = wv + (0x0F0F0F0Fu - refs);
         const uint32_t nan_k = ((wk & 0x7F7F7F7Fu) + 0x01010101u) & wk & 0x80808080u;
-        if (__any_sync(kFull, (nan_k | ((x4 | (x4 + 0x09090909u)) & 0xE0E0E0E0u)) != 0u)) {
+        if (__any_sync(kFull, (nan_k | ((x4 | (x4 + 0x09090909u)) & 0xE0E0E0E0u) |
+                               (wv & (wv << 1) & ~refs & 0x80808080u)) != 0u)) {
           x4 = 0u;
 #pragma unroll
           for (int c = 0; c < GR; ++c) {
@@ -689,7 +693,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
             const int top = __reduce_max_sync(kFull, e);
             if (top > ref + 7) {
-              const int up = top - 5 - ref;
+              const int up = min(top - 5, 248) - ref;
               ref += up;
               refs += (uint32_t)up << (8 * c);
               const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);

@@ -229,6 +229,32 @@ def test_decode_scales_of_any_size(splits):
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("d,act", [(64, BF16), (128, BF16)])
+def test_decode_scales_from_one_end_of_their_range_to_the_other(splits, d, act):
+    # V's scale bytes 1 .. 13 in the first tokens, then 241 .. 243 among them (and the other way round): their
+    # difference, 15 more, passes 255
+    lens = [300, 300, 40]
+    c = Mx4Case(act, 1, d, 16, lens, seed=8)
+    low = c.rng.integers(1, 14, c.vs.shape).astype(np.uint8)
+    high = c.rng.integers(241, 244, c.vs.shape).astype(np.uint8)
+    mixed = np.where(c.rng.integers(0, 3, c.vs.shape[:3] + (1,)) == 0, low, high)
+    c.vs = torch.from_numpy(mixed)
+    for i in range(10):
+        c.vs[c.tables[0, i]] = torch.from_numpy(low[c.tables[0, i]])
+    for i in range(10, 19):
+        c.vs[c.tables[1, i]] = torch.from_numpy(low[c.tables[1, i]])
+    c.cuda()
+    q = c.rows(3, 4).cuda()
+    out, lse = run_decode(c, q, 4, lens, splits=splits)
+    ref = decode_ref(c, q, 4, lens)
+    got, want, x = to_f64(out), ref[0], ref[2]
+    # as above; a token's value is at most vmax, so that the flushed ones and f16's least steps count to it
+    tol = 2.0 ** -8 * np.abs(want) + x["mass"] * 2.0 ** -10 + x["vmax"][..., None] * (2.0 ** -17 + x["seen"][..., None] * 2.0 ** -24)
+    assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) / tol)
+    assert np.max(np.abs(want)) > 2.0 ** 110 and pkv.get_device_error() == 0
+
+
 def test_decode_ignores_what_lies_past_the_end_and_keeps_nan():
     c = Mx4Case(BF16, 1, 128, 16, [21, 40], seed=3)
     blk = c.tables[0, 1]
