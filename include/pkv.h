@@ -753,7 +753,7 @@ pkv_status pkv_paged_extend_attn_mx4(const pkv_cache_desc* desc, const void* k_c
  * every layer -- and move the same blocks or tokens in each, in one launch (128
  * pools a launch).  A pool is [num_blocks][num_kv_heads][block_size][row_bytes]
  * bytes of any type; a scale per block and kv head is a pool with block_size 1.
- * `pools` is host memory, read during the call.  The stream order is that of the
+ * `pools` is host memory, read during the call; no two pools overlap.  The stream order is that of the
  * block-scaled calls.
  * ------------------------------------------------------------------------- */
 typedef struct {

@@ -991,6 +991,10 @@ class KvPools:
                 raise ValueError(f"pool {i} is empty or too large: {tuple(shape)}")
             rows.append((t.data_ptr(), nb, hkv, bs, size))
             self._index = index
+        order = sorted(range(self._count), key=lambda i: rows[i][0])
+        for i, j in zip(order, order[1:]):
+            if rows[i][0] + rows[i][1] * rows[i][2] * rows[i][3] * rows[i][4] > rows[j][0]:
+                raise ValueError(f"pools {i} and {j} overlap")
         self._array = (Pool * self._count)(*rows)
         self._at = ctypes.addressof(self._array)
 

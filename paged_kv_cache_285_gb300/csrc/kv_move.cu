@@ -144,14 +144,14 @@ __device__ __forceinline__ void compact_rows(const CompactParams& p, const Pool&
   const int vph = vpr * p.heads;                   // per row
   const int rows = max(1, min(NT, NT * kMoveUnroll / vph));  // per CTA and pass
   const int rank = CL ? (int)(blockIdx.x & ((1u << p.cluster_shift) - 1u)) : 0;
-  const int step = CL ? rows << p.cluster_shift : rows, passes = (n + step - 1) / step;
+  const int step = CL ? rows << p.cluster_shift : rows, passes = n / step + (n % step != 0);
   const int vecs = rows * vph;  // at most what the threads hold (the launcher picks p.heads so)
   auto look_up = [&](int pass) {
     if ((int)threadIdx.x < rows) {
       const int i = pass * step + rank * rows + threadIdx.x;
       RowMove m;
       m.src_blk = -1;
-      if (i < n) m = find_move(p, b, r0, i, dst0, report);
+      if ((unsigned)i < (unsigned)n) m = find_move(p, b, r0, i, dst0, report);  // (i may pass 2^31)
       s_row[pass % 3][threadIdx.x] = m;
     }
   };
@@ -250,12 +250,22 @@ cudaError_t launch_copy_blocks(CopyBlocksParams& p, int num_pairs, cudaStream_t 
   int64_t most = 0;
   for (int k = 0; k < p.num_pools; ++k) most = std::max(most, p.pool[k].block_bytes);
   const int64_t pieces = (most + kPieceBytes - 1) / kPieceBytes;
-  const int64_t ctas = pieces * p.num_pools * num_pairs;
-  if (ctas <= 0 || ctas > INT32_MAX) return cudaErrorInvalidValue;
+  if (pieces * p.num_pools > INT32_MAX) return cudaErrorInvalidValue;
   p.pieces = (int)pieces;
   p.div_pieces = make_fastdiv((uint32_t)pieces);
   p.div_pools = make_fastdiv((uint32_t)p.num_pools);
-  return launch_dependent(copy_blocks_kernel, (unsigned)ctas, kCopyThreads, stream, p);
+  // as many pairs a launch as a grid holds
+  const int most_pairs = (int)(INT32_MAX / (pieces * p.num_pools));
+  for (int left = num_pairs; left > 0;) {
+    const int n = std::min(left, most_pairs);
+    const cudaError_t e =
+        launch_dependent(copy_blocks_kernel, (unsigned)(pieces * p.num_pools * n), kCopyThreads, stream, p);
+    if (e != cudaSuccess) return e;
+    left -= n;
+    p.src += n;
+    p.dst += n;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_compact(CompactParams& p, int sm_count, cudaStream_t stream) {

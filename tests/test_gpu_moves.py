@@ -65,6 +65,14 @@ def test_copy_blocks_of_pools_in_the_middle_of_a_tensor():
         np.testing.assert_array_equal(raw(store.view(1, -1))[0], want)
 
 
+def test_pools_that_overlap_are_refused():
+    t = torch.zeros((8, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    for pools in ([t, t], [t[4:], t[2:6]], [t[2:6], t[:4], t[4:]]):
+        with pytest.raises(ValueError, match="overlap"):
+            pkv.KvPools(pools)
+    pkv.KvPools([t[4:], t[:4]])
+
+
 def test_copy_blocks_reports():
     pools = pools_of(["bf16", "mx"], 12, 2, 16, 64, seed=1)
     before = [raw(t) for t in pools]
