@@ -730,7 +730,9 @@ pkv_status pkv_paged_decode_attn_mx4(const pkv_cache_desc* desc, const void* k_c
  *            pkv_extend_mx4_workspace_bytes() bytes or more, 256-byte aligned, any
  *            contents, a call with many rows per request first widens each block
  *            that its rows see, once, into 16-bit copies there, K as code * scale
- *            in the act dtype (bf16 queries are then taken as they are), V as above.
+ *            in the act dtype (bf16 queries are then taken as they are), V as above;
+ *            a call with few rows over long or uneven prefixes shares their keys
+ *            out over all SMs and adds the parts up there.
  *            Calls that run at the same time need workspaces of their own.
  * ------------------------------------------------------------------------- */
 size_t pkv_extend_mx4_workspace_bytes(const pkv_cache_desc* desc);

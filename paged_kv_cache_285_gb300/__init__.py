@@ -936,7 +936,7 @@ def paged_decode_attn_mx4(k_cache, v_cache, k_scales, v_scales, q, out, block_ta
 
 def extend_mx4_workspace_bytes(k_cache) -> int:
     """pkv_extend_mx4_workspace_bytes: the optional workspace of paged_extend_attn_mx4 (16-bit copies
-    of the K and V pools, and the per-block claims)."""
+    of the K and V pools and the per-block claims, or the parts of calls that are shared out)."""
     return int(load().pkv_extend_mx4_workspace_bytes(_desc_mx4(k_cache)))
 
 
@@ -946,7 +946,7 @@ def paged_extend_attn_mx4(k_cache, v_cache, k_scales, v_scales, q, out, q_indptr
     """pkv_paged_extend_attn_mx4: paged_extend_attn over e2m1 codes with microscales; window 0: every
     key, else as paged_extend_attn_window.  workspace: None, or a uint8 device tensor of
     extend_mx4_workspace_bytes() bytes or more (calls with many rows per request then widen the pages
-    they read once per block)."""
+    they read once per block, calls with few rows over long prefixes are shared out over all SMs)."""
     if _direct is not None:
         st = _direct.extend_mx4(k_cache, v_cache, k_scales, v_scales, q, out, q_indptr, prefix_lens,
                                 block_tables, sm_scale, max_suffix_len, max_total_len, window,

@@ -191,6 +191,14 @@ bool plan_extend(ExtendParams& p, int batch, int num_kv_heads, int group, int ma
   return true;
 }
 
+// The key tiles of an item, at most.
+int64_t view_tiles(const ExtendParams& p, int max_total_len) {
+  const int64_t tiles = ((int64_t)max_total_len + 127) / 128;
+  if (p.window <= 0) return tiles;
+  return std::min<int64_t>(tiles, ((int64_t)p.window + 2 * p.tok + 15 + 127) / 128 + 1 +
+                                      ((int64_t)p.sink_tokens + 127) / 128);
+}
+
 // How an extend call with a window and / or block scales takes its items: in
 // whole tiles or, where every request's rows fit one row tile, in half tiles; and
 // with its key tiles split over a cluster of `splits` CTAs when the items are too
@@ -202,11 +210,8 @@ bool plan_extend(ExtendParams& p, int batch, int num_kv_heads, int group, int ma
 // 63 tiles 115 / 66 / 39 / 25; the last in half tiles 100 / 55 / 33 / 22.5, and
 // 512 of 1 to 4 tiles 44 whole, 56 in half tiles.  (Two of these at each end
 // again with launches set up early: 257, 44; the order is the same.)
-void plan_view_items(ExtendParams& p, int max_total_len, int sm_count) {
-  int64_t tiles = ((int64_t)max_total_len + 127) / 128;
-  if (p.window > 0)
-    tiles = std::min<int64_t>(tiles, ((int64_t)p.window + 2 * p.tok + 15 + 127) / 128 + 1 +
-                                         ((int64_t)p.sink_tokens + 127) / 128);
+double plan_view_items(ExtendParams& p, int max_total_len, int sm_count) {
+  const int64_t tiles = view_tiles(p, max_total_len);
   const double sms = sm_count > 0 ? sm_count : 152;
   double best = 1e30;
   for (int half = 0; half <= (p.tiles_per_head <= 1 ? 1 : 0); ++half) {
@@ -223,6 +228,25 @@ void plan_view_items(ExtendParams& p, int max_total_len, int sm_count) {
       }
     }
   }
+  return best;
+}
+
+// Runs of key tiles instead, which the device cuts by the requests' lengths: 1.75 us a
+// tile, all items' tiles over all SMs as far as their number is known (a request with
+// rows has a pair of row tiles, half a pair more than its rows fill), and 13 us for what
+// CTAs find out, their parts and the launch that sums them up.  cost: the plan's
+// estimate.  Measured, us, plan / runs: 8 requests of 20 to 120 rows over 200 to 2,500
+// 45.6 / 37.5, 37.9 / 29.5 and 44.9 / 46.6 by their lengths; 5 over 200 to 8,000 106 /
+// 47, 121 / 64; 4 of 100 to 250 over 200 to 3,000 53.8 / 57.4; 8 of 120 over 2,000
+// each 41.6 / 45.1; 8 of 64 over 512 15.3 / 19.5.  Not where every request's rows fit
+// one row tile (16 of 1 to 32 over 200 to 4,000, half tiles: 56.2 / 60.6).
+int plan_runs(const ExtendParams& p, int total_q_rows, int max_total_len, int sm_count, double cost) {
+  const int runs = std::min(kMaxRuns, sm_count > 0 ? sm_count : 1) / p.num_kv_heads;
+  const int units = p.num_items / p.num_kv_heads;
+  if (p.half || units > runs || p.div_pairs.d >= 16) return 0;
+  const int64_t tiles = view_tiles(p, max_total_len);
+  const double used = std::min<double>(units, std::max<double>(p.batch, total_q_rows / (2.0 * p.tok) + 0.5 * p.batch));
+  return 1.75 * tiles * used / runs + 13. < 0.93 * cost ? runs : 0;
 }
 
 // Softmax scale in base 2 with an fp8 cache's k_scale folded in (scores are
@@ -1275,6 +1299,12 @@ static size_t plain_widen_bytes(const pkv_cache_desc* d) {
   return pools ? pools + align256((1 + 2 * (size_t)d->num_blocks) * sizeof(int32_t)) : 0;
 }
 
+// The parts of an extend in runs of key tiles: per run the rows of a pair of row tiles
+// and their (max, sum).
+static size_t runs_bytes(const pkv_cache_desc* d) {
+  return (size_t)kMaxRuns * (256 * (d->head_dim * sizeof(float) + sizeof(float2)) + 2 * sizeof(int4));
+}
+
 static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
                                 const void* v_cache, const void* k_new, const void* v_new,
                                 const void* q, void* out, pkv_dtype act_dtype,
@@ -1413,8 +1443,14 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
   int cache_dt = (int)desc->cache_dtype;
   bool widen_pages = widen_plain;
   if (view) {
-    plan_view_items(p, max_total_len, ds->sm_count);
-    if (p.splits > 1 || p.half) p.out_tma = 0;  // (every row leaves with its parts' sum)
+    const double cost = plan_view_items(p, max_total_len, ds->sm_count);
+    if (mx4 && workspace && aligned(workspace, 256) && workspace_bytes >= runs_bytes(desc)) {
+      p.runs = plan_runs(p, total_q_rows, max_total_len, ds->sm_count, cost);
+      p.run_o = static_cast<float*>(workspace);
+      p.run_ml = reinterpret_cast<float2*>(p.run_o + (size_t)kMaxRuns * 256 * desc->head_dim);
+      p.run_of = reinterpret_cast<int4*>(p.run_ml + (size_t)kMaxRuns * 256);
+    }
+    if (p.splits > 1 || p.half || p.runs) p.out_tma = 0;  // (every row leaves with its parts' sum)
     const int64_t units = total_q_rows / (2 * p.tok) + (int64_t)batch;
     p.num_blocks_dyn = p.num_items;
     p.div_rows = make_fastdiv((uint32_t)(2 * p.tok));
@@ -1428,7 +1464,7 @@ static pkv_status extend_common(const pkv_cache_desc* desc, const void* k_cache,
     // pairs: 804 against 957 us), the pass itself three launches and three
     // times the pages' bytes (300 rows, 10 pairs: 140 against 132; 16 rows: 123
     // against 68).
-    if (p.splits > 1 || p.half || (p.tiles_per_head + 1) / 2 < 16) widen_pages = false;
+    if (p.splits > 1 || p.half || p.runs || (p.tiles_per_head + 1) / 2 < 16) widen_pages = false;
     if (mx4 && !widen_pages) {
       if ((st = make_page_map(&kmap, k_cache, desc)) != PKV_OK) return st;
       if ((st = make_page_map(&vmap, v_cache, desc)) != PKV_OK) return st;
@@ -1539,7 +1575,7 @@ pkv_status pkv_paged_extend_attn_block_scaled(
 
 size_t pkv_extend_mx4_workspace_bytes(const pkv_cache_desc* desc) {
   if (check_desc_mx4(desc) != PKV_OK) return 0;
-  return plain_widen_bytes(desc);
+  return std::max(plain_widen_bytes(desc), runs_bytes(desc));
 }
 
 pkv_status pkv_paged_extend_attn_mx4(const pkv_cache_desc* desc, const void* k_cache,

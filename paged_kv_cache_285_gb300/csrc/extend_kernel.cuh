@@ -82,11 +82,11 @@
 // takes its key row's into registers and, once its warp has, writes the row as
 // f16(code * scale), K and V alike.  A row's codes, its scales and its 16-bit form lie
 // in the 4 KB that the row's warp converts, so a __syncwarp orders them and no warp waits
-// for another (8 turns of 20-120 rows: 48 us, where pages widened once per call, three
-// launches more, took 61; 80 with the path of scales that f16 cannot hold inlined for each
+// for another (8 turns of 20-120 rows: 48 us (35 in runs, below), where pages widened once per call,
+// three launches more, took 61; 80 with the path of scales that f16 cannot hold inlined for each
 // 32 values: the loop left the instruction cache).  With many row tiles to a key
 // tile (16 pairs, as for block scales) the pages are widened once per call instead:
-// 4 chunks of 2,000 rows over up to 9,000 tokens 738 us.
+// 4 chunks of 2,000 rows over up to 9,000 tokens 714 us.
 //
 // Items taken as they come (DYN = true; the kernels of calls with a window or
 // block scales): the grid has a CTA per item, one fits an SM, and a running CTA
@@ -119,6 +119,17 @@
 // runs: barriers and TMEM are set up, then they wait for its end before their
 // first load (plain loads; calls one after another, a short prompt 12.3 -> 10.3
 // us, 8 chat turns 45.1 -> 44).
+//
+// Runs (RUN = true), for calls with about as many items as SMs, which differ in length:
+// one CTA an SM, and each finds out on its own (from the requests' lengths, which the
+// host does not know) which run of which item's key tiles it takes, such that the runs
+// are as short as the number of CTAs allows (find_run).  An item of one run is finished
+// by its CTA; parts of an item go to a workspace and are summed up by a second launch.
+// 8 turns of 20-120 rows over 200-2,500 tokens: 48.4 -> 34.8 us (9 key tiles in the
+// longest run, 19 in the longest item); 3.4 us more where nothing can be cut, which
+// the host's rule weighs.  What a run is made of passes through shuffles: taken from
+// shared memory as it is, the compiler keeps the loops' addresses per lane, 1.87 us a
+// key tile against 1.75.
 //
 // Half tiles (HALF = true, with CL): where every request's rows fit one row tile,
 // tile B would be empty.  Both tiles then hold the same rows and share the keys
@@ -216,6 +227,10 @@ struct ExtCfg {
   static constexpr int OFF_SCHED = OFF_SCALE + 2 * NSC * 8 * 4;
   static constexpr int SMEM_DYN = OFF_SCHED + 3 * 16 + NSCHED * 8 + 1024;
   static_assert(OFF_SCHED % 16 == 0 && SMEM_DYN <= 232448, "shared memory per CTA");
+  // RUN: its run in the ring of items, and an int per unit
+  static constexpr int OFF_RUN = OFF_SCHED + 3 * 16 + NSCHED * 8;
+  static constexpr int SMEM_RUN = OFF_RUN + kMaxRuns * 4 + 1024;
+  static_assert(SMEM_RUN <= 232448, "shared memory per CTA");
   // CL: the fp32 parts of the CTA's share of the rows over the rings, their
   // (max, sum) and the softmax warps' buffers (4 KB each) over the Q tiles
   static constexpr int OFF_CO = OFF_K;
@@ -787,11 +802,77 @@ __device__ __forceinline__ int item_by_rows(const int32_t* q_indptr, int batch, 
   return pair >= 0 && pair < pairs ? (lo * heads + g) * pairs + pair : num_items;
 }
 
+// RUN: the run of key tiles of this CTA, (item, part, parts of the item, tiles of a
+// part), item num_items where there is none.  All heads' items of a (request, pair)
+// -- a unit -- are cut alike: into parts of the least length with which the units
+// together have at most p.runs of them (there are no more units than that).  The
+// whole warp; `tiles`: shared memory, an int per unit.
+template <bool WIN>
+__device__ __forceinline__ int4 find_run(const ExtendParams& p, int* tiles) {
+  const int lane = threadIdx.x & 31, heads = p.num_kv_heads, pairs = (int)p.div_pairs.d;
+  const int units = p.batch * pairs;
+  const int j = (int)p.div_hkv.div(blockIdx.x), g = blockIdx.x - j * heads;
+  uint32_t sum = 0u, most = 0u;
+  for (int u = lane; u < units; u += 32) {
+    const int b = (int)p.div_pairs.div((uint32_t)u);
+    const int item = b * heads * pairs + (u - b * pairs);  // head 0
+    typename ItemOf<WIN, false>::T it;
+    tiles[u] = derive<false, false, WIN>(p, item, load_raw<false, true>(p, item), it) ? it.T : 0;
+    sum += (uint32_t)tiles[u];
+    most = max(most, (uint32_t)tiles[u]);
+  }
+  __syncwarp();
+  sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  // the least length between sum / runs and the longest unit's, 32 tried at a time
+  uint32_t lo = max(1u, (sum + p.runs - 1) / (uint32_t)p.runs), hi = max(lo, most);
+  while (lo < hi) {
+    const uint32_t step = (hi - lo + 30) / 31, len = min(lo + lane * step, hi);
+    uint32_t n = 0u;
+#pragma unroll 4
+    for (int u = 0; u < units; ++u) n += ((uint32_t)tiles[u] + len - 1) / len;
+    const int first = __ffs(__ballot_sync(0xFFFFFFFFu, n <= (uint32_t)p.runs)) - 1;  // (hi fits)
+    hi = min(lo + first * step, hi);
+    if (first > 0) lo += (first - 1) * step + 1;
+  }
+  // the unit of part j: 32 units' parts counted at a time
+  int start = 0;
+  for (int u0 = 0; u0 < units; u0 += 32) {
+    const int u = u0 + lane, T = u < units ? tiles[u] : 0, n = (T + (int)lo - 1) / (int)lo;
+    int end = n;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, end, k);
+      if (lane >= k) end += v;
+    }
+    end += start;
+    const unsigned here = __ballot_sync(0xFFFFFFFFu, j < end);
+    if (here) {
+      const int at = __ffs(here) - 1, v = u0 + at;
+      const int tv = __shfl_sync(0xFFFFFFFFu, T, at), nv = __shfl_sync(0xFFFFFFFFu, n, at);
+      const int part = j - (__shfl_sync(0xFFFFFFFFu, end, at) - nv);
+      const int per = (tv + nv - 1) / nv, parts = (tv + per - 1) / per;
+      const int b = (int)p.div_pairs.div((uint32_t)v);
+      return make_int4(part < parts ? (b * heads + g) * pairs + (v - b * pairs) : p.num_items, part, parts, per);
+    }
+    start = __shfl_sync(0xFFFFFFFFu, end, 31);
+  }
+  return make_int4(p.num_items, 0, 0, 1);
+}
+
 // derive for any kernel; CL: then the CTA's share of the item's key tiles.
-template <bool PP, bool SX, bool WIN, bool CL, bool HALF = false>
+// RUN: `run` is the CTA's (find_run).
+template <bool PP, bool SX, bool WIN, bool CL, bool HALF, bool RUN>
 __device__ __forceinline__ bool derive_any(const ExtendParams& p, int item, const ItemRaw& r,
-                                           typename ItemOf<WIN, CL>::T& it) {
-  if constexpr (CL) {
+                                           typename ItemOf<WIN, CL || (RUN && WIN)>::T& it, const int4* run) {
+  if constexpr (RUN) {
+    if (!derive<PP, SX, WIN>(p, item, r, it)) return false;
+    const int per = __shfl_sync(0xFFFFFFFFu, run->w, 0), kt0 = __shfl_sync(0xFFFFFFFFu, run->y, 0) * per;
+    it.T = __shfl_sync(0xFFFFFFFFu, min(per, it.T - kt0), 0);
+    if constexpr (WIN) it.kt0 = kt0;
+    else it.k_lo = kt0 * BN;
+    return it.T > 0;
+  } else if constexpr (CL) {
     it.kt0 = 0;
     it.rows = false;
     if (!derive<PP, SX, WIN>(p, item, r, it)) return false;
@@ -881,18 +962,20 @@ __device__ __forceinline__ void combine_parts(const ExtendParams& p, const Split
 // prefix pass; SX: shared-prefix extend; WIN: a window with sink tokens; BSC:
 // fp8 codes with scales per block and kv head; CL: key tiles split over a
 // cluster; TAKE: items taken as they come (DYN), from blocks counted by the
-// length hint (1) or by rows (2); HALF: both tiles hold the same rows and half of
+// length hint (1) or by rows (2), or one run of key tiles per CTA (3: RUN); HALF: both tiles hold the same rows and half of
 // each key tile.
 template <int HD, int CT, int AT, bool PP, bool SX, bool WIN, bool BSC, bool CL, int TAKE, bool HALF>
 __global__ void __launch_bounds__(NTHREADS, 1)
 extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
               const ExtendParams p, const ExtendPartialParams pp) {
-  constexpr bool DYN = TAKE != 0;
-  constexpr bool DEP = WIN || BSC || CL || DYN;
+  constexpr bool DYN = TAKE == 1 || TAKE == 2, RUN = TAKE == 3;
+  constexpr bool SPL = CL || RUN;  // the CTA takes a part of an item's key tiles
+  constexpr bool SPK = CL || (RUN && WIN);  // ... from tile kt0 on, else from key k_lo on
+  constexpr bool DEP = WIN || BSC || SPL || DYN;
   static_assert(!HALF || CL, "half tiles are combined as parts");
   constexpr int SN = HALF ? BN / 2 : BN;  // keys of a key tile that one row tile takes
-  static_assert(!((WIN || BSC || CL || DYN) && (PP || SX)) && !(CL && DYN) && (!BSC || CT == DT_E4M3),
+  static_assert(!((WIN || BSC || SPL || DYN) && (PP || SX)) && !(CL && TAKE != 0) && (!BSC || CT == DT_E4M3),
                 "unsupported combination");
   using C = ExtCfg<HD, CT, AT>;
   constexpr int NST = C::NST;
@@ -979,6 +1062,15 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
   if constexpr (DEP) grid_dependency_wait();
+  if constexpr (RUN) {
+    if (warp == 0) {
+      const int4 run = find_run<WIN>(p, reinterpret_cast<int*>(smem + C::OFF_RUN));
+      if (lane == 0) sched[0] = run;
+    }
+    __syncthreads();
+    item0 = __shfl_sync(0xFFFFFFFFu, sched[0].x, 0);
+    stride = p.num_items;
+  }
 
   // DYN: the CTA's next item and its request's values, from the K producer
   // (past the last: num_items); the seq-th (from 1) is in slot seq & 1.  (The
@@ -995,10 +1087,12 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int4 v = sched[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(sbar(C::B_ITAKEN + slot));
-    raw.r0 = v.y;
-    raw.r1 = v.z;
-    raw.prefix = v.w;
-    return v.x;
+    // (the same in every lane, which the compiler takes from the shuffles alone: without
+    // them the loops below keep per-lane copies)
+    raw.r0 = __shfl_sync(0xFFFFFFFFu, v.y, 0);
+    raw.r1 = __shfl_sync(0xFFFFFFFFu, v.z, 0);
+    raw.prefix = __shfl_sync(0xFFFFFFFFu, v.w, 0);
+    return __shfl_sync(0xFFFFFFFFu, v.x, 0);
   };
 
   // registers: launched with 128 per thread (512 x 128); the two softmax
@@ -1022,13 +1116,13 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint32_t srow = tmem + lane_addr + tm_s(x);
     const uint32_t orow = tmem + lane_addr + tm_o<HD>(x);
     int n = 0, js = 0;
-    float m_fin = -INFINITY, l_fin = 0.f;  // CL
+    float m_fin = -INFINITY, l_fin = 0.f;  // SPL
     ItemRaw nxt_raw = load_raw<SX, DEP>(p, DYN ? p.num_items : item0);
     for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
       const ItemRaw raw = nxt_raw;
       if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
-      typename ItemOf<WIN, CL>::T it;
-      if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
+      typename ItemOf<WIN, SPK>::T it;
+      if (!derive_any<PP, SX, WIN, CL, HALF, RUN>(p, item, raw, it, sched)) continue;
       const int i0x = it.i0 + (HALF ? 0 : x * TOK);  // first token of this tile
       // a row's last visible key is kdiag + its token (prefix pass: the chunk's
       // last key for all)
@@ -1049,7 +1143,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int kt = 0; kt < it.T; ++kt, ++n, seg_advance<SX>(p, it, si)) {
         if (!mbar_wait(bar(C::B_SDONE + x), n & 1)) { ok = false; break; }
         tc_fence_after();
-        const int key0 = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, CL>(it, kt) + (HALF ? x * SN : 0);
+        const int key0 = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, SPK>(it, kt) + (HALF ? x * SN : 0);
         // keys key0 .. key0 + nvis of the tile are visible to this row
         int nvis;
         bool masked;
@@ -1145,9 +1239,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                                fmaxf(mx[6], mx[7])) * (BSC ? 1.f : p.scale_log2);
         float m_new = m_run;
         if (mt > m_run + 8.f) m_new = mt;
-        // SX, WIN, CL: a row that has seen no key yet keeps m = -inf and takes 0 as
+        // SX, WIN, CL, RUN: a row that has seen no key yet keeps m = -inf and takes 0 as
         // the exponent's base, so its masked scores give exact zeros
-        const float m_base = ((SX || WIN || CL) && m_new == -INFINITY) ? 0.f : m_new;
+        const float m_base = ((SX || WIN || SPL) && m_new == -INFINITY) ? 0.f : m_new;
         const float alpha = fast_exp2(m_run - m_base);
         const bool mine = (m_new != m_run);
         if (kt >= 1 && __any_sync(0xFFFFFFFFu, mine)) {
@@ -1204,8 +1298,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // each thread)
       const bool staged = out_tma_for<HD, CT, SX>() && !PP && p.out_tma && it.ntok[x] == TOK;
       const float osc = p.out_scale / l_run;
-      if constexpr (CL) {
-        // O stays in TMEM until the whole cluster is done with its rings
+      if constexpr (SPL) {
+        // O stays in TMEM: CL, until the whole cluster is done with its rings; RUN, to
+        // be written once, behind the loop, whose registers it would take
         m_fin = m_run;
         l_fin = l_run;
       } else if constexpr (PP) {
@@ -1298,11 +1393,41 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
       ++js;
     }
+    if constexpr (RUN) {
+      typename ItemOf<WIN, SPK>::T fin;
+      if (ok && js > 0 && derive_any<PP, SX, WIN, CL, HALF, RUN>(p, item0, load_raw<SX, DEP>(p, item0), fin, sched)) {
+        const bool valid = rtok < fin.ntok[x], whole = sched[0].z == 1;
+        const int64_t at = (int64_t)blockIdx.x * (2 * BM) + x * BM + r;
+        const int64_t qrow = (int64_t)(fin.row0 + fin.i0 + x * TOK + rtok) * p.num_q_heads + fin.g * G + rhead;
+        const float f = p.out_scale / l_fin;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(orow + c * 32, o);
+          tmem_wait_ld();
+          if (!valid) continue;
+          if (whole) {  // the item's only run
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + qrow * HD + c * 32);
+            uint32_t w[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              w[q] = pack2<AT == DT_BF16>(__uint_as_float(o[2 * q]) * f, __uint_as_float(o[2 * q + 1]) * f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          } else {  // a part: unnormalised
+#pragma unroll
+            for (int q = 0; q < 4; ++q) st_global_v8(p.run_o + at * HD + c * 32 + 8 * q, &o[8 * q]);
+          }
+        }
+        if (valid && whole && p.lse_out) p.lse_out[qrow] = (m_fin + log2f(l_fin)) * kLn2f;
+        if (valid && !whole) p.run_ml[at] = make_float2(m_fin, l_fin);
+      }
+    }
     if constexpr (CL) {
       // the item once more, whether or not the CTA has a key tile of it (kept
       // through the key loop it would take the registers of that loop)
       SplitItem fin;
-      derive_any<PP, SX, WIN, CL, HALF>(p, item0, load_raw<SX, DEP>(p, item0), fin);
+      derive_any<PP, SX, WIN, CL, HALF, RUN>(p, item0, load_raw<SX, DEP>(p, item0), fin, sched);
       // every CTA of the cluster is done with its rings: the rows go to the CTA
       // that combines them, unnormalised, with their (max, sum)
       cluster_sync();
@@ -1419,8 +1544,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           if (blk < 0) break;
           nxt = item_of(blk);
           raw = load_raw<SX, DEP>(p, nxt);
-          typename ItemOf<WIN, CL>::T it;
-          more = nxt >= p.num_items || !derive_any<PP, SX, WIN, CL, HALF>(p, nxt, raw, it);
+          typename ItemOf<WIN, SPK>::T it;
+          more = nxt >= p.num_items || !derive_any<PP, SX, WIN, CL, HALF, RUN>(p, nxt, raw, it, sched);
         }
         if (use > 0 && !mbar_wait(sbar(C::B_ITAKEN + slot), (use - 1) & 1)) ok = false;
         if (ok) {
@@ -1437,8 +1562,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = DYN ? (is_k ? ask_item(nxt_raw) : next_item(nxt_raw)) : item0; ok && item < p.num_items; item = DYN ? (is_k ? ask_item(nxt_raw) : next_item(nxt_raw)) : item + stride) {
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
-        typename ItemOf<WIN, CL>::T it;
-        if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
+        typename ItemOf<WIN, SPK>::T it;
+        if (!derive_any<PP, SX, WIN, CL, HALF, RUN>(p, item, raw, it, sched)) continue;
         if (is_k && !load_q(it, j, 0)) { ok = false; break; }
         SegIter si;
         seg_begin<SX>(p, it, si);
@@ -1448,7 +1573,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         auto fetch = [&](int wi) -> int {
           const int st16 = wi * 32 + lane;  // sub-tile = 16 keys
           int key0 = sk_lo + st16 * 16;
-          if constexpr (WIN || CL) key0 = tile_key<WIN, CL>(it, st16 >> 3) + (st16 & 7) * 16;
+          if constexpr (WIN || SPK) key0 = tile_key<WIN, SPK>(it, st16 >> 3) + (st16 & 7) * 16;
           bool read = key0 < sk_hi;
           if constexpr (WIN) read = read && !unseen(it, key0, 16);
           int page = -1;
@@ -1493,7 +1618,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           if constexpr (C::MX) {
             const int q = lane / C::MXUNITS & 7;
             mx_page = __shfl_sync(0xFFFFFFFFu, cur, (st & 3) * 8 + q);
-            const int rip = ((WIN || CL ? tile_key<WIN, CL>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
+            const int rip = ((WIN || SPK ? tile_key<WIN, SPK>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
             mx_src = (is_k ? p.k_mx : p.v_mx) +
                      (((int64_t)max(mx_page, 0) << p.bs_shift) + rip) * (HD / kMxGroup) + lane % C::MXUNITS * 16;
             mx_dst = (q >> 1) * C::MXWARP + C::MXSCALES + lane % (2 * C::MXUNITS) * 16;
@@ -1510,7 +1635,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               mbar_arrive_expect_tx(fb, BN * C::MXROW);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const int rip = ((WIN || CL ? tile_key<WIN, CL>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
+                const int rip = ((WIN || SPK ? tile_key<WIN, SPK>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
                 tma_load_3d(slot + (q >> 1) * C::MXWARP + (q & 1) * 16 * C::MXROW, map, fb, 0, rip, pg[q]);
               }
             }
@@ -1522,7 +1647,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               mbar_arrive_expect_tx(fb, C::T8);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const int rip = ((WIN || CL ? tile_key<WIN, CL>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
+                const int rip = ((WIN || SPK ? tile_key<WIN, SPK>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
                 tma_load_3d(dst + q * 16 * HD, map, fb, 0, rip, pg[q]);
               }
             } else {
@@ -1530,7 +1655,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               mbar_arrive_expect_tx(fb, C::T16);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const int rip = ((WIN || CL ? tile_key<WIN, CL>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
+                const int rip = ((WIN || SPK ? tile_key<WIN, SPK>(it, kt) : sk_lo + st * BN) + 16 * q) & ((1 << p.bs_shift) - 1);
 #pragma unroll
                 for (int c = 0; c < C::NCH; ++c)
                   tma_load_3d(dst + c * CHUNK + q * 2048, map, fb, c * 64, rip, pg[q]);
@@ -1571,8 +1696,15 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
-        typename ItemOf<WIN, CL>::T it;
-        if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
+        typename ItemOf<WIN, SPK>::T it;
+        if (!derive_any<PP, SX, WIN, CL, HALF, RUN>(p, item, raw, it, sched)) continue;
+        if constexpr (RUN) {
+          // what the sum of the parts has to know
+          if (lane == 0) {
+            p.run_of[2 * blockIdx.x] = make_int4(sched[0].z, sched[0].y, it.g, 0);
+            p.run_of[2 * blockIdx.x + 1] = make_int4(it.row0 + it.i0, it.ntok[0], it.ntok[1], 0);
+          }
+        }
         const uint32_t stg = s_base + C::OFF_Q + ((2 * js + 1) % NQB) * C::T16;
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
@@ -1592,6 +1724,9 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           if (lane == 0) mbar_arrive(bar(C::B_EFREE + x));
         }
         ++js;
+      }
+      if constexpr (RUN) {
+        if (js == 0 && lane == 0) p.run_of[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
       }
       // the stores complete before the CTA exits
       if (lane == 0) bulk_wait_all();
@@ -1653,8 +1788,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
-        typename ItemOf<WIN, CL>::T it;
-        if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
+        typename ItemOf<WIN, SPK>::T it;
+        if (!derive_any<PP, SX, WIN, CL, HALF, RUN>(p, item, raw, it, sched)) continue;
         const int qa = (2 * j) % NQB, qb = (2 * j + 1) % NQB;
         for (int kt = 0; kt < it.T; ++kt, ++n) {
           if constexpr (C::FP8 && HD == 128) {
@@ -1750,8 +1885,8 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int item = DYN ? next_item(nxt_raw) : item0; ok && item < p.num_items; item = DYN ? next_item(nxt_raw) : item + stride) {
         const ItemRaw raw = nxt_raw;
         if constexpr (!DYN) nxt_raw = load_raw<SX, DEP>(p, item + stride);
-        typename ItemOf<WIN, CL>::T it;
-        if (!derive_any<PP, SX, WIN, CL, HALF>(p, item, raw, it)) continue;
+        typename ItemOf<WIN, SPK>::T it;
+        if (!derive_any<PP, SX, WIN, CL, HALF, RUN>(p, item, raw, it, sched)) continue;
         SegIter si;
         seg_begin<SX>(p, it, si);
         for (int kt = 0; kt < it.T; ++kt, ++n, seg_advance<SX>(p, it, si)) {
@@ -1779,7 +1914,7 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           // keys at or past the segment's end are zeroed (a shared prefix's
           // last tile reaches into one member's own keys, which no row of the
           // segment sees; WIN: the item's end, later tokens being other items')
-          const int kbase = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, CL>(it, kt);
+          const int kbase = SX ? si.sg.k_lo + si.st * BN : tile_key<WIN, SPK>(it, kt);
           const int kv_end = SX ? si.sg.kv_total : WIN ? it.k_hi : it.kv_total;
           // WIN: keys between the sinks and the first row's window too
           bool zero = kbase + t >= kv_end, hole = false;
@@ -1855,6 +1990,7 @@ cudaError_t launch_extend_t(const CUtensorMap& kmap, const CUtensorMap& vmap, co
   auto k = extend_kernel<HD, CT, AT, PP, SX, WIN, BSC, false, TAKE, false>;
   using C = ExtCfg<HD, CT, AT>;
   constexpr bool DYN = TAKE != 0;
+  static_assert(TAKE < 3, "runs are launched with their merge");
   constexpr int smem = DYN ? C::SMEM_DYN : BSC ? C::SMEM_BSC : C::SMEM;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

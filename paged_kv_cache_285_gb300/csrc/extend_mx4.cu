@@ -11,6 +11,7 @@ cudaError_t launch_extend_mx4(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (p.num_items <= 0 || p.num_ctas <= 0 || p.tok != BM / p.group || p.window < 0 || p.sink_tokens < 0 ||
       !p.k_mx || !p.v_mx || p.k_scales)
     return cudaErrorInvalidValue;
+  if (p.runs > 0) return launch_extend_mx4_runs(kmap, vmap, qmap, omap, p, head_dim, act_dt, stream);
   if (p.half) return launch_extend_mx4_half(kmap, vmap, qmap, omap, p, head_dim, act_dt, stream);
   if (p.splits > 1) return launch_extend_mx4_split(kmap, vmap, qmap, omap, p, head_dim, act_dt, stream);
   if (p.by_rows) return launch_extend_mx4_by_rows(kmap, vmap, qmap, omap, p, head_dim, act_dt, stream);

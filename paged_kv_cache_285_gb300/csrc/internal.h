@@ -305,7 +305,17 @@ struct ExtendParams {
   FastDiv div_rows;     // by 2 tok
   const uint8_t* k_mx;  // launches over e2m1 codes: their microscales
   const uint8_t* v_mx;
+  // launches in runs of key tiles: CTAs per kv head (at least batch x pairs of row
+  // tiles), and per CTA the part's rows [256][head_dim], their (max, sum) [256] and two records
+  // (parts of its item, part, head, -) and (first row, tokens of tile A, of tile B, -)
+  int runs;
+  float* run_o;
+  float2* run_ml;
+  int4* run_of;
 };
+
+// CTAs of a launch in runs of key tiles, at most (one per SM).
+constexpr int kMaxRuns = 152;
 
 // Partial output of the extend kernel's prefix pass: row q (request b, head h:
 // q = b * num_q_heads + h) over key chunk c writes O / l to
@@ -397,6 +407,9 @@ cudaError_t launch_extend_mx4(const CUtensorMap& kmap, const CUtensorMap& vmap,
 cudaError_t launch_extend_mx4_split(const CUtensorMap& kmap, const CUtensorMap& vmap,
                               const CUtensorMap& qmap, const CUtensorMap& omap,
                                     const ExtendParams& p, int head_dim, int act_dt, cudaStream_t stream);
+cudaError_t launch_extend_mx4_runs(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                   const CUtensorMap& qmap, const CUtensorMap& omap,
+                                   const ExtendParams& p, int head_dim, int act_dt, cudaStream_t stream);
 cudaError_t launch_extend_mx4_half(const CUtensorMap& kmap, const CUtensorMap& vmap,
                               const CUtensorMap& qmap, const CUtensorMap& omap,
                                    const ExtendParams& p, int head_dim, int act_dt, cudaStream_t stream);
