@@ -68,16 +68,15 @@
 //     2^ref, near the tile's largest V scale, multiplied back in fp32 at the end.
 //     A tile is a quarter of a 16-bit one and the arithmetic the same, so the kernel is
 //     bound by instructions (57 % of the ALU pipe's cycles and 58 % of the issue slots
-//     with two tiles a turn, memory 67 % of the copy's rate) and everything in it saves
+//     with two tiles a turn, memory 74 % of the copy's rate) and everything in it saves
 //     those: V's codes are merged by nibbles into the operands of two products (a token
 //     of each in one byte, where a convert per nibble needed a permute each); scales are
 //     unpacked by one lane per token and passed through shared memory; the running
 //     maximum is looked at by a vote and reduced only when a score exceeds it by 8; NaN
 //     scales, a growing ref and scales below f16's range share one rare path.  Lanes
 //     copy 16 bytes each (cp.async): one lane issuing TMA copies of 1 KB was the longest
-//     chain of a turn (128 requests in a window of 4,096: 164 us; 113 now, 5.0 TB/s;
-//     copies alone 90, arithmetic alone 101).  64 requests of 512-4,096 tokens 40.6 us,
-//     3 of up to 700 3.8.
+//     chain of a turn (128 requests in a window of 4,096: 164 us; 110 now, 5.2 TB/s;
+//     copies alone 90).  64 requests of 512-4,096 tokens 39.9 us, 3 of up to 700 3.8.
 //     Not kept, on the window: masks by a multiply of f16 pairs instead of a permute
 //     (123 against 114), five CTAs an SM by spilling (131), three stages or L2 prefetches
 //     (no change), K and V in copy groups of their own (117 against 114), rolled loops
@@ -259,7 +258,10 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // split is the slowest grid dimension: every request's first chunk runs
   // before any second chunk, so the partial and empty last splits form the tail
   const int b = blockIdx.y, split = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (MX: the warp's number through a shuffle, from which the compiler knows that it is
+  // the same in all lanes and keeps what depends on it in uniform registers: 114 -> 110 us)
+  const int warp = MX ? __shfl_sync(kFull, (int)(threadIdx.x >> 5), 0) : (int)(threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = p.group;
   // kv head g, chunk hc of its query heads: heads hb .. hb + GC - 1
