@@ -250,6 +250,7 @@ struct CompactParams {
   int heads;             // kv heads that a CTA takes
   int head_groups;       // ceil(num_kv_heads / heads)
   int cluster_shift;     // log2(CTAs per item)
+  int by_length;         // the requests with most rows first (up to 32 requests)
   FastDiv div_heads;
   FastDiv div_groups;
   FastDiv div_pools;

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_
 // loads are under way its threads look up the next pass's rows, so that there is
 // one barrier a pass.  32 layers x 8 requests of 4,000 of 8,000 tokens (8 heads x
 // 128 dims, bf16, 8.4 GB): 1.27 ms, 97 % of the measured copy; 8 layers x 6 of 4,000
-// to 16,000 (fp8, 1.8 GB) 306 us, 87 %, since the longest requests' CTAs end last;
+// to 16,000 (fp8, 1.8 GB) 295 us, 90 %, since the longest requests' CTAs end last;
 // one layer of one request, 16,000 tokens, 52 us (clusters of 8; 235 without).
 // Loads of the next pass ahead of a pass's stores took registers from CTAs (306 ->
 // 444 us), eight vectors a thread too (332), pointers kept from load to store 317.
@@ -190,6 +190,21 @@ __device__ __forceinline__ void compact_rows(const CompactParams& p, const Pool&
   }
 }
 
+// The request with the rank-th most rows, of up to 32 (the whole warp): a request's CTAs
+// take the longer the more rows it has, and those that start last should be short.
+// (A count that wraps, of an invalid row_indptr, still gives each its rank.)
+__device__ __forceinline__ uint32_t by_length(const CompactParams& p, int rank) {
+  const int lane = threadIdx.x & 31;
+  uint32_t n = 0u;
+  if (lane < p.batch) n = (uint32_t)*(p.row_indptr + lane + 1) - (uint32_t)*(p.row_indptr + lane);
+  int above = 0;
+  for (int l = 0; l < p.batch; ++l) {
+    const uint32_t other = __shfl_sync(0xFFFFFFFFu, n, l);
+    above += other > n || (other == n && l < lane);
+  }
+  return (uint32_t)(__ffs(__ballot_sync(0xFFFFFFFFu, lane < p.batch && above == rank)) - 1);
+}
+
 template <bool CL, int NT>
 __global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ CompactParams p) {
   __shared__ RowMove s_row[3][NT];
@@ -197,8 +212,9 @@ __global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ Com
   const uint32_t item = CL ? blockIdx.x >> p.cluster_shift : blockIdx.x;
   const uint32_t rest = p.div_groups.div(item);
   const int hg = (int)(item - rest * p.div_groups.d);
-  const uint32_t b = p.div_pools.div(rest);
+  uint32_t b = p.div_pools.div(rest);
   const int k = (int)(rest - b * p.div_pools.d);
+  if (!CL && p.by_length) b = by_length(p, (int)b);
   const bool report = k == 0 && hg == 0;
   const int r0 = *(p.row_indptr + b), r1 = *(p.row_indptr + b + 1), dst0 = *(p.dst_starts + b);
   if (r0 == r1) return;  // (the same for every CTA of a cluster, as the returns below)
@@ -239,6 +255,9 @@ cudaError_t launch_compact_t(CompactParams& p, int vpr, int sm_count, cudaStream
   while (shift < 3 && (items << shift) < sm_count && passes > (1 << shift)) ++shift;
   p.cluster_shift = shift;
   const int64_t ctas = items << shift;
+  // longest requests first where CTAs start in several rounds (8 layers x 6 requests of
+  // 4,000 to 16,000 tokens: 309 -> 295 us; one round of equal ones lost 1 us of 32)
+  p.by_length = p.batch > 1 && p.batch <= 32 && passes > 1 && items > (int64_t)sm_count * (1024 / NT) ? 1 : 0;
   if (ctas <= 0 || ctas > INT32_MAX) return cudaErrorInvalidValue;
   return shift > 0 ? launch_dependent(compact_kernel<true, NT>, (unsigned)ctas, NT, stream, p, 1u << shift)
                    : launch_dependent(compact_kernel<false, NT>, (unsigned)ctas, NT, stream, p);

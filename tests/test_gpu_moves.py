@@ -110,6 +110,9 @@ COMPACTS = [
     (TOKENS * 27, 2, 16, 64, [3, 9], [20, 33], 2),                # more pools than a launch takes
     (["bf16", "mx"], 40, 16, 128, [3], [50], 2),                  # two heads a CTA
     (["bf16"] * 4, 150, 16, 128, [3, 0], [9, 1], 2),              # 14 heads a CTA, the last one fewer
+    (["bf16"] * 12, 8, 16, 128, [0, 9, 3, 0, 1], [40, 900, 0, 500, 700], 1.5),  # rounds of CTAs, the longest first
+    (["bf16"] * 4, 8, 16, 64, [0] * 32, [70, 20] * 15 + [300, 300], 1.5),
+    (["fp8"] * 4, 8, 32, 128, [0, 1, 2] * 11, [300] + [70, 1] * 16, 1.5),       # ... and more requests than are ranked
 ]
 
 
