@@ -69,8 +69,10 @@ def test_attention_refusals(lib):
     assert decode(most=-1) == 1 and decode(q=None) == 1
     assert decode(most=10000, splits=2) in (3, 4)
     assert extend(rows=0) == 0 and extend(hq=2 * 129) == 2
-    need = lib.pkv_extend_mx4_workspace_bytes(ctypes.byref(mx4()))
-    assert need == 2 * 8 * 2 * 16 * 128 * 2 + 256
+    # the larger of the pools' 16-bit copies with their claims, and 152 parts of 256 rows (fp32, maximum and sum)
+    need = lambda blocks: lib.pkv_extend_mx4_workspace_bytes(ctypes.byref(mx4(num_blocks=blocks)))  # noqa: E731
+    assert need(8) == 152 * (256 * (128 * 4 + 8) + 32)
+    assert need(8192) == 2 * 8192 * 2 * 16 * 128 * 2 + 256 * 257
     assert lib.pkv_extend_mx4_workspace_bytes(ctypes.byref(_desc())) == 0
     assert lib.pkv_decode_mx4_workspace_bytes(ctypes.byref(_desc()), 2, 8, 1000, 0, 0, 4) == 0
     f = lib.pkv_decode_mx4_workspace_bytes
