@@ -92,6 +92,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_
 // 128 dims, bf16, 8.4 GB): 1.27 ms, 97 % of the measured copy; 8 layers x 6 of 4,000
 // to 16,000 (fp8, 1.8 GB) 295 us, 90 %, since the longest requests' CTAs end last;
 // one layer of one request, 16,000 tokens, 52 us (clusters of 8; 235 without).
+// A launch whose requests all pass at once (ONE) keeps no state for passes: 34 registers
+// and six CTAs of 256 an SM; 1 to 6 rows of 16 requests in 64 pools 5.3 -> 4.6 us.
 // Loads of the next pass ahead of a pass's stores took registers from CTAs (306 ->
 // 444 us), eight vectors a thread too (332), pointers kept from load to store 317.
 constexpr int kMoveUnroll = 4;
@@ -134,7 +136,7 @@ template <> struct MoveVec<8> { using T = uint2; };
 template <> struct MoveVec<4> { using T = uint32_t; };
 template <> struct MoveVec<2> { using T = uint16_t; };
 
-template <int VEC, bool CL, int NT>
+template <int VEC, bool CL, int NT, bool ONE>
 __device__ __forceinline__ void compact_rows(const CompactParams& p, const Pool& pool, int b, int r0,
                                              int n, int dst0, int h0, int heads, bool report,
                                              RowMove (*s_row)[NT]) {
@@ -172,6 +174,25 @@ __device__ __forceinline__ void compact_rows(const CompactParams& p, const Pool&
   };
   look_up(0);
   __syncthreads();
+  if constexpr (ONE) {  // the longest request passes at once
+    T x[kMoveUnroll];
+    T* to[kMoveUnroll];
+#pragma unroll
+    for (int e = 0; e < kMoveUnroll; ++e) {
+      RowMove m;
+      int h, c;
+      to[e] = nullptr;
+      if (place(e * NT + (int)threadIdx.x, 0, m, h, c)) {
+        x[e] = *address(m.src_blk, m.off & 255, h, c);
+        to[e] = address(m.dst_blk, m.off >> 8, h, c);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kMoveUnroll; ++e)
+      if (to[e]) *to[e] = x[e];
+    return;
+  }
   for (int pass = 0; pass < passes; ++pass) {
     T x[kMoveUnroll];
     RowMove m;
@@ -205,9 +226,9 @@ __device__ __forceinline__ uint32_t by_length(const CompactParams& p, int rank) 
   return (uint32_t)(__ffs(__ballot_sync(0xFFFFFFFFu, lane < p.batch && above == rank)) - 1);
 }
 
-template <bool CL, int NT>
-__global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ RowMove s_row[3][NT];
+template <bool CL, int NT, bool ONE>
+__global__ void __launch_bounds__(NT, ONE ? 6 : 0) compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ RowMove s_row[ONE ? 1 : 3][NT];
   grid_dependency_wait();
   const uint32_t item = CL ? blockIdx.x >> p.cluster_shift : blockIdx.x;
   const uint32_t rest = p.div_groups.div(item);
@@ -230,10 +251,10 @@ __global__ void __launch_bounds__(NT) compact_kernel(const __grid_constant__ Com
   const int h0 = hg * p.heads, heads = min(p.heads, p.num_kv_heads - h0);
   const Pool& pool = p.pool[k];
   const uint64_t a = reinterpret_cast<uint64_t>(pool.base) | pool.row_bytes;
-  if ((a & 15) == 0) compact_rows<16, CL, NT>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
-  else if ((a & 7) == 0) compact_rows<8, CL, NT>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
-  else if ((a & 3) == 0) compact_rows<4, CL, NT>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
-  else compact_rows<2, CL, NT>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+  if ((a & 15) == 0) compact_rows<16, CL, NT, ONE>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+  else if ((a & 7) == 0) compact_rows<8, CL, NT, ONE>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+  else if ((a & 3) == 0) compact_rows<4, CL, NT, ONE>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
+  else compact_rows<2, CL, NT, ONE>(p, pool, b, r0, n, dst0, h0, heads, report, s_row);
 }
 
 template <int NT>
@@ -259,8 +280,12 @@ cudaError_t launch_compact_t(CompactParams& p, int vpr, int sm_count, cudaStream
   // 4,000 to 16,000 tokens: 309 -> 295 us; one round of equal ones lost 1 us of 32)
   p.by_length = p.batch > 1 && p.batch <= 32 && passes > 1 && items > (int64_t)sm_count * (1024 / NT) ? 1 : 0;
   if (ctas <= 0 || ctas > INT32_MAX) return cudaErrorInvalidValue;
-  return shift > 0 ? launch_dependent(compact_kernel<true, NT>, (unsigned)ctas, NT, stream, p, 1u << shift)
-                   : launch_dependent(compact_kernel<false, NT>, (unsigned)ctas, NT, stream, p);
+  if constexpr (NT == 256) {
+    // (its rows found by a thread each)
+    if (passes <= 1 && p.max_rows <= NT) return launch_dependent(compact_kernel<false, NT, true>, (unsigned)ctas, NT, stream, p);
+  }
+  return shift > 0 ? launch_dependent(compact_kernel<true, NT, false>, (unsigned)ctas, NT, stream, p, 1u << shift)
+                   : launch_dependent(compact_kernel<false, NT, false>, (unsigned)ctas, NT, stream, p);
 }
 
 }  // namespace
