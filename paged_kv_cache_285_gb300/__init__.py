@@ -971,6 +971,11 @@ class KvPools:
     def __init__(self, pools):
         self.tensors = tuple(pools)
         self._count, self._index = len(self.tensors), -1
+        if _direct is not None:
+            got = _direct.pools(self.tensors)
+            if got is not None:
+                self._array, self._at, self._index = got
+                return
         rows = []
         for i, t in enumerate(self.tensors):
             if not isinstance(t, torch.Tensor) or t.dim() < 2:

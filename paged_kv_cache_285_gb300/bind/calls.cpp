@@ -17,7 +17,10 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <utility>
+#include <vector>
 
 #include "pkv.h"
 
@@ -252,6 +255,45 @@ PyObject* gather_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// tuple of pools -> (bytes of their pkv_pool structs, the bytes' address, device), or
+// None (64 pools: 120 us when read from Python).
+PyObject* pools(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 1 || !PyTuple_CheckExact(a[0])) Py_RETURN_NONE;
+  const Py_ssize_t count = PyTuple_GET_SIZE(a[0]);
+  try {
+    std::vector<pkv_pool> got((size_t)count);
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans((size_t)count);
+    int device = -1;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      const at::Tensor& t = tensor(PyTuple_GET_ITEM(a[0], i));
+      if (t.layout() != at::kStrided || t.dim() < 2 || !t.is_cuda() || !t.is_contiguous()) throw Unplain();
+      if (i == 0) device = t.get_device();
+      int64_t row = (int64_t)t.element_size();
+      for (int64_t d = 3; d < t.dim(); ++d) row = i32(row * i32(t.size(d)));
+      pkv_pool& q = got[(size_t)i];
+      q.base = t.data_ptr();
+      q.num_blocks = i32(t.size(0));
+      q.num_kv_heads = i32(t.size(1));
+      q.block_size = t.dim() > 2 ? i32(t.size(2)) : 1;
+      q.row_bytes = i32(row);
+      if (t.get_device() != device || q.num_blocks != got[0].num_blocks || q.num_blocks <= 0 ||
+          q.num_kv_heads <= 0 || q.block_size <= 0 || q.row_bytes <= 0)
+        throw Unplain();
+      spans[(size_t)i] = {(uintptr_t)q.base, (uintptr_t)q.base + (uintptr_t)t.nbytes()};
+    }
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+      if (spans[i - 1].second > spans[i].first) throw Unplain();
+    PyObject* bytes = PyBytes_FromStringAndSize(reinterpret_cast<const char*>(got.data()),
+                                                (Py_ssize_t)(got.size() * sizeof(pkv_pool)));
+    if (!bytes) return nullptr;
+    return Py_BuildValue("(NNi)", bytes, PyLong_FromVoidPtr(PyBytes_AS_STRING(bytes)), device);
+  } catch (...) {  // what the Python way refuses by name, or converts
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+}
+
 // The pools of a KvPools: the address and number of its pkv_pool structs.
 struct PoolSet {
   const pkv_pool* at;
@@ -417,6 +459,7 @@ PyMethodDef methods[] = {FN("append_block_scaled", append_block_scaled),
                          FN("gather_mx4", gather_mx4),
                          FN("decode_mx4", decode<MX4>),
                          FN("extend_mx4", extend<MX4>),
+                         FN("pools", pools),
                          FN("copy_blocks", copy_blocks),
                          FN("compact", compact),
                          {nullptr, nullptr, 0, nullptr}};

@@ -73,6 +73,28 @@ def test_pools_that_overlap_are_refused():
     pkv.KvPools([t[4:], t[:4]])
 
 
+def test_pools_read_by_the_compiled_and_the_python_way():
+    class Named(torch.Tensor):
+        pass
+
+    pools = pools_of(ALL, 9, 3, 32, 64, seed=1) + [torch.zeros((9, 3), device="cuda").as_subclass(Named)]
+    direct, got = pkv._direct, []
+    assert direct is not None and direct.pools(tuple(pools)) is None and direct.pools(tuple(pools[:6])) is not None
+    try:
+        for way in (direct, None):
+            pkv._direct = way
+            p = pkv.KvPools(pools[:6])
+            got.append((bytes(p._array), p._count, p._index))
+        assert got[0] == got[1] and pkv.KvPools([])._count == 0
+    finally:
+        pkv._direct = direct
+    assert pkv.KvPools(pools)._count == 7
+    for bad in (pools[:1] + [pools[1][:5]], pools[:1] + [pools[1].cpu()], pools[:1] + [None], [pools[1][:, :2]], [pools[1][:0]]):
+        assert direct.pools(tuple(bad)) is None
+        with pytest.raises((ValueError, TypeError)):
+            pkv.KvPools(bad)
+
+
 def test_copy_blocks_reports():
     pools = pools_of(["bf16", "mx"], 12, 2, 16, 64, seed=1)
     before = [raw(t) for t in pools]
