@@ -987,7 +987,10 @@ extend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const uint32_t s_base = smem_u32(smem);
   auto bar = [&](int i) -> uint32_t { return smem_u32(&bars[i]); };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (through a shuffle: the compiler then knows the warp's number to be the same in all
+  // its lanes and keeps what depends on it in uniform registers; 256 suffixes of 100
+  // rows over 1,900 shared tokens 784 -> 742 us)
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int G = p.group;
   const int TOK = p.tok;
   // CL: one item per cluster, the first pair of tiles of every (request, head)
