@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(128) append_scaled_kernel(const AppendScaledPa
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   PageTask t;
-  if (!find_page_task<BS>(p, blockIdx.x * 4u + __shfl_sync(kFull, threadIdx.x >> 5, 0), t)) return;
+  if (!find_page_task<BS>(p, blockIdx.x * 4u + (threadIdx.x >> 5), t)) return;
   const bool isv = t.isv;
   const int h = t.h, blk = t.blk, start = t.start, end = t.end;
   const uint16_t* src = reinterpret_cast<const uint16_t*>(isv ? p.v_new : p.k_new) + h * HD;
