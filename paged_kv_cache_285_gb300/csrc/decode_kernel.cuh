@@ -78,7 +78,7 @@
 //     chain of a turn (128 requests in a window of 4,096: 164 us; 110 now, 5.2 TB/s;
 //     copies alone 90).  64 requests of 512-4,096 tokens 39.9 us, 3 of up to 700 3.8.
 //     Not kept, on the window: masks by a multiply of f16 pairs instead of a permute
-//     (123 against 114), five CTAs an SM by spilling (131), three stages or L2 prefetches
+//     (123 against 114), five CTAs an SM at 96 registers (112 against 110), three stages or L2 prefetches
 //     (no change), K and V in copy groups of their own (117 against 114), rolled loops
 //     over the two tiles (125).
 //   * warps are combined through shared memory with their (max, sum); a split
