@@ -681,7 +681,10 @@ static int visible_bound(int max_seq_len, int window, int sink_tokens) {
 // so that an SM reads at less than its share of the bandwidth (236 tokens per us at
 // 128 dims, 416 at 64, a CTA alone 140 and 205); falling splits pay from 2,500
 // tokens on (24 x 2,048 23.4 -> 29.0 us with them, 32 of 100-1,500 21.0 -> 25.1; 20 of
-// 500-8,192 43.0 -> 34.8, 64 of 512-4,096 44.3 -> 40.9).
+// 500-8,192 43.0 -> 34.8, 64 of 512-4,096 44.3 -> 40.9).  In a window, whose sequences
+// are of one length, two splits, the second 0.4 of the first, from 3,500 tokens on (a
+// window of 4,096, 8 kv heads: 40 requests 55.6 -> 50.7, 90 101 -> 97; of 8,192: 64 127 ->
+// 121, 90 166 -> 158; but 32 of 4,096 45 -> 50, 128 of 4,096 109.8 -> 113.7).
 static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_seq_len, int window,
                             int sink_tokens, int forced, int sm_count) {
   // (so far below 2^31 that whole splits stay below it too)
@@ -733,11 +736,13 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   }
   // splits of falling length: see above
   const double fill = items / slots;
-  const bool falling = window > 0 ? fill <= 1.5 && 2.0 * len * d->head_dim * value_bytes(d->cache_dtype) >= 0.9e6
+  const bool two = mx4 && window > 0;
+  const bool falling = two          ? fill >= 0.5 && fill <= 1.5 && len >= 3500
+                       : window > 0 ? fill <= 1.5 && 2.0 * len * d->head_dim * value_bytes(d->cache_dtype) >= 0.9e6
                                   : len >= (mx4 ? 2500 : 1000) && fill <= len / 800.0;
   if (fill >= 0.25 && falling) {
-    const double ratio = std::min(0.78, std::max(0.45, 0.45 + 0.75 * (0.75 - fill)));
-    int k = kMaxCuts;
+    const double ratio = two ? 0.4 : std::min(0.78, std::max(0.45, 0.45 + 0.75 * (0.75 - fill)));
+    int k = two ? 2 : kMaxCuts;
     double first = 0;
     for (; k > 1; --k) {  // the last one of 192 tokens at least
       first = len * (1 - ratio) / (1 - std::pow(ratio, k));

@@ -7,6 +7,7 @@ import torch
 import paged_kv_cache_285_gb300 as pkv
 from oracle import block_scaled_ref as R
 from oracle import mx4_ref as M
+from tests import paths_testlib as P
 from tests.mx4_testlib import Mx4Case, decode_ref, extend_ref, indptr, run_decode, run_extend
 from tests.pkv_testlib import BF16, F16, to_f64
 from tests.scaled_testlib import TDT, check_attention, ints
@@ -163,7 +164,7 @@ def test_decode(cfg, splits, window, sinks):
 
 
 MANY = [
-    # batch, hq, hkv, d, bs, act, most: enough CTAs for splits of falling length
+    # batch, hq, hkv, d, bs, act, most: splits of one length, joined by a second launch or not at all
     (28, 8, 8, 64, 16, BF16, 1100),
     (80, 16, 8, 128, 32, F16, 1000),
     (40, 18, 2, 64, 16, F16, 1500),
@@ -191,6 +192,28 @@ def test_decode_of_many_requests(cfg):
     ref = [r[kept] if isinstance(r, np.ndarray) else {k: v[kept] for k, v in r.items()} for r in ref]
     check_attention(again[kept], lse[kept], ref, act, d, f"{cfg} hint")
     assert pkv.get_device_error() == 3 and bool(torch.isfinite(again).all())
+
+
+@pytest.mark.parametrize("act,hq,hkv,d,bs,longest,window,sinks", [
+    (BF16, 4, 2, 128, 16, 2600, 0, 0), (F16, 32, 4, 64, 32, 3100, 0, 0),
+    (BF16, 4, 4, 128, 16, 4800, 3600, 33), (F16, 24, 8, 64, 32, 6000, 5000, 0), (BF16, 80, 1, 64, 16, 4500, 3600, 20)])
+def test_decode_in_splits_of_falling_length(act, hq, hkv, d, bs, longest, window, sinks):
+    # most requests short, some at, before and behind the ends of the splits
+    batch, rng = 80, np.random.default_rng(longest)
+    seen = min(longest, window + sinks) if window else longest
+    long = [longest, longest - 1, longest - 16, 16 * (seen // 32), 16 * (seen // 64) + 1] + \
+        [16 * int(seen * x / 16) + y for x in (0.3, 0.714, 0.715) for y in (-1, 0, 1, 16)]
+    lens = [int(n) for n in rng.permutation(long + [0, 1] + list(rng.integers(0, 90, batch - len(long) - 2)))]
+    c = Mx4Case(act, hkv, d, bs, lens, seed=longest)
+    for b, n in enumerate(lens):                                # what lies behind the last token
+        if n % bs:
+            c.ks[int(c.tables[b, n // bs]), :, n % bs:], c.vs[int(c.tables[b, n // bs]), :, n % bs:] = 255, 255
+    c.cuda()
+    q = c.rows(batch, hq).cuda()
+    (out, lse), ran = P.profiled(lambda: run_decode(c, q, hq, lens, window, sinks))
+    ref = P.attention(*c.values(), to_f64(q), range(batch + 1), [n - 1 for n in lens], c.tables, hq, 1 / d ** 0.5, window, sinks)
+    check_attention(out, lse, ref, act, d)
+    assert pkv.get_device_error() == 0 and (ran is None or len(ran["merge_kernel"]) == 1), ran
 
 
 @pytest.mark.parametrize("batch,hq,hkv,d,bs,act,most", [(90, 16, 8, 128, 16, BF16, 130), (80, 8, 8, 64, 32, F16, 400),
