@@ -678,7 +678,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // usual case and need no borrow; else, and for a NaN, byte by byte.  (What passes
         // 0 .. 22 shows in the sum's upper bits, unless it comes round to 0 .. 22 again:
         // a byte of 241 or more over a ref of 13 or less, whose upper bits show it; ref
-        // is 248 at most, so that none comes round from below.)
+        // is 247 at most, so that a NaN's byte, 255, gives 23 or more, and none comes
+        // round from below.)
         uint32_t x4 = wv + (0x0F0F0F0Fu - refs);
         const uint32_t nan_k = ((wk & 0x7F7F7F7Fu) + 0x01010101u) & wk & 0x80808080u;
         if (__any_sync(kFull, (nan_k | ((x4 | (x4 + 0x09090909u)) & 0xE0E0E0E0u) |
@@ -696,7 +697,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
             const int top = __reduce_max_sync(kFull, e);
             if (top > ref + 7) {
-              const int up = min(top - 5, 248) - ref;
+              const int up = min(top - 5, 247) - ref;
               ref += up;
               refs += (uint32_t)up << (8 * c);
               const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
