@@ -65,7 +65,13 @@
 //     a row, so K's scale multiplies the partial product of its 32 dims
 //     (s[t] = sum_g 2^(kb[t][g]) (K_g q_g)[t], fp32) and V's, which sits on the
 //     contracted side (tokens), goes into P: O_g += V_g^T (P 2^(vb[t][g] - ref)), with
-//     2^ref, near the tile's largest V scale, multiplied back in fp32 at the end.
+//     2^ref, near the tokens' V scales, multiplied back in fp32 at the end.  Where 32
+//     tokens' scales of a group span more than 2^11, or lie below what ref takes in, that
+//     group's P 2^vb gets a reference for each head and tile, and its product is added
+//     up in fp32: a token of large V and next to no weight would take the others' bits
+//     otherwise.  (Every tile so, scales drawn from 2^-17 to 2^-2: 2.2 to 2.7 times the
+//     call's time; where it does not happen the code for it costs 0.2 us in 3.7, 0.8 in
+//     40, 0.6 in 110.)
 //     A tile is a quarter of a 16-bit one and the arithmetic the same, so the kernel is
 //     bound by instructions (57 % of the ALU pipe's cycles and 58 % of the issue slots
 //     with two tiles a turn, memory 74 % of the copy's rate) and everything in it saves
@@ -75,8 +81,8 @@
 //     maximum is looked at by a vote and reduced only when a score exceeds it by 8; NaN
 //     scales, a growing ref and scales below f16's range share one rare path.  Lanes
 //     copy 16 bytes each (cp.async): one lane issuing TMA copies of 1 KB was the longest
-//     chain of a turn (128 requests in a window of 4,096: 164 us; 110 now, 5.2 TB/s;
-//     copies alone 90).  64 requests of 512-4,096 tokens 39.9 us, 3 of up to 700 3.8.
+//     chain of a turn (128 requests in a window of 4,096: 164 us; 110.5 now, 5.1 TB/s;
+//     copies alone 90).  64 requests of 512-4,096 tokens 40.7 us, 3 of up to 700 3.9.
 //     Not kept, on the window: masks by a multiply of f16 pairs instead of a permute
 //     (123 against 114), five CTAs an SM at 96 registers (112 against 110), three stages or L2 prefetches
 //     (no change), K and V in copy groups of their own (117 against 114), rolled loops
@@ -623,11 +629,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     __syncthreads();
     // The sums of group c's dims are held relative to 2^(ref - 127), ref byte c of
-    // refs: V's scales enter as f16 factors 2^(byte - ref) of the weights, of at most
-    // 2^7 (with weights of at most 2^8 their products stay inside f16).  When a byte
-    // above ref + 7 comes, ref moves to 5 below the largest one and the sums follow.
-    // A factor below 2^-14 is 0: a token whose scale is 2^20 below the largest so far
-    // adds nothing.
+    // refs: V's scales enter as f16 factors 2^(byte - ref) of the weights, of 2^-4 (below
+    // that weights would lose bits that count where the larger scales have none) to 2^7
+    // (with weights of at most 2^8 their products stay inside f16).  When larger bytes
+    // come, ref moves to 5 (7) below the largest of them and the sums follow.  Where
+    // a pair of tiles has bytes that no ref spans, or smaller ones than ref spans, the
+    // group is added up apart (`wide`): weights times scales have a reference of
+    // their own there, per head and tile, whatever the other tokens' scales are.
     uint32_t refs = 0u;
     // the lane's rows for ldmatrix: groups 0 and 1 of K's tokens, of V's (groups 2 and
     // 3 are 32 bytes on, with the swizzle: bit 5 flipped)
@@ -663,42 +671,58 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       };
 
       // ---- the tokens' scales, unpacked for the warp: lane = token ---------------
+      uint32_t wide;  // bit c: group c is added up apart
       {
         const uint32_t at = mxstage_s + st * C::MXSTAGEB + (lane >> 4) * 2 * C::MXB + (lane & 15) * GR;
         const uint32_t wk = lds_u<GR>(at);
         uint32_t wv = lds_u<GR>(at + C::MXB);
         // what a hidden token holds does not count (K: its score is masked; V: its
         // weight is 0)
-        if (edge && (lane < 16 ? hidden(0, lane) : hidden(1, lane - 16))) wv = refs;
+        const bool off = edge && (lane < 16 ? hidden(0, lane) : hidden(1, lane - 16));
+        if (off) wv = refs;
         float fk[GR];
 #pragma unroll
         for (int c = 0; c < GR; ++c)
           fk[c] = __uint_as_float((c == 3 ? wk >> 1 : wk << (23 - 8 * c)) & 0x7F800000u) * p.scale_log2;
-        // V's factors 2^(byte - ref): their f16 exponents, 15 more, are 0 .. 22 in the
-        // usual case and need no borrow; else, and for a NaN, byte by byte.  (What passes
-        // 0 .. 22 shows in the sum's upper bits, unless it comes round to 0 .. 22 again:
-        // a byte of 241 or more over a ref of 13 or less, whose upper bits show it; ref
-        // is 247 at most, so that a NaN's byte, 255, gives 23 or more, and none comes
-        // round from below.)
-        uint32_t x4 = wv + (0x0F0F0F0Fu - refs);
+        // V's factors 2^(byte - ref), 4 more as y4, are 0 .. 11 in the usual case and
+        // need no borrow; else, and for a NaN, byte by byte.  (What passes 0 .. 11
+        // shows in the sum's upper bits, unless it comes round to 0 .. 11 again: a byte
+        // of 252 or more over a ref of 3 or less, whose upper bits show it; ref is 247 at
+        // most, so that a NaN's byte, 255, gives 12 or more, and none comes round from
+        // below.)  x4: the f16 exponents.
+        uint32_t x4 = wv + (0x04040404u - refs);
         const uint32_t nan_k = ((wk & 0x7F7F7F7Fu) + 0x01010101u) & wk & 0x80808080u;
-        if (__any_sync(kFull, (nan_k | ((x4 | (x4 + 0x09090909u)) & 0xE0E0E0E0u) |
-                               (wv & (wv << 1) & ~refs & 0x80808080u)) != 0u)) {
+        const bool rare = __any_sync(kFull, (nan_k | ((x4 | (x4 + 0x14141414u)) & 0xE0E0E0E0u) |
+                                             (wv & (wv << 1) & ~refs & 0x80808080u)) != 0u);
+        x4 += 0x0B0B0B0Bu;
+        wide = 0u;
+        if (rare) {
           x4 = 0u;
 #pragma unroll
           for (int c = 0; c < GR; ++c) {
             if ((nan_k >> (8 * c)) & 0x80u) fk[c] = __uint_as_float(0x7FC00000u);
-            int e = (int)((wv >> (8 * c)) & 0xFFu), ref = (int)((refs >> (8 * c)) & 0xFFu);
+            int e = off ? 0 : (int)((wv >> (8 * c)) & 0xFFu);
+            int ref = (int)((refs >> (8 * c)) & 0xFFu);
             if (__any_sync(kFull, e == 255)) {  // a NaN: every head's sums of these dims
 #pragma unroll
               for (int q4 = 0; q4 < 4; ++q4)
                 acc[2 * c][q4] = acc[2 * c + 1][q4] = __uint_as_float(0x7FC00000u);
               if (e == 255) e = 0;
             }
-            const int top = __reduce_max_sync(kFull, e);
-            if (top > ref + 7) {
-              const int up = min(top - 5, 247) - ref;
-              ref += up;
+            // Bytes 0 and 1 (1: the scale of 32 zeros) do not count: such a token adds
+            // nothing beside scales that leave it out, 6 2^-126 at most.
+            const int top = __reduce_max_sync(kFull, e), low = __reduce_min_sync(kFull, e > 1 ? e : 255);
+            bool apart = false;
+            if (top > ref + 7 || low < ref - 4) {
+              int to = ref;
+              if (top > ref + 7 && top - low <= 11) {
+                to = min(top - (top - low <= 9 ? 5 : 7), 247);
+              } else {  // (the sums stay below 2^128)
+                apart = true;
+                to = max(ref, top - 90);
+              }
+              const int up = to - ref;
+              ref = to;
               refs += (uint32_t)up << (8 * c);
               const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
@@ -707,7 +731,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 acc[2 * c + 1][q4] *= f;
               }
             }
-            x4 |= (uint32_t)max(e - ref + 15, 0) << (8 * c);
+            if (apart) wide |= 1u << c;
+            x4 |= (apart || e < ref - 4 ? 0u : (uint32_t)(e - ref + 15)) << (8 * c);
           }
         }
         const uint32_t y4 = __shfl_xor_sync(kFull, x4, 1);  // the other token of the pair
@@ -726,14 +751,12 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // One ldmatrix row is 32 codes of one token (a group): thread (gid, tig)
       // receives codes 8 tig .. 8 tig + 7, four for each of two steps; the group's
       // sum is scaled per token as it is added up.
-      float sc[2][4];
       const uint32_t kat = wstage_s + st * C::STAGEB + kunit;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      auto scores = [&](int x, float (&s4)[4]) {
         uint32_t ka[GR], kc[GR];
         lds_v<GR>(mxk + (16 * x + gid) * GR * 4, ka);
         lds_v<GR>(mxk + (16 * x + gid + 8) * GR * 4, kc);
-        sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
+        s4[0] = s4[1] = s4[2] = s4[3] = 0.f;
 #pragma unroll
         for (int kp = 0; kp < HD / 64; ++kp) {
           uint32_t r[4];
@@ -750,13 +773,16 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             const uint32_t a0[4] = {a[0], b2[0], a[1], b2[1]}, a1[4] = {a[2], b2[2], a[3], b2[3]};
             mma16816_f16_zero(part, a0, f[0], f[1]);
             mma16816<false>(part, a1, f[2], f[3]);
-            sc[x][0] = fmaf(part[0], __uint_as_float(ka[c]), sc[x][0]);
-            sc[x][1] = fmaf(part[1], __uint_as_float(ka[c]), sc[x][1]);
-            sc[x][2] = fmaf(part[2], __uint_as_float(kc[c]), sc[x][2]);
-            sc[x][3] = fmaf(part[3], __uint_as_float(kc[c]), sc[x][3]);
+            s4[0] = fmaf(part[0], __uint_as_float(ka[c]), s4[0]);
+            s4[1] = fmaf(part[1], __uint_as_float(ka[c]), s4[1]);
+            s4[2] = fmaf(part[2], __uint_as_float(kc[c]), s4[2]);
+            s4[3] = fmaf(part[3], __uint_as_float(kc[c]), s4[3]);
           }
         }
-      }
+      };
+      float sc[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) scores(x, sc[x]);
 
       // ---- online softmax (base 2), per head column -------------------------------
       if (edge) {
@@ -836,6 +862,70 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             mma16816<false>(acc[2 * c], a, w0[c], w1[c]);
             e2m1x8_to_f16x8(odd, a);
             mma16816<false>(acc[2 * c + 1], a, w0[c], w1[c]);
+          }
+        }
+      }
+
+      if (wide != 0u) {
+        // Groups apart: a column's weights times scales relative to the largest of the
+        // tile's (2^(top - 127), from the exponents), its product in fp32 under that.
+        // The weights are computed once more: kept for this they cost calls without
+        // such groups as much again as this code does (a window of 4,096: 111.3 us, 110.4).
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          float w4[4];
+          scores(x, w4);
+          const int tok = t0 + kSubTokens * (warp + (i + x) * NW);
+          int from = 0, sink = 0;  // rows below `from` are hidden unless below `sink`
+          if constexpr (WIN) {
+            const int at = tok + (tok >= ws.sv ? ws.skip : 0);
+            from = ws.w0 - at;
+            sink = ws.sinks - at;
+          }
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const int row = gid + (q4 >> 1) * 8;
+            w4[q4] = row >= t1 - tok || (row < from && row >= sink) ? 0.f : fast_exp2(w4[q4] - (q4 & 1 ? m_o : m_e));
+          }
+          const uint32_t vb = mxstage_s + st * C::MXSTAGEB + (2 * x + 1) * C::MXB + gid * GR;
+          const uint32_t b0 = lds_u<GR>(vb), b1 = lds_u<GR>(vb + 8 * GR);
+#pragma unroll
+          for (int c = 0; c < GR; ++c) {
+            if (((wide >> c) & 1u) == 0u) continue;
+            const int ref = (int)((refs >> (8 * c)) & 0xFFu);
+            const int e[2] = {(int)((b0 >> (8 * c)) & 0xFFu), (int)((b1 >> (8 * c)) & 0xFFu)};
+            int top[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {  // the lane's columns
+              top[q] = 0;
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (w4[2 * y + q] > 0.f) top[q] = max(top[q], (int)(__float_as_uint(w4[2 * y + q]) >> 23) + e[y]);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) top[q] = max(top[q], __shfl_xor_sync(kFull, top[q], off));
+            }
+            uint32_t bw[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float w[2];
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                w[q] = w4[2 * y + q] * __uint_as_float((uint32_t)min(max(e[y] - top[q] + 254, 0), 254) << 23);
+              bw[y] = movmatrix_t(pack2<false>(w[0], w[1]));
+            }
+            uint32_t r[4], a[4];
+            float part[4];
+            ldsm_x4_t((vat ^ (32 * (c / 2))) + x * 2 * C::TILEB, r);
+            const uint32_t ra = r[c & 1], rb = r[2 + (c & 1)];
+#pragma unroll
+            for (int odd = 0; odd < 2; ++odd) {
+              e2m1x8_to_f16x8(odd ? ((ra >> 4) & 0x0F0F0F0Fu) | (rb & 0xF0F0F0F0u)
+                                  : (ra & 0x0F0F0F0Fu) | ((rb << 4) & 0xF0F0F0F0u), a);
+              mma16816_f16_zero(part, a, bw[0], bw[1]);
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4)
+                acc[2 * c + odd][q4] += part[q4] * __uint_as_float((uint32_t)min(max(top[q4 & 1] - ref, 0), 254) << 23);
+            }
           }
         }
       }
