@@ -736,9 +736,13 @@ pkv_status pkv_paged_decode_attn_mx4(const pkv_cache_desc* desc, const void* k_c
  *            in the act dtype (bf16 queries are then taken as they are), V as above;
  *            a call with few rows over long or uneven prefixes shares their keys
  *            out over all SMs and adds the parts up there.
+ *            A smaller one of pkv_extend_mx4_runs_workspace_bytes() bytes or more (20.3 MB
+ *            at 128 dims, 10.3 at 64, whatever the pools' size) serves the calls of few
+ *            rows alone, a still smaller or misaligned one none.
  *            Calls that run at the same time need workspaces of their own.
  * ------------------------------------------------------------------------- */
 size_t pkv_extend_mx4_workspace_bytes(const pkv_cache_desc* desc);
+size_t pkv_extend_mx4_runs_workspace_bytes(const pkv_cache_desc* desc);
 
 pkv_status pkv_paged_extend_attn_mx4(const pkv_cache_desc* desc, const void* k_cache,
                                      const void* v_cache, const uint8_t* k_scales,

@@ -54,6 +54,7 @@ __all__ = ["F16", "BF16", "FP8_E4M3", "PkvError", "CacheDesc", "lib_path", "load
            "paged_extend_attn_window", "extend_block_scaled_workspace_bytes",
            "paged_extend_attn_block_scaled", "MX4", "kv_append_mx4", "kv_gather_mx4",
            "decode_mx4_workspace_bytes", "paged_decode_attn_mx4", "extend_mx4_workspace_bytes",
+           "extend_mx4_runs_workspace_bytes",
            "paged_extend_attn_mx4", "KvPools", "kv_copy_blocks", "kv_compact"]
 
 F16, BF16, FP8_E4M3, MX4 = 0, 1, 2, 3
@@ -183,6 +184,8 @@ def load():
         lib.pkv_paged_decode_attn_mx4.restype = I
         lib.pkv_extend_mx4_workspace_bytes.argtypes = [D]
         lib.pkv_extend_mx4_workspace_bytes.restype = SZ
+        lib.pkv_extend_mx4_runs_workspace_bytes.argtypes = [D]
+        lib.pkv_extend_mx4_runs_workspace_bytes.restype = SZ
         lib.pkv_paged_extend_attn_mx4.argtypes = lib.pkv_paged_extend_attn_block_scaled.argtypes
         lib.pkv_paged_extend_attn_mx4.restype = I
         lib.pkv_kv_copy_blocks.argtypes = [P, I32, P, P, I32, P]
@@ -940,13 +943,20 @@ def extend_mx4_workspace_bytes(k_cache) -> int:
     return int(load().pkv_extend_mx4_workspace_bytes(_desc_mx4(k_cache)))
 
 
+def extend_mx4_runs_workspace_bytes(k_cache) -> int:
+    """pkv_extend_mx4_runs_workspace_bytes: the part of it that calls with few rows over long prefixes
+    use, which does not grow with the pools."""
+    return int(load().pkv_extend_mx4_runs_workspace_bytes(_desc_mx4(k_cache)))
+
+
 def paged_extend_attn_mx4(k_cache, v_cache, k_scales, v_scales, q, out, q_indptr, prefix_lens,
                           block_tables, sm_scale, max_suffix_len, max_total_len, window=0,
                           sink_tokens=0, lse_out=None, workspace=None, stream=None):
     """pkv_paged_extend_attn_mx4: paged_extend_attn over e2m1 codes with microscales; window 0: every
     key, else as paged_extend_attn_window.  workspace: None, or a uint8 device tensor of
     extend_mx4_workspace_bytes() bytes or more (calls with many rows per request then widen the pages
-    they read once per block, calls with few rows over long prefixes are shared out over all SMs)."""
+    they read once per block, calls with few rows over long prefixes are shared out over all SMs), or of
+    extend_mx4_runs_workspace_bytes() (the latter alone)."""
     if _direct is not None:
         st = _direct.extend_mx4(k_cache, v_cache, k_scales, v_scales, q, out, q_indptr, prefix_lens,
                                 block_tables, sm_scale, max_suffix_len, max_total_len, window,

@@ -1583,6 +1583,10 @@ size_t pkv_extend_mx4_workspace_bytes(const pkv_cache_desc* desc) {
   return std::max(plain_widen_bytes(desc), runs_bytes(desc));
 }
 
+size_t pkv_extend_mx4_runs_workspace_bytes(const pkv_cache_desc* desc) {
+  return check_desc_mx4(desc) == PKV_OK ? runs_bytes(desc) : 0;
+}
+
 pkv_status pkv_paged_extend_attn_mx4(const pkv_cache_desc* desc, const void* k_cache,
                                      const void* v_cache, const uint8_t* k_scales,
                                      const uint8_t* v_scales, const void* q, void* out,
