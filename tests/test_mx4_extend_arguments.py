@@ -27,3 +27,13 @@ def test_workspace_of_calls_with_few_rows(lib):
     for bad in (_desc(), _desc(cache_dtype=2), mx4(head_dim=96), mx4(num_blocks=0)):
         assert lib.pkv_extend_mx4_runs_workspace_bytes(ctypes.byref(bad)) == 0
     assert lib.pkv_extend_mx4_runs_workspace_bytes(None) == 0
+
+
+@pytest.mark.parametrize("window", [0, 5])
+def test_softmax_scales(lib, window):
+    def extend(scale):
+        return lib.pkv_paged_extend_attn_mx4(ctypes.byref(mx4()), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE, 4, 2,
+                                             4, scale, 20, 10, 100, window, 0, None, None, 0, None)
+
+    for scale in (0.0, -0.0, -0.125, -float("inf"), float("inf"), float("nan")):
+        assert extend(scale) == 1, scale
