@@ -150,10 +150,10 @@ __device__ __forceinline__ void compact_rows(const CompactParams& p, const Pool&
   const int vecs = rows * vph;  // at most what the threads hold (the launcher picks p.heads so)
   auto look_up = [&](int pass) {
     if ((int)threadIdx.x < rows) {
-      const int i = pass * step + rank * rows + threadIdx.x;
+      const uint32_t i = (uint32_t)pass * step + rank * rows + threadIdx.x;  // (may pass 2^31)
       RowMove m;
       m.src_blk = -1;
-      if ((unsigned)i < (unsigned)n) m = find_move(p, b, r0, i, dst0, report);  // (i may pass 2^31)
+      if (i < (uint32_t)n) m = find_move(p, b, r0, (int)i, dst0, report);
       s_row[pass % 3][threadIdx.x] = m;
     }
   };
