@@ -82,9 +82,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 int elem_bytes(pkv_dtype d) { return d == PKV_FP8_E4M3 ? 1 : 2; }
 
-// Bytes that a value takes in a cache, its share of the scales included.
-double value_bytes(pkv_dtype d) { return d == PKV_MX4 ? 0.5 + 1.0 / kMxGroup : (double)elem_bytes(d); }
-
 bool valid_dtype(pkv_dtype d) { return d == PKV_F16 || d == PKV_BF16 || d == PKV_FP8_E4M3; }
 
 pkv_status check_desc(const pkv_cache_desc* d) {
@@ -698,7 +695,7 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
                         : d->head_dim != 128 ? 160.0 : window > 0 ? 90.0 : 100.0;
   const double over = window > 0 && !mx4 ? 1.25 : 1.0;
   const double sm_rate = mx4 ? (d->head_dim != 128 ? 416.0 : 236.0)
-                             : 44600.0 / (2.0 * d->head_dim * value_bytes(d->cache_dtype));
+                             : 44600.0 / (2.0 * d->head_dim * elem_bytes(d->cache_dtype));
   const double slots = 4.0 * sms;
   double best = 1e30;
   int best_s = 1;
@@ -738,7 +735,7 @@ static DecodePlan plan_view(const pkv_cache_desc* d, int batch, int hq, int max_
   const double fill = items / slots;
   const bool two = mx4 && window > 0;
   const bool falling = two          ? fill >= 0.5 && fill <= 1.5 && len >= 3500
-                       : window > 0 ? fill <= 1.5 && 2.0 * len * d->head_dim * value_bytes(d->cache_dtype) >= 0.9e6
+                       : window > 0 ? fill <= 1.5 && 2.0 * len * d->head_dim * elem_bytes(d->cache_dtype) >= 0.9e6
                                   : len >= (mx4 ? 2500 : 1000) && fill <= len / 800.0;
   if (fill >= 0.25 && falling) {
     const double ratio = two ? 0.4 : std::min(0.78, std::max(0.45, 0.45 + 0.75 * (0.75 - fill)));
