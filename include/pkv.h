@@ -728,7 +728,8 @@ pkv_status pkv_paged_decode_attn_mx4(const pkv_cache_desc* desc, const void* k_c
  * pkv_paged_extend_attn_mx4 -- pkv_paged_extend_attn over such a cache, optionally
  * under a window (0: none; as pkv_paged_extend_attn_window).  The kernel reads the
  * codes; K and V take part as f16(code * scale) (finite values beyond f16's range
- * become its largest, values below 2^-14 lose bits), bf16 queries as f16.
+ * become its largest; exact for scales from 2^-23 on, smaller ones lose bits), bf16
+ * queries as f16 (beyond its range infinite).
  * workspace: optional, as for pkv_paged_extend_attn: given
  *            pkv_extend_mx4_workspace_bytes() bytes or more, 256-byte aligned, any
  *            contents, a call with many rows per request first widens each block

@@ -72,17 +72,17 @@
 //     otherwise.  (Every tile so, scales drawn from 2^-17 to 2^-2: 2.2 to 2.7 times the
 //     call's time; where it does not happen the code for it costs 0.2 us in 3.7, 0.8 in
 //     40, 0.6 in 110.)
-//     A tile is a quarter of a 16-bit one and the arithmetic the same, so the kernel is
-//     bound by instructions (57 % of the ALU pipe's cycles and 58 % of the issue slots
-//     with two tiles a turn, memory 74 % of the copy's rate) and everything in it saves
-//     those: V's codes are merged by nibbles into the operands of two products (a token
+//     A tile is a quarter of a 16-bit one and the arithmetic the same, so instructions
+//     take longer than copies (a window of 4,096: arithmetic alone 101 us, copies alone
+//     90, which overlap to 110; ALU pipe 52 % and issue slots 59 % of their cycles, so
+//     neither is full), and everything in it saves those: V's codes are merged by nibbles into the operands of two products (a token
 //     of each in one byte, where a convert per nibble needed a permute each); scales are
 //     unpacked by one lane per token and passed through shared memory; the running
 //     maximum is looked at by a vote and reduced only when a score exceeds it by 8; NaN
 //     scales, a growing ref and scales below f16's range share one rare path.  Lanes
 //     copy 16 bytes each (cp.async): one lane issuing TMA copies of 1 KB was the longest
-//     chain of a turn (128 requests in a window of 4,096: 164 us; 110.5 now, 5.1 TB/s;
-//     copies alone 90).  64 requests of 512-4,096 tokens 40.7 us, 3 of up to 700 3.9.
+//     chain of a turn (128 requests in a window of 4,096: 164 us; 110.5 now, 5.1
+//     TB/s).  64 requests of 512-4,096 tokens 40.7 us, 3 of up to 700 3.9.
 //     Not kept, on the window: masks by a multiply of f16 pairs instead of a permute
 //     (123 against 114), five CTAs an SM at 96 registers (112 against 110), three stages or L2 prefetches
 //     (no change), K and V in copy groups of their own (117 against 114), rolled loops
@@ -125,7 +125,7 @@ struct DecodeCfg {
   static constexpr int COMB_BYTES = NW * 8 * HD * 4 + NW * 8 * 2 * 4;
   static constexpr int AREA = STAGE_AREA > COMB_BYTES ? STAGE_AREA : COMB_BYTES;
   // (MX: no TMA, so neither the slack to align a tile to its swizzle nor barriers;
-  // at 128 dims and three stages a CTA takes a quarter of an SM's shared memory)
+  // four CTAs of 39 KB an SM at 128 dims)
   static constexpr int SLACK = MX ? 0 : 1024;
   static constexpr int SMEM = SLACK + AREA + (MX ? 0 : NW * NS * 8);
   static constexpr int SMEM_BSC = SMEM + NW * NS * 8;  // and a tile's two scales per stage

@@ -84,7 +84,9 @@
 // in the 4 KB that the row's warp converts, so a __syncwarp orders them and no warp waits
 // for another (8 turns of 20-120 rows: 48 us (35 in runs, below), where pages widened once per call,
 // three launches more, took 61; 80 with the path of scales that f16 cannot hold inlined for each
-// 32 values: the loop left the instruction cache).  With many row tiles to a key
+// 32 values: the loop left the instruction cache).  That path takes a whole row where one
+// group's scale lies outside 2^-14 to 2^13, that of 32 zeros (2^-126) among them: rows of
+// 80 or 96 dims filled up to 128 with zeros all go through it.  With many row tiles to a key
 // tile (16 pairs, as for block scales) the pages are widened once per call instead:
 // 4 chunks of 2,000 rows over up to 9,000 tokens 714 us.
 //

@@ -31,8 +31,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(const ExtendP
     float m = -INFINITY, l = 0.f;
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int c0 = 0; c0 < parts; c0 += 2) {
-      // two parts at a time, all loads before their use (of a part without a key for
-      // the row nothing was written: its values are not used)
+      // two parts at a time, all loads before their use (the values of a part without a
+      // key for the row are not used: its weights' sum is 0)
       float2 s[2];
       uint32_t v[2][8];
 #pragma unroll

@@ -15,8 +15,8 @@ namespace pkv {
 namespace {
 
 // ---- pages ------------------------------------------------------------------
-// One CTA takes one piece of a pair's block in one pool: every thread has four
-// vectors in flight.  (Vectors of 32 bytes where the pool's blocks allow it.)
+// One CTA takes one piece of a pair's block in one pool: every thread has two
+// vectors of 32 bytes in flight, four of 16 or eight of 4, as the pool's blocks allow.
 constexpr int kCopyThreads = 256, kCopyUnroll = 2;
 constexpr int kPieceBytes = kCopyThreads * kCopyUnroll * 32;
 
