@@ -74,7 +74,7 @@
 //     40, 0.6 in 110.)
 //     A tile is a quarter of a 16-bit one and the arithmetic the same, so instructions
 //     take longer than copies (a window of 4,096: arithmetic alone 101 us, copies alone
-//     90, which overlap to 110; ALU pipe 52 % and issue slots 59 % of their cycles, so
+//     90, which overlap to 110; ALU pipe 56 % and issue slots 59 % of their cycles, so
 //     neither is full), and everything in it saves those: V's codes are merged by nibbles into the operands of two products (a token
 //     of each in one byte, where a convert per nibble needed a permute each); scales are
 //     unpacked by one lane per token and passed through shared memory; the running
