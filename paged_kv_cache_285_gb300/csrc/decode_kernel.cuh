@@ -69,7 +69,7 @@
 //     tokens' scales of a group span more than 2^11, or lie below what ref takes in, that
 //     group's P 2^vb gets a reference for each head and tile, and its product is added
 //     up in fp32: a token of large V and next to no weight would take the others' bits
-//     otherwise.  (Every tile so, scales drawn from 2^-17 to 2^-2: 2.2 to 2.7 times the
+//     otherwise.  (Every tile so, scales drawn from 2^-17 to 2^-1: 2.2 to 2.7 times the
 //     call's time; where it does not happen the code for it costs 0.2 us in 3.7, 0.8 in
 //     40, 0.6 in 110.)
 //     A tile is a quarter of a 16-bit one and the arithmetic the same, so instructions
@@ -684,12 +684,12 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
         for (int c = 0; c < GR; ++c)
           fk[c] = __uint_as_float((c == 3 ? wk >> 1 : wk << (23 - 8 * c)) & 0x7F800000u) * p.scale_log2;
-        // V's factors 2^(byte - ref), 4 more as y4, are 0 .. 11 in the usual case and
-        // need no borrow; else, and for a NaN, byte by byte.  (What passes 0 .. 11
+        // V's factors 2^(byte - ref): the exponents, 4 more, are 0 .. 11 in the usual case
+        // and need no borrow; else, and for a NaN, byte by byte.  (What passes 0 .. 11
         // shows in the sum's upper bits, unless it comes round to 0 .. 11 again: a byte
         // of 252 or more over a ref of 3 or less, whose upper bits show it; ref is 247 at
         // most, so that a NaN's byte, 255, gives 12 or more, and none comes round from
-        // below.)  x4: the f16 exponents.
+        // below.)  Then x4 has their f16 exponents.
         uint32_t x4 = wv + (0x04040404u - refs);
         const uint32_t nan_k = ((wk & 0x7F7F7F7Fu) + 0x01010101u) & wk & 0x80808080u;
         const bool rare = __any_sync(kFull, (nan_k | ((x4 | (x4 + 0x14141414u)) & 0xE0E0E0E0u) |
