@@ -701,9 +701,10 @@ pkv_status pkv_kv_gather_mx4(const pkv_cache_desc* desc, const void* k_cache, co
  * pkv_paged_decode_attn_mx4 -- pkv_paged_decode_attn over such a cache, optionally
  * under a window (0: none; as pkv_paged_decode_attn_window).  K's scales multiply
  * the scores' parts in fp32; weights and V's scales are multiplied in f16 relative to
- * a scale that is at most 2^4 times the token's, or, where tokens' scales lie too far
- * apart for that (more than 2^11 among 32, slower), to the largest weight times scale
- * of 16 tokens: a token of large V and little weight does not touch the others' bits.
+ * a scale that is at most 2^8 times the token's and 2^-4 of the largest weight, or,
+ * where tokens' scales lie too far apart for that (more than 2^15 among 32, slower),
+ * to the largest weight times scale of 16 tokens: a token of large V and little weight
+ * does not touch the others' bits.
  * Beside larger scales those of 2^-126 (rows of zeros have it) count as 0, and so may
  * those 2^100 below the largest; bf16 queries are taken as f16, as
  * over the fp8 caches.  A block id outside the pool reads zeros

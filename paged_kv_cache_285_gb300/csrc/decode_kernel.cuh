@@ -66,12 +66,13 @@
 //     (s[t] = sum_g 2^(kb[t][g]) (K_g q_g)[t], fp32) and V's, which sits on the
 //     contracted side (tokens), goes into P: O_g += V_g^T (P 2^(vb[t][g] - ref)), with
 //     2^ref, near the tokens' V scales, multiplied back in fp32 at the end.  Where 32
-//     tokens' scales of a group span more than 2^11, or lie below what ref takes in, that
+//     tokens' scales of a group span more than 2^15, or lie below what ref takes in, that
 //     group's P 2^vb gets a reference for each head and tile, and its product is added
 //     up in fp32: a token of large V and next to no weight would take the others' bits
-//     otherwise.  (Every tile so, scales drawn from 2^-17 to 2^-1: 2.2 to 2.7 times the
-//     call's time; where it does not happen the code for it costs 0.2 us in 3.7, 0.8 in
-//     40, 0.6 in 110.)
+//     otherwise.  (Every tile so, scales drawn from 2^-17 to 2^-1: 2.0 to 2.4 times the call's
+//     time; tokens' sizes log-normal, the logarithm's deviation 1: as without, 1.5: 128 ->
+//     150 us from a cold L2 in a window of 4,096.  Where it does not happen the code for
+//     it costs 0.2 us in 3.7, 0.8 in 40, 1 in 110.)
 //     A tile is a quarter of a 16-bit one and the arithmetic the same, so instructions
 //     take longer than copies (a window of 4,096: arithmetic alone 101 us, copies alone
 //     90, which overlap to 110; ALU pipe 56 % and issue slots 59 % of their cycles, so
@@ -81,7 +82,7 @@
 //     maximum is looked at by a vote and reduced only when a score exceeds it by 8; NaN
 //     scales, a growing ref and scales below f16's range share one rare path.  Lanes
 //     copy 16 bytes each (cp.async): one lane issuing TMA copies of 1 KB was the longest
-//     chain of a turn (128 requests in a window of 4,096: 164 us; 110.5 now, 5.1
+//     chain of a turn (128 requests in a window of 4,096: 164 us; 111 now, 5.1
 //     TB/s).  64 requests of 512-4,096 tokens 40.7 us, 3 of up to 700 3.9.
 //     Not kept, on the window: masks by a multiply of f16 pairs instead of a permute
 //     (123 against 114), five CTAs an SM at 96 registers (112 against 110), three stages or L2 prefetches
@@ -629,8 +630,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     __syncthreads();
     // The sums of group c's dims are held relative to 2^(ref - 127), ref byte c of
-    // refs: V's scales enter as f16 factors 2^(byte - ref) of the weights, of 2^-4 (below
-    // that weights would lose bits that count where the larger scales have none) to 2^7
+    // refs: V's scales enter as f16 factors 2^(byte - ref) of the weights, of 2^-8 (below
+    // that weights would lose bits that count where larger scales carry no weight) to 2^7
     // (with weights of at most 2^8 their products stay inside f16).  When larger bytes
     // come, ref moves to 5 (7) below the largest of them and the sums follow.  Where
     // a pair of tiles has bytes that no ref spans, or smaller ones than ref spans, the
@@ -684,17 +685,16 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
         for (int c = 0; c < GR; ++c)
           fk[c] = __uint_as_float((c == 3 ? wk >> 1 : wk << (23 - 8 * c)) & 0x7F800000u) * p.scale_log2;
-        // V's factors 2^(byte - ref): the exponents, 4 more, are 0 .. 11 in the usual case
-        // and need no borrow; else, and for a NaN, byte by byte.  (What passes 0 .. 11
-        // shows in the sum's upper bits, unless it comes round to 0 .. 11 again: a byte
-        // of 252 or more over a ref of 3 or less, whose upper bits show it; ref is 247 at
-        // most, so that a NaN's byte, 255, gives 12 or more, and none comes round from
-        // below.)  Then x4 has their f16 exponents.
-        uint32_t x4 = wv + (0x04040404u - refs);
+        // V's factors 2^(byte - ref): their f16 exponents, 15 more, are 7 .. 22 in the
+        // usual case and need no borrow; else, and for a NaN, byte by byte.  (What leaves
+        // 7 .. 22 shows in the sum's upper bits, unless it comes round to 7 .. 22 again: a
+        // byte of 248 or more over a ref of 7 or less, whose upper bits show it; ref is
+        // 247 at most, so that a NaN's byte, 255, gives 23 or more, and none comes round
+        // from below.)
+        uint32_t x4 = wv + (0x0F0F0F0Fu - refs);
         const uint32_t nan_k = ((wk & 0x7F7F7F7Fu) + 0x01010101u) & wk & 0x80808080u;
-        const bool rare = __any_sync(kFull, (nan_k | ((x4 | (x4 + 0x14141414u)) & 0xE0E0E0E0u) |
+        const bool rare = __any_sync(kFull, (nan_k | (((x4 + 0x09090909u) & 0xF0F0F0F0u) ^ 0x10101010u) |
                                              (wv & (wv << 1) & ~refs & 0x80808080u)) != 0u);
-        x4 += 0x0B0B0B0Bu;
         wide = 0u;
         if (rare) {
           x4 = 0u;
@@ -713,10 +713,10 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             // nothing beside scales that leave it out, 6 2^-126 at most.
             const int top = __reduce_max_sync(kFull, e), low = __reduce_min_sync(kFull, e > 1 ? e : 255);
             bool apart = false;
-            if (top > ref + 7 || low < ref - 4) {
+            if (top > ref + 7 || low < ref - 8) {
               int to = ref;
-              if (top > ref + 7 && top - low <= 11) {
-                to = min(top - (top - low <= 9 ? 5 : 7), 247);
+              if (top > ref + 7 && top - low <= 15) {
+                to = min(top - (top - low <= 13 ? 5 : 7), 247);
               } else {  // (the sums stay below 2^128)
                 apart = true;
                 to = max(ref, top - 90);
@@ -732,7 +732,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               }
             }
             if (apart) wide |= 1u << c;
-            x4 |= (apart || e < ref - 4 ? 0u : (uint32_t)(e - ref + 15)) << (8 * c);
+            x4 |= (apart || e < ref - 8 ? 0u : (uint32_t)(e - ref + 15)) << (8 * c);
           }
         }
         const uint32_t y4 = __shfl_xor_sync(kFull, x4, 1);  // the other token of the pair
@@ -792,8 +792,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           for (int q4 = 0; q4 < 4; ++q4)
             if (hidden(x, gid + (q4 >> 1) * 8)) sc[x][q4] = -INFINITY;
       }
-      // The base of the exponents moves only when a score passes it by more than
-      // 2^8: as long as no lane has one, the columns' maxima are not needed.
+      // The base of the exponents moves only when a score passes it by more than 8 (to
+      // 4 below: the largest weight is 2^4 to 2^8, so that small factors leave small
+      // weights f16's bits): as long as no lane has one, the columns' maxima are not needed.
       float mx_e = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
       float mx_o = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
       if (__any_sync(kFull, mx_e > m_e + 8.f || mx_o > m_o + 8.f)) {
@@ -802,7 +803,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           mx_e = fmaxf(mx_e, __shfl_xor_sync(kFull, mx_e, off));
           mx_o = fmaxf(mx_o, __shfl_xor_sync(kFull, mx_o, off));
         }
-        const float mn_e = mx_e > m_e + 8.f ? mx_e : m_e, mn_o = mx_o > m_o + 8.f ? mx_o : m_o;
+        const float mn_e = mx_e > m_e + 8.f ? mx_e - 4.f : m_e, mn_o = mx_o > m_o + 8.f ? mx_o - 4.f : m_o;
         const float al_e = mn_e == m_e ? 1.f : fast_exp2(m_e - mn_e);
         const float al_o = mn_o == m_o ? 1.f : fast_exp2(m_o - mn_o);
         m_e = mn_e;
@@ -936,10 +937,14 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (++st == NS) st = 0;
     }
     cp_async_wait<0>();
-    // the sums in their own scale
+    // the sums in their own scale, and as of weights 2^4 smaller (see the base above)
+    l_e *= 0.0625f;
+    l_o *= 0.0625f;
+    m_e += 4.f;
+    m_o += 4.f;
 #pragma unroll
     for (int c = 0; c < GR; ++c) {
-      const float f = e8m0_to_f32((refs >> (8 * c)) & 0xFFu);
+      const float f = e8m0_to_f32((refs >> (8 * c)) & 0xFFu) * 0.0625f;
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) {
         acc[2 * c][q4] *= f;

@@ -7,8 +7,8 @@ dims, |v| <= 6 s; L2 norms are not used, every term is a worst case):
     the relative error of a weight, twice that with the sum's;
   * weights times scales in f16: 2^-11 relative, once for the weight and (slow path) once for the product;
     where they are subnormal less than themselves, and less than 2^-25 in units of the reference, which is at
-    most 2^4 scales of a token that shares one with others: min(w, 2^-21) s, twice (the weight's own step, and
-    the product's);
+    most 2^8 scales of a token that shares one with others, and 2^-4 of the largest weight: min(w, 2^-21) s,
+    twice (the weight's own step, and the product's);
   * tokens that share no reference (tiles of 16): 2^-25 of twice the largest w s of the tile, for each token;
   * fp32 sums over n tokens: n 2^-23; the output's own rounding: half its last place.
 """
